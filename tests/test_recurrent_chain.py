@@ -1,0 +1,118 @@
+"""The operators together, as a layer uses them: convolution -> gated
+recurrence and back, decoding after a prefill, and rotated C and B into the
+SSD."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import selective_state_space_31_amd as pkg
+from oracle import gated as og
+from selective_state_space_31_amd.workloads import make_ssd_problem
+from tests import _gated_bound as gb
+from tests._recurrent import Gated, f32, np64, within
+from tests._ssd_bound import silu, ssd_budget
+from tests.test_conv1d_bwd import Case as ConvCase
+from tests.test_conv1d_bwd import check as conv_check
+from tests.test_gated import backward_ok, forward_ok
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_training_step_through_convolution_and_recurrence(dtype):
+    """Every stage against float64 on its own inputs; for float32 also the
+    whole chain's gradients against differences of the float64 loss."""
+    b, L, d = 2, 300, 66
+    c = ConvCase(b, L, d, 4, dtype, 1, dfinal=False)
+    p = Gated((b, L), b, d, dtype, DEV, 2)
+    p.x = pkg.ssm_causal_conv1d_fwd(c.x, c.w, c.bias, c.state)
+    out, last, mid = pkg.ssm_gated_scan_fwd(*p.args(), return_last_state=True, return_chunk_states=True, **p.kw())
+    forward_ok(p, out, last, mid)
+    g = pkg.ssm_gated_scan_bwd(*p.args(), p.dout, dlast_state=p.dlast, chunk_states=mid, **p.kw())
+    backward_ok(p, g)
+    c.dout = g["dx"]
+    gc = pkg.ssm_causal_conv1d_bwd(*c.args(), **c.kw())
+    conv_check(c, gc)
+    if dtype == "bf16":
+        return
+    h, dout, dl = p.host()
+    rng = np.random.default_rng(3)
+    base = dict(x=np64(c.x), w=np64(c.w), bias=np64(c.bias), state=np64(c.state))
+
+    def loss(v):
+        before = v["state"].transpose(0, 2, 1)
+        xx = np.concatenate([before, v["x"]], 1)
+        pre = v["bias"] + sum(v["w"][:, k] * xx[:, k:k + L] for k in range(4))
+        o, l, _ = og.gated_scan(**dict(h, x=pre / (1 + np.exp(-pre))))
+        return (o * dout).sum() + (l * dl).sum()
+    for key, grad in (("x", "dx"), ("w", "dweight"), ("bias", "dbias"), ("state", "dinitial_conv_state")):
+        way = rng.standard_normal(base[key].shape)
+        e = 1e-5  # the difference's own error is e^2 of third derivatives and 1e-16 / e of the loss
+        want = (loss(dict(base, **{key: base[key] + e * way})) - loss(dict(base, **{key: base[key] - e * way}))) / (2 * e)
+        terms = np64(gc[grad]) * way
+        # each gradient value is within 1e-4 of its size (the stages' bounds); a sum of n such terms
+        assert abs(terms.sum() - want) <= 1e-4 * np.abs(terms).sum() + 1e-6, key
+
+
+def test_decode_after_prefill():
+    """Convolution and recurrence decoded token by token, behind a prefill,
+    equal the whole sequence at once."""
+    b, L, d, cut = 3, 50, 130, 37
+    c = ConvCase(b, L, d, 4, "fp32", 4)
+    p = Gated((b, L), b, d, "fp32", DEV, 5)
+    u = pkg.ssm_causal_conv1d_fwd(c.x, c.w, c.bias, c.state)
+    p.x = u
+    whole, last = pkg.ssm_gated_scan_fwd(*p.args(), return_last_state=True, **p.kw())
+    part = lambda t, s: t[:, s].contiguous()
+    pre = slice(0, cut)
+    u0, cs = pkg.ssm_causal_conv1d_fwd(part(c.x, pre), c.w, c.bias, c.state, return_final_state=True)
+    kw = dict(rgate_bias=p.rb, igate_bias=p.ib)
+    o, state = pkg.ssm_gated_scan_fwd(u0, part(p.r, pre), part(p.i, pre), p.A, z=part(p.z, pre),
+                                      initial_state=p.h0, return_last_state=True, **kw)
+    outs = [o]
+    for t in range(cut, L):
+        x1 = pkg.ssm_causal_conv1d_update(cs, part(c.x, t), c.w, c.bias)
+        outs.append(pkg.ssm_gated_state_update(state, x1, part(p.r, t), part(p.i, t), p.A, z=part(p.z, t), **kw)[:, None])
+    h, _, _ = p.host()
+    bo, bl, _, _ = gb.forward(**h)
+    # two float32 results, each within its bound; the convolution's own rounding reaches the recurrence as 8 e of x
+    within(torch.cat(outs, 1), np64(whole), 4 * bo, "out")
+    within(state, np64(last), 4 * bl, "state")
+
+
+def test_rotated_keys_and_queries_feed_the_ssd():
+    """C and B as slices of one projection, normalised and rotated, into
+    ssm_ssd_fwd: within the SSD's own bound on those inputs, and unchanged
+    (to the inputs' rounding) when every position moves by the same amount."""
+    b, L, H, P, N, G = 1, 200, 4, 64, 64, 2
+    s = make_ssd_problem(b, L, H, P, N, G, seed=6, device=DEV, gate=True)
+    rng = np.random.default_rng(7)
+    rows = torch.from_numpy(rng.standard_normal((b, L, 2 * G * N + 32)).astype(np.float32)).to(torch.bfloat16).to(DEV)
+    C, B = rows[..., :G * N].unflatten(-1, (G, N)), rows[..., G * N:2 * G * N].unflatten(-1, (G, N))
+    freq = torch.from_numpy((1000.0 ** (-np.arange(N // 2) / (N // 2))).astype(np.float32)).to(DEV)
+    qw, kw = 1.0 + f32(rng, (N,), DEV, 0.1), 1.0 + f32(rng, (N,), DEV, 0.1)
+    outs = []
+    for first in (0, 4096):
+        pos = (torch.arange(L, dtype=torch.int32, device=DEV) + first).expand(b, L).contiguous()
+        Cr, Br = pkg.ssm_qk_norm_rotate_fwd(C, B, freq, q_weight=qw, k_weight=kw, positions=pos)
+        out = pkg.ssm_ssd_fwd(s.x, s.dt, s.A, Br, Cr, D=s.D, z=s.z, dt_bias=s.dt_bias)
+        h = [t.to(torch.float32).cpu().numpy() for t in (s.x, s.dt, s.A, Br, Cr)]
+        ref, _ = oracle.ssd_scan(*h, D=s.D.cpu().numpy(), z=s.z.float().cpu().numpy(), dt_bias=s.dt_bias.cpu().numpy())
+        E1, E2, _ = ssd_budget(*h, dt_bias=s.dt_bias.cpu().numpy())
+        gate = np.abs(silu(s.z.float().cpu().numpy()))
+        u = 2.0 ** -8
+        within(out, ref, 2 * u * np.abs(ref) + 2 * u * (E1 + E2) * gate + 1e-6, "ssd at %d" % first)
+        outs.append((np64(out), u, E1, E2, gate, ref))
+    (a, u, E1, E2, gate, ref), (c, *_) = outs
+    # C and B round to bf16 differently at the two places: |C.B| moves by at most 2 u |C||B| (norms sqrt(N) each, up to
+    # the weights), which E1's |C.B| does not bound; compare with the sum of the weights times that
+    w = np.abs(qw.cpu().numpy()).max() * np.abs(kw.cpu().numpy()).max() * N
+    dt = np.log1p(np.exp(s.dt.float().cpu().numpy() + s.dt_bias.cpu().numpy()))
+    x = np.abs(s.x.float().cpu().numpy())
+    acc, lim = np.zeros((b, H, P)), np.zeros((b, L, H, P))
+    for t in range(L):
+        acc = acc * np.exp(dt[:, t] * s.A.cpu().numpy())[..., None] + dt[:, t][..., None] * x[:, t]
+        lim[:, t] = acc
+    within(a, c, 2 * (2 * u * np.abs(ref) + 2 * u * (E1 + E2) * gate) + 2 * u * w * lim * gate + 1e-6, "moved")
