@@ -55,7 +55,8 @@ extern "C" {
  *                       or NULL; receives the state before every
  *                       SSM_GATED_CHUNK-th token, for ssm_gated_scan_bwd
  *   batch, dim >= 1; seqlen >= 0 (0 only copies the initial state);
- *   dim <= 2^24; batch <= 65535 (SSM_ERR_SHAPE beyond).
+ *   dim <= 2^24; batch <= 65535; batch * ceil(seqlen / 128) * ceil(dim / 64)
+ *   < 2^31 (SSM_ERR_SHAPE beyond).
  *   workspace         : at least ssm_gated_scan_fwd_workspace_bytes(...) bytes
  * Bitwise reproducible run to run on one device.
  */

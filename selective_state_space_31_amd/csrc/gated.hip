@@ -9,37 +9,271 @@
 
 namespace ssm {
 
-// One lane per (sequence, channel) walks the tokens.
-template <typename TA, bool NORM>
-__global__ void __launch_bounds__(64) gated_fwd_kernel(GatedFwdArgs<TA> p) {
-  const int c = blockIdx.x * 64 + threadIdx.x;
-  const int64_t s = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;
-  const int64_t nseq = p.cu ? p.nseq : p.rows;
-  if (c >= p.dim || s >= nseq) return;
-  int64_t t0, t1;
-  seq_range(p.cu, s, p.L, t0, t1);
-  const float A = p.A[c], rb = p.rb ? p.rb[c] : 0.0f, ib = p.ib ? p.ib[c] : 0.0f;
-  const int64_t nch = (p.L + SSM_GATED_CHUNK - 1) / SSM_GATED_CHUNK;
-  float h = p.h0 ? p.h0[s * p.dim + c] : 0.0f;
-  for (int64_t t = t0; t < t1; ++t) {
-    const int64_t tr = p.cu ? t : t - t0;  // token in its row
-    if (p.chunk_states && tr % SSM_GATED_CHUNK == 0)
-      p.chunk_states[((p.cu ? 0 : s) * nch + tr / SSM_GATED_CHUNK) * p.dim + c] = h;
-    const int64_t o = t * p.dim + c;
-    float a, m;
-    decay<NORM>(A * sigmoid_f32(to_f32(p.r[o]) + rb), a, m);
-    h = __builtin_fmaf(a, h, m * sigmoid_f32(to_f32(p.i[o]) + ib) * to_f32(p.x[o]));
-    store_act(p.out + o, p.z ? h * silu_f32(to_f32(p.z[o])) : h);
+// Ones into the published words, zero into the counter; empty sequences'
+// states.  A grid-stride loop over each.
+__global__ void __launch_bounds__(256) gated_init_kernel(uint64_t* words, int64_t nwords,
+                                                         uint32_t* turn, const int32_t* cu,
+                                                         int64_t nstates, int dim,
+                                                         const float* from, float* to) {
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t i = i0; i < nwords; i += step) words[i] = ~uint64_t{0};
+  if (i0 == 0 && turn) *turn = 0;
+  for (int64_t i = i0; i < nstates; i += step) {
+    const int64_t s = i / dim;
+    if (!cu || cu[s + 1] <= cu[s]) to[i] = from ? from[i] : 0.0f;
   }
-  if (p.last) p.last[s * p.dim + c] = h;
 }
 
-template <typename TA, bool NORM>
-int launch_gated_fwd(const GatedFwdArgs<TA>& a, const char* fn, hipStream_t s) {
-  const int64_t nseq = a.cu ? a.nseq : a.rows;
-  const unsigned gy = static_cast<unsigned>(nseq < 65535 ? nseq : 65535);
-  const dim3 grid((a.dim + 63) / 64, gy, static_cast<unsigned>((nseq + gy - 1) / gy));
-  hipLaunchKernelGGL((gated_fwd_kernel<TA, NORM>), grid, dim3(64), 0, s, a);
+int launch_gated_init(void* ws, size_t bytes, const int32_t* cu, int64_t nseq, int64_t L, int dim,
+                      const float* from, float* to, const char* fn, hipStream_t s) {
+  const int64_t nwords = bytes ? static_cast<int64_t>(bytes - 256) / 8 : 0;
+  const int64_t nstates = to && (cu || L == 0) ? nseq * dim : 0;
+  const int64_t n = nwords > nstates ? nwords : nstates;
+  if (n == 0) return SSM_OK;
+  uint32_t* turn = bytes ? reinterpret_cast<uint32_t*>(static_cast<uint64_t*>(ws) + nwords) : nullptr;
+  const int64_t blocks = (n + 255) / 256;
+  hipLaunchKernelGGL(gated_init_kernel, dim3(static_cast<unsigned>(blocks < 2048 ? blocks : 2048)),
+                     dim3(256), 0, s, static_cast<uint64_t*>(ws), nwords, turn, cu, nstates, dim, from,
+                     to);
+  return launch_status(fn);
+}
+
+// One pass over the data: a workgroup loads its tokens once, turns them into
+// (a, b) in registers and composes its chunk's map; publishes that; waits for
+// the state that enters the chunk; and walks its tokens from there.  Chunks
+// come in groups of kGatedGroup.  A chunk reads the maps of the chunks before
+// it in its group, which exist as soon as those workgroups have read their
+// data, and one state per group, which the last chunk of the group before
+// hands on: the chain over the sequence is one step per 2048 tokens.  The
+// folds have a fixed order, so results repeat bit for bit.
+// Units are handed out by a counter, earlier chunks first: a workgroup waits
+// only for ones that are running or done.
+template <typename TA, int V, bool NORM, bool GATE, bool VL>
+__global__ void __launch_bounds__(64 * kGatedWaves, 4) gated_fwd_kernel(GatedFwdArgs<TA> p, GatedPlan pl) {
+  constexpr int T = kGatedT, W = kGatedWaves, C = 64 * V;
+  using IO = Cell<TA, V>;
+  __shared__ float2 s_agg[W][C];
+  __shared__ float2 s_in[kGatedGroup][C];
+  __shared__ float s_carry[C];
+  __shared__ uint32_t s_turn;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int dim = p.dim;
+  uint64_t* const agg = static_cast<uint64_t*>(p.ws);
+  uint64_t* const carries = agg + pl.chunks * pl.cells;
+  uint32_t unit = blockIdx.x;
+  if (pl.chunks > 1) {
+    if (threadIdx.x == 0)
+      s_turn = atomicAdd(reinterpret_cast<uint32_t*>(agg + (pl.chunks + pl.groups) * pl.cells), 1u);
+    __syncthreads();
+    unit = __builtin_amdgcn_readfirstlane(s_turn);
+    if (unit >= pl.units) return;  // (a workspace that another call uses at the same time)
+  }
+  const uint32_t lines = static_cast<uint32_t>(pl.units / pl.chunks);  // rows * tiles
+  const uint32_t c = unit / lines, line = unit % lines;
+  const uint32_t row = line / static_cast<uint32_t>(pl.tiles), tile = line % static_cast<uint32_t>(pl.tiles);
+  const int col0 = static_cast<int>(tile) * C, col = col0 + lane * V;
+  const bool have = col < dim;
+  const int64_t t0 = static_cast<int64_t>(c) * SSM_GATED_CHUNK + w * T;
+  int64_t end = p.L;
+  if (VL) {
+    const int64_t e = p.cu[p.nseq];
+    end = e < 0 ? 0 : (e < end ? e : end);
+  }
+  const int n = end <= t0 ? 0 : (end - t0 < T ? static_cast<int>(end - t0) : T);  // the wave's tokens
+
+  float a[V][T], b[V][T], y[V], H[V];  // y: first the sum of log decays
+  Marks mk{0, 0, 0};
+  uint32_t voff = have ? static_cast<uint32_t>(lane * V * sizeof(TA)) : kNoColumn;
+  const uint32_t rowb = static_cast<uint32_t>(dim) * sizeof(TA);
+  const int64_t base = (static_cast<int64_t>(row) * p.L + t0) * dim + col0;
+  const uint32_t span = n > 0 ? (static_cast<uint32_t>(n) * rowb - col0 * static_cast<uint32_t>(sizeof(TA))) : 0;
+  typename IO::raw_t zr[GATE ? T : 1];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    y[v] = 0.0f;
+    H[v] = 0.0f;
+  }
+  if (n > 0) {
+    typename IO::raw_t xr[T], rr[T], ir[T];
+    const rsrc_t rx = make_rsrc(p.x + base, span), rg = make_rsrc(p.r + base, span),
+                 ri = make_rsrc(p.i + base, span);
+#pragma unroll
+    for (int j = 0; j < T; ++j) {  // rows behind the last are that one again
+      const uint32_t so = static_cast<uint32_t>(j < n ? j : n - 1) * rowb;
+      rr[j] = IO::load(rg, voff, so);
+      ir[j] = IO::load(ri, voff, so);
+      xr[j] = IO::load(rx, voff, so);
+    }
+    if (VL) mk = find_marks(p.cu, static_cast<int>(p.nseq), t0, n);
+    float A[V], rb[V], ib[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      A[v] = have ? p.A[col + v] : 0.0f;
+      rb[v] = have && p.rb ? p.rb[col + v] : 0.0f;
+      ib[v] = have && p.ib ? p.ib[col + v] : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      if (j < n) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float m;
+          const float la = A[v] * sigmoid_f32(IO::get(rr[j], v) + rb[v]);
+          decay<NORM>(la, a[v][j], m);
+          y[v] += la;
+          b[v][j] = m * sigmoid_f32(IO::get(ir[j], v) + ib[v]) * IO::get(xr[j], v);
+        }
+        if (VL && (mk.starts >> j & 1)) {
+          const int64_t s = __builtin_amdgcn_readlane(mk.seq, j);
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            if (p.h0 && have) b[v][j] = __builtin_fmaf(a[v][j], p.h0[s * dim + col + v], b[v][j]);
+            H[v] = b[v][j];
+          }
+        } else {
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            H[v] = __builtin_fmaf(a[v][j], H[v], b[v][j]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          a[v][j] = 1.0f;
+          b[v][j] = 0.0f;
+        }
+      }
+    }
+    if (GATE) {
+      const rsrc_t rz = make_rsrc(p.z + base, span);
+#pragma unroll
+      for (int j = 0; j < T; ++j) zr[j] = IO::load(rz, voff, static_cast<uint32_t>(j < n ? j : n - 1) * rowb);
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    y[v] = VL && mk.starts ? kCut : keep_of(y[v]);
+    s_agg[w][lane * V + v] = make_float2(y[v], H[v]);
+  }
+  __syncthreads();
+  // the map of the waves before this one; the last wave also the chunk's
+  float yw[V], Hw[V], yt[V], Ht[V], h[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    yw[v] = -0.0f;
+    Hw[v] = 0.0f;
+  }
+  for (int k = 0; k < w; ++k) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float2 f = s_agg[k][lane * V + v];
+      compose<VL>(yw[v], Hw[v], f.x, f.y);
+    }
+  }
+  const int64_t cell = static_cast<int64_t>(line) * C + lane * V;
+  if (w == W - 1) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      yt[v] = yw[v];
+      Ht[v] = Hw[v];
+      compose<VL>(yt[v], Ht[v], y[v], H[v]);
+      if (c + 1 < pl.chunks) publish(agg + c * pl.cells + cell + v, yt[v], Ht[v]);
+    }
+  }
+  // the state that enters the chunk
+  if (c == 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = !VL && p.h0 && have ? p.h0[static_cast<int64_t>(row) * dim + col + v] : 0.0f;
+  } else {
+    const uint32_t first = c / kGatedGroup * kGatedGroup;
+    for (uint32_t j = first + w; j < c; j += W) {
+      float lo[V], hi[V];
+      await<V>(agg + j * pl.cells + cell, lo, hi);
+#pragma unroll
+      for (int v = 0; v < V; ++v) s_in[j - first][lane * V + v] = make_float2(lo[v], hi[v]);
+    }
+    if (w == W - 1) {
+      float lo[V], hi[V];
+      if (first > 0) {
+        await<V>(carries + c / kGatedGroup * pl.cells + cell, lo, hi);
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          hi[v] = !VL && p.h0 && have ? p.h0[static_cast<int64_t>(row) * dim + col + v] : 0.0f;
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) s_carry[lane * V + v] = hi[v];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = s_carry[lane * V + v];
+    for (uint32_t j = 0; j < c - first; ++j) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float2 f = s_in[j][lane * V + v];
+        h[v] = pass<VL>(f.x, f.y, h[v]);
+      }
+    }
+  }
+  if (w == W - 1 && (c + 1) % kGatedGroup == 0 && c + 1 < pl.chunks) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      publish(carries + (c + 1) / kGatedGroup * pl.cells + cell + v, 0.0f, pass<VL>(yt[v], Ht[v], h[v]));
+  }
+  if (w == 0 && p.chunk_states && have && p.L > 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      p.chunk_states[(static_cast<int64_t>(row) * pl.chunks + c) * dim + col + v] = h[v];
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = pass<VL>(yw[v], Hw[v], h[v]);
+  if (n > 0) {
+    const rsrc_t ro = make_rsrc(p.out + base, span);
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      if (j < n) {
+        float o[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          h[v] = VL && (mk.starts >> j & 1) ? b[v][j] : __builtin_fmaf(a[v][j], h[v], b[v][j]);
+          o[v] = GATE ? h[v] * silu_f32(IO::get(zr[j], v)) : h[v];
+        }
+        IO::store(ro, o, voff, static_cast<uint32_t>(j) * rowb);
+        if (VL && p.last && (mk.ends >> j & 1) && have) {
+          const int64_t s = __builtin_amdgcn_readlane(mk.seq, j);
+#pragma unroll
+          for (int v = 0; v < V; ++v) p.last[s * dim + col + v] = h[v];
+        }
+      }
+    }
+  }
+  if (!VL && p.last && c + 1 == pl.chunks && w == W - 1 && have && p.L > 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) p.last[static_cast<int64_t>(row) * dim + col + v] = h[v];
+  }
+}
+
+template <typename TA, int V>
+int launch_gated_fwd(const GatedFwdArgs<TA>& a, bool norm, const char* fn, hipStream_t s) {
+  const GatedPlan pl = gated_plan(a.rows, a.L, a.dim, V);
+  const int rc = launch_gated_init(a.ws, pl.bytes, a.cu, a.cu ? a.nseq : a.rows, a.L, a.dim, a.h0, a.last,
+                                   fn, s);
+  if (rc != SSM_OK || a.L == 0) return rc;
+  const dim3 grid(static_cast<unsigned>(pl.units)), block(64 * kGatedWaves);
+#define SSM_GATED_CASE(N, G, VLN)                                                              \
+  if (norm == N && (a.z != nullptr) == G && (a.cu != nullptr) == VLN)                          \
+    hipLaunchKernelGGL((gated_fwd_kernel<TA, V, N, G, VLN>), grid, block, 0, s, a, pl);
+  SSM_GATED_CASE(true, true, false)
+  SSM_GATED_CASE(true, false, false)
+  SSM_GATED_CASE(false, true, false)
+  SSM_GATED_CASE(false, false, false)
+  SSM_GATED_CASE(true, true, true)
+  SSM_GATED_CASE(true, false, true)
+  SSM_GATED_CASE(false, true, true)
+  SSM_GATED_CASE(false, false, true)
+#undef SSM_GATED_CASE
   return launch_status(fn);
 }
 
@@ -73,7 +307,15 @@ constexpr int64_t kGatedMaxSeqs = int64_t{1} << 24;
 // Whether batch, seqlen (or nseq, total_len) and dim can be launched.
 bool gated_sizes_ok(int64_t rows, int64_t L, int64_t nseq, int64_t dim, bool packed) {
   if (dim < 1 || dim > kGatedMaxDim || L < 0 || L > (int64_t{1} << 40) / dim) return false;
-  return packed ? (nseq >= 1 && nseq < kGatedMaxSeqs) : (rows >= 1 && rows <= 65535);
+  if (packed ? (nseq < 1 || nseq >= kGatedMaxSeqs) : (rows < 1 || rows > 65535)) return false;
+  // one launch: a workgroup per chunk and tile of at least 64 channels
+  return rows * ((L + SSM_GATED_CHUNK - 1) / SSM_GATED_CHUNK) * ((dim + 63) / 64) < (int64_t{1} << 31);
+}
+
+// Workspace of a time-split walk: for the narrowest tiles a call may take.
+size_t gated_walk_bytes(int64_t rows, int64_t L, int64_t dim) {
+  const GatedPlan one = gated_plan(rows, L, dim, 1), two = gated_plan(rows, L, dim, 2);
+  return one.bytes > two.bytes ? one.bytes : two.bytes;
 }
 
 namespace {
@@ -106,36 +348,40 @@ int gated_fwd(const char* fn, const void* x, const void* r, const void* i, const
   const size_t st = static_cast<size_t>(packed ? nseq : rows) * dim * 4;
   const size_t cst = static_cast<size_t>(rows) * ((L + SSM_GATED_CHUNK - 1) / SSM_GATED_CHUNK) * dim * 4;
   const size_t pd = static_cast<size_t>(dim) * 4;
+  const size_t need = gated_walk_bytes(rows, L, dim);
   const Span ins[] = {{x, tok, "x"}, {r, tok, "rgate"}, {i, tok, "igate"}, {z, z ? tok : 0, "z"},
                       {A, pd, "A"}, {rb, rb ? pd : 0, "rgate_bias"}, {ib, ib ? pd : 0, "igate_bias"},
                       {cu, packed ? static_cast<size_t>(nseq + 1) * 4 : 0, "cu_seqlens"},
                       {h0, h0 ? st : 0, "initial_state"}};
   const Span outs[] = {{out, tok, "out"}, {last, last ? st : 0, "last_state"},
-                       {chunk_states, chunk_states ? cst : 0, "chunk_states"}};
+                       {chunk_states, chunk_states ? cst : 0, "chunk_states"},
+                       {ws, ws ? need : 0, "workspace"}};
   for (const auto& o : outs)
     for (const auto& n : ins)
       if (overlap(o, n) && !(o.p == last && n.p == h0 && last == h0 && !packed))
         return fail(SSM_ERR_ALIAS, "%s: output %s overlaps input %s", fn, o.name, n.name);
-  for (int a = 0; a < 3; ++a)
-    for (int b = a + 1; b < 3; ++b)
+  for (int a = 0; a < 4; ++a)
+    for (int b = a + 1; b < 4; ++b)
       if (overlap(outs[a], outs[b]))
         return fail(SSM_ERR_ALIAS, "%s: %s overlaps %s", fn, outs[a].name, outs[b].name);
-  (void)ws;
-  (void)ws_bytes;
-  if (dtype == SSM_DTYPE_F32) {
-    GatedFwdArgs<float> a{static_cast<const float*>(x), static_cast<const float*>(r),
-                          static_cast<const float*>(i), static_cast<const float*>(z), A, rb, ib,
-                          static_cast<float*>(out), last, h0, chunk_states, cu, rows, L, nseq,
-                          static_cast<int>(dim), ws};
-    return normalize ? launch_gated_fwd<float, true>(a, fn, stream)
-                     : launch_gated_fwd<float, false>(a, fn, stream);
-  }
-  GatedFwdArgs<bf16_t> a{static_cast<const bf16_t*>(x), static_cast<const bf16_t*>(r),
-                         static_cast<const bf16_t*>(i), static_cast<const bf16_t*>(z), A, rb, ib,
-                         static_cast<bf16_t*>(out), last, h0, chunk_states, cu, rows, L, nseq,
-                         static_cast<int>(dim), ws};
-  return normalize ? launch_gated_fwd<bf16_t, true>(a, fn, stream)
-                   : launch_gated_fwd<bf16_t, false>(a, fn, stream);
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(SSM_ERR_WORKSPACE, "%s: workspace of %zu bytes given, %zu needed", fn,
+                ws ? ws_bytes : 0, need);
+  if (need > 0 && !aligned(ws, 256))
+    return fail(SSM_ERR_ALIGN, "%s: workspace is not 256-byte aligned", fn);
+  const auto args = [&](auto tag) {
+    using TA = decltype(tag);
+    return GatedFwdArgs<TA>{static_cast<const TA*>(x), static_cast<const TA*>(r),
+                            static_cast<const TA*>(i), static_cast<const TA*>(z), A, rb, ib,
+                            static_cast<TA*>(out), last, h0, chunk_states, packed ? cu : nullptr,
+                            rows, L, nseq, static_cast<int>(dim), ws};
+  };
+  if (dtype == SSM_DTYPE_F32) return launch_gated_fwd<float, 1>(args(float{}), normalize != 0, fn, stream);
+  // two channels a lane where every row starts on four bytes
+  const bool pairs = dim % 2 == 0 && aligned(x, 4) && aligned(r, 4) && aligned(i, 4) &&
+                     (!z || aligned(z, 4)) && aligned(out, 4);
+  return pairs ? launch_gated_fwd<bf16_t, 2>(args(bf16_t{}), normalize != 0, fn, stream)
+               : launch_gated_fwd<bf16_t, 1>(args(bf16_t{}), normalize != 0, fn, stream);
 }
 
 }  // namespace
@@ -155,7 +401,12 @@ int ssm_gated_scan_fwd(const void* x, const void* rgate, const void* igate, cons
                    dtype, false, workspace, workspace_bytes, stream);
 }
 
-size_t ssm_gated_scan_fwd_workspace_bytes(int64_t, int64_t, int64_t, int) { return 0; }
+size_t ssm_gated_scan_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int dtype) {
+  if ((dtype != SSM_DTYPE_F32 && dtype != SSM_DTYPE_BF16) ||
+      !gated_sizes_ok(batch, seqlen, batch, dim, false))
+    return 0;
+  return gated_walk_bytes(batch, seqlen, dim);
+}
 
 int ssm_gated_scan_fwd_varlen(const void* x, const void* rgate, const void* igate, const float* A,
                               const float* rgate_bias, const float* igate_bias, int normalize,
@@ -169,7 +420,13 @@ int ssm_gated_scan_fwd_varlen(const void* x, const void* rgate, const void* igat
                    total_len, dim, dtype, true, workspace, workspace_bytes, stream);
 }
 
-size_t ssm_gated_scan_fwd_varlen_workspace_bytes(int64_t, int64_t, int64_t, int) { return 0; }
+size_t ssm_gated_scan_fwd_varlen_workspace_bytes(int64_t nseq, int64_t total_len, int64_t dim,
+                                                 int dtype) {
+  if ((dtype != SSM_DTYPE_F32 && dtype != SSM_DTYPE_BF16) ||
+      !gated_sizes_ok(1, total_len, nseq, dim, true))
+    return 0;
+  return gated_walk_bytes(1, total_len, dim);
+}
 
 int ssm_gated_state_update(float* state, const void* x, const void* rgate, const void* igate,
                            const float* A, const float* rgate_bias, const float* igate_bias,

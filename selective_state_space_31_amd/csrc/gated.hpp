@@ -26,8 +26,7 @@ __device__ __forceinline__ float sigmoid_f32(float v) {
 // adds up) and m = sqrt(E (2 - E)) loses nothing to cancellation.  |la| <
 // 1/8: Taylor series of -expm1 to la^5 (the next term is below 2^-24 of it).
 // Elsewhere a <= 0.883 and E = 1 - a is exact enough (2^-24 / 0.117).
-template <bool NORM>
-__device__ __forceinline__ void decay(float la, float& a, float& m) {
+__device__ __forceinline__ float decay_parts(float la, float& a) {
   const float ex = __builtin_amdgcn_exp2f(la * kLog2e);
   float q = __builtin_fmaf(la, 1.0f / 120.0f, 1.0f / 24.0f);
   q = __builtin_fmaf(la, q, 1.0f / 6.0f);
@@ -36,8 +35,199 @@ __device__ __forceinline__ void decay(float la, float& a, float& m) {
   const bool near = __builtin_fabsf(la) < 0.125f;
   const float E = near ? -la * q : 1.0f - ex;
   a = near ? 1.0f - E : ex;
+  return E;
+}
+template <bool NORM>
+__device__ __forceinline__ void decay(float la, float& a, float& m) {
+  const float E = decay_parts(la, a);
   m = NORM ? __builtin_amdgcn_sqrtf(__builtin_fmaxf(E * (2.0f - E), 0.0f)) : 1.0f;
 }
+
+// ----------------------------------------------------------------------------
+// The walk over time.  A workgroup holds SSM_GATED_CHUNK tokens of a tile of
+// channels: wave w tokens [16 w, 16 w + 16), a lane V channels side by side,
+// everything in registers.  A stretch of tokens maps the state before it to
+// the state after it, h -> P h + H; the maps of waves and chunks compose.
+// ----------------------------------------------------------------------------
+constexpr int kGatedT = 16;                          // tokens of a wave
+constexpr int kGatedWaves = SSM_GATED_CHUNK / kGatedT;  // waves of a workgroup
+constexpr int kGatedGroup = 16;                      // chunks of a group (see gated.hip)
+
+// A lane's V channels of one token: the raw bits as loaded, widened at use.
+template <typename TA, int V>
+struct Cell;
+template <>
+struct Cell<float, 1> {
+  using raw_t = uint32_t;
+  __device__ static raw_t load(rsrc_t r, uint32_t vo, uint32_t so) {
+    return __builtin_amdgcn_raw_buffer_load_b32(r, vo, so, 0);
+  }
+  __device__ static float get(raw_t v, int) { return __uint_as_float(v); }
+  __device__ static void store(rsrc_t r, const float (&v)[1], uint32_t vo, uint32_t so) {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), r, vo, so, kStoreStream);
+  }
+};
+__device__ __forceinline__ uint32_t bf16_bits(float v) {
+  const __bf16 b = static_cast<__bf16>(v);  // round to nearest even
+  return __builtin_bit_cast(uint16_t, b);
+}
+template <>
+struct Cell<bf16_t, 1> {
+  using raw_t = uint16_t;
+  __device__ static raw_t load(rsrc_t r, uint32_t vo, uint32_t so) {
+    return __builtin_amdgcn_raw_buffer_load_b16(r, vo, so, 0);
+  }
+  __device__ static float get(raw_t v, int) {
+    return __uint_as_float(static_cast<uint32_t>(v) << 16);
+  }
+  __device__ static void store(rsrc_t r, const float (&v)[1], uint32_t vo, uint32_t so) {
+    __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(bf16_bits(v[0])), r, vo, so,
+                                          kStoreStream);
+  }
+};
+template <>
+struct Cell<bf16_t, 2> {
+  using raw_t = uint32_t;
+  __device__ static raw_t load(rsrc_t r, uint32_t vo, uint32_t so) {
+    return __builtin_amdgcn_raw_buffer_load_b32(r, vo, so, 0);
+  }
+  __device__ static float get(raw_t v, int k) {
+    return __uint_as_float(k ? (v & 0xffff0000u) : (v << 16));
+  }
+  __device__ static void store(rsrc_t r, const float (&v)[2], uint32_t vo, uint32_t so) {
+    __builtin_amdgcn_raw_buffer_store_b32(bf16_bits(v[0]) | (bf16_bits(v[1]) << 16), r, vo, so,
+                                          kStoreStream);
+  }
+};
+
+// Byte offset that no descriptor here covers (a wave's rows span at most
+// 16 * 2^24 * 4 = 2^30 bytes): lanes beyond the last channel use it, so their
+// loads give 0 and their stores are dropped by the range check.
+constexpr uint32_t kNoColumn = 0x7fffff00u;
+
+// The map h -> P h + H of a stretch is kept as (y, H).  y >= +0 is P itself;
+// y with the sign set is P - 1, for P from 1/2 to 1: a product of decays next
+// to 1 loses the same way at every factor when it is rounded (1 - p)(1 - e) ->
+// 1 - p - e, which a memory of thousands of tokens shows (1.1e-5 at 6000
+// tokens with decays of 1 - 1e-5 to 1 - 1e-3, against 1e-6 in this form).
+// kCut: a sequence starts inside the stretch, nothing of the incoming state
+// passes; it is left out rather than multiplied by zero, so that a NaN or an
+// infinity stays in its own sequence.
+constexpr float kCut = -2.0f;
+__device__ __forceinline__ bool below_one(float y) { return __float_as_int(y) < 0; }
+
+// y of a stretch whose log decays add up to S (the identity for 0).
+__device__ __forceinline__ float keep_of(float S) {
+  float a;
+  const float E = decay_parts(S, a);
+  return E < 0.5f && E >= 0.0f ? -__builtin_fabsf(E) : a;
+}
+template <bool VL>
+__device__ __forceinline__ float pass(float y, float H, float h) {
+  const float r = __builtin_fmaf(y, h, below_one(y) ? h : 0.0f) + H;
+  if constexpr (VL) return y == kCut ? H : r;
+  return r;
+}
+// (y1, H1) followed by (y2, H2).
+template <bool VL>
+__device__ __forceinline__ void compose(float& y1, float& H1, float y2, float H2) {
+  H1 = pass<VL>(y2, H2, H1);
+  const bool n1 = below_one(y1), n2 = below_one(y2);
+  const float both = __builtin_fmaf(y1, y2, y1) + y2;  // (1 + y1)(1 + y2) - 1
+  float y = n1 ? (n2 ? (both >= -0.5f ? both : 1.0f + both) : __builtin_fmaf(y1, y2, y2))
+               : __builtin_fmaf(y1, y2, n2 ? y1 : 0.0f);
+  if constexpr (VL) {
+    if (y1 == kCut || y2 == kCut) y = kCut;
+  }
+  y1 = y;
+}
+
+// Which of a wave's tokens start and end their sequence (bit per token), and
+// each token's sequence (held by lane j for token j).
+struct Marks {
+  uint32_t starts, ends;
+  int seq;
+};
+__device__ __forceinline__ Marks find_marks(const int32_t* cu, int nseq, int64_t t0, int n) {
+  const int lane = threadIdx.x & 63;
+  Marks m{0, 0, 0};
+  bool st = false, en = false;
+  if (lane < n) {
+    const int64_t t = t0 + lane;
+    int lo = 0, hi = nseq;  // the last s < nseq with cu[s] <= t: empty sequences are passed over
+    while (hi - lo > 1) {
+      const int mid = lo + ((hi - lo) >> 1);
+      if (cu[mid] <= t) lo = mid; else hi = mid;
+    }
+    m.seq = lo;
+    st = cu[lo] == t;
+    en = cu[lo + 1] == t + 1;
+  }
+  m.starts = static_cast<uint32_t>(__ballot(st));
+  m.ends = static_cast<uint32_t>(__ballot(en));
+  return m;
+}
+
+// Publishing between workgroups.  A word is written once, as a whole, and
+// says by itself that it is there: the launch before fills the words with
+// ones, which no published word equals.  Relaxed 64-bit atomics at device
+// scope, so nothing has to be flushed or invalidated around them.
+__device__ __forceinline__ void publish(uint64_t* at, float lo, float hi) {
+  uint32_t a = __float_as_uint(lo);
+  if (a == 0xffffffffu) a = 0x7fc00000u;  // a NaN of another payload
+  __hip_atomic_store(at, (static_cast<uint64_t>(__float_as_uint(hi)) << 32) | a, __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+// The lane's V words, once they are all there.  Every wait is for a
+// workgroup that took its turn earlier and publishes without waiting for a
+// later one, so it ends.  Should the words be overwritten meanwhile (a
+// workspace given to two calls at once), the wait still ends, after a second,
+// and gives NaN.
+constexpr int kWaitLimit = 1 << 20;
+template <int V>
+__device__ __forceinline__ void await(uint64_t* at, float (&lo)[V], float (&hi)[V]) {
+  uint64_t w[V];
+  for (int n = 0;; ++n) {
+    bool there = true;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      w[v] = __hip_atomic_load(at + v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      there = there && w[v] != ~uint64_t{0};
+    }
+    if (__all(there) || n >= kWaitLimit) break;
+    __builtin_amdgcn_s_sleep(1);
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    lo[v] = __uint_as_float(static_cast<uint32_t>(w[v]));
+    hi[v] = __uint_as_float(static_cast<uint32_t>(w[v] >> 32));
+  }
+}
+
+// The workspace of a time-split launch.  `cells` channel slots (rows * tiles
+// * 64 V), chunk-major, so that a chunk's words lie together:
+//   agg   (chunks, cells): a chunk's map (y, H)
+//   carry (groups, cells): the state that enters a group, {0, h}
+//   turn  the counter that hands out the units
+struct GatedPlan {
+  int64_t chunks, groups, tiles, cells, units;
+  size_t bytes;  // 0: one chunk per row, no workspace
+};
+inline GatedPlan gated_plan(int64_t rows, int64_t L, int64_t dim, int V) {
+  GatedPlan p;
+  p.chunks = L > 0 ? (L + SSM_GATED_CHUNK - 1) / SSM_GATED_CHUNK : 1;
+  p.groups = (p.chunks + kGatedGroup - 1) / kGatedGroup;
+  p.tiles = (dim + 64 * V - 1) / (64 * V);
+  p.cells = rows * p.tiles * 64 * V;
+  p.units = rows * p.tiles * p.chunks;
+  p.bytes = p.chunks > 1 ? static_cast<size_t>(p.chunks + p.groups) * p.cells * 8 + 256 : 0;
+  return p;
+}
+
+// Fills the words with ones and the counter with zero, and moves the state
+// of empty sequences (`empty_to`, packed only) through unchanged.
+int launch_gated_init(void* ws, size_t bytes, const int32_t* cu, int64_t nseq, int64_t L, int dim,
+                      const float* empty_from, float* empty_to, const char* fn, hipStream_t s);
 
 // Arguments of the forward over `rows` rows of `L` tokens (dense: rows = batch;
 // packed: one row of total_len tokens, with cu set).
@@ -66,19 +256,5 @@ struct GatedBwdArgs {
   int dim;
   void* ws;
 };
-
-// Tokens [t0, t1) of sequence s (clamped: offsets that break the rule stay in
-// the buffers).
-__device__ __forceinline__ void seq_range(const int32_t* cu, int64_t s, int64_t L, int64_t& t0,
-                                          int64_t& t1) {
-  if (!cu) {
-    t0 = s * L;
-    t1 = t0 + L;
-    return;
-  }
-  const int64_t a = cu[s], b = cu[s + 1];
-  t0 = a < 0 ? 0 : (a > L ? L : a);
-  t1 = b < t0 ? t0 : (b > L ? L : b);
-}
 
 }  // namespace ssm

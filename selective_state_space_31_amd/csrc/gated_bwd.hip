@@ -14,6 +14,20 @@ namespace ssm {
 
 bool gated_sizes_ok(int64_t rows, int64_t L, int64_t nseq, int64_t dim, bool packed);
 
+// Tokens [t0, t1) of sequence s (clamped: offsets that break the rule stay in
+// the buffers).
+__device__ __forceinline__ void seq_range(const int32_t* cu, int64_t s, int64_t L, int64_t& t0,
+                                          int64_t& t1) {
+  if (!cu) {
+    t0 = s * L;
+    t1 = t0 + L;
+    return;
+  }
+  const int64_t a = cu[s], b = cu[s + 1];
+  t0 = a < 0 ? 0 : (a > L ? L : a);
+  t1 = b < t0 ? t0 : (b > L ? L : b);
+}
+
 // One lane per (sequence, channel): a walk forward that leaves every h_{t-1}
 // in the workspace, then one back.  Partial sums per sequence, (3, nseq, dim).
 template <typename TA, bool NORM>
