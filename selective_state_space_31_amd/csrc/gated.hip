@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) gated_fwd_kernel(GatedFwd
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) h[v] = pass<VL>(yw[v], Hw[v], h[v]);
-  if (n > 0) {
+  if (n > 0 && p.out) {  // (without out: the chunks' states alone)
     const rsrc_t ro = make_rsrc(p.out + base, span);
 #pragma unroll
     for (int j = 0; j < T; ++j) {
@@ -318,6 +318,34 @@ size_t gated_walk_bytes(int64_t rows, int64_t L, int64_t dim) {
   return one.bytes > two.bytes ? one.bytes : two.bytes;
 }
 
+// The forward's launch for either type; bf16 with two channels a lane where
+// every row starts on four bytes.
+template <typename TA>
+int run_gated_fwd(const char* fn, const void* x, const void* r, const void* i, const float* A,
+                  const float* rb, const float* ib, bool norm, const void* z, void* out, float* last,
+                  const float* h0, float* states, const int32_t* cu, int64_t nseq, int64_t rows,
+                  int64_t L, int dim, void* ws, hipStream_t stream) {
+  const GatedFwdArgs<TA> a{static_cast<const TA*>(x), static_cast<const TA*>(r),
+                           static_cast<const TA*>(i), static_cast<const TA*>(z), A, rb, ib,
+                           static_cast<TA*>(out), last, h0, states, cu, rows, L, nseq, dim, ws};
+  if constexpr (sizeof(TA) == 2) {
+    if (dim % 2 == 0 && aligned(x, 4) && aligned(r, 4) && aligned(i, 4) && aligned(z, 4) && aligned(out, 4))
+      return launch_gated_fwd<TA, 2>(a, norm, fn, stream);
+  }
+  return launch_gated_fwd<TA, 1>(a, norm, fn, stream);
+}
+
+int gated_states(const char* fn, const void* x, const void* r, const void* i, const float* A,
+                 const float* rb, const float* ib, int normalize, const float* h0, float* states,
+                 const int32_t* cu, int64_t nseq, int64_t rows, int64_t L, int dim, int dtype,
+                 void* ws, hipStream_t stream) {
+  return dtype == SSM_DTYPE_F32
+             ? run_gated_fwd<float>(fn, x, r, i, A, rb, ib, normalize != 0, nullptr, nullptr, nullptr, h0,
+                                    states, cu, nseq, rows, L, dim, ws, stream)
+             : run_gated_fwd<bf16_t>(fn, x, r, i, A, rb, ib, normalize != 0, nullptr, nullptr, nullptr, h0,
+                                     states, cu, nseq, rows, L, dim, ws, stream);
+}
+
 namespace {
 
 int gated_fwd(const char* fn, const void* x, const void* r, const void* i, const float* A,
@@ -369,19 +397,13 @@ int gated_fwd(const char* fn, const void* x, const void* r, const void* i, const
                 ws ? ws_bytes : 0, need);
   if (need > 0 && !aligned(ws, 256))
     return fail(SSM_ERR_ALIGN, "%s: workspace is not 256-byte aligned", fn);
-  const auto args = [&](auto tag) {
-    using TA = decltype(tag);
-    return GatedFwdArgs<TA>{static_cast<const TA*>(x), static_cast<const TA*>(r),
-                            static_cast<const TA*>(i), static_cast<const TA*>(z), A, rb, ib,
-                            static_cast<TA*>(out), last, h0, chunk_states, packed ? cu : nullptr,
-                            rows, L, nseq, static_cast<int>(dim), ws};
-  };
-  if (dtype == SSM_DTYPE_F32) return launch_gated_fwd<float, 1>(args(float{}), normalize != 0, fn, stream);
-  // two channels a lane where every row starts on four bytes
-  const bool pairs = dim % 2 == 0 && aligned(x, 4) && aligned(r, 4) && aligned(i, 4) &&
-                     (!z || aligned(z, 4)) && aligned(out, 4);
-  return pairs ? launch_gated_fwd<bf16_t, 2>(args(bf16_t{}), normalize != 0, fn, stream)
-               : launch_gated_fwd<bf16_t, 1>(args(bf16_t{}), normalize != 0, fn, stream);
+  const int32_t* const offsets = packed ? cu : nullptr;
+  return dtype == SSM_DTYPE_F32
+             ? run_gated_fwd<float>(fn, x, r, i, A, rb, ib, normalize != 0, z, out, last, h0, chunk_states,
+                                    offsets, nseq, rows, L, static_cast<int>(dim), ws, stream)
+             : run_gated_fwd<bf16_t>(fn, x, r, i, A, rb, ib, normalize != 0, z, out, last, h0,
+                                     chunk_states, offsets, nseq, rows, L, static_cast<int>(dim), ws,
+                                     stream);
 }
 
 }  // namespace

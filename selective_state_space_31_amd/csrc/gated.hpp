@@ -134,7 +134,7 @@ __device__ __forceinline__ void compose(float& y1, float& H1, float y2, float H2
   H1 = pass<VL>(y2, H2, H1);
   const bool n1 = below_one(y1), n2 = below_one(y2);
   const float both = __builtin_fmaf(y1, y2, y1) + y2;  // (1 + y1)(1 + y2) - 1
-  float y = n1 ? (n2 ? (both >= -0.5f ? both : 1.0f + both) : __builtin_fmaf(y1, y2, y2))
+  float y = n1 ? (n2 ? (both >= -0.5f ? -__builtin_fabsf(both) : 1.0f + both) : __builtin_fmaf(y1, y2, y2))
                : __builtin_fmaf(y1, y2, n2 ? y1 : 0.0f);
   if constexpr (VL) {
     if (y1 == kCut || y2 == kCut) y = kCut;
@@ -255,6 +255,16 @@ struct GatedBwdArgs {
   int64_t rows, L, nseq;
   int dim;
   void* ws;
+  float* part;  // partial sums
 };
+
+// Whether these sizes can be launched; the walk's words for the narrowest
+// tiles a call may take; the states at the chunks' starts alone (gated.hip).
+bool gated_sizes_ok(int64_t rows, int64_t L, int64_t nseq, int64_t dim, bool packed);
+size_t gated_walk_bytes(int64_t rows, int64_t L, int64_t dim);
+int gated_states(const char* fn, const void* x, const void* r, const void* i, const float* A,
+                 const float* rb, const float* ib, int normalize, const float* h0, float* states,
+                 const int32_t* cu, int64_t nseq, int64_t rows, int64_t L, int dim, int dtype,
+                 void* ws, hipStream_t stream);
 
 }  // namespace ssm
