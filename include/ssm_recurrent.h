@@ -34,7 +34,7 @@ extern "C" {
 #endif
 
 /* Tokens between the states that the forward hands to the backward. */
-#define SSM_GATED_CHUNK 128
+#define SSM_GATED_CHUNK 64
 
 /*
  * Gated linear recurrence over whole sequences.  Per sequence b and channel d,
@@ -55,7 +55,7 @@ extern "C" {
  *                       or NULL; receives the state before every
  *                       SSM_GATED_CHUNK-th token, for ssm_gated_scan_bwd
  *   batch, dim >= 1; seqlen >= 0 (0 only copies the initial state);
- *   dim <= 2^24; batch <= 65535; batch * ceil(seqlen / 128) * ceil(dim / 64)
+ *   dim <= 2^24; batch <= 65535; batch * ceil(seqlen / 64) * ceil(dim / 64)
  *   < 2^31 (SSM_ERR_SHAPE beyond).
  *   workspace         : at least ssm_gated_scan_fwd_workspace_bytes(...) bytes
  * Bitwise reproducible run to run on one device.
@@ -83,7 +83,8 @@ size_t ssm_gated_scan_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t
  *   initial_state, last_state : (nseq, dim) float32 or NULL.  last_state may
  *                      not overlap initial_state.
  *   chunk_states     : (ceil(total_len / SSM_GATED_CHUNK), dim) float32 or
- *                      NULL; receives the state that enters token 128 c from
+ *                      NULL; receives the state that enters token
+ *                      SSM_GATED_CHUNK c from
  *                      the one before it (zero for c = 0)
  *   1 <= nseq < 2^24; total_len >= 0.
  * Nothing passes from one sequence into another, a NaN or an infinity neither.

@@ -65,14 +65,13 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) gated_fwd_kernel(GatedFwd
   uint32_t unit = blockIdx.x;
   if (pl.chunks > 1) {
     if (threadIdx.x == 0)
-      s_turn = atomicAdd(reinterpret_cast<uint32_t*>(agg + (pl.chunks + pl.groups) * pl.cells), 1u);
+      s_turn = atomicAdd(reinterpret_cast<uint32_t*>(carries + pl.groups * pl.cells), 1u);
     __syncthreads();
     unit = __builtin_amdgcn_readfirstlane(s_turn);
     if (unit >= pl.units) return;  // (a workspace that another call uses at the same time)
   }
-  const uint32_t lines = static_cast<uint32_t>(pl.units / pl.chunks);  // rows * tiles
-  const uint32_t c = unit / lines, line = unit % lines;
-  const uint32_t row = line / static_cast<uint32_t>(pl.tiles), tile = line % static_cast<uint32_t>(pl.tiles);
+  const uint32_t c = unit / pl.lines, line = unit % pl.lines;
+  const uint32_t row = line / pl.tiles, tile = line % pl.tiles;
   const int col0 = static_cast<int>(tile) * C, col = col0 + lane * V;
   const bool have = col < dim;
   const int64_t t0 = static_cast<int64_t>(c) * SSM_GATED_CHUNK + w * T;
@@ -83,12 +82,17 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) gated_fwd_kernel(GatedFwd
   }
   const int n = end <= t0 ? 0 : (end - t0 < T ? static_cast<int>(end - t0) : T);  // the wave's tokens
 
-  float a[V][T], b[V][T], y[V], H[V];  // y: first the sum of log decays
+  float a[V][T], b[V][T], y[V], H[V];  // y: first the sum of the tokens' v
   Marks mk{0, 0, 0};
-  uint32_t voff = have ? static_cast<uint32_t>(lane * V * sizeof(TA)) : kNoColumn;
+  const uint32_t voff = have ? static_cast<uint32_t>(lane * V * sizeof(TA)) : kNoColumn;
   const uint32_t rowb = static_cast<uint32_t>(dim) * sizeof(TA);
   const int64_t base = (static_cast<int64_t>(row) * p.L + t0) * dim + col0;
   const uint32_t span = n > 0 ? (static_cast<uint32_t>(n) * rowb - col0 * static_cast<uint32_t>(sizeof(TA))) : 0;
+  const uint32_t lastrow = n > 0 ? static_cast<uint32_t>(n - 1) * rowb : 0;
+  const auto at = [&](int j) {  // rows behind the last are that one again
+    const uint32_t o = static_cast<uint32_t>(j) * rowb;
+    return o < lastrow ? o : lastrow;
+  };
   typename IO::raw_t zr[GATE ? T : 1];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -100,56 +104,54 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) gated_fwd_kernel(GatedFwd
     const rsrc_t rx = make_rsrc(p.x + base, span), rg = make_rsrc(p.r + base, span),
                  ri = make_rsrc(p.i + base, span);
 #pragma unroll
-    for (int j = 0; j < T; ++j) {  // rows behind the last are that one again
-      const uint32_t so = static_cast<uint32_t>(j < n ? j : n - 1) * rowb;
-      rr[j] = IO::load(rg, voff, so);
-      ir[j] = IO::load(ri, voff, so);
-      xr[j] = IO::load(rx, voff, so);
+    for (int j = 0; j < T; ++j) {
+      rr[j] = IO::load(rg, voff, at(j));
+      ir[j] = IO::load(ri, voff, at(j));
+      xr[j] = IO::load(rx, voff, at(j));
     }
     if (VL) mk = find_marks(p.cu, static_cast<int>(p.nseq), t0, n);
-    float A[V], rb[V], ib[V];
+    Params pr[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      A[v] = have ? p.A[col + v] : 0.0f;
-      rb[v] = have && p.rb ? p.rb[col + v] : 0.0f;
-      ib[v] = have && p.ib ? p.ib[col + v] : 0.0f;
-    }
+    for (int v = 0; v < V; ++v) pr[v] = load_params(p.A, p.rb, p.ib, col + v, have);
+    // every token as if it were there (rows behind the last repeat it), y
+    // over the n that are
 #pragma unroll
     for (int j = 0; j < T; ++j) {
-      if (j < n) {
+      const float there = j < n ? 1.0f : 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float d = pr[v].A2 * sigmoid2(__builtin_fmaf(IO::get(rr[j], v), -kLog2e, pr[v].rb2));
+        float m;
+        decay<NORM>(d, a[v][j], m);
+        b[v][j] = m * sigmoid2(__builtin_fmaf(IO::get(ir[j], v), -kLog2e, pr[v].ib2)) * IO::get(xr[j], v);
+        y[v] = __builtin_fmaf(d, there, y[v]);
+        H[v] = __builtin_fmaf(a[v][j], H[v], b[v][j]);
+      }
+      // two tokens overlap; more would not fit the registers
+      if (j & 1) __builtin_amdgcn_sched_barrier(0);
+    }
+    if (n < T || (VL && mk.starts)) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) H[v] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < T; ++j) {
+        const bool start = VL && (mk.starts >> j & 1);
+        const int64_t s = start ? __builtin_amdgcn_readlane(mk.seq, j) : 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          float m;
-          const float la = A[v] * sigmoid_f32(IO::get(rr[j], v) + rb[v]);
-          decay<NORM>(la, a[v][j], m);
-          y[v] += la;
-          b[v][j] = m * sigmoid_f32(IO::get(ir[j], v) + ib[v]) * IO::get(xr[j], v);
-        }
-        if (VL && (mk.starts >> j & 1)) {
-          const int64_t s = __builtin_amdgcn_readlane(mk.seq, j);
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            if (p.h0 && have) b[v][j] = __builtin_fmaf(a[v][j], p.h0[s * dim + col + v], b[v][j]);
-            H[v] = b[v][j];
+          if (j >= n) {
+            a[v][j] = 1.0f;
+            b[v][j] = 0.0f;
           }
-        } else {
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            H[v] = __builtin_fmaf(a[v][j], H[v], b[v][j]);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          a[v][j] = 1.0f;
-          b[v][j] = 0.0f;
+          if (start && p.h0 && have) b[v][j] = __builtin_fmaf(a[v][j], p.h0[s * dim + col + v], b[v][j]);
+          H[v] = start ? b[v][j] : __builtin_fmaf(a[v][j], H[v], b[v][j]);
         }
       }
     }
     if (GATE) {
       const rsrc_t rz = make_rsrc(p.z + base, span);
 #pragma unroll
-      for (int j = 0; j < T; ++j) zr[j] = IO::load(rz, voff, static_cast<uint32_t>(j < n ? j : n - 1) * rowb);
+      for (int j = 0; j < T; ++j) zr[j] = IO::load(rz, voff, at(j));
     }
   }
 #pragma unroll
@@ -188,28 +190,36 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) gated_fwd_kernel(GatedFwd
     for (int v = 0; v < V; ++v) h[v] = !VL && p.h0 && have ? p.h0[static_cast<int64_t>(row) * dim + col + v] : 0.0f;
   } else {
     const uint32_t first = c / kGatedGroup * kGatedGroup;
-    for (uint32_t j = first + w; j < c; j += W) {
-      float lo[V], hi[V];
-      await<V>(agg + j * pl.cells + cell, lo, hi);
+    const int there = static_cast<int>(c - first);  // chunks of the group before this one
+    {
+      float lo[kGatedPolls][V], hi[kGatedPolls][V];
+      const int polls = there > w ? (there - w + W - 1) / W : 0;  // chunks w, w + W, ...
+      if (polls > 0)
+        await<V>(agg + (first + w) * pl.cells + cell, W * pl.cells, polls, lo, hi);
 #pragma unroll
-      for (int v = 0; v < V; ++v) s_in[j - first][lane * V + v] = make_float2(lo[v], hi[v]);
+      for (int k = 0; k < kGatedPolls; ++k) {
+        if (k < polls) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) s_in[w + k * W][lane * V + v] = make_float2(lo[k][v], hi[k][v]);
+        }
+      }
     }
     if (w == W - 1) {
-      float lo[V], hi[V];
+      float lo[1][V], hi[1][V];
       if (first > 0) {
-        await<V>(carries + c / kGatedGroup * pl.cells + cell, lo, hi);
+        await<V>(carries + c / kGatedGroup * pl.cells + cell, 0, 1, lo, hi);
       } else {
 #pragma unroll
         for (int v = 0; v < V; ++v)
-          hi[v] = !VL && p.h0 && have ? p.h0[static_cast<int64_t>(row) * dim + col + v] : 0.0f;
+          hi[0][v] = !VL && p.h0 && have ? p.h0[static_cast<int64_t>(row) * dim + col + v] : 0.0f;
       }
 #pragma unroll
-      for (int v = 0; v < V; ++v) s_carry[lane * V + v] = hi[v];
+      for (int v = 0; v < V; ++v) s_carry[lane * V + v] = hi[0][v];
     }
     __syncthreads();
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = s_carry[lane * V + v];
-    for (uint32_t j = 0; j < c - first; ++j) {
+    for (int j = 0; j < there; ++j) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float2 f = s_in[j][lane * V + v];
@@ -231,20 +241,32 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) gated_fwd_kernel(GatedFwd
   for (int v = 0; v < V; ++v) h[v] = pass<VL>(yw[v], Hw[v], h[v]);
   if (n > 0 && p.out) {  // (without out: the chunks' states alone)
     const rsrc_t ro = make_rsrc(p.out + base, span);
+    const auto emit = [&](int j) {
+      float o[V];
 #pragma unroll
-    for (int j = 0; j < T; ++j) {
-      if (j < n) {
-        float o[V];
+      for (int v = 0; v < V; ++v) o[v] = GATE ? h[v] * silu_f32(IO::get(zr[j], v)) : h[v];
+      IO::store(ro, o, voff, static_cast<uint32_t>(j) * rowb);
+    };
+    if (n == T && (!VL || !(mk.starts | mk.ends))) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          h[v] = VL && (mk.starts >> j & 1) ? b[v][j] : __builtin_fmaf(a[v][j], h[v], b[v][j]);
-          o[v] = GATE ? h[v] * silu_f32(IO::get(zr[j], v)) : h[v];
-        }
-        IO::store(ro, o, voff, static_cast<uint32_t>(j) * rowb);
-        if (VL && p.last && (mk.ends >> j & 1) && have) {
-          const int64_t s = __builtin_amdgcn_readlane(mk.seq, j);
+      for (int j = 0; j < T; ++j) {
 #pragma unroll
-          for (int v = 0; v < V; ++v) p.last[s * dim + col + v] = h[v];
+        for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(a[v][j], h[v], b[v][j]);
+        emit(j);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < T; ++j) {
+        if (j < n) {
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            h[v] = VL && (mk.starts >> j & 1) ? b[v][j] : __builtin_fmaf(a[v][j], h[v], b[v][j]);
+          emit(j);
+          if (VL && p.last && (mk.ends >> j & 1) && have) {
+            const int64_t s = __builtin_amdgcn_readlane(mk.seq, j);
+#pragma unroll
+            for (int v = 0; v < V; ++v) p.last[s * dim + col + v] = h[v];
+          }
         }
       }
     }
@@ -294,8 +316,9 @@ __global__ void __launch_bounds__(256) gated_step_kernel(GatedStepArgs<TA> p) {
   if (o >= p.n) return;
   const int c = static_cast<int>(o % p.dim);
   float a, m;
-  decay<NORM>(p.A[c] * sigmoid_f32(to_f32(p.r[o]) + (p.rb ? p.rb[c] : 0.0f)), a, m);
-  const float u = sigmoid_f32(to_f32(p.i[o]) + (p.ib ? p.ib[c] : 0.0f));
+  const Params pr = load_params(p.A, p.rb, p.ib, c, true);
+  decay<NORM>(pr.A2 * sigmoid2(__builtin_fmaf(to_f32(p.r[o]), -kLog2e, pr.rb2)), a, m);
+  const float u = sigmoid2(__builtin_fmaf(to_f32(p.i[o]), -kLog2e, pr.ib2));
   const float h = __builtin_fmaf(a, p.state[o], m * u * to_f32(p.x[o]));
   p.state[o] = h;
   store_act(p.out + o, p.z ? h * silu_f32(to_f32(p.z[o])) : h);

@@ -13,34 +13,54 @@
 
 namespace ssm {
 
-// sigma(v) = 1 / (1 + e^-v): one hardware exp2 and one reciprocal (an ulp
+// sigma of v given t = -v log2 e: one hardware exp2 and one reciprocal (an ulp
 // each).  v below -88 gives 0 and v = +-inf its limit.
-__device__ __forceinline__ float sigmoid_f32(float v) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));
+__device__ __forceinline__ float sigmoid2(float t) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t));
 }
+__device__ __forceinline__ float sigmoid_f32(float v) { return sigmoid2(v * -kLog2e); }
 
-// The decay a = e^la and the input's scale m = sqrt(1 - a^2) of one token.
-// Both come from E = 1 - a = -expm1(la): next to a = 1, where a long memory
-// lives, E has its full precision, so a = 1 - E is rounded to nearest (the
-// hardware exp2 rounds low on average, which a memory of thousands of tokens
-// adds up) and m = sqrt(E (2 - E)) loses nothing to cancellation.  |la| <
-// 1/8: Taylor series of -expm1 to la^5 (the next term is below 2^-24 of it).
-// Elsewhere a <= 0.883 and E = 1 - a is exact enough (2^-24 / 0.117).
-__device__ __forceinline__ float decay_parts(float la, float& a) {
-  const float ex = __builtin_amdgcn_exp2f(la * kLog2e);
-  float q = __builtin_fmaf(la, 1.0f / 120.0f, 1.0f / 24.0f);
-  q = __builtin_fmaf(la, q, 1.0f / 6.0f);
-  q = __builtin_fmaf(la, q, 0.5f);
-  q = __builtin_fmaf(la, q, 1.0f);
-  const bool near = __builtin_fabsf(la) < 0.125f;
-  const float E = near ? -la * q : 1.0f - ex;
-  a = near ? 1.0f - E : ex;
-  return E;
+// The decay a = 2^-v (v = -la log2 e, la the log of the decay) and E = 1 - a.
+// Next to a = 1, where a long memory lives, E comes from v q(v) and keeps its
+// full precision: a = 1 - E is then rounded to nearest (the hardware exp2
+// rounds low on average, which a memory of thousands of tokens adds up), and
+// m = sqrt(1 - a^2) = sqrt(E (2 - E)) loses nothing to cancellation.  q(v) =
+// (1 - 2^-v) / v as a cubic fitted at Chebyshev points of [0, 3/16], within
+// 4.1e-8 of it.  Beyond, a <= 0.879 and E = 1 - a is exact enough.
+__device__ __forceinline__ float decay_parts(float v, float& a) {
+  const float ex = __builtin_amdgcn_exp2f(-v);
+  float q = __builtin_fmaf(v, -0.009133012033998966f, 0.055447835475206375f);
+  q = __builtin_fmaf(v, q, -0.24022440612316132f);
+  q = __builtin_fmaf(v, q, 0.6931471824645996f);
+  const bool near = __builtin_fabsf(v) < 0.1875f;
+  // both sides are computed and one is selected: left to itself the compiler
+  // branches around each side, and the tokens no longer overlap
+  float En = v * q, Ef = 1.0f - ex, an = 1.0f - En;
+  asm("" : "+v"(En), "+v"(Ef), "+v"(an));
+  a = near ? an : ex;
+  return near ? En : Ef;
+}
+// m^2 = 1 - a^2, 0 for a growing state (the clamp costs nothing: it is a
+// modifier of the product).
+__device__ __forceinline__ float input_scale2(float E) {
+  return __builtin_amdgcn_fmed3f(E * (2.0f - E), 0.0f, 1.0f);
 }
 template <bool NORM>
-__device__ __forceinline__ void decay(float la, float& a, float& m) {
-  const float E = decay_parts(la, a);
-  m = NORM ? __builtin_amdgcn_sqrtf(__builtin_fmaxf(E * (2.0f - E), 0.0f)) : 1.0f;
+__device__ __forceinline__ void decay(float v, float& a, float& m) {
+  const float E = decay_parts(v, a);
+  m = NORM ? __builtin_amdgcn_sqrtf(input_scale2(E)) : 1.0f;
+}
+
+// A channel's parameters as the kernels use them: -A log2 e and the biases
+// times -log2 e.
+struct Params {
+  float A2, rb2, ib2;
+};
+__device__ __forceinline__ Params load_params(const float* A, const float* rb, const float* ib, int c,
+                                              bool have) {
+  float A2 = have ? A[c] * -kLog2e : 0.0f;
+  if (A2 > 1e30f) A2 = 1e30f;  // (finite: a token that is masked takes it times 0)
+  return Params{A2, have && rb ? rb[c] * -kLog2e : 0.0f, have && ib ? ib[c] * -kLog2e : 0.0f};
 }
 
 // ----------------------------------------------------------------------------
@@ -52,6 +72,7 @@ __device__ __forceinline__ void decay(float la, float& a, float& m) {
 constexpr int kGatedT = 16;                          // tokens of a wave
 constexpr int kGatedWaves = SSM_GATED_CHUNK / kGatedT;  // waves of a workgroup
 constexpr int kGatedGroup = 16;                      // chunks of a group (see gated.hip)
+constexpr int kGatedPolls = kGatedGroup / kGatedWaves;  // chunks whose maps a wave fetches
 
 // A lane's V channels of one token: the raw bits as loaded, widened at use.
 template <typename TA, int V>
@@ -116,7 +137,7 @@ constexpr uint32_t kNoColumn = 0x7fffff00u;
 constexpr float kCut = -2.0f;
 __device__ __forceinline__ bool below_one(float y) { return __float_as_int(y) < 0; }
 
-// y of a stretch whose log decays add up to S (the identity for 0).
+// y of a stretch whose v add up to S (the identity for 0).
 __device__ __forceinline__ float keep_of(float S) {
   float a;
   const float E = decay_parts(S, a);
@@ -184,23 +205,40 @@ __device__ __forceinline__ void publish(uint64_t* at, float lo, float hi) {
 // workspace given to two calls at once), the wait still ends, after a second,
 // and gives NaN.
 constexpr int kWaitLimit = 1 << 20;
-template <int V>
-__device__ __forceinline__ void await(uint64_t* at, float (&lo)[V], float (&hi)[V]) {
-  uint64_t w[V];
-  for (int n = 0;; ++n) {
+// K words a lane at once: at + k * stride for k < n (n <= K, uniform).
+template <int V, int K>
+__device__ __forceinline__ void await(uint64_t* at, int64_t stride, int n, float (&lo)[K][V],
+                                      float (&hi)[K][V]) {
+  uint64_t w[K][V];
+  for (int tries = 0;; ++tries) {
     bool there = true;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      w[v] = __hip_atomic_load(at + v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      there = there && w[v] != ~uint64_t{0};
+    for (int k = 0; k < K; ++k) {
+      if (k < n) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          w[k][v] = __hip_atomic_load(at + k * stride + v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
     }
-    if (__all(there) || n >= kWaitLimit) break;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k < n) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) there = there && w[k][v] != ~uint64_t{0};
+      }
+    }
+    if (__all(there) || tries >= kWaitLimit) break;
     __builtin_amdgcn_s_sleep(1);
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    lo[v] = __uint_as_float(static_cast<uint32_t>(w[v]));
-    hi[v] = __uint_as_float(static_cast<uint32_t>(w[v] >> 32));
+  for (int k = 0; k < K; ++k) {
+    if (k < n) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        lo[k][v] = __uint_as_float(static_cast<uint32_t>(w[k][v]));
+        hi[k][v] = __uint_as_float(static_cast<uint32_t>(w[k][v] >> 32));
+      }
+    }
   }
 }
 
@@ -210,18 +248,19 @@ __device__ __forceinline__ void await(uint64_t* at, float (&lo)[V], float (&hi)[
 //   carry (groups, cells): the state that enters a group, {0, h}
 //   turn  the counter that hands out the units
 struct GatedPlan {
-  int64_t chunks, groups, tiles, cells, units;
+  uint32_t chunks, groups, tiles, lines, units;  // lines = rows * tiles, units = lines * chunks
+  int64_t cells;
   size_t bytes;  // 0: one chunk per row, no workspace
 };
 inline GatedPlan gated_plan(int64_t rows, int64_t L, int64_t dim, int V) {
-  GatedPlan p;
-  p.chunks = L > 0 ? (L + SSM_GATED_CHUNK - 1) / SSM_GATED_CHUNK : 1;
-  p.groups = (p.chunks + kGatedGroup - 1) / kGatedGroup;
-  p.tiles = (dim + 64 * V - 1) / (64 * V);
-  p.cells = rows * p.tiles * 64 * V;
-  p.units = rows * p.tiles * p.chunks;
-  p.bytes = p.chunks > 1 ? static_cast<size_t>(p.chunks + p.groups) * p.cells * 8 + 256 : 0;
-  return p;
+  const int64_t chunks = L > 0 ? (L + SSM_GATED_CHUNK - 1) / SSM_GATED_CHUNK : 1;
+  const int64_t groups = (chunks + kGatedGroup - 1) / kGatedGroup;
+  const int64_t tiles = (dim + 64 * V - 1) / (64 * V);
+  const int64_t cells = rows * tiles * 64 * V;
+  return GatedPlan{static_cast<uint32_t>(chunks), static_cast<uint32_t>(groups),
+                   static_cast<uint32_t>(tiles), static_cast<uint32_t>(rows * tiles),
+                   static_cast<uint32_t>(rows * tiles * chunks), cells,
+                   chunks > 1 ? static_cast<size_t>(chunks + groups) * cells * 8 + 256 : 0};
 }
 
 // Fills the words with ones and the counter with zero, and moves the state

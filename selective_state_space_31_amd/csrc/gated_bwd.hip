@@ -15,7 +15,7 @@ namespace ssm {
 // Partial sums of dA, drb, dib: (rows * chunks, 3, dim), one row per chunk.
 
 // The forward's layout with the adjoint running back: a workgroup takes one
-// chunk of 128 tokens and reads its data once.  The states inside the chunk
+// chunk of 64 tokens and reads its data once.  The states inside the chunk
 // come from the one the forward left at its start, without waiting; the
 // adjoint k_t = a_t G_t that enters from the chunk behind is handed over as
 // the forward hands over states (maps within a group of chunks, one value per
@@ -24,7 +24,7 @@ namespace ssm {
 // (a, g, s and the factors of G in dx, di and dla), so a lane has one channel:
 // two would need 200 registers, and one workgroup per CU.
 template <typename TA, int V, bool NORM, bool GATE, bool VL>
-__global__ void __launch_bounds__(64 * kGatedWaves, 4) gated_bwd_kernel(GatedBwdArgs<TA> p, GatedPlan pl) {
+__global__ void __launch_bounds__(64 * kGatedWaves, 3) gated_bwd_kernel(GatedBwdArgs<TA> p, GatedPlan pl) {
   constexpr int T = kGatedT, W = kGatedWaves, C = 64 * V;
   using IO = Cell<TA, V>;
   __shared__ float2 s_fwd[W][C], s_rev[W][C];
@@ -39,15 +39,14 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) gated_bwd_kernel(GatedBwd
   uint32_t unit = blockIdx.x;
   if (pl.chunks > 1) {
     if (threadIdx.x == 0)
-      s_turn = atomicAdd(reinterpret_cast<uint32_t*>(maps + (pl.chunks + pl.groups) * pl.cells), 1u);
+      s_turn = atomicAdd(reinterpret_cast<uint32_t*>(carries + pl.groups * pl.cells), 1u);
     __syncthreads();
     unit = __builtin_amdgcn_readfirstlane(s_turn);
     if (unit >= pl.units) return;  // (a workspace that another call uses at the same time)
   }
-  const uint32_t chunks = static_cast<uint32_t>(pl.chunks);
-  const uint32_t lines = static_cast<uint32_t>(pl.units / pl.chunks);  // rows * tiles
-  const uint32_t c = chunks - 1 - unit / lines, line = unit % lines;
-  const uint32_t row = line / static_cast<uint32_t>(pl.tiles), tile = line % static_cast<uint32_t>(pl.tiles);
+  const uint32_t chunks = pl.chunks;
+  const uint32_t c = chunks - 1 - unit / pl.lines, line = unit % pl.lines;
+  const uint32_t row = line / pl.tiles, tile = line % pl.tiles;
   const int col0 = static_cast<int>(tile) * C, col = col0 + lane * V;
   const bool have = col < dim;
   const int64_t t0 = static_cast<int64_t>(c) * SSM_GATED_CHUNK + w * T;
@@ -86,47 +85,57 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) gated_bwd_kernel(GatedBwd
       xr[j] = IO::load(rx, voff, so);
     }
     if (VL) mk = find_marks(p.cu, static_cast<int>(p.nseq), t0, n);
-    float rb[V], ib[V];
+    Params pr[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      rb[v] = have && p.rb ? p.rb[col + v] : 0.0f;
-      ib[v] = have && p.ib ? p.ib[col + v] : 0.0f;
-    }
+    for (int v = 0; v < V; ++v) pr[v] = load_params(p.A, p.rb, p.ib, col + v, have);
+    // every token as if it were there (rows behind the last repeat it), y
+    // over the n that are
 #pragma unroll
     for (int j = 0; j < T; ++j) {
+      const float there = j < n ? 1.0f : 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float s = sigmoid_f32(IO::get(rr[j], v) + rb[v]);
-        const float u = sigmoid_f32(IO::get(ir[j], v) + ib[v]);
-        const float x = IO::get(xr[j], v), la = A[v] * s;
-        const float E = decay_parts(la, a[v][j]);
+        const float s = sigmoid2(__builtin_fmaf(IO::get(rr[j], v), -kLog2e, pr[v].rb2));
+        const float u = sigmoid2(__builtin_fmaf(IO::get(ir[j], v), -kLog2e, pr[v].ib2));
+        const float x = IO::get(xr[j], v), d = pr[v].A2 * s;
+        const float E = decay_parts(d, a[v][j]);
         float m = 1.0f;
         cl[v][j] = 0.0f;
         if (NORM) {
-          const float M = E * (2.0f - E);  // m^2 = 1 - a^2
+          const float M = input_scale2(E);
           const float inv = M > 0.0f ? __builtin_amdgcn_rsqf(M) : 0.0f;
-          m = M > 0.0f ? M * inv : 0.0f;
+          m = M * inv;
           cl[v][j] = u * x * (a[v][j] * a[v][j] * inv);
         }
         sr[v][j] = s;
         cx[v][j] = m * u;
         g[v][j] = cx[v][j] * x;
         ci[v][j] = g[v][j] * (1.0f - u);
-        if (j < n) {
-          y[v] += la;
-        } else {
-          a[v][j] = 1.0f;
-          g[v][j] = 0.0f;
-        }
+        y[v] = __builtin_fmaf(d, there, y[v]);
+        H[v] = __builtin_fmaf(a[v][j], H[v], g[v][j]);
+        // (the six values are formed here: moved to where they are used, their
+        // sources would have to stay as well)
+        asm volatile("" : "+v"(a[v][j]), "+v"(g[v][j]), "+v"(cl[v][j]), "+v"(cx[v][j]), "+v"(ci[v][j]),
+                     "+v"(sr[v][j]));
       }
-      if (VL && (mk.starts >> j & 1)) {
-        const int64_t s = __builtin_amdgcn_readlane(mk.seq, j);
+      if (j & 1) __builtin_amdgcn_sched_barrier(0);
+    }
+    if (n < T || (VL && mk.starts)) {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          H[v] = p.h0 && have ? __builtin_fmaf(a[v][j], p.h0[s * dim + col + v], g[v][j]) : g[v][j];
-      } else {
+      for (int v = 0; v < V; ++v) H[v] = 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) H[v] = __builtin_fmaf(a[v][j], H[v], g[v][j]);
+      for (int j = 0; j < T; ++j) {
+        const bool start = VL && (mk.starts >> j & 1);
+        const int64_t s = start ? __builtin_amdgcn_readlane(mk.seq, j) : 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (j >= n) {
+            a[v][j] = 1.0f;
+            g[v][j] = 0.0f;
+          }
+          const float before = start ? (p.h0 && have ? p.h0[s * dim + col + v] : 0.0f) : H[v];
+          H[v] = __builtin_fmaf(a[v][j], before, g[v][j]);
+        }
       }
     }
 #pragma unroll
@@ -173,12 +182,20 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) gated_bwd_kernel(GatedBwd
         if (GATE) {
           const float z = IO::get(zr[j], v), sz = sigmoid_f32(z);
           dz[v] = dout * h[v] * sz * __builtin_fmaf(z, 1.0f - sz, 1.0f);
-          g[v][j] = j < n ? dout * (z * sz) : 0.0f;
+          g[v][j] = dout * (z * sz);
         } else {
-          g[v][j] = j < n ? dout : 0.0f;
+          g[v][j] = dout;
         }
       }
       if (GATE && j < n) IO::store(rdz, dz, voff, static_cast<uint32_t>(j) * rowb);
+      if (j & 1) __builtin_amdgcn_sched_barrier(0);
+    }
+    if (n < T) {
+#pragma unroll
+      for (int j = 0; j < T; ++j) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) g[v][j] = j < n ? g[v][j] : 0.0f;
+      }
     }
     // the map of the wave's tokens on the adjoint that enters from behind
 #pragma unroll
@@ -229,31 +246,39 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) gated_bwd_kernel(GatedBwd
   // the adjoint that enters the chunk from behind
   const uint32_t first = c / kGatedGroup * kGatedGroup;
   const uint32_t lastc = first + kGatedGroup < chunks ? first + kGatedGroup - 1 : chunks - 1;
-  for (uint32_t j = c + 1 + w; j <= lastc; j += W) {
-    float lo[V], hi[V];
-    await<V>(maps + j * pl.cells + cell, lo, hi);
+  const int there = static_cast<int>(lastc - c);  // chunks of the group behind this one
+  {
+    float lo[kGatedPolls][V], hi[kGatedPolls][V];
+    const int polls = there > w ? (there - w + W - 1) / W : 0;  // chunks c + 1 + w, c + 1 + w + W, ...
+    if (polls > 0)
+      await<V>(maps + (c + 1 + w) * pl.cells + cell, W * pl.cells, polls, lo, hi);
 #pragma unroll
-    for (int v = 0; v < V; ++v) s_in[j - first][lane * V + v] = make_float2(lo[v], hi[v]);
+    for (int k2 = 0; k2 < kGatedPolls; ++k2) {
+      if (k2 < polls) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) s_in[w + k2 * W][lane * V + v] = make_float2(lo[k2][v], hi[k2][v]);
+      }
+    }
   }
   if (w == W - 1) {
-    float lo[V], hi[V];
+    float lo[1][V], hi[1][V];
     if (lastc + 1 < chunks) {
-      await<V>(carries + (c / kGatedGroup + 1) * pl.cells + cell, lo, hi);
+      await<V>(carries + (c / kGatedGroup + 1) * pl.cells + cell, 0, 1, lo, hi);
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        hi[v] = !VL && p.dlast && have ? p.dlast[static_cast<int64_t>(row) * dim + col + v] : 0.0f;
+        hi[0][v] = !VL && p.dlast && have ? p.dlast[static_cast<int64_t>(row) * dim + col + v] : 0.0f;
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) s_carry[lane * V + v] = hi[v];
+    for (int v = 0; v < V; ++v) s_carry[lane * V + v] = hi[0][v];
   }
   __syncthreads();
 #pragma unroll
   for (int v = 0; v < V; ++v) k[v] = s_carry[lane * V + v];
-  for (uint32_t j = lastc; j > c; --j) {
+  for (int j = there - 1; j >= 0; --j) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float2 f = s_in[j - first][lane * V + v];
+      const float2 f = s_in[j][lane * V + v];
       k[v] = pass<VL>(f.x, f.y, k[v]);
     }
   }

@@ -1,14 +1,17 @@
 """Rounding bounds of the gated recurrence in float32, per element.
 
 With e = 2^-24 (half a float32 step, relative), v = r + rb, w = i + ib:
-  * the logistic function: forming v rounds by e|v|, its product with log2 e
-    by e|v| again, the hardware exp2 and reciprocal are within 2e each, the
-    sum 1 + e^-v rounds by e: s and u are within (2|v| + 6) e of themselves;
+  * the logistic function: -v log2 e is formed as r (-log2 e) + rb (-log2 e)
+    in one fused operation, which rounds by e|v|, on a product that rounds by
+    e|rb|, with a constant off by less than e/4: (5/4 |v| + |rb|) e; below v
+    and w stand for |v| + |rb| and |w| + |ib|.  The hardware exp2 and
+    reciprocal are within 2e each, the sum 1 + e^-v rounds by e: s and u are
+    within (2|v| + 6) e of themselves;
   * la = A s: one rounding more, (2|v| + 7) e |la|;
-  * a = e^la: that times a, the product with log2 e (e|la|), the exp2 (2e) or
-    the series and the difference 1 - E (2e): a (|la| (2|v| + 8) + 2) e;
-  * m: E is within (2|v| + 8 + 4) e where the series is used; elsewhere E >=
-    0.117, a/E <= 7.6 and |la| a/E <= 1, so within (2|v| + 8 + 16) e; the root
+  * a = e^la: that times a, A log2 e (e|la|), the exp2 (2e) or the polynomial
+    and the difference 1 - E (2e): a (|la| (2|v| + 8) + 2) e;
+  * m: E is within (2|v| + 8 + 4) e where the polynomial (within 4.1e-8 < e)
+    is used; elsewhere E >= 0.121, a/E <= 7.3 and |la| a/E <= 1, so within (2|v| + 8 + 16) e; the root
     halves it, the product and the root itself add 3e: (|v| + 15) e;
   * b = m u x: (|v| + 15 + 2|w| + 6 + 2) e = (|v| + 2|w| + 23) e;
   * h = a h' + b adds e|h|.
@@ -34,7 +37,7 @@ def _in(v, b):
 
 def _coeff(x, r, i, A, rb, ib, normalize):
     s, u, la, a, m = og.gates(x, r, i, A, rb, ib, normalize)
-    v, w = np.abs(_in(r, rb)), np.abs(_in(i, ib))
+    v, w = np.abs(_in(r, rb)) + np.abs(_in(0.0, rb)), np.abs(_in(i, ib)) + np.abs(_in(0.0, ib))
     ca = (np.abs(la) * (2 * v + 8) + 2) * E
     cb = (v + 2 * w + 23) * E
     return s, u, la, a, m, v, w, ca, cb
@@ -115,7 +118,7 @@ def backward(x, r, i, A, dout, z=None, rb=None, ib=None, normalize=True, h0=None
     aA = np.abs(A)
     res["drgate"] = el * aA * ss + dla * aA * (as_ + ss * 4 * E)
     res["dinitial_state"] = ek
-    steps = (128 + 16 + n * (L // 128 + 2)) * E
+    steps = (64 + 16 + n * (L // 64 + 2)) * E
     for name, e, mag in (("dA", el * s + dla * s * (2 * v + 8) * E, dla * s),
                          ("drgate_bias", res["drgate"], dla * aA * ss),
                          ("digate_bias", res["digate"], Ga * mx * uu)):

@@ -23,7 +23,8 @@ def forward_ok(p, out, last, mid=None, what=""):
     within(last, rl, bl, what + " last_state")
     if mid is not None:
         L = p.x.shape[1]
-        within(mid, H[:, 0:L:128], bs[:, 0:L:128], what + " chunk_states")
+        n = pkg.SSM_GATED_CHUNK
+        within(mid, H[:, 0:L:n], bs[:, 0:L:n], what + " chunk_states")
 
 
 def backward_ok(p, g, what=""):
