@@ -39,6 +39,8 @@ int launch_gated_init(void* ws, size_t bytes, const int32_t* cu, int64_t nseq, i
   return launch_status(fn);
 }
 
+constexpr int kFwdWaves = 8;  // a chunk is 128 tokens
+
 // One pass over the data: a workgroup loads its tokens once, turns them into
 // (a, b) in registers and composes its chunk's map; publishes that; waits for
 // the state that enters the chunk; and walks its tokens from there.  Chunks
@@ -50,8 +52,9 @@ int launch_gated_init(void* ws, size_t bytes, const int32_t* cu, int64_t nseq, i
 // Units are handed out by a counter, earlier chunks first: a workgroup waits
 // only for ones that are running or done.
 template <typename TA, int V, bool NORM, bool GATE, bool VL>
-__global__ void __launch_bounds__(64 * kGatedWaves, 4) gated_fwd_kernel(GatedFwdArgs<TA> p, GatedPlan pl) {
-  constexpr int T = kGatedT, W = kGatedWaves, C = 64 * V;
+__global__ void __launch_bounds__(64 * kFwdWaves, 4) gated_fwd_kernel(GatedFwdArgs<TA> p, GatedPlan pl) {
+  constexpr int T = kGatedT, W = kFwdWaves, C = 64 * V, kPolls = kGatedGroup / W;
+  constexpr int kPerState = SSM_GATED_CHUNK / T;  // waves from one chunk state to the next
   using IO = Cell<TA, V>;
   __shared__ float2 s_agg[W][C];
   __shared__ float2 s_in[kGatedGroup][C];
@@ -74,7 +77,7 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) gated_fwd_kernel(GatedFwd
   const uint32_t row = line / pl.tiles, tile = line % pl.tiles;
   const int col0 = static_cast<int>(tile) * C, col = col0 + lane * V;
   const bool have = col < dim;
-  const int64_t t0 = static_cast<int64_t>(c) * SSM_GATED_CHUNK + w * T;
+  const int64_t t0 = static_cast<int64_t>(c) * (T * W) + w * T;
   int64_t end = p.L;
   if (VL) {
     const int64_t e = p.cu[p.nseq];
@@ -192,12 +195,12 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) gated_fwd_kernel(GatedFwd
     const uint32_t first = c / kGatedGroup * kGatedGroup;
     const int there = static_cast<int>(c - first);  // chunks of the group before this one
     {
-      float lo[kGatedPolls][V], hi[kGatedPolls][V];
+      float lo[kPolls][V], hi[kPolls][V];
       const int polls = there > w ? (there - w + W - 1) / W : 0;  // chunks w, w + W, ...
       if (polls > 0)
         await<V>(agg + (first + w) * pl.cells + cell, W * pl.cells, polls, lo, hi);
 #pragma unroll
-      for (int k = 0; k < kGatedPolls; ++k) {
+      for (int k = 0; k < kPolls; ++k) {
         if (k < polls) {
 #pragma unroll
           for (int v = 0; v < V; ++v) s_in[w + k * W][lane * V + v] = make_float2(lo[k][v], hi[k][v]);
@@ -232,13 +235,14 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) gated_fwd_kernel(GatedFwd
     for (int v = 0; v < V; ++v)
       publish(carries + (c + 1) / kGatedGroup * pl.cells + cell + v, 0.0f, pass<VL>(yt[v], Ht[v], h[v]));
   }
-  if (w == 0 && p.chunk_states && have && p.L > 0) {
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      p.chunk_states[(static_cast<int64_t>(row) * pl.chunks + c) * dim + col + v] = h[v];
-  }
 #pragma unroll
   for (int v = 0; v < V; ++v) h[v] = pass<VL>(yw[v], Hw[v], h[v]);
+  if (w % kPerState == 0 && p.chunk_states && have && t0 < p.L) {
+    const int64_t states = (p.L + SSM_GATED_CHUNK - 1) / SSM_GATED_CHUNK;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      p.chunk_states[(row * states + t0 / SSM_GATED_CHUNK) * dim + col + v] = h[v];
+  }
   if (n > 0 && p.out) {  // (without out: the chunks' states alone)
     const rsrc_t ro = make_rsrc(p.out + base, span);
     const auto emit = [&](int j) {
@@ -279,11 +283,11 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) gated_fwd_kernel(GatedFwd
 
 template <typename TA, int V>
 int launch_gated_fwd(const GatedFwdArgs<TA>& a, bool norm, const char* fn, hipStream_t s) {
-  const GatedPlan pl = gated_plan(a.rows, a.L, a.dim, V);
+  const GatedPlan pl = gated_plan(a.rows, a.L, a.dim, V, kFwdWaves * kGatedT);
   const int rc = launch_gated_init(a.ws, pl.bytes, a.cu, a.cu ? a.nseq : a.rows, a.L, a.dim, a.h0, a.last,
                                    fn, s);
   if (rc != SSM_OK || a.L == 0) return rc;
-  const dim3 grid(static_cast<unsigned>(pl.units)), block(64 * kGatedWaves);
+  const dim3 grid(static_cast<unsigned>(pl.units)), block(64 * kFwdWaves);
 #define SSM_GATED_CASE(N, G, VLN)                                                              \
   if (norm == N && (a.z != nullptr) == G && (a.cu != nullptr) == VLN)                          \
     hipLaunchKernelGGL((gated_fwd_kernel<TA, V, N, G, VLN>), grid, block, 0, s, a, pl);
@@ -335,10 +339,15 @@ bool gated_sizes_ok(int64_t rows, int64_t L, int64_t nseq, int64_t dim, bool pac
   return rows * ((L + SSM_GATED_CHUNK - 1) / SSM_GATED_CHUNK) * ((dim + 63) / 64) < (int64_t{1} << 31);
 }
 
-// Workspace of a time-split walk: for the narrowest tiles a call may take.
+// Workspace of a time-split walk: for the narrowest tiles and the shortest
+// chunks a call may take.
 size_t gated_walk_bytes(int64_t rows, int64_t L, int64_t dim) {
-  const GatedPlan one = gated_plan(rows, L, dim, 1), two = gated_plan(rows, L, dim, 2);
-  return one.bytes > two.bytes ? one.bytes : two.bytes;
+  size_t most = 0;
+  for (int V = 1; V <= 2; ++V) {
+    const size_t b = gated_plan(rows, L, dim, V, SSM_GATED_CHUNK).bytes;
+    most = b > most ? b : most;
+  }
+  return most;
 }
 
 // The forward's launch for either type; bf16 with two channels a lane where

@@ -64,15 +64,16 @@ __device__ __forceinline__ Params load_params(const float* A, const float* rb, c
 }
 
 // ----------------------------------------------------------------------------
-// The walk over time.  A workgroup holds SSM_GATED_CHUNK tokens of a tile of
+// The walk over time.  A workgroup holds a chunk of tokens of a tile of
 // channels: wave w tokens [16 w, 16 w + 16), a lane V channels side by side,
 // everything in registers.  A stretch of tokens maps the state before it to
 // the state after it, h -> P h + H; the maps of waves and chunks compose.
 // ----------------------------------------------------------------------------
 constexpr int kGatedT = 16;                          // tokens of a wave
-constexpr int kGatedWaves = SSM_GATED_CHUNK / kGatedT;  // waves of a workgroup
-constexpr int kGatedGroup = 16;                      // chunks of a group (see gated.hip)
-constexpr int kGatedPolls = kGatedGroup / kGatedWaves;  // chunks whose maps a wave fetches
+#ifndef FG
+#define FG 16
+#endif
+constexpr int kGatedGroup = FG;                      // chunks of a group (see gated.hip)
 
 // A lane's V channels of one token: the raw bits as loaded, widened at use.
 template <typename TA, int V>
@@ -116,8 +117,10 @@ struct Cell<bf16_t, 2> {
     return __uint_as_float(k ? (v & 0xffff0000u) : (v << 16));
   }
   __device__ static void store(rsrc_t r, const float (&v)[2], uint32_t vo, uint32_t so) {
-    __builtin_amdgcn_raw_buffer_store_b32(bf16_bits(v[0]) | (bf16_bits(v[1]) << 16), r, vo, so,
-                                          kStoreStream);
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 b = __builtin_convertvector((f32x2{v[0], v[1]}), bf16x2);  // one conversion for the pair
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, b), r, vo, so, kStoreStream);
   }
 };
 
@@ -205,13 +208,15 @@ __device__ __forceinline__ void publish(uint64_t* at, float lo, float hi) {
 // workspace given to two calls at once), the wait still ends, after a second,
 // and gives NaN.
 constexpr int kWaitLimit = 1 << 20;
-// K words a lane at once: at + k * stride for k < n (n <= K, uniform).
+// K words a lane at once: at + k * stride for k < n (n <= K, uniform).  While
+// some are missing the wave polls one of them alone: reading all of them over
+// and over would take a third of the memory traffic.
 template <int V, int K>
 __device__ __forceinline__ void await(uint64_t* at, int64_t stride, int n, float (&lo)[K][V],
                                       float (&hi)[K][V]) {
   uint64_t w[K][V];
-  for (int tries = 0;; ++tries) {
-    bool there = true;
+  for (int tries = 0;;) {
+    uint64_t* missing = nullptr;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (k < n) {
@@ -221,14 +226,25 @@ __device__ __forceinline__ void await(uint64_t* at, int64_t stride, int n, float
       }
     }
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
+    for (int k = K - 1; k >= 0; --k) {
       if (k < n) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) there = there && w[k][v] != ~uint64_t{0};
+        for (int v = 0; v < V; ++v)
+          if (w[k][v] == ~uint64_t{0}) missing = at + k * stride + v;
       }
     }
-    if (__all(there) || tries >= kWaitLimit) break;
-    __builtin_amdgcn_s_sleep(1);
+    const uint64_t lanes = __ballot(missing != nullptr);
+    if (lanes == 0 || tries >= kWaitLimit) break;
+    const int l = __builtin_ctzll(lanes);
+    const uint64_t p = reinterpret_cast<uint64_t>(missing);
+    uint64_t* const one = reinterpret_cast<uint64_t*>(
+        static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(p), l))) |
+        static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(p >> 32), l))) << 32);
+    for (; tries < kWaitLimit; ++tries) {
+      if (__hip_atomic_load(one, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != ~uint64_t{0}) break;
+      __builtin_amdgcn_s_sleep(1);
+    }
+    ++tries;
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -252,8 +268,8 @@ struct GatedPlan {
   int64_t cells;
   size_t bytes;  // 0: one chunk per row, no workspace
 };
-inline GatedPlan gated_plan(int64_t rows, int64_t L, int64_t dim, int V) {
-  const int64_t chunks = L > 0 ? (L + SSM_GATED_CHUNK - 1) / SSM_GATED_CHUNK : 1;
+inline GatedPlan gated_plan(int64_t rows, int64_t L, int64_t dim, int V, int chunk) {
+  const int64_t chunks = L > 0 ? (L + chunk - 1) / chunk : 1;
   const int64_t groups = (chunks + kGatedGroup - 1) / kGatedGroup;
   const int64_t tiles = (dim + 64 * V - 1) / (64 * V);
   const int64_t cells = rows * tiles * 64 * V;

@@ -14,6 +14,8 @@ namespace ssm {
 
 // Partial sums of dA, drb, dib: (rows * chunks, 3, dim), one row per chunk.
 
+constexpr int kBwdWaves = SSM_GATED_CHUNK / kGatedT;
+
 // The forward's layout with the adjoint running back: a workgroup takes one
 // chunk of 64 tokens and reads its data once.  The states inside the chunk
 // come from the one the forward left at its start, without waiting; the
@@ -24,8 +26,8 @@ namespace ssm {
 // (a, g, s and the factors of G in dx, di and dla), so a lane has one channel:
 // two would need 200 registers, and one workgroup per CU.
 template <typename TA, int V, bool NORM, bool GATE, bool VL>
-__global__ void __launch_bounds__(64 * kGatedWaves, 3) gated_bwd_kernel(GatedBwdArgs<TA> p, GatedPlan pl) {
-  constexpr int T = kGatedT, W = kGatedWaves, C = 64 * V;
+__global__ void __launch_bounds__(64 * kBwdWaves, 3) gated_bwd_kernel(GatedBwdArgs<TA> p, GatedPlan pl) {
+  constexpr int T = kGatedT, W = kBwdWaves, C = 64 * V, kPolls = kGatedGroup / W;
   using IO = Cell<TA, V>;
   __shared__ float2 s_fwd[W][C], s_rev[W][C];
   __shared__ float2 s_in[kGatedGroup][C];
@@ -248,12 +250,12 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 3) gated_bwd_kernel(GatedBwd
   const uint32_t lastc = first + kGatedGroup < chunks ? first + kGatedGroup - 1 : chunks - 1;
   const int there = static_cast<int>(lastc - c);  // chunks of the group behind this one
   {
-    float lo[kGatedPolls][V], hi[kGatedPolls][V];
+    float lo[kPolls][V], hi[kPolls][V];
     const int polls = there > w ? (there - w + W - 1) / W : 0;  // chunks c + 1 + w, c + 1 + w + W, ...
     if (polls > 0)
       await<V>(maps + (c + 1 + w) * pl.cells + cell, W * pl.cells, polls, lo, hi);
 #pragma unroll
-    for (int k2 = 0; k2 < kGatedPolls; ++k2) {
+    for (int k2 = 0; k2 < kPolls; ++k2) {
       if (k2 < polls) {
 #pragma unroll
         for (int v = 0; v < V; ++v) s_in[w + k2 * W][lane * V + v] = make_float2(lo[k2][v], hi[k2][v]);
@@ -387,7 +389,7 @@ int launch_gated_bwd(const GatedBwdArgs<TA>& a, const GatedPlan& pl, bool norm, 
   int rc = launch_gated_init(a.ws, pl.bytes, a.cu, a.cu ? a.nseq : a.rows, a.L, a.dim, a.dlast, a.dh0, fn, s);
   if (rc != SSM_OK) return rc;
   if (a.L > 0) {
-    const dim3 grid(static_cast<unsigned>(pl.units)), block(64 * kGatedWaves);
+    const dim3 grid(static_cast<unsigned>(pl.units)), block(64 * kBwdWaves);
 #define SSM_GATED_CASE(N, G, VLN)                                                              \
   if (norm == N && (a.z != nullptr) == G && (a.cu != nullptr) == VLN)                          \
     hipLaunchKernelGGL((gated_bwd_kernel<TA, V, N, G, VLN>), grid, block, 0, s, a, pl);
@@ -510,7 +512,7 @@ int gated_bwd(const char* fn, const void* x, const void* r, const void* i, const
                        static_cast<TA*>(dx), static_cast<TA*>(dr), static_cast<TA*>(di),
                        static_cast<TA*>(dz), dA, drb, dib, dh0, packed ? cu : nullptr, rows, L, nseq,
                        static_cast<int>(dim), ws, reinterpret_cast<float*>(at + sp.part)};
-    return launch_gated_bwd<TA, 1>(a, gated_plan(rows, L, dim, 1), normalize != 0, fn, stream);
+    return launch_gated_bwd<TA, 1>(a, gated_plan(rows, L, dim, 1, SSM_GATED_CHUNK), normalize != 0, fn, stream);
   };
   return dtype == SSM_DTYPE_F32 ? go(float{}) : go(bf16_t{});
 }
