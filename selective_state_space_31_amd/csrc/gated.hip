@@ -9,6 +9,11 @@
 
 namespace ssm {
 
+// Whether a call goes through the sequence without a time split.
+bool gated_streams(int64_t rows, int64_t L, int64_t dim) {
+  return dim <= (int64_t{1} << 20) && L > SSM_GATED_CHUNK && rows * ((dim + 31) / 32) >= 160;
+}
+
 // Ones into the published words, zero into the counter; empty sequences'
 // states.  A grid-stride loop over each.
 __global__ void __launch_bounds__(256) gated_init_kernel(uint64_t* words, int64_t nwords,
@@ -39,7 +44,8 @@ int launch_gated_init(void* ws, size_t bytes, const int32_t* cu, int64_t nseq, i
   return launch_status(fn);
 }
 
-constexpr int kFwdWaves = 8;  // a chunk is 128 tokens
+constexpr int kFwdT = 32, kFwdBatch = 8;
+constexpr int kFwdWaves = 4;  // a chunk is 128 tokens
 
 // One pass over the data: a workgroup loads its tokens once, turns them into
 // (a, b) in registers and composes its chunk's map; publishes that; waits for
@@ -53,7 +59,7 @@ constexpr int kFwdWaves = 8;  // a chunk is 128 tokens
 // only for ones that are running or done.
 template <typename TA, int V, bool NORM, bool GATE, bool VL>
 __global__ void __launch_bounds__(64 * kFwdWaves, 4) gated_fwd_kernel(GatedFwdArgs<TA> p, GatedPlan pl) {
-  constexpr int T = kGatedT, W = kFwdWaves, C = 64 * V, kPolls = kGatedGroup / W;
+  constexpr int T = kFwdT, W = kFwdWaves, C = 64 * V, kPolls = kGatedGroup / W;
   constexpr int kPerState = SSM_GATED_CHUNK / T;  // waves from one chunk state to the next
   using IO = Cell<TA, V>;
   __shared__ float2 s_agg[W][C];
@@ -96,22 +102,29 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gated_fwd_kernel(GatedFwdAr
     const uint32_t o = static_cast<uint32_t>(j) * rowb;
     return o < lastrow ? o : lastrow;
   };
-  typename IO::raw_t zr[GATE ? T : 1];
+  constexpr int ZB = 16;  // rows of z in flight
+  typename IO::raw_t zr[GATE ? ZB : 1];
+  const rsrc_t rz = make_rsrc(GATE && n > 0 ? p.z + base : p.z, GATE ? span : 0);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     y[v] = 0.0f;
     H[v] = 0.0f;
   }
   if (n > 0) {
-    typename IO::raw_t xr[T], rr[T], ir[T];
+    constexpr int NB = kFwdBatch;
+    typename IO::raw_t xr[2][NB], rr[2][NB], ir[2][NB];
     const rsrc_t rx = make_rsrc(p.x + base, span), rg = make_rsrc(p.r + base, span),
                  ri = make_rsrc(p.i + base, span);
+    const auto fetch = [&](int k) {
 #pragma unroll
-    for (int j = 0; j < T; ++j) {
-      rr[j] = IO::load(rg, voff, at(j));
-      ir[j] = IO::load(ri, voff, at(j));
-      xr[j] = IO::load(rx, voff, at(j));
-    }
+      for (int j = 0; j < NB; ++j) {
+        rr[k & 1][j] = IO::load(rg, voff, at(k * NB + j));
+        ir[k & 1][j] = IO::load(ri, voff, at(k * NB + j));
+        xr[k & 1][j] = IO::load(rx, voff, at(k * NB + j));
+      }
+    };
+    fetch(0);
+    fetch(1);
     if (VL) mk = find_marks(p.cu, static_cast<int>(p.nseq), t0, n);
     Params pr[V];
 #pragma unroll
@@ -119,19 +132,33 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gated_fwd_kernel(GatedFwdAr
     // every token as if it were there (rows behind the last repeat it), y
     // over the n that are
 #pragma unroll
-    for (int j = 0; j < T; ++j) {
-      const float there = j < n ? 1.0f : 0.0f;
+    for (int k = 0; k < T / NB; ++k) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float d = pr[v].A2 * sigmoid2(__builtin_fmaf(IO::get(rr[j], v), -kLog2e, pr[v].rb2));
-        float m;
-        decay<NORM>(d, a[v][j], m);
-        b[v][j] = m * sigmoid2(__builtin_fmaf(IO::get(ir[j], v), -kLog2e, pr[v].ib2)) * IO::get(xr[j], v);
-        y[v] = __builtin_fmaf(d, there, y[v]);
-        H[v] = __builtin_fmaf(a[v][j], H[v], b[v][j]);
+      for (int jj = 0; jj < NB; ++jj) {
+        const int j = k * NB + jj;
+        const float there = j < n ? 1.0f : 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float d = pr[v].A2 * sigmoid2(__builtin_fmaf(IO::get(rr[k & 1][jj], v), -kLog2e, pr[v].rb2));
+          float m;
+          decay<NORM>(d, a[v][j], m);
+          b[v][j] = m * sigmoid2(__builtin_fmaf(IO::get(ir[k & 1][jj], v), -kLog2e, pr[v].ib2)) *
+                    IO::get(xr[k & 1][jj], v);
+          y[v] = __builtin_fmaf(d, there, y[v]);
+          H[v] = __builtin_fmaf(a[v][j], H[v], b[v][j]);
+        }
+        // a few tokens overlap; more would not fit the registers
+        if ((j & 3) == 3) __builtin_amdgcn_sched_barrier(0);
       }
-      // two tokens overlap; more would not fit the registers
-      if (j & 1) __builtin_amdgcn_sched_barrier(0);
+      if (k + 2 < T / NB) {
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          rr[k & 1][j] = IO::load(rg, voff, at((k + 2) * NB + j));
+          ir[k & 1][j] = IO::load(ri, voff, at((k + 2) * NB + j));
+          xr[k & 1][j] = IO::load(rx, voff, at((k + 2) * NB + j));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
     if (n < T || (VL && mk.starts)) {
 #pragma unroll
@@ -152,9 +179,8 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gated_fwd_kernel(GatedFwdAr
       }
     }
     if (GATE) {
-      const rsrc_t rz = make_rsrc(p.z + base, span);
 #pragma unroll
-      for (int j = 0; j < T; ++j) zr[j] = IO::load(rz, voff, at(j));
+      for (int j = 0; j < ZB; ++j) zr[j] = IO::load(rz, voff, at(j));
     }
   }
 #pragma unroll
@@ -248,7 +274,8 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gated_fwd_kernel(GatedFwdAr
     const auto emit = [&](int j) {
       float o[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) o[v] = GATE ? h[v] * silu_f32(IO::get(zr[j], v)) : h[v];
+      for (int v = 0; v < V; ++v) o[v] = GATE ? h[v] * silu_f32(IO::get(zr[GATE ? j % ZB : 0], v)) : h[v];
+      if (GATE && j + ZB < T) zr[j % ZB] = IO::load(rz, voff, at(j + ZB));
       IO::store(ro, o, voff, static_cast<uint32_t>(j) * rowb);
     };
     if (n == T && (!VL || !(mk.starts | mk.ends))) {
@@ -281,9 +308,166 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gated_fwd_kernel(GatedFwdAr
   }
 }
 
+// The walk without a time split, for calls whose channels fill the device: a
+// workgroup takes 32 channels of one row through the whole sequence, 512
+// tokens a turn.  A wave's lanes are 32 channels and two stretches of 32
+// tokens, so a row access is 64 bytes (bf16) and the other half of the line
+// belongs to the next workgroup, which runs on the same XCD.  The state goes
+// from turn to turn through LDS, one barrier a turn; nothing is handed between
+// workgroups, and there is no workspace and no second launch.  The next turn's
+// inputs are loaded into registers as this turn's are used up (a wave has all
+// 256 registers: one workgroup fits a CU).
+constexpr int kStreamT = 32, kStreamC = 32, kStreamWaves = 8;
+constexpr int kStreamTurn = kStreamWaves * 64 / kStreamC * kStreamT;  // tokens
+constexpr int kXcds = 8;  // workgroups are dealt to the XCDs in turn
+
+template <typename TA, bool NORM, bool GATE>
+__global__ void __launch_bounds__(64 * kStreamWaves, 2)
+    gated_stream_kernel(GatedFwdArgs<TA> p, uint32_t tiles, uint32_t units) {
+  constexpr int T = kStreamT, C = kStreamC, W = kStreamWaves, NB = 8;
+  using IO = Cell<TA, 1>;
+  __shared__ float2 s_map[2][2 * W][C];
+  __shared__ float s_carry[2][C];
+  static_assert(SSM_GATED_CHUNK == 2 * T, "a wave starts where a chunk state is kept");
+  const uint32_t unit = blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+  if (unit >= units) return;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane % C, seg = lane / C;
+  const uint32_t row = unit / tiles, tile = unit % tiles;
+  const int dim = p.dim, col0 = static_cast<int>(tile) * C, col = col0 + c;
+  const bool have = col < dim;
+  const uint32_t rowb = static_cast<uint32_t>(dim) * sizeof(TA);
+  const uint32_t voff = have ? seg * T * rowb + c * static_cast<uint32_t>(sizeof(TA)) : kNoColumn;
+  const Params pr = load_params(p.A, p.rb, p.ib, col, have);
+  const int turns = static_cast<int>((p.L + kStreamTurn - 1) / kStreamTurn);
+  const int64_t states = (p.L + SSM_GATED_CHUNK - 1) / SSM_GATED_CHUNK;
+
+  // a wave's rows of one turn: [t0, t0 + n), n <= 64, from its column on
+  struct Rows {
+    int64_t t0, base;
+    int n;
+    uint32_t span;
+  };
+  const auto rows_of = [&](int turn) {
+    Rows r;
+    r.t0 = static_cast<int64_t>(turn) * kStreamTurn + w * (2 * T);
+    const int64_t left = p.L - r.t0;
+    r.n = left <= 0 ? 0 : (left < 2 * T ? static_cast<int>(left) : 2 * T);
+    r.base = r.n > 0 ? (static_cast<int64_t>(row) * p.L + r.t0) * dim + col0 : 0;
+    r.span = r.n > 0 ? r.n * rowb - col0 * static_cast<uint32_t>(sizeof(TA)) : 0;
+    return r;
+  };
+  // (the scalar offset stays inside the span; what is behind it reads as 0)
+  const auto at = [&](const Rows& r, int j) { return static_cast<uint32_t>(j < r.n ? j : (r.n > 0 ? r.n - 1 : 0)) * rowb; };
+
+  typename IO::raw_t xr[T], rr[T], ir[T], zr[GATE ? T : 1];
+  Rows now = rows_of(0);
+  {
+    const rsrc_t rx = make_rsrc(p.x + now.base, now.span), rg = make_rsrc(p.r + now.base, now.span),
+                 ri = make_rsrc(p.i + now.base, now.span);
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      rr[j] = IO::load(rg, voff, at(now, j));
+      ir[j] = IO::load(ri, voff, at(now, j));
+      xr[j] = IO::load(rx, voff, at(now, j));
+    }
+  }
+  if (threadIdx.x < C) s_carry[0][c] = p.h0 && have ? p.h0[static_cast<int64_t>(row) * dim + col] : 0.0f;
+  for (int turn = 0; turn < turns; ++turn) {
+    const Rows next = rows_of(turn + 1);
+    if (GATE) {
+      const rsrc_t rz = make_rsrc(p.z + now.base, now.span);
+#pragma unroll
+      for (int j = 0; j < T; ++j) zr[j] = IO::load(rz, voff, at(now, j));
+    }
+    const rsrc_t rx = make_rsrc(p.x + next.base, next.span), rg = make_rsrc(p.r + next.base, next.span),
+                 ri = make_rsrc(p.i + next.base, next.span);
+    // Tokens behind the row's end take part with what they read: only
+    // stretches behind them would see it, and those have no token.
+    float a[T], b[T], y = 0.0f, H = 0.0f;
+#pragma unroll
+    for (int k = 0; k < T / NB; ++k) {
+#pragma unroll
+      for (int jj = 0; jj < NB; ++jj) {
+        const int j = k * NB + jj;
+        const float d = pr.A2 * sigmoid2(__builtin_fmaf(IO::get(rr[j], 0), -kLog2e, pr.rb2));
+        float m;
+        decay<NORM>(d, a[j], m);
+        b[j] = m * sigmoid2(__builtin_fmaf(IO::get(ir[j], 0), -kLog2e, pr.ib2)) * IO::get(xr[j], 0);
+        y += d;
+        H = __builtin_fmaf(a[j], H, b[j]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int jj = 0; jj < NB; ++jj) {
+        const int j = k * NB + jj;
+        rr[j] = IO::load(rg, voff, at(next, j));
+        ir[j] = IO::load(ri, voff, at(next, j));
+        xr[j] = IO::load(rx, voff, at(next, j));
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    s_map[turn & 1][2 * w + seg][c] = make_float2(keep_of(y), H);
+    __syncthreads();
+    float h = s_carry[turn & 1][c];
+#pragma unroll 4
+    for (int k = 0; k < 2 * w; ++k) {
+      const float2 f = s_map[turn & 1][k][c];
+      h = pass<false>(f.x, f.y, h);
+    }
+    if (seg) {
+      const float2 f = s_map[turn & 1][2 * w][c];
+      h = pass<false>(f.x, f.y, h);
+    }
+    if (p.chunk_states && seg == 0 && have && now.n > 0)
+      p.chunk_states[(row * states + now.t0 / SSM_GATED_CHUNK) * dim + col] = h;
+    // (without out, for the states alone, every store is out of range)
+    const rsrc_t ro = make_rsrc(p.out + now.base, p.out ? now.span : 0);
+    const uint32_t outb = p.out ? rowb : 0;
+    if (now.n == 2 * T) {
+#pragma unroll
+      for (int j = 0; j < T; ++j) {
+        h = __builtin_fmaf(a[j], h, b[j]);
+        const float o[1] = {GATE ? h * silu_f32(IO::get(zr[GATE ? j : 0], 0)) : h};
+        IO::store(ro, o, voff, static_cast<uint32_t>(j) * outb);
+      }
+    } else {
+      const int mine = now.n - seg * T;  // tokens of this lane's stretch
+#pragma unroll
+      for (int j = 0; j < T; ++j) {
+        if (j < now.n) {
+          const float g = __builtin_fmaf(a[j], h, b[j]);
+          h = j < mine ? g : h;
+          const float o[1] = {GATE ? g * silu_f32(IO::get(zr[GATE ? j : 0], 0)) : g};
+          IO::store(ro, o, voff, static_cast<uint32_t>(j) * outb);  // (dropped behind the last row)
+        }
+      }
+    }
+    // the row's last token is this lane's last one
+    if (p.last && have && now.t0 + seg * T < p.L && now.t0 + seg * T + T >= p.L)
+      p.last[static_cast<int64_t>(row) * dim + col] = h;
+    if (w == W - 1 && seg == 1) s_carry[(turn + 1) & 1][c] = h;
+    now = next;
+  }
+}
+
 template <typename TA, int V>
 int launch_gated_fwd(const GatedFwdArgs<TA>& a, bool norm, const char* fn, hipStream_t s) {
-  const GatedPlan pl = gated_plan(a.rows, a.L, a.dim, V, kFwdWaves * kGatedT);
+  if (!a.cu && a.L > 0 && gated_streams(a.rows, a.L, a.dim)) {
+    const uint32_t tiles = (a.dim + kStreamC - 1) / kStreamC;
+    const uint32_t units = static_cast<uint32_t>(a.rows * tiles);
+    const dim3 grid((units + kXcds - 1) / kXcds * kXcds), block(64 * kStreamWaves);
+#define SSM_GATED_CASE(N, G)                                                                  \
+  if (norm == N && (a.z != nullptr) == G)                                                      \
+    hipLaunchKernelGGL((gated_stream_kernel<TA, N, G>), grid, block, 0, s, a, tiles, units);
+    SSM_GATED_CASE(true, true)
+    SSM_GATED_CASE(true, false)
+    SSM_GATED_CASE(false, true)
+    SSM_GATED_CASE(false, false)
+#undef SSM_GATED_CASE
+    return launch_status(fn);
+  }
+  const GatedPlan pl = gated_plan(a.rows, a.L, a.dim, V, kFwdWaves * kFwdT);
   const int rc = launch_gated_init(a.ws, pl.bytes, a.cu, a.cu ? a.nseq : a.rows, a.L, a.dim, a.h0, a.last,
                                    fn, s);
   if (rc != SSM_OK || a.L == 0) return rc;
@@ -362,7 +546,7 @@ int run_gated_fwd(const char* fn, const void* x, const void* r, const void* i, c
                            static_cast<TA*>(out), last, h0, states, cu, rows, L, nseq, dim, ws};
   if constexpr (sizeof(TA) == 2) {
     if (dim % 2 == 0 && aligned(x, 4) && aligned(r, 4) && aligned(i, 4) && aligned(z, 4) && aligned(out, 4))
-      return launch_gated_fwd<TA, 2>(a, norm, fn, stream);
+      return launch_gated_fwd<TA, 1>(a, norm, fn, stream);
   }
   return launch_gated_fwd<TA, 1>(a, norm, fn, stream);
 }

@@ -39,7 +39,9 @@ def backward_ok(p, g, what=""):
 
 
 SHAPES = [(1, 1, 1), (2, 17, 5), (3, 16, 64), (1, 127, 33), (1, 128, 130), (2, 129, 70), (4, 300, 128),
-          (1, 2500, 66), (2, 1025, 257)]
+          (1, 2500, 66), (2, 1025, 257),
+          # enough channels to go through the sequence without a time split
+          (160, 65, 3), (81, 130, 63), (5, 1030, 1025), (40, 513, 100), (8, 576, 640)]
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
@@ -58,8 +60,9 @@ def test_forward_and_gradients(shape, dtype):
 @pytest.mark.parametrize("gate,normalize,bias,state,dlast", [
     (False, True, True, True, True), (True, False, True, True, False), (False, False, False, False, False),
     (True, True, False, False, True)])
-def test_optional_parts(dtype, gate, normalize, bias, state, dlast):
-    p = Gated((2, 200), 2, 100, dtype, DEV, 5, gate, normalize, bias, state, dlast)
+@pytest.mark.parametrize("b,d", [(2, 100), (41, 100)])
+def test_optional_parts(b, d, dtype, gate, normalize, bias, state, dlast):
+    p = Gated((b, 200), b, d, dtype, DEV, 5, gate, normalize, bias, state, dlast)
     out, last = pkg.ssm_gated_scan_fwd(*p.args(), return_last_state=True, **p.kw())
     forward_ok(p, out, last)
     assert torch.equal(pkg.ssm_gated_scan_fwd(*p.args(), **p.kw()), out)
