@@ -34,7 +34,7 @@ extern "C" {
 #endif
 
 /* Tokens between the states that the forward hands to the backward. */
-#define SSM_GATED_CHUNK 64
+#define SSM_GATED_CHUNK 16
 
 /*
  * Gated linear recurrence over whole sequences.  Per sequence b and channel d,
@@ -55,7 +55,7 @@ extern "C" {
  *                       or NULL; receives the state before every
  *                       SSM_GATED_CHUNK-th token, for ssm_gated_scan_bwd
  *   batch, dim >= 1; seqlen >= 0 (0 only copies the initial state);
- *   dim <= 2^24; batch <= 65535; batch * ceil(seqlen / 64) * ceil(dim / 64)
+ *   dim <= 2^22; batch <= 65535; batch * ceil(seqlen / 128) * ceil(dim / 64)
  *   < 2^31 (SSM_ERR_SHAPE beyond).
  *   workspace         : at least ssm_gated_scan_fwd_workspace_bytes(...) bytes
  * Bitwise reproducible run to run on one device.
@@ -224,7 +224,8 @@ size_t ssm_qk_norm_rotate_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int
  *     dx                : (batch, seqlen, dim) act
  *     dweight           : (dim, width) float32;  dbias : (dim) float32 or NULL
  *     dinitial_conv_state : (batch, dim, width-1) act or NULL
- *   2 <= width <= 4; batch, dim >= 1; seqlen >= 0; limits as the forward.
+ *   2 <= width <= 4; batch, dim >= 1; seqlen >= 0; dim <= 2^22, the other
+ *   limits as the forward.
  * Sums over tokens and sequences in a fixed order.
  */
 int ssm_causal_conv1d_bwd(const void* x, const float* weight, const float* bias,

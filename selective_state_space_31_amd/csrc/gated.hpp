@@ -64,69 +64,45 @@ __device__ __forceinline__ Params load_params(const float* A, const float* rb, c
 }
 
 // ----------------------------------------------------------------------------
-// The walk over time.  A workgroup holds a chunk of tokens of a tile of
-// channels: wave w tokens [16 w, 16 w + 16), a lane V channels side by side,
-// everything in registers.  A stretch of tokens maps the state before it to
-// the state after it, h -> P h + H; the maps of waves and chunks compose.
+// The walk over time.  A workgroup holds a chunk of tokens of 64 channels: a
+// lane has one channel, wave w the tokens [T w, T w + T), everything in
+// registers.  A stretch of tokens maps the state before it to the state after
+// it, h -> P h + H; the maps of waves and chunks compose.
 // ----------------------------------------------------------------------------
-constexpr int kGatedT = 16;                          // tokens of a wave
-#ifndef FG
-#define FG 16
-#endif
-constexpr int kGatedGroup = FG;                      // chunks of a group (see gated.hip)
+constexpr int kGatedC = 64;      // channels of a workgroup
+constexpr int kGatedGroup = 16;  // chunks of a group (see gated.hip)
 
-// A lane's V channels of one token: the raw bits as loaded, widened at use.
-template <typename TA, int V>
+// A lane's value of one token: the raw bits as loaded, widened at use.
+template <typename TA>
 struct Cell;
 template <>
-struct Cell<float, 1> {
+struct Cell<float> {
   using raw_t = uint32_t;
   __device__ static raw_t load(rsrc_t r, uint32_t vo, uint32_t so) {
     return __builtin_amdgcn_raw_buffer_load_b32(r, vo, so, 0);
   }
-  __device__ static float get(raw_t v, int) { return __uint_as_float(v); }
-  __device__ static void store(rsrc_t r, const float (&v)[1], uint32_t vo, uint32_t so) {
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), r, vo, so, kStoreStream);
+  __device__ static float get(raw_t v) { return __uint_as_float(v); }
+  __device__ static void store(rsrc_t r, float v, uint32_t vo, uint32_t so) {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, vo, so, kStoreStream);
   }
 };
-__device__ __forceinline__ uint32_t bf16_bits(float v) {
-  const __bf16 b = static_cast<__bf16>(v);  // round to nearest even
-  return __builtin_bit_cast(uint16_t, b);
-}
 template <>
-struct Cell<bf16_t, 1> {
+struct Cell<bf16_t> {
   using raw_t = uint16_t;
   __device__ static raw_t load(rsrc_t r, uint32_t vo, uint32_t so) {
     return __builtin_amdgcn_raw_buffer_load_b16(r, vo, so, 0);
   }
-  __device__ static float get(raw_t v, int) {
-    return __uint_as_float(static_cast<uint32_t>(v) << 16);
-  }
-  __device__ static void store(rsrc_t r, const float (&v)[1], uint32_t vo, uint32_t so) {
-    __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(bf16_bits(v[0])), r, vo, so,
-                                          kStoreStream);
-  }
-};
-template <>
-struct Cell<bf16_t, 2> {
-  using raw_t = uint32_t;
-  __device__ static raw_t load(rsrc_t r, uint32_t vo, uint32_t so) {
-    return __builtin_amdgcn_raw_buffer_load_b32(r, vo, so, 0);
-  }
-  __device__ static float get(raw_t v, int k) {
-    return __uint_as_float(k ? (v & 0xffff0000u) : (v << 16));
-  }
-  __device__ static void store(rsrc_t r, const float (&v)[2], uint32_t vo, uint32_t so) {
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    const bf16x2 b = __builtin_convertvector((f32x2{v[0], v[1]}), bf16x2);  // one conversion for the pair
-    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, b), r, vo, so, kStoreStream);
+  __device__ static float get(raw_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+  __device__ static void store(rsrc_t r, float v, uint32_t vo, uint32_t so) {
+    const __bf16 b = static_cast<__bf16>(v);  // round to nearest even
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, b), r, vo, so, kStoreStream);
   }
 };
 
 // Byte offset that no descriptor here covers (a wave's rows span at most
-// 16 * 2^24 * 4 = 2^30 bytes): lanes beyond the last channel use it, so their
-// loads give 0 and their stores are dropped by the range check.
+// 64 * 2^22 * 4 = 2^30 bytes: see gated_sizes_ok): lanes beyond the last
+// channel use it, so their loads give 0 and their stores are dropped
+// by the range check.
 constexpr uint32_t kNoColumn = 0x7fffff00u;
 
 // The map h -> P h + H of a stretch is kept as (y, H).  y >= +0 is P itself;
@@ -166,10 +142,10 @@ __device__ __forceinline__ void compose(float& y1, float& H1, float y2, float H2
   y1 = y;
 }
 
-// Which of a wave's tokens start and end their sequence (bit per token), and
-// each token's sequence (held by lane j for token j).
+// Which of a wave's tokens (64 at most) start and end their sequence, a bit
+// each, and each token's sequence (held by lane j for token j).
 struct Marks {
-  uint32_t starts, ends;
+  uint64_t starts, ends;
   int seq;
 };
 __device__ __forceinline__ Marks find_marks(const int32_t* cu, int nseq, int64_t t0, int n) {
@@ -187,8 +163,8 @@ __device__ __forceinline__ Marks find_marks(const int32_t* cu, int nseq, int64_t
     st = cu[lo] == t;
     en = cu[lo + 1] == t + 1;
   }
-  m.starts = static_cast<uint32_t>(__ballot(st));
-  m.ends = static_cast<uint32_t>(__ballot(en));
+  m.starts = __ballot(st);
+  m.ends = __ballot(en);
   return m;
 }
 
@@ -209,30 +185,18 @@ __device__ __forceinline__ void publish(uint64_t* at, float lo, float hi) {
 // and gives NaN.
 constexpr int kWaitLimit = 1 << 20;
 // K words a lane at once: at + k * stride for k < n (n <= K, uniform).  While
-// some are missing the wave polls one of them alone: reading all of them over
-// and over would take a third of the memory traffic.
-template <int V, int K>
-__device__ __forceinline__ void await(uint64_t* at, int64_t stride, int n, float (&lo)[K][V],
-                                      float (&hi)[K][V]) {
-  uint64_t w[K][V];
+// some are missing the wave polls one of them alone.
+template <int K>
+__device__ __forceinline__ void await(uint64_t* at, int64_t stride, int n, float (&lo)[K], float (&hi)[K]) {
+  uint64_t w[K];
   for (int tries = 0;;) {
     uint64_t* missing = nullptr;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (k < n) {
+    for (int k = 0; k < K; ++k)
+      if (k < n) w[k] = __hip_atomic_load(at + k * stride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          w[k][v] = __hip_atomic_load(at + k * stride + v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
-    }
-#pragma unroll
-    for (int k = K - 1; k >= 0; --k) {
-      if (k < n) {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (w[k][v] == ~uint64_t{0}) missing = at + k * stride + v;
-      }
-    }
+    for (int k = K - 1; k >= 0; --k)
+      if (k < n && w[k] == ~uint64_t{0}) missing = at + k * stride;
     const uint64_t lanes = __ballot(missing != nullptr);
     if (lanes == 0 || tries >= kWaitLimit) break;
     const int l = __builtin_ctzll(lanes);
@@ -249,17 +213,14 @@ __device__ __forceinline__ void await(uint64_t* at, int64_t stride, int n, float
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     if (k < n) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        lo[k][v] = __uint_as_float(static_cast<uint32_t>(w[k][v]));
-        hi[k][v] = __uint_as_float(static_cast<uint32_t>(w[k][v] >> 32));
-      }
+      lo[k] = __uint_as_float(static_cast<uint32_t>(w[k]));
+      hi[k] = __uint_as_float(static_cast<uint32_t>(w[k] >> 32));
     }
   }
 }
 
 // The workspace of a time-split launch.  `cells` channel slots (rows * tiles
-// * 64 V), chunk-major, so that a chunk's words lie together:
+// * 64), chunk-major, so that a chunk's words lie together:
 //   agg   (chunks, cells): a chunk's map (y, H)
 //   carry (groups, cells): the state that enters a group, {0, h}
 //   turn  the counter that hands out the units
@@ -268,11 +229,11 @@ struct GatedPlan {
   int64_t cells;
   size_t bytes;  // 0: one chunk per row, no workspace
 };
-inline GatedPlan gated_plan(int64_t rows, int64_t L, int64_t dim, int V, int chunk) {
+inline GatedPlan gated_plan(int64_t rows, int64_t L, int64_t dim, int chunk) {
   const int64_t chunks = L > 0 ? (L + chunk - 1) / chunk : 1;
   const int64_t groups = (chunks + kGatedGroup - 1) / kGatedGroup;
-  const int64_t tiles = (dim + 64 * V - 1) / (64 * V);
-  const int64_t cells = rows * tiles * 64 * V;
+  const int64_t tiles = (dim + kGatedC - 1) / kGatedC;
+  const int64_t cells = rows * tiles * kGatedC;
   return GatedPlan{static_cast<uint32_t>(chunks), static_cast<uint32_t>(groups),
                    static_cast<uint32_t>(tiles), static_cast<uint32_t>(rows * tiles),
                    static_cast<uint32_t>(rows * tiles * chunks), cells,
@@ -313,10 +274,10 @@ struct GatedBwdArgs {
   float* part;  // partial sums
 };
 
-// Whether these sizes can be launched; the walk's words for the narrowest
-// tiles a call may take; the states at the chunks' starts alone (gated.hip).
+// Whether these sizes can be launched; bytes of the forward's words; the
+// states at the chunks' starts alone (gated.hip).
 bool gated_sizes_ok(int64_t rows, int64_t L, int64_t nseq, int64_t dim, bool packed);
-size_t gated_walk_bytes(int64_t rows, int64_t L, int64_t dim);
+size_t gated_fwd_bytes(int64_t rows, int64_t L, int64_t dim);
 int gated_states(const char* fn, const void* x, const void* r, const void* i, const float* A,
                  const float* rb, const float* ib, int normalize, const float* h0, float* states,
                  const int32_t* cu, int64_t nseq, int64_t rows, int64_t L, int dim, int dtype,

@@ -12,24 +12,24 @@
 
 namespace ssm {
 
-// Partial sums of dA, drb, dib: (rows * chunks, 3, dim), one row per chunk.
+// Tokens of a lane, rows in flight (a ring of registers), waves.
+constexpr int kBwdT = 16, kBwdBatch = 2, kBwdRing = 2;
+constexpr int kBwdWaves = 8;
+constexpr int kBwdChunk = kBwdT * kBwdWaves;
+static_assert(SSM_GATED_CHUNK == kBwdT, "a wave starts where the forward kept the state");
 
-constexpr int kBwdWaves = SSM_GATED_CHUNK / kGatedT;
-
-// The forward's layout with the adjoint running back: a workgroup takes one
-// chunk of 64 tokens and reads its data once.  The states inside the chunk
-// come from the one the forward left at its start, without waiting; the
-// adjoint k_t = a_t G_t that enters from the chunk behind is handed over as
-// the forward hands over states (maps within a group of chunks, one value per
-// group), with the units given out last chunk first.
-// Per token and channel six values stay in registers between the two walks
-// (a, g, s and the factors of G in dx, di and dla), so a lane has one channel:
-// two would need 200 registers, and one workgroup per CU.
-template <typename TA, int V, bool NORM, bool GATE, bool VL>
-__global__ void __launch_bounds__(64 * kBwdWaves, 3) gated_bwd_kernel(GatedBwdArgs<TA> p, GatedPlan pl) {
-  constexpr int T = kGatedT, W = kBwdWaves, C = 64 * V, kPolls = kGatedGroup / W;
-  using IO = Cell<TA, V>;
-  __shared__ float2 s_fwd[W][C], s_rev[W][C];
+// The forward's layout with the adjoint running back: one pass over the data,
+// a wave starts from the state that the forward left at its first token, and
+// the adjoint k_t = a_t G_t that enters from the chunk behind is handed over
+// as the forward hands over states (maps within a group of chunks, one value
+// per group), the units given out last chunk first.
+// Per token six values stay in registers between the walk that rebuilds the
+// states and the walk back: a, g, s and the factors of G in dx, di and dla.
+template <typename TA, bool NORM, bool GATE, bool VL>
+__global__ void __launch_bounds__(64 * kBwdWaves, 4) gated_bwd_kernel(GatedBwdArgs<TA> p, GatedPlan pl) {
+  constexpr int T = kBwdT, W = kBwdWaves, C = kGatedC, NB = kBwdBatch, kPolls = (kGatedGroup + W - 1) / W;
+  using IO = Cell<TA>;
+  __shared__ float2 s_rev[W][C];
   __shared__ float2 s_in[kGatedGroup][C];
   __shared__ float s_carry[C];
   __shared__ uint32_t s_turn;
@@ -40,8 +40,7 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 3) gated_bwd_kernel(GatedBwdAr
   uint64_t* const carries = maps + pl.chunks * pl.cells;
   uint32_t unit = blockIdx.x;
   if (pl.chunks > 1) {
-    if (threadIdx.x == 0)
-      s_turn = atomicAdd(reinterpret_cast<uint32_t*>(carries + pl.groups * pl.cells), 1u);
+    if (threadIdx.x == 0) s_turn = atomicAdd(reinterpret_cast<uint32_t*>(carries + pl.groups * pl.cells), 1u);
     __syncthreads();
     unit = __builtin_amdgcn_readfirstlane(s_turn);
     if (unit >= pl.units) return;  // (a workspace that another call uses at the same time)
@@ -49,9 +48,9 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 3) gated_bwd_kernel(GatedBwdAr
   const uint32_t chunks = pl.chunks;
   const uint32_t c = chunks - 1 - unit / pl.lines, line = unit % pl.lines;
   const uint32_t row = line / pl.tiles, tile = line % pl.tiles;
-  const int col0 = static_cast<int>(tile) * C, col = col0 + lane * V;
+  const int col0 = static_cast<int>(tile) * C, col = col0 + lane;
   const bool have = col < dim;
-  const int64_t t0 = static_cast<int64_t>(c) * SSM_GATED_CHUNK + w * T;
+  const int64_t t0 = static_cast<int64_t>(c) * kBwdChunk + w * T;
   int64_t end = p.L;
   if (VL) {
     const int64_t e = p.cu[p.nseq];
@@ -59,301 +58,188 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 3) gated_bwd_kernel(GatedBwdAr
   }
   const int n = end <= t0 ? 0 : (end - t0 < T ? static_cast<int>(end - t0) : T);  // the wave's tokens
 
-  // a; b, then g; the subtrahend of dla / G, then dla / G; dx / G; di / G; s
-  float a[V][T], g[V][T], cl[V][T], cx[V][T], ci[V][T], sr[V][T], y[V], H[V], A[V];
-  Marks mk{0, 0, 0};
-  const uint32_t voff = have ? static_cast<uint32_t>(lane * V * sizeof(TA)) : kNoColumn;
+  const uint32_t voff = have ? static_cast<uint32_t>(lane * sizeof(TA)) : kNoColumn;
   const uint32_t rowb = static_cast<uint32_t>(dim) * sizeof(TA);
   const int64_t base = (static_cast<int64_t>(row) * p.L + t0) * dim + col0;
   const uint32_t span = n > 0 ? (static_cast<uint32_t>(n) * rowb - col0 * static_cast<uint32_t>(sizeof(TA))) : 0;
-  const int64_t mid = (static_cast<int64_t>(row) * chunks + c) * dim + col;
-  float h[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    y[v] = H[v] = 0.0f;
-    A[v] = have ? p.A[col + v] : 0.0f;
-    h[v] = have ? p.chunk_states[mid + v] : 0.0f;
-  }
-  typename IO::raw_t zr[GATE ? T : 1], dr[T];
+  const uint32_t lastrow = n > 0 ? static_cast<uint32_t>(n - 1) * rowb : 0;
+  const auto at = [&](int j) {  // rows behind the last are that one again
+    const uint32_t o = static_cast<uint32_t>(j) * rowb;
+    return o < lastrow ? o : lastrow;
+  };
+  const auto only = [&](int j) { return j < n ? voff : kNoColumn; };  // stores of tokens that are not there are dropped
+  const Params pr = load_params(p.A, p.rb, p.ib, col, have);
+
+  // a; g; dla / G; dx / G; di / G; s
+  float a[T], g[T], cl[T], cx[T], ci[T], sr[T], y = 0.0f, Q = 0.0f;
+  Marks mk{0, 0, 0};
   if (n > 0) {
-    typename IO::raw_t xr[T], rr[T], ir[T];
+    constexpr int R = kBwdRing;
+    typename IO::raw_t xr[R][NB], rr[R][NB], ir[R][NB], dr[R][NB], zr[GATE ? R : 1][NB];
     const rsrc_t rx = make_rsrc(p.x + base, span), rg = make_rsrc(p.r + base, span),
-                 ri = make_rsrc(p.i + base, span), rd = make_rsrc(p.dout + base, span);
+                 ri = make_rsrc(p.i + base, span), rd = make_rsrc(p.dout + base, span),
+                 rz = make_rsrc(GATE ? p.z + base : p.z, GATE ? span : 0),
+                 rdz = make_rsrc(GATE ? p.dz + base : p.dz, GATE ? span : 0);
 #pragma unroll
-    for (int j = 0; j < T; ++j) {  // rows behind the last are that one again
-      const uint32_t so = static_cast<uint32_t>(j < n ? j : n - 1) * rowb;
-      rr[j] = IO::load(rg, voff, so);
-      ir[j] = IO::load(ri, voff, so);
-      xr[j] = IO::load(rx, voff, so);
+    for (int j = 0; j < R * NB; ++j) {
+      rr[j / NB][j % NB] = IO::load(rg, voff, at(j));
+      ir[j / NB][j % NB] = IO::load(ri, voff, at(j));
+      xr[j / NB][j % NB] = IO::load(rx, voff, at(j));
+      dr[j / NB][j % NB] = IO::load(rd, voff, at(j));
+      if (GATE) zr[j / NB][j % NB] = IO::load(rz, voff, at(j));
     }
+    float h = have ? p.chunk_states[(row * ((p.L + T - 1) / T) + t0 / T) * dim + col] : 0.0f;
     if (VL) mk = find_marks(p.cu, static_cast<int>(p.nseq), t0, n);
-    Params pr[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) pr[v] = load_params(p.A, p.rb, p.ib, col + v, have);
     // every token as if it were there (rows behind the last repeat it), y
     // over the n that are
 #pragma unroll
-    for (int j = 0; j < T; ++j) {
-      const float there = j < n ? 1.0f : 0.0f;
+    for (int k = 0; k < T / NB; ++k) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float s = sigmoid2(__builtin_fmaf(IO::get(rr[j], v), -kLog2e, pr[v].rb2));
-        const float u = sigmoid2(__builtin_fmaf(IO::get(ir[j], v), -kLog2e, pr[v].ib2));
-        const float x = IO::get(xr[j], v), d = pr[v].A2 * s;
-        const float E = decay_parts(d, a[v][j]);
-        float m = 1.0f;
-        cl[v][j] = 0.0f;
+      for (int jj = 0; jj < NB; ++jj) {
+        const int j = k * NB + jj;
+        const float there = j < n ? 1.0f : 0.0f;
+        const float s = sigmoid2(__builtin_fmaf(IO::get(rr[k % R][jj]), -kLog2e, pr.rb2));
+        const float u = sigmoid2(__builtin_fmaf(IO::get(ir[k % R][jj]), -kLog2e, pr.ib2));
+        const float x = IO::get(xr[k % R][jj]), dout = IO::get(dr[k % R][jj]), d = pr.A2 * s;
+        const float E = decay_parts(d, a[j]);
+        float m = 1.0f, sub = 0.0f;
         if (NORM) {
           const float M = input_scale2(E);
           const float inv = M > 0.0f ? __builtin_amdgcn_rsqf(M) : 0.0f;
           m = M * inv;
-          cl[v][j] = u * x * (a[v][j] * a[v][j] * inv);
+          sub = u * x * (a[j] * a[j] * inv);
         }
-        sr[v][j] = s;
-        cx[v][j] = m * u;
-        g[v][j] = cx[v][j] * x;
-        ci[v][j] = g[v][j] * (1.0f - u);
-        y[v] = __builtin_fmaf(d, there, y[v]);
-        H[v] = __builtin_fmaf(a[v][j], H[v], g[v][j]);
+        if (VL && (mk.starts >> j & 1))
+          h = p.h0 && have ? p.h0[static_cast<int64_t>(__builtin_amdgcn_readlane(mk.seq, j)) * dim + col] : 0.0f;
+        sr[j] = s;
+        cx[j] = m * u;
+        const float b = cx[j] * x, ah = a[j] * h;
+        ci[j] = b * (1.0f - u);
+        cl[j] = ah - sub;
+        h = __builtin_fmaf(a[j], h, b);
+        y = __builtin_fmaf(d, there, y);
+        if (GATE) {
+          const float z = IO::get(zr[k % R][jj]), sz = sigmoid_f32(z);
+          IO::store(rdz, dout * h * sz * __builtin_fmaf(z, 1.0f - sz, 1.0f), only(j), at(j));
+          g[j] = dout * (z * sz);
+        } else {
+          g[j] = dout;
+        }
         // (the six values are formed here: moved to where they are used, their
         // sources would have to stay as well)
-        asm volatile("" : "+v"(a[v][j]), "+v"(g[v][j]), "+v"(cl[v][j]), "+v"(cx[v][j]), "+v"(ci[v][j]),
-                     "+v"(sr[v][j]));
+        asm volatile("" : "+v"(a[j]), "+v"(g[j]), "+v"(cl[j]), "+v"(cx[j]), "+v"(ci[j]), "+v"(sr[j]));
       }
-      if (j & 1) __builtin_amdgcn_sched_barrier(0);
-    }
-    if (n < T || (VL && mk.starts)) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (k + R < T / NB) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) H[v] = 0.0f;
-#pragma unroll
-      for (int j = 0; j < T; ++j) {
-        const bool start = VL && (mk.starts >> j & 1);
-        const int64_t s = start ? __builtin_amdgcn_readlane(mk.seq, j) : 0;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          if (j >= n) {
-            a[v][j] = 1.0f;
-            g[v][j] = 0.0f;
-          }
-          const float before = start ? (p.h0 && have ? p.h0[s * dim + col + v] : 0.0f) : H[v];
-          H[v] = __builtin_fmaf(a[v][j], before, g[v][j]);
+        for (int jj = 0; jj < NB; ++jj) {
+          const uint32_t o = at((k + R) * NB + jj);
+          rr[k % R][jj] = IO::load(rg, voff, o);
+          ir[k % R][jj] = IO::load(ri, voff, o);
+          xr[k % R][jj] = IO::load(rx, voff, o);
+          dr[k % R][jj] = IO::load(rd, voff, o);
+          if (GATE) zr[k % R][jj] = IO::load(rz, voff, o);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
-    }
-#pragma unroll
-    for (int j = 0; j < T; ++j) dr[j] = IO::load(rd, voff, static_cast<uint32_t>(j < n ? j : n - 1) * rowb);
-    if (GATE) {
-      const rsrc_t rz = make_rsrc(p.z + base, span);
-#pragma unroll
-      for (int j = 0; j < T; ++j) zr[j] = IO::load(rz, voff, static_cast<uint32_t>(j < n ? j : n - 1) * rowb);
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    y[v] = keep_of(y[v]);
-    s_fwd[w][lane * V + v] = make_float2(VL && mk.starts ? kCut : y[v], H[v]);
-  }
-  __syncthreads();
-  for (int k = 0; k < w; ++k) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float2 f = s_fwd[k][lane * V + v];
-      h[v] = pass<VL>(f.x, f.y, h[v]);
-    }
-  }
-  // the states inside the wave's tokens: dz, and what multiplies G in dla
-  float Q[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) Q[v] = 0.0f;
-  if (n > 0) {
-    const rsrc_t rdz = make_rsrc(p.dz + (GATE ? base : 0), GATE ? span : 0);
-#pragma unroll
-    for (int j = 0; j < T; ++j) {
-      float dz[V];
-      if (VL && (mk.starts >> j & 1)) {
-        const int64_t s = __builtin_amdgcn_readlane(mk.seq, j);
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = p.h0 && have ? p.h0[s * dim + col + v] : 0.0f;
-      }
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float ah = a[v][j] * h[v];
-        h[v] = __builtin_fmaf(a[v][j], h[v], g[v][j]);
-        cl[v][j] = ah - cl[v][j];
-        const float dout = IO::get(dr[j], v);
-        if (GATE) {
-          const float z = IO::get(zr[j], v), sz = sigmoid_f32(z);
-          dz[v] = dout * h[v] * sz * __builtin_fmaf(z, 1.0f - sz, 1.0f);
-          g[v][j] = dout * (z * sz);
-        } else {
-          g[v][j] = dout;
-        }
-      }
-      if (GATE && j < n) IO::store(rdz, dz, voff, static_cast<uint32_t>(j) * rowb);
-      if (j & 1) __builtin_amdgcn_sched_barrier(0);
     }
     if (n < T) {
 #pragma unroll
       for (int j = 0; j < T; ++j) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) g[v][j] = j < n ? g[v][j] : 0.0f;
+        if (j >= n) {
+          a[j] = 1.0f;
+          g[j] = cl[j] = cx[j] = ci[j] = 0.0f;
+        }
       }
     }
     // the map of the wave's tokens on the adjoint that enters from behind
 #pragma unroll
     for (int j = T - 1; j >= 0; --j) {
-      if (VL && (mk.ends >> j & 1)) {
-        const int64_t s = __builtin_amdgcn_readlane(mk.seq, j);
-#pragma unroll
-        for (int v = 0; v < V; ++v) Q[v] = p.dlast && have ? p.dlast[s * dim + col + v] : 0.0f;
-      }
-      if (VL && (mk.starts >> j & 1)) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) Q[v] = 0.0f;
-      } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) Q[v] = a[v][j] * (g[v][j] + Q[v]);
-      }
+      if (VL && (mk.ends >> j & 1))
+        Q = p.dlast && have ? p.dlast[static_cast<int64_t>(__builtin_amdgcn_readlane(mk.seq, j)) * dim + col] : 0.0f;
+      Q = VL && (mk.starts >> j & 1) ? 0.0f : a[j] * (g[j] + Q);
     }
   }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    if (VL && (mk.starts | mk.ends)) y[v] = kCut;
-    s_rev[w][lane * V + v] = make_float2(y[v], Q[v]);
-  }
+  y = VL && (mk.starts | mk.ends) ? kCut : keep_of(y);
+  s_rev[w][lane] = make_float2(y, Q);
   __syncthreads();
-  float yw[V], Qw[V], yt[V], Qt[V], k[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    yw[v] = -0.0f;
-    Qw[v] = 0.0f;
-  }
+  float yw = -0.0f, Qw = 0.0f, yt = 0.0f, Qt = 0.0f;
   for (int q = W - 1; q > w; --q) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float2 f = s_rev[q][lane * V + v];
-      compose<VL>(yw[v], Qw[v], f.x, f.y);
-    }
+    const float2 f = s_rev[q][lane];
+    compose<VL>(yw, Qw, f.x, f.y);
   }
-  const int64_t cell = static_cast<int64_t>(line) * C + lane * V;
+  const int64_t cell = static_cast<int64_t>(line) * C + lane;
   if (w == 0) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      yt[v] = yw[v];
-      Qt[v] = Qw[v];
-      compose<VL>(yt[v], Qt[v], y[v], Q[v]);
-      if (c > 0) publish(maps + c * pl.cells + cell + v, yt[v], Qt[v]);
-    }
+    yt = yw;
+    Qt = Qw;
+    compose<VL>(yt, Qt, y, Q);
+    if (c > 0) publish(maps + c * pl.cells + cell, yt, Qt);
   }
   // the adjoint that enters the chunk from behind
   const uint32_t first = c / kGatedGroup * kGatedGroup;
   const uint32_t lastc = first + kGatedGroup < chunks ? first + kGatedGroup - 1 : chunks - 1;
   const int there = static_cast<int>(lastc - c);  // chunks of the group behind this one
   {
-    float lo[kPolls][V], hi[kPolls][V];
+    float lo[kPolls], hi[kPolls];
     const int polls = there > w ? (there - w + W - 1) / W : 0;  // chunks c + 1 + w, c + 1 + w + W, ...
-    if (polls > 0)
-      await<V>(maps + (c + 1 + w) * pl.cells + cell, W * pl.cells, polls, lo, hi);
+    if (polls > 0) await(maps + (c + 1 + w) * pl.cells + cell, W * pl.cells, polls, lo, hi);
 #pragma unroll
-    for (int k2 = 0; k2 < kPolls; ++k2) {
-      if (k2 < polls) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) s_in[w + k2 * W][lane * V + v] = make_float2(lo[k2][v], hi[k2][v]);
-      }
-    }
+    for (int q = 0; q < kPolls; ++q)
+      if (q < polls) s_in[w + q * W][lane] = make_float2(lo[q], hi[q]);
   }
   if (w == W - 1) {
-    float lo[1][V], hi[1][V];
-    if (lastc + 1 < chunks) {
-      await<V>(carries + (c / kGatedGroup + 1) * pl.cells + cell, 0, 1, lo, hi);
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        hi[0][v] = !VL && p.dlast && have ? p.dlast[static_cast<int64_t>(row) * dim + col + v] : 0.0f;
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) s_carry[lane * V + v] = hi[0][v];
+    float zero[1], from[1] = {!VL && p.dlast && have ? p.dlast[static_cast<int64_t>(row) * dim + col] : 0.0f};
+    if (lastc + 1 < chunks) await(carries + (c / kGatedGroup + 1) * pl.cells + cell, 0, 1, zero, from);
+    s_carry[lane] = from[0];
   }
   __syncthreads();
-#pragma unroll
-  for (int v = 0; v < V; ++v) k[v] = s_carry[lane * V + v];
+  float k = s_carry[lane];
   for (int j = there - 1; j >= 0; --j) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float2 f = s_in[j][lane * V + v];
-      k[v] = pass<VL>(f.x, f.y, k[v]);
-    }
+    const float2 f = s_in[j][lane];
+    k = pass<VL>(f.x, f.y, k);
   }
-  if (w == 0 && c == first && c > 0) {
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      publish(carries + c / kGatedGroup * pl.cells + cell + v, 0.0f, pass<VL>(yt[v], Qt[v], k[v]));
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) k[v] = pass<VL>(yw[v], Qw[v], k[v]);
-  float dA[V], drb[V], dib[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) dA[v] = drb[v] = dib[v] = 0.0f;
+  if (w == 0 && c == first && c > 0)
+    publish(carries + c / kGatedGroup * pl.cells + cell, 0.0f, pass<VL>(yt, Qt, k));
+  k = pass<VL>(yw, Qw, k);
+  float dA = 0.0f, drb = 0.0f, dib = 0.0f;
   if (n > 0) {
     const rsrc_t rdx = make_rsrc(p.dx + base, span), rdr = make_rsrc(p.dr + base, span),
                  rdi = make_rsrc(p.di + base, span);
+    const float A = have ? p.A[col] : 0.0f;
 #pragma unroll
     for (int j = T - 1; j >= 0; --j) {
-      if (j < n) {
-        if (VL && (mk.ends >> j & 1)) {
-          const int64_t s = __builtin_amdgcn_readlane(mk.seq, j);
-#pragma unroll
-          for (int v = 0; v < V; ++v) k[v] = p.dlast && have ? p.dlast[s * dim + col + v] : 0.0f;
-        }
-        float ox[V], orr[V], oi[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float G = g[v][j] + k[v], dla = G * cl[v][j], s = sr[v][j];
-          ox[v] = G * cx[v][j];
-          oi[v] = G * ci[v][j];
-          orr[v] = dla * (A[v] * s * (1.0f - s));
-          dA[v] = __builtin_fmaf(dla, s, dA[v]);
-          drb[v] += orr[v];
-          dib[v] += oi[v];
-          k[v] = a[v][j] * G;
-        }
-        const uint32_t so = static_cast<uint32_t>(j) * rowb;
-        IO::store(rdx, ox, voff, so);
-        IO::store(rdr, orr, voff, so);
-        IO::store(rdi, oi, voff, so);
-        if (VL && (mk.starts >> j & 1)) {
-          const int64_t s = __builtin_amdgcn_readlane(mk.seq, j);
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            if (p.dh0 && have) p.dh0[s * dim + col + v] = k[v];
-            k[v] = 0.0f;
-          }
-        }
+      if (VL && (mk.ends >> j & 1))
+        k = p.dlast && have ? p.dlast[static_cast<int64_t>(__builtin_amdgcn_readlane(mk.seq, j)) * dim + col] : 0.0f;
+      const float G = g[j] + k, dla = G * cl[j], s = sr[j];
+      const float di = G * ci[j], drr = dla * (A * s * (1.0f - s));
+      dA = __builtin_fmaf(dla, s, dA);
+      drb += drr;
+      dib += di;
+      k = a[j] * G;
+      IO::store(rdx, G * cx[j], only(j), at(j));
+      IO::store(rdr, drr, only(j), at(j));
+      IO::store(rdi, di, only(j), at(j));
+      if (VL && (mk.starts >> j & 1)) {
+        if (p.dh0 && have) p.dh0[static_cast<int64_t>(__builtin_amdgcn_readlane(mk.seq, j)) * dim + col] = k;
+        k = 0.0f;
       }
     }
   }
-  if (!VL && p.dh0 && c == 0 && w == 0 && have) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) p.dh0[static_cast<int64_t>(row) * dim + col + v] = k[v];
-  }
+  if (!VL && p.dh0 && c == 0 && w == 0 && have) p.dh0[static_cast<int64_t>(row) * dim + col] = k;
   // the chunk's sums: over the waves, last tokens first
   __syncthreads();
   float* const s_sum = reinterpret_cast<float*>(&s_in[0][0]);  // (W, 3, C)
   static_assert(sizeof(s_in) >= sizeof(float) * W * 3 * C, "the sums fit where the maps were");
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    s_sum[(w * 3 + 0) * C + lane * V + v] = dA[v];
-    s_sum[(w * 3 + 1) * C + lane * V + v] = drb[v];
-    s_sum[(w * 3 + 2) * C + lane * V + v] = dib[v];
-  }
+  s_sum[(w * 3 + 0) * C + lane] = dA;
+  s_sum[(w * 3 + 1) * C + lane] = drb;
+  s_sum[(w * 3 + 2) * C + lane] = dib;
   __syncthreads();
   for (int q = threadIdx.x; q < 3 * C; q += 64 * W) {
     float v = 0.0f;
 #pragma unroll
     for (int k2 = W - 1; k2 >= 0; --k2) v += s_sum[k2 * 3 * C + q];
     const int what = q / C, cc = col0 + q % C;
-    if (cc < dim)
-      p.part[((static_cast<int64_t>(row) * chunks + c) * 3 + what) * dim + cc] = v;
+    if (cc < dim) p.part[((static_cast<int64_t>(row) * chunks + c) * 3 + what) * dim + cc] = v;
   }
 }
 
@@ -383,7 +269,7 @@ __global__ void __launch_bounds__(64 * kSumWaves) gated_sum_kernel(const float* 
   }
 }
 
-template <typename TA, int V>
+template <typename TA>
 int launch_gated_bwd(const GatedBwdArgs<TA>& a, const GatedPlan& pl, bool norm, const char* fn,
                      hipStream_t s) {
   int rc = launch_gated_init(a.ws, pl.bytes, a.cu, a.cu ? a.nseq : a.rows, a.L, a.dim, a.dlast, a.dh0, fn, s);
@@ -392,7 +278,7 @@ int launch_gated_bwd(const GatedBwdArgs<TA>& a, const GatedPlan& pl, bool norm, 
     const dim3 grid(static_cast<unsigned>(pl.units)), block(64 * kBwdWaves);
 #define SSM_GATED_CASE(N, G, VLN)                                                              \
   if (norm == N && (a.z != nullptr) == G && (a.cu != nullptr) == VLN)                          \
-    hipLaunchKernelGGL((gated_bwd_kernel<TA, V, N, G, VLN>), grid, block, 0, s, a, pl);
+    hipLaunchKernelGGL((gated_bwd_kernel<TA, N, G, VLN>), grid, block, 0, s, a, pl);
     SSM_GATED_CASE(true, true, false)
     SSM_GATED_CASE(true, false, false)
     SSM_GATED_CASE(false, true, false)
@@ -418,10 +304,12 @@ struct BwdSpace {
 };
 BwdSpace bwd_space(int64_t rows, int64_t L, int64_t dim, bool have_states) {
   const auto up = [](size_t v) { return (v + 255) & ~size_t{255}; };
-  const size_t chunks = static_cast<size_t>(rows) * ((L + SSM_GATED_CHUNK - 1) / SSM_GATED_CHUNK);
+  const size_t own = gated_plan(rows, L, dim, kBwdChunk).bytes, fwd = have_states ? 0 : gated_fwd_bytes(rows, L, dim);
+  const size_t states = static_cast<size_t>(rows) * ((L + SSM_GATED_CHUNK - 1) / SSM_GATED_CHUNK);
+  const size_t chunks = static_cast<size_t>(rows) * ((L + kBwdChunk - 1) / kBwdChunk);
   BwdSpace b;
-  b.states = up(gated_walk_bytes(rows, L, dim));
-  b.part = b.states + (have_states ? 0 : up(chunks * dim * 4));
+  b.states = up(own > fwd ? own : fwd);
+  b.part = b.states + (have_states ? 0 : up(states * dim * 4));
   b.bytes = b.part + up(chunks * 3 * dim * 4);
   return b;
 }
@@ -512,7 +400,7 @@ int gated_bwd(const char* fn, const void* x, const void* r, const void* i, const
                        static_cast<TA*>(dx), static_cast<TA*>(dr), static_cast<TA*>(di),
                        static_cast<TA*>(dz), dA, drb, dib, dh0, packed ? cu : nullptr, rows, L, nseq,
                        static_cast<int>(dim), ws, reinterpret_cast<float*>(at + sp.part)};
-    return launch_gated_bwd<TA, 1>(a, gated_plan(rows, L, dim, 1, SSM_GATED_CHUNK), normalize != 0, fn, stream);
+    return launch_gated_bwd<TA>(a, gated_plan(rows, L, dim, kBwdChunk), normalize != 0, fn, stream);
   };
   return dtype == SSM_DTYPE_F32 ? go(float{}) : go(bf16_t{});
 }

@@ -15,7 +15,7 @@ import torch
 from . import ops
 from .ops import _DTYPES, _check, _ptr, _raise
 
-SSM_GATED_CHUNK = 64
+SSM_GATED_CHUNK = 16
 
 EXPORTS = ("ssm_gated_scan_fwd", "ssm_gated_scan_fwd_workspace_bytes", "ssm_gated_scan_fwd_varlen",
            "ssm_gated_scan_fwd_varlen_workspace_bytes", "ssm_gated_scan_bwd",

@@ -118,7 +118,7 @@ def backward(x, r, i, A, dout, z=None, rb=None, ib=None, normalize=True, h0=None
     aA = np.abs(A)
     res["drgate"] = el * aA * ss + dla * aA * (as_ + ss * 4 * E)
     res["dinitial_state"] = ek
-    steps = (64 + 16 + n * (L // 64 + 2)) * E
+    steps = (128 + 16 + n * (L // 128 + 2)) * E
     for name, e, mag in (("dA", el * s + dla * s * (2 * v + 8) * E, dla * s),
                          ("drgate_bias", res["drgate"], dla * aA * ss),
                          ("digate_bias", res["digate"], Ga * mx * uu)):
