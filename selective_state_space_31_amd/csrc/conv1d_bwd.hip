@@ -24,85 +24,236 @@ struct ConvBwdArgs {
   const TA *state0, *dout, *dstate1;  // state0, dstate1: (batch, dim, W-1) or NULL
   TA* dx;
   TA* dstate0;
-  float* part;  // (W + 1, batch, dim)
+  float* part;  // (batch * chunks, W + 1, dim)
   int64_t batch, L;
   int dim;
+  uint32_t tiles, chunks;  // of 64 V channels, of kConvBwdChunk tokens
 };
 
-// One lane per (sequence, channel) walks the tokens with the last W - 1
-// inputs and gradients in registers.
-template <typename TA, int W, bool SILU>
-__global__ void __launch_bounds__(64) conv_bwd_kernel(ConvBwdArgs<TA> a) {
-  const int c = blockIdx.x * 64 + threadIdx.x;
-  const int64_t b = blockIdx.y;
-  if (c >= a.dim) return;
-  const int64_t row = b * a.dim + c, L = a.L;
-  float w[W], xw[W], dw[W] = {}, db = 0.0f;
-  float dd[W] = {};  // dd[j]: gradient so far of the input j steps back
+constexpr int kConvBwdT = 32;     // tokens of a wave
+constexpr int kConvBwdWaves = 4;  // waves of a workgroup, one stretch after the other
+constexpr int kConvBwdChunk = kConvBwdT * kConvBwdWaves;
+
+// V channels of one token: raw bits as loaded, widened at use (as in the
+// forward: for bf16 two channels a lane, 4-byte accesses).
+template <typename TA, int V>
+struct ConvCell;
+template <>
+struct ConvCell<float, 1> {
+  using raw_t = uint32_t;
+  __device__ static raw_t load(rsrc_t r, uint32_t vo, uint32_t so) {
+    return __builtin_amdgcn_raw_buffer_load_b32(r, vo, so, 0);
+  }
+  __device__ static float get(raw_t v, int) { return __uint_as_float(v); }
+  __device__ static void store(rsrc_t r, const float (&v)[1], uint32_t vo, uint32_t so) {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), r, vo, so, kStoreStream);
+  }
+};
+template <>
+struct ConvCell<bf16_t, 1> {
+  using raw_t = uint16_t;
+  __device__ static raw_t load(rsrc_t r, uint32_t vo, uint32_t so) {
+    return __builtin_amdgcn_raw_buffer_load_b16(r, vo, so, 0);
+  }
+  __device__ static float get(raw_t v, int) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+  __device__ static void store(rsrc_t r, const float (&v)[1], uint32_t vo, uint32_t so) {
+    const __bf16 b = static_cast<__bf16>(v[0]);  // round to nearest even
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, b), r, vo, so, kStoreStream);
+  }
+};
+template <>
+struct ConvCell<bf16_t, 2> {
+  using raw_t = uint32_t;
+  __device__ static raw_t load(rsrc_t r, uint32_t vo, uint32_t so) {
+    return __builtin_amdgcn_raw_buffer_load_b32(r, vo, so, 0);
+  }
+  __device__ static float get(raw_t v, int k) { return __uint_as_float(k ? (v & 0xffff0000u) : (v << 16)); }
+  __device__ static void store(rsrc_t r, const float (&v)[2], uint32_t vo, uint32_t so) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 b = __builtin_convertvector((f32x2{v[0], v[1]}), bf16x2);
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, b), r, vo, so, kStoreStream);
+  }
+};
+// Byte offset that no descriptor here covers (a stretch spans less than 2^30
+// bytes): loads give 0, stores are dropped.
+constexpr uint32_t kConvNoColumn = 0x7fffff00u;
+
+// One pass: a wave takes kConvBwdT tokens of 64 V channels.  Going through
+// them it keeps the last W inputs and the last W gradients before the SiLU in
+// registers; the W - 1 tokens behind its stretch are computed once more for
+// the inputs at its end, and the rows around the stretch are the neighbouring
+// waves' (found in cache).  All loads are issued before the first use.  The
+// sums over tokens stay in registers, are added over the workgroup's waves in
+// LDS and leave one row of partials per workgroup.
+template <typename TA, int V, int W, bool SILU>
+__global__ void __launch_bounds__(64 * kConvBwdWaves) conv_bwd_kernel(ConvBwdArgs<TA> a) {
+  constexpr int T = kConvBwdT, C = 64 * V, K = W - 1;
+  using IO = ConvCell<TA, V>;
+  __shared__ float s_sum[kConvBwdWaves][W + 1][C];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t tile = blockIdx.x % a.tiles, rest = blockIdx.x / a.tiles;
+  const uint32_t chunk = rest % a.chunks, b = rest / a.chunks;
+  const int dim = a.dim, col0 = static_cast<int>(tile) * C, col = col0 + lane * V;
+  const bool have = col < dim;
+  const int64_t L = a.L, t0 = static_cast<int64_t>(chunk) * kConvBwdChunk + w * T;
+  const int n = t0 >= L ? 0 : (L - t0 < T ? static_cast<int>(L - t0) : T);  // the wave's tokens
+  float dw[V][W], db[V];
 #pragma unroll
-  for (int k = 0; k < W; ++k) w[k] = a.w[static_cast<size_t>(c) * W + k];
+  for (int v = 0; v < V; ++v) {
 #pragma unroll
-  for (int k = 0; k + 1 < W; ++k)
-    xw[k + 1] = a.state0 ? to_f32(a.state0[row * (W - 1) + k]) : 0.0f;
-  const float bias = a.bias ? a.bias[c] : 0.0f;
-  // after the last token the window still holds W - 1 inputs
-  for (int64_t t = 0; t < L + W - 1; ++t) {
-    float d = 0.0f, x = 0.0f;
-    if (t < L) {
-      x = to_f32(a.x[(b * L + t) * a.dim + c]);
-      d = to_f32(a.dout[(b * L + t) * a.dim + c]);
+    for (int k = 0; k < W; ++k) dw[v][k] = 0.0f;
+    db[v] = 0.0f;
+  }
+  // (an empty sequence's first wave moves the state's gradient through)
+  if (n > 0 || (L == 0 && t0 == 0)) {
+    const uint32_t rowb = static_cast<uint32_t>(dim) * sizeof(TA);
+    const uint32_t voff = have ? static_cast<uint32_t>(lane * V * sizeof(TA)) : kConvNoColumn;
+    // rows [t0, min(t0 + T + K, L)) of this sequence, from the wave's column on
+    const int rows = L - t0 < T + K ? static_cast<int>(L - t0) : T + K;
+    const int64_t base = (static_cast<int64_t>(b) * L + t0) * dim + col0;
+    const uint32_t span = rows > 0 ? static_cast<uint32_t>(rows) * rowb - col0 * static_cast<uint32_t>(sizeof(TA)) : 0;
+    const rsrc_t rx = make_rsrc(a.x + base, span), rd = make_rsrc(a.dout + base, span);
+    const uint32_t lastrow = rows > 0 ? static_cast<uint32_t>(rows - 1) * rowb : 0;
+    const auto at = [&](int j) {  // rows behind the last are that one again
+      const uint32_t o = static_cast<uint32_t>(j) * rowb;
+      return o < lastrow ? o : lastrow;
+    };
+    typename IO::raw_t xr[T + K], dr[T + K], xb[K];
+    if (rows > 0) {
+#pragma unroll
+      for (int j = 0; j < T + K; ++j) {
+        xr[j] = IO::load(rx, voff, at(j));
+        dr[j] = IO::load(rd, voff, at(j));
+      }
     }
+    float wt[V][W], bias[V], xw[V][W], dd[V][W];  // the last W inputs and gradients, the newest last
 #pragma unroll
-    for (int k = 0; k + 1 < W; ++k) xw[k] = xw[k + 1];
-    xw[W - 1] = x;
-    if (SILU && t < L) {
-      float pre = bias;
+    for (int v = 0; v < V; ++v) {
 #pragma unroll
-      for (int k = 0; k < W; ++k) pre = __builtin_fmaf(w[k], xw[k], pre);
-      const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-pre * kLog2e));
-      d *= s * (1.0f + pre * (1.0f - s));
+      for (int k = 0; k < W; ++k) {
+        wt[v][k] = have ? a.w[static_cast<size_t>(col + v) * W + k] : 0.0f;
+        dd[v][k] = 0.0f;
+        xw[v][k] = 0.0f;
+      }
+      bias[v] = have && a.bias ? a.bias[col + v] : 0.0f;
     }
+    if (t0 > 0) {  // the K rows before
+      const rsrc_t rb = make_rsrc(a.x + base - static_cast<int64_t>(K) * dim, K * rowb);
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
-      dw[k] = __builtin_fmaf(d, xw[k], dw[k]);
-      dd[W - 1 - k] = __builtin_fmaf(d, w[k], dd[W - 1 - k]);
+      for (int j = 0; j < K; ++j) xb[j] = IO::load(rb, voff, static_cast<uint32_t>(j) * rowb);
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) xw[v][j + 1] = IO::get(xb[j], v);
+    } else if (a.state0 && have) {
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          xw[v][j + 1] = to_f32(a.state0[(static_cast<int64_t>(b) * dim + col + v) * K + j]);
     }
-    db += d;
-    // the input W - 1 steps back is done
-    const int64_t s = t - (W - 1);
-    float g = dd[W - 1];
-    if (a.dstate1 && s >= L - (W - 1))
-      g += to_f32(a.dstate1[row * (W - 1) + (s - (L - (W - 1)))]);
-    if (s >= 0)
-      store_act(a.dx + (b * L + s) * a.dim + c, g);
-    else if (a.dstate0)
-      store_act(a.dstate0 + row * (W - 1) + (s + W - 1), g);
+    const rsrc_t ro = make_rsrc(a.dx + base, n > 0 ? static_cast<uint32_t>(n) * rowb - col0 * static_cast<uint32_t>(sizeof(TA)) : 0);
 #pragma unroll
-    for (int k = W - 1; k > 0; --k) dd[k] = dd[k - 1];
-    dd[0] = 0.0f;
+    for (int j = 0; j < T + K; ++j) {
+      float o[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          xw[v][k] = xw[v][k + 1];
+          dd[v][k] = dd[v][k + 1];
+        }
+        xw[v][K] = rows > 0 ? IO::get(xr[j], v) : 0.0f;
+        float d = rows > 0 ? IO::get(dr[j], v) : 0.0f;
+        if (SILU) {
+          float pre = bias[v];
+#pragma unroll
+          for (int k = 0; k < W; ++k) pre = __builtin_fmaf(wt[v][k], xw[v][k], pre);
+          const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-pre * kLog2e));
+          d *= s * __builtin_fmaf(pre, 1.0f - s, 1.0f);
+        }
+        d = j < rows ? d : 0.0f;  // tokens behind the sequence
+        dd[v][K] = d;
+        if (j < T && j < n) {  // (not d = 0 times what a window behind the end holds)
+#pragma unroll
+          for (int k = 0; k < W; ++k) dw[v][k] = __builtin_fmaf(d, xw[v][k], dw[v][k]);
+          db[v] += d;
+        }
+        // the input K tokens back has all its gradients now
+        o[v] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) o[v] = __builtin_fmaf(wt[v][K - k], dd[v][k], o[v]);
+      }
+      const int64_t s = t0 + j - K;
+      if (j < K) {  // before the stretch: the wave in front has it, or the state
+        if (t0 == 0 && a.dstate0 && have) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const int64_t st = (static_cast<int64_t>(b) * dim + col + v) * K;
+            const int64_t f = s - (L - K);  // its place in the final state
+            if (a.dstate1 && f >= 0) o[v] += to_f32(a.dstate1[st + f]);
+            store_act(a.dstate0 + st + j, o[v]);
+          }
+        }
+      } else if (j - K < n) {
+        if (a.dstate1 && s >= L - K && have) {
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            o[v] += to_f32(a.dstate1[(static_cast<int64_t>(b) * dim + col + v) * K + (s - (L - K))]);
+        }
+        IO::store(ro, o, voff, static_cast<uint32_t>(j - K) * rowb);
+      }
+    }
   }
 #pragma unroll
-  for (int k = 0; k < W; ++k) a.part[(k * a.batch + b) * a.dim + c] = dw[k];
-  a.part[(W * a.batch + b) * a.dim + c] = db;
+  for (int v = 0; v < V; ++v) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) s_sum[w][k][lane * V + v] = dw[v][k];
+    s_sum[w][W][lane * V + v] = db[v];
+  }
+  __syncthreads();
+  for (int q = threadIdx.x; q < (W + 1) * C; q += 64 * kConvBwdWaves) {
+    const int k = q / C, cc = q % C;
+    float v = s_sum[0][k][cc];
+#pragma unroll
+    for (int u = 1; u < kConvBwdWaves; ++u) v += s_sum[u][k][cc];
+    if (col0 + cc < dim)
+      a.part[((static_cast<int64_t>(b) * a.chunks + chunk) * (W + 1) + k) * dim + col0 + cc] = v;
+  }
 }
 
-// Sums of the partials, in sequence order: one lane per channel, a row of
-// workgroups per tap (the last one the bias).
-__global__ void __launch_bounds__(64) conv_bwd_sum_kernel(const float* part, int64_t n, int dim, int W,
-                                                          float* dweight, float* dbias) {
-  const int c = blockIdx.x * 64 + threadIdx.x, k = blockIdx.y;
-  if (c >= dim || (k == W && !dbias)) return;
+// Sums of the workgroups' partials: a workgroup takes 64 channels of one tap
+// (the last one the bias), wave w every kConvSumWaves-th row, and the waves'
+// sums are added in order.
+constexpr int kConvSumWaves = 8;
+__global__ void __launch_bounds__(64 * kConvSumWaves) conv_bwd_sum_kernel(const float* part, int64_t n, int dim,
+                                                                          int W, float* dweight, float* dbias) {
+  __shared__ float s_part[kConvSumWaves][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane, k = blockIdx.y;
+  if (k == W && !dbias) return;
   float v = 0.0f;
-  for (int64_t j = 0; j < n; ++j) v += part[(k * n + j) * dim + c];
-  if (k == W)
-    dbias[c] = v;
-  else
-    dweight[static_cast<size_t>(c) * W + k] = v;
+  if (c < dim) {
+    const float* from = part + static_cast<int64_t>(k) * dim + c;
+#pragma unroll 8
+    for (int64_t j = w; j < n; j += kConvSumWaves) v += from[j * (W + 1) * dim];
+  }
+  s_part[w][lane] = v;
+  __syncthreads();
+  if (w == 0 && c < dim) {
+#pragma unroll
+    for (int u = 1; u < kConvSumWaves; ++u) v += s_part[u][lane];
+    if (k == W)
+      dbias[c] = v;
+    else
+      dweight[static_cast<size_t>(c) * W + k] = v;
+  }
 }
 
 namespace {
 
-constexpr int64_t kConvBwdMaxDim = int64_t{1} << 24;
+constexpr int64_t kConvBwdMaxDim = int64_t{1} << 22;
 
 bool conv_bwd_sizes_ok(int64_t batch, int64_t L, int64_t dim) {
   return batch >= 1 && dim >= 1 && L >= 0 && dim <= kConvBwdMaxDim && batch <= 65535 &&
@@ -110,16 +261,20 @@ bool conv_bwd_sizes_ok(int64_t batch, int64_t L, int64_t dim) {
          batch * ((L + 15) / 16) * ((dim + 63) / 64) < (int64_t{1} << 25);
 }
 
-template <typename TA>
-int conv_bwd_launch(const ConvBwdArgs<TA>& a, int W, bool silu, float* dweight, float* dbias,
-                    hipStream_t s) {
-  const dim3 grid((a.dim + 63) / 64, static_cast<unsigned>(a.batch)), block(64);
+int64_t conv_bwd_chunks(int64_t L) { return L > 0 ? (L + kConvBwdChunk - 1) / kConvBwdChunk : 1; }
+
+template <typename TA, int V>
+int conv_bwd_launch(ConvBwdArgs<TA> a, int W, bool silu, float* dweight, float* dbias, hipStream_t s) {
+  a.tiles = static_cast<uint32_t>((a.dim + 64 * V - 1) / (64 * V));
+  a.chunks = static_cast<uint32_t>(conv_bwd_chunks(a.L));
+  const int64_t n = a.batch * a.chunks;
+  const dim3 grid(static_cast<unsigned>(n * a.tiles)), block(64 * kConvBwdWaves);
 #define SSM_CONV_BWD_CASE(WW)                                                            \
   case WW:                                                                               \
     if (silu)                                                                            \
-      hipLaunchKernelGGL((conv_bwd_kernel<TA, WW, true>), grid, block, 0, s, a);         \
+      hipLaunchKernelGGL((conv_bwd_kernel<TA, V, WW, true>), grid, block, 0, s, a);      \
     else                                                                                 \
-      hipLaunchKernelGGL((conv_bwd_kernel<TA, WW, false>), grid, block, 0, s, a);        \
+      hipLaunchKernelGGL((conv_bwd_kernel<TA, V, WW, false>), grid, block, 0, s, a);     \
     break;
   switch (W) {
     SSM_CONV_BWD_CASE(2)
@@ -128,8 +283,8 @@ int conv_bwd_launch(const ConvBwdArgs<TA>& a, int W, bool silu, float* dweight, 
     default: break;
   }
 #undef SSM_CONV_BWD_CASE
-  hipLaunchKernelGGL(conv_bwd_sum_kernel, dim3((a.dim + 63) / 64, W + 1), block, 0, s, a.part, a.batch,
-                     a.dim, W, dweight, dbias);
+  hipLaunchKernelGGL(conv_bwd_sum_kernel, dim3((a.dim + 63) / 64, W + 1), dim3(64 * kConvSumWaves), 0, s, a.part,
+                     n, a.dim, W, dweight, dbias);
   return launch_status("ssm_causal_conv1d_bwd");
 }
 
@@ -143,7 +298,7 @@ extern "C" {
 size_t ssm_causal_conv1d_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim,
                                              int64_t width) {
   if (!conv_bwd_sizes_ok(batch, seqlen, dim) || width < 2 || width > 4) return 0;
-  return static_cast<size_t>(width + 1) * batch * dim * sizeof(float);
+  return static_cast<size_t>(width + 1) * batch * conv_bwd_chunks(seqlen) * dim * sizeof(float);
 }
 
 int ssm_causal_conv1d_bwd(const void* x, const float* weight, const float* bias,
@@ -203,8 +358,13 @@ int ssm_causal_conv1d_bwd(const void* x, const float* weight, const float* bias,
                       static_cast<const TA*>(initial_conv_state), static_cast<const TA*>(dout),
                       static_cast<const TA*>(dfinal_conv_state), static_cast<TA*>(dx),
                       static_cast<TA*>(dinitial_conv_state), static_cast<float*>(workspace), batch,
-                      seqlen, static_cast<int>(dim)};
-    return conv_bwd_launch(a, static_cast<int>(width), silu != 0, dweight, dbias, stream);
+                      seqlen, static_cast<int>(dim), 0, 0};
+    if constexpr (sizeof(TA) == 2) {
+      // two channels a lane where every row starts on four bytes
+      if (dim % 2 == 0 && aligned(x, 4) && aligned(dout, 4) && aligned(dx, 4))
+        return conv_bwd_launch<TA, 2>(a, static_cast<int>(width), silu != 0, dweight, dbias, stream);
+    }
+    return conv_bwd_launch<TA, 1>(a, static_cast<int>(width), silu != 0, dweight, dbias, stream);
   };
   return dtype == SSM_DTYPE_F32 ? go(float{}) : go(bf16_t{});
 }

@@ -100,6 +100,18 @@ def test_empty_sequence():
     assert not g["dweight"].any() and not g["dbias"].any()
 
 
+def test_infinite_input_at_the_end():
+    """Without SiLU an infinite last input gives infinite weight gradients,
+    not NaN from the tokens behind the sequence."""
+    for L in (7, 32, 40):
+        c = Case(1, L, 64, 4, "fp32", 8, silu=False, state=False, dfinal=False)
+        c.x[0, L - 1, 5] = float("inf")
+        c.dout[:] = 1.0
+        g = pkg.ssm_causal_conv1d_bwd(*c.args(), **c.kw())
+        assert torch.isinf(g["dweight"][5, 3]) and torch.isfinite(g["dweight"][5, :3]).all()
+        assert torch.isfinite(g["dx"]).all()
+
+
 def test_large_inputs_and_nan():
     """Pre-activations past where the logistic function saturates, and a NaN
     that reaches only its own neighbourhood and channel."""
