@@ -63,9 +63,10 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
-// One wave per row (token, head); lane l holds elements l, l + 64, ...
+// Head sizes and alignments that no vector access fits: one wave per row
+// (token, head); lane l holds elements l, l + 64, ...
 template <typename TA, bool INTER, bool BWD>
-__global__ void __launch_bounds__(64 * kRotWaves) rotate_kernel(RotArgs<TA> p) {
+__global__ void __launch_bounds__(64 * kRotWaves) rotate_any_kernel(RotArgs<TA> p) {
   const int lane = threadIdx.x & 63;
   const int64_t wave = static_cast<int64_t>(blockIdx.x) * kRotWaves + (threadIdx.x >> 6);
   const int64_t nwaves = static_cast<int64_t>(gridDim.x) * kRotWaves;
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(64 * kRotWaves) rotate_kernel(RotArgs<TA> p) {
       }
       ss += v[n] * v[n];
     }
-    const float rstd = 1.0f / __builtin_sqrtf(wave_sum(ss) / static_cast<float>(p.D) + p.eps);
+    const float rstd = __builtin_amdgcn_rsqf(wave_sum(ss) / static_cast<float>(p.D) + p.eps);
     float res[kRotElems], dot = 0.0f;
 #pragma unroll
     for (int n = 0; n < kRotElems; ++n) {
@@ -140,15 +141,234 @@ __global__ void __launch_bounds__(64 * kRotWaves) rotate_kernel(RotArgs<TA> p) {
   }
 }
 
-// Sum of the partial weight gradients, in wave order: one lane per element.
-__global__ void __launch_bounds__(64) rotate_sum_kernel(const float* part, int n, int D, float* dqw,
-                                                        float* dkw) {
-  const int e = blockIdx.x * 64 + threadIdx.x;
+// E values moved as one access of 4, 8 or 16 bytes.
+template <typename TA, int E>
+struct RotVec;
+template <int E>
+struct RotVec<float, E> {
+  typedef float vec_t __attribute__((ext_vector_type(E)));
+  __device__ static void load(const float* p, float (&v)[E]) {
+    const vec_t r = *reinterpret_cast<const vec_t*>(p);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = r[e];
+  }
+  __device__ static void store(float* p, const float (&v)[E]) {
+    vec_t r;
+#pragma unroll
+    for (int e = 0; e < E; ++e) r[e] = v[e];
+    __builtin_nontemporal_store(r, reinterpret_cast<vec_t*>(p));
+  }
+};
+template <int E>
+struct RotVec<bf16_t, E> {
+  typedef uint32_t vec_t __attribute__((ext_vector_type(E / 2)));
+  __device__ static void load(const bf16_t* p, float (&v)[E]) {
+    const vec_t r = *reinterpret_cast<const vec_t*>(p);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+      v[2 * e] = __uint_as_float(r[e] << 16);
+      v[2 * e + 1] = __uint_as_float(r[e] & 0xffff0000u);
+    }
+  }
+  __device__ static void store(bf16_t* p, const float (&v)[E]) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    vec_t r;
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+      const bf16x2 b = __builtin_convertvector((f32x2{v[2 * e], v[2 * e + 1]}), bf16x2);
+      r[e] = __builtin_bit_cast(uint32_t, b);
+    }
+    __builtin_nontemporal_store(r, reinterpret_cast<vec_t*>(p));
+  }
+};
+
+// Sum over the lanes of one row (a power of two of neighbours).
+template <int N>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// A row of D values is cut into blocks of E; a lane holds two of them that
+// form pairs: block l and the block R/2 values on while l is in the rotated
+// part (with interleaved pairs any two), two neighbouring blocks behind it.
+// So a rotation needs no other lane, and a row takes N = D / (2 E) lanes,
+// rounded up to a power of two; a wave holds 64 / N tokens and goes through
+// their heads, forming the sines and cosines once per token.
+template <typename TA, int E, int N, bool INTER, bool BWD>
+__global__ void __launch_bounds__(64 * kRotWaves) rotate_kernel(RotArgs<TA> p, int head_step) {
+  using IO = RotVec<TA, E>;
+  constexpr int S = 64 / N;  // tokens of a wave
+  __shared__ float s_w[BWD ? kRotWaves : 1][2][BWD ? 2 * E * N : 1];
+  const int lane = threadIdx.x & 63, l = lane % N, slot = lane / N;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int heads = p.Hq + p.Hk, half = p.R / 2;
+  const bool have = l < p.D / (2 * E);
+  const int turned = p.R / (2 * E);  // lanes with rotated values
+  const int e0 = l < turned ? (INTER ? 2 * E * l : E * l) : p.R + 2 * E * (l - turned);
+  const int e1 = l < turned && !INTER ? E * l + half : e0 + E;
+  float wq[2 * E], wk[2 * E], dwq[BWD ? 2 * E : 1], dwk[BWD ? 2 * E : 1];
+#pragma unroll
+  for (int e = 0; e < 2 * E; ++e) {
+    const int at = e < E ? e0 + e : e1 + e - E;
+    wq[e] = have && p.qw ? p.qw[at] : 1.0f;
+    wk[e] = have && p.kw ? p.kw[at] : 1.0f;
+    if (BWD) dwq[e] = dwk[e] = 0.0f;
+  }
+  const float mean = 1.0f / static_cast<float>(p.D);
+  // (blockIdx.y: a range of heads, where there are few tokens)
+  const int h0 = blockIdx.y * head_step, h1 = h0 + head_step < heads ? h0 + head_step : heads;
+  for (int64_t g = static_cast<int64_t>(blockIdx.x) * kRotWaves + wave; g * S < p.tokens;
+       g += static_cast<int64_t>(gridDim.x) * kRotWaves) {
+    const int64_t tok = g * S + slot;
+    const bool on = have && tok < p.tokens;
+    const int64_t tk = tok < p.tokens ? tok : p.tokens - 1;
+    const TA* const q = p.q + tk * p.qs;
+    const TA* const k = p.k + tk * p.ks;
+    const auto row = [&](int h) { return h < p.Hq ? q + h * p.D : k + (h - p.Hq) * p.D; };
+    const auto place = [&](int h) { return h < p.Hq ? (tk * p.Hq + h) * p.D : (tk * p.Hk + h - p.Hq) * p.D; };
+    float sn[E], cs[E];
+    const int32_t pos = p.pos ? p.pos[tk] : static_cast<int32_t>(tk % p.L);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      sn[e] = 0.0f;
+      cs[e] = 1.0f;
+      if (l < turned) turn_f32(pos, p.freq[E * l + e], sn[e], cs[e]);
+      if (BWD) sn[e] = -sn[e];
+    }
+    // pair i of the lane: values (i, i + E), or (2i, 2i + 1) when interleaved
+    const auto rotate = [&](float (&v)[2 * E]) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int a = INTER ? 2 * i : i, b = INTER ? 2 * i + 1 : i + E;
+        const float x = v[a], y = v[b];
+        v[a] = __builtin_fmaf(x, cs[i], -(y * sn[i]));
+        v[b] = __builtin_fmaf(x, sn[i], y * cs[i]);
+      }
+    };
+    const auto fetch = [&](const TA* r, float (&v)[2 * E]) {
+      float lo[E], hi[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) lo[e] = hi[e] = 0.0f;
+      if (have) {
+        IO::load(r + e0, lo);
+        IO::load(r + e1, hi);
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        v[e] = lo[e];
+        v[e + E] = hi[e];
+      }
+    };
+    const auto put = [&](TA* r, const float (&v)[2 * E]) {
+      float lo[E], hi[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        lo[e] = v[e];
+        hi[e] = v[e + E];
+      }
+      if (on) {
+        IO::store(r + e0, lo);
+        IO::store(r + e1, hi);
+      }
+    };
+    float next[2 * E], nextd[BWD ? 2 * E : 1];
+    fetch(row(h0), next);
+    if constexpr (BWD) fetch((h0 < p.Hq ? p.dqo : p.dko) + place(h0), nextd);
+    for (int h = h0; h < h1; ++h) {
+      const bool isq = h < p.Hq;
+      float v[2 * E], d[BWD ? 2 * E : 1], ss = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 2 * E; ++e) {
+        v[e] = next[e];
+        if (BWD) d[e] = nextd[e];
+      }
+      if (h + 1 < h1) {  // the next head's row while this one is worked on
+        fetch(row(h + 1), next);
+        if constexpr (BWD) fetch((h + 1 < p.Hq ? p.dqo : p.dko) + place(h + 1), nextd);
+      }
+#pragma unroll
+      for (int e = 0; e < 2 * E; ++e) ss = __builtin_fmaf(v[e], v[e], ss);
+      const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum<N>(ss), mean, p.eps));
+      TA* const out = (isq ? p.qo : p.ko) + place(h);
+      if constexpr (!BWD) {
+#pragma unroll
+        for (int e = 0; e < 2 * E; ++e) v[e] = v[e] * rstd * (isq ? wq[e] : wk[e]);
+        rotate(v);
+        put(out, v);
+      } else {
+        rotate(d);
+        float dot = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 2 * E; ++e) {
+          v[e] *= rstd;  // vhat
+          if (isq) dwq[e] += on ? d[e] * v[e] : 0.0f;
+          else dwk[e] += on ? d[e] * v[e] : 0.0f;
+          d[e] *= isq ? wq[e] : wk[e];
+          dot = __builtin_fmaf(d[e], v[e], dot);
+        }
+        dot = row_sum<N>(dot) * mean;
+#pragma unroll
+        for (int e = 0; e < 2 * E; ++e) d[e] = rstd * (d[e] - v[e] * dot);
+        put(out, d);
+      }
+    }
+  }
+  if constexpr (BWD) {
+    // over the wave's tokens, then over the waves, in a fixed order
+#pragma unroll
+    for (int e = 0; e < 2 * E; ++e) {
+#pragma unroll
+      for (int o = N; o < 64; o <<= 1) {
+        dwq[e] += __shfl_xor(dwq[e], o);
+        dwk[e] += __shfl_xor(dwk[e], o);
+      }
+      if (slot == 0) {
+        s_w[wave][0][l * 2 * E + e] = dwq[e];
+        s_w[wave][1][l * 2 * E + e] = dwk[e];
+      }
+    }
+    __syncthreads();
+    float* const part = p.part + (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 2 * p.D;
+    for (int i = threadIdx.x; i < 2 * 2 * E * N; i += 64 * kRotWaves) {
+      const int what = i / (2 * E * N), ll = i % (2 * E * N) / (2 * E), e = i % (2 * E);
+      if (ll >= p.D / (2 * E)) continue;
+      const int b0 = ll < turned ? (INTER ? 2 * E * ll : E * ll) : p.R + 2 * E * (ll - turned);
+      const int b1 = ll < turned && !INTER ? E * ll + half : b0 + E;
+      float v = 0.0f;
+#pragma unroll
+      for (int u = 0; u < kRotWaves; ++u) v += s_w[u][what][ll * 2 * E + e];
+      part[what * p.D + (e < E ? b0 + e : b1 + e - E)] = v;
+    }
+  }
+}
+
+// Sum of the partial weight gradients: a workgroup takes 64 elements of one of
+// the two, wave w every kRotSumWaves-th row, and the waves' sums are added in
+// order.
+constexpr int kRotSumWaves = 16;
+__global__ void __launch_bounds__(64 * kRotSumWaves) rotate_sum_kernel(const float* part, int n, int D, float* dqw,
+                                                                       float* dkw) {
+  __shared__ float s_part[kRotSumWaves][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int e = blockIdx.x * 64 + lane;
   float* to = blockIdx.y == 0 ? dqw : dkw;
-  if (e >= D || !to) return;
+  if (!to) return;
   float v = 0.0f;
-  for (int k = 0; k < n; ++k) v += part[(k * 2 + blockIdx.y) * static_cast<int64_t>(D) + e];
-  to[e] = v;
+  if (e < D) {
+    const float* from = part + blockIdx.y * D + e;
+#pragma unroll 16
+    for (int k = w; k < n; k += kRotSumWaves) v += from[static_cast<int64_t>(k) * 2 * D];
+  }
+  s_part[w][lane] = v;
+  __syncthreads();
+  if (w == 0 && e < D) {
+#pragma unroll
+    for (int k = 1; k < kRotSumWaves; ++k) v += s_part[k][lane];
+    to[e] = v;
+  }
 }
 
 namespace {
@@ -161,11 +381,13 @@ bool rot_sizes_ok(int64_t batch, int64_t L, int64_t Hq, int64_t Hk, int64_t D) {
          D <= 256 && D % 2 == 0;
 }
 
-// Workgroups of the backward: each wave leaves one partial row of weight
-// gradients, so their number is bounded.
-int64_t rot_bwd_blocks(int64_t rows) {
-  const int64_t want = (rows + kRotWaves * 4 - 1) / (kRotWaves * 4);
-  return want < 1 ? 1 : want > 1024 ? 1024 : want;
+// Rows of partial weight gradients the backward may leave at most: as many as
+// there are waves (any layout) or workgroups (vectors), bounded so that their
+// sum stays short.
+constexpr int64_t kRotMaxParts = 512;
+int64_t rot_parts(int64_t rows) {
+  const int64_t want = (rows + kRotWaves - 1) / kRotWaves * kRotWaves;
+  return want < kRotWaves ? kRotWaves : want > kRotMaxParts ? kRotMaxParts : want;
 }
 
 struct RotCall {
@@ -186,6 +408,54 @@ struct RotCall {
   bool bwd;
 };
 
+// Launch shape of a vector kernel: tokens a wave holds, workgroups over tokens
+// (x) and over ranges of heads (y).  Heads stay together, so that a token's
+// sines and cosines are formed once, unless there are too few tokens for a
+// few waves per SIMD.
+template <typename TA, int E, int N>
+void rot_launch_vec(const RotCall& c, const RotArgs<TA>& a, int64_t* parts) {
+  const int heads = a.Hq + a.Hk;
+  const int64_t groups = (a.tokens + 64 / N - 1) / (64 / N);
+  int64_t x = (groups + kRotWaves - 1) / kRotWaves;
+  x = x < 1 ? 1 : x;
+  int step = heads;
+  const int64_t most = c.bwd ? rot_parts(a.tokens * heads) : int64_t{1} << 20;
+  while (step > 1 && x * ((heads + step - 1) / step) * 2 <= (most < kRotMaxParts ? most : kRotMaxParts)) step = (step + 1) / 2;
+  const int64_t y = (heads + step - 1) / step;
+  x = x * y > most ? (most / y < 1 ? 1 : most / y) : x;
+  const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(y)), block(64 * kRotWaves);
+  *parts = x * y;
+#define SSM_ROT_CASE(I, B)                                                                   \
+  if ((c.interleaved != 0) == I && c.bwd == B)                                               \
+    hipLaunchKernelGGL((rotate_kernel<TA, E, N, I, B>), grid, block, 0, c.stream, a, step);
+  SSM_ROT_CASE(false, false)
+  SSM_ROT_CASE(true, false)
+  SSM_ROT_CASE(false, true)
+  SSM_ROT_CASE(true, true)
+#undef SSM_ROT_CASE
+}
+
+// Whether rows can be moved in vectors of E values, two blocks to a lane.
+template <typename TA>
+bool rot_fits(const RotCall& c, int E) {
+  const size_t bytes = E * sizeof(TA);
+  if (c.D % (2 * E) || c.R % (2 * E) || c.D / (2 * E) > 64) return false;
+  if (c.qs % E || !aligned(c.q, bytes) || !aligned(c.qo, bytes) || (c.bwd && !aligned(c.dqo, bytes))) return false;
+  return !c.Hk || (c.ks % E == 0 && aligned(c.k, bytes) && aligned(c.ko, bytes) && (!c.bwd || aligned(c.dko, bytes)));
+}
+
+template <typename TA, int E>
+bool rot_try(const RotCall& c, const RotArgs<TA>& a, int64_t* parts) {
+  if (!rot_fits<TA>(c, E)) return false;
+  const int lanes = static_cast<int>(c.D / (2 * E));
+  if (lanes <= 4) rot_launch_vec<TA, E, 4>(c, a, parts);
+  else if (lanes <= 8) rot_launch_vec<TA, E, 8>(c, a, parts);
+  else if (lanes <= 16) rot_launch_vec<TA, E, 16>(c, a, parts);
+  else if (lanes <= 32) rot_launch_vec<TA, E, 32>(c, a, parts);
+  else rot_launch_vec<TA, E, 64>(c, a, parts);
+  return true;
+}
+
 template <typename TA>
 int rot_launch(const RotCall& c) {
   RotArgs<TA> a{static_cast<const TA*>(c.q), static_cast<const TA*>(c.k), c.qw, c.kw, c.freq, c.pos,
@@ -193,23 +463,27 @@ int rot_launch(const RotCall& c) {
                 static_cast<TA*>(c.ko), static_cast<float*>(c.ws), c.eps, c.batch * c.L, c.L, c.qs,
                 c.ks, static_cast<int>(c.Hq), static_cast<int>(c.Hk), static_cast<int>(c.D),
                 static_cast<int>(c.R)};
-  const int64_t rows = c.batch * c.L * (c.Hq + c.Hk);
-  const int64_t want = (rows + kRotWaves - 1) / kRotWaves;
-  const int64_t blocks = c.bwd ? rot_bwd_blocks(rows) : want > (1 << 20) ? (1 << 20) : want;
-  const dim3 grid(static_cast<unsigned>(blocks)), block(64 * kRotWaves);
-  if (c.bwd) {
-    if (c.interleaved)
-      hipLaunchKernelGGL((rotate_kernel<TA, true, true>), grid, block, 0, c.stream, a);
-    else
-      hipLaunchKernelGGL((rotate_kernel<TA, false, true>), grid, block, 0, c.stream, a);
-    if (c.dqw || c.dkw)
-      hipLaunchKernelGGL(rotate_sum_kernel, dim3((a.D + 63) / 64, 2), dim3(64), 0, c.stream, a.part,
-                         static_cast<int>(blocks * kRotWaves), a.D, c.dqw, c.dkw);
-  } else if (c.interleaved) {
-    hipLaunchKernelGGL((rotate_kernel<TA, true, false>), grid, block, 0, c.stream, a);
-  } else {
-    hipLaunchKernelGGL((rotate_kernel<TA, false, false>), grid, block, 0, c.stream, a);
+  // the widest access that the head size, the strides and the addresses allow
+  constexpr int E = 16 / sizeof(TA);
+  int64_t parts = 0;
+  if (!rot_try<TA, E>(c, a, &parts) && !rot_try<TA, E / 2>(c, a, &parts)) {
+    const int64_t rows = c.batch * c.L * (c.Hq + c.Hk);
+    const int64_t want = (rows + kRotWaves - 1) / kRotWaves;
+    const int64_t blocks = c.bwd ? rot_parts(rows) / kRotWaves : want > (1 << 20) ? (1 << 20) : want;
+    const dim3 grid(static_cast<unsigned>(blocks)), block(64 * kRotWaves);
+    parts = blocks * kRotWaves;
+#define SSM_ROT_CASE(I, B)                                                                   \
+  if ((c.interleaved != 0) == I && c.bwd == B)                                               \
+    hipLaunchKernelGGL((rotate_any_kernel<TA, I, B>), grid, block, 0, c.stream, a);
+    SSM_ROT_CASE(false, false)
+    SSM_ROT_CASE(true, false)
+    SSM_ROT_CASE(false, true)
+    SSM_ROT_CASE(true, true)
+#undef SSM_ROT_CASE
   }
+  if (c.bwd && (c.dqw || c.dkw))
+    hipLaunchKernelGGL(rotate_sum_kernel, dim3((a.D + 63) / 64, 2), dim3(64 * kRotSumWaves), 0, c.stream, a.part,
+                       static_cast<int>(parts), a.D, c.dqw, c.dkw);
   return launch_status(c.fn);
 }
 
@@ -321,7 +595,7 @@ size_t ssm_qk_norm_rotate_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int
                                               int64_t nheads_k, int64_t headdim) {
   if (!rot_sizes_ok(batch, seqlen, nheads_q, nheads_k, headdim)) return 0;
   const int64_t rows = batch * seqlen * (nheads_q + nheads_k);
-  return static_cast<size_t>(rot_bwd_blocks(rows)) * kRotWaves * 2 * headdim * sizeof(float);
+  return static_cast<size_t>(rot_parts(rows)) * 2 * headdim * sizeof(float);
 }
 
 }  // extern "C"
