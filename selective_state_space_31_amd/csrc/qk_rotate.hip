@@ -55,6 +55,7 @@ struct RotArgs {
 };
 
 constexpr int kRotWaves = 4;     // waves of a workgroup
+constexpr int kRotAhead = 4;     // rows of a token in flight (half as many in the backward, two tensors)
 constexpr int kRotElems = 4;     // elements of a row per lane (headdim <= 256)
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -147,11 +148,7 @@ struct RotVec;
 template <int E>
 struct RotVec<float, E> {
   typedef float vec_t __attribute__((ext_vector_type(E)));
-  __device__ static void load(const float* p, float (&v)[E]) {
-    const vec_t r = *reinterpret_cast<const vec_t*>(p);
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = r[e];
-  }
+  __device__ static float get(const vec_t& r, int e) { return r[e]; }
   __device__ static void store(float* p, const float (&v)[E]) {
     vec_t r;
 #pragma unroll
@@ -162,13 +159,8 @@ struct RotVec<float, E> {
 template <int E>
 struct RotVec<bf16_t, E> {
   typedef uint32_t vec_t __attribute__((ext_vector_type(E / 2)));
-  __device__ static void load(const bf16_t* p, float (&v)[E]) {
-    const vec_t r = *reinterpret_cast<const vec_t*>(p);
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e) {
-      v[2 * e] = __uint_as_float(r[e] << 16);
-      v[2 * e + 1] = __uint_as_float(r[e] & 0xffff0000u);
-    }
+  __device__ static float get(const vec_t& r, int e) {
+    return __uint_as_float(e & 1 ? r[e / 2] & 0xffff0000u : r[e / 2] << 16);
   }
   __device__ static void store(bf16_t* p, const float (&v)[E]) {
     typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -183,11 +175,22 @@ struct RotVec<bf16_t, E> {
   }
 };
 
-// Sum over the lanes of one row (a power of two of neighbours).
+// Sum over the lanes of one row (N neighbours, a power of two), in every one
+// of them.  Up to 16 lanes by lane moves inside the vector instructions
+// (neighbour, pair, half row and row mirrored): a head waits for its sums, and
+// exchanges through LDS take ten times as long.
+template <int CTRL>
+__device__ __forceinline__ float moved(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
 template <int N>
 __device__ __forceinline__ float row_sum(float v) {
+  if constexpr (N > 1) v += moved<0xb1>(v);   // lane ^ 1
+  if constexpr (N > 2) v += moved<0x4e>(v);   // lane ^ 2
+  if constexpr (N > 4) v += moved<0x141>(v);  // 7 - lane within 8
+  if constexpr (N > 8) v += moved<0x140>(v);  // 15 - lane within 16
 #pragma unroll
-  for (int o = N / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  for (int o = 16; o < N; o <<= 1) v += __shfl_xor(v, o);
   return v;
 }
 
@@ -207,16 +210,12 @@ __global__ void __launch_bounds__(64 * kRotWaves) rotate_kernel(RotArgs<TA> p, i
   const int heads = p.Hq + p.Hk, half = p.R / 2;
   const bool have = l < p.D / (2 * E);
   const int turned = p.R / (2 * E);  // lanes with rotated values
-  const int e0 = l < turned ? (INTER ? 2 * E * l : E * l) : p.R + 2 * E * (l - turned);
-  const int e1 = l < turned && !INTER ? E * l + half : e0 + E;
-  float wq[2 * E], wk[2 * E], dwq[BWD ? 2 * E : 1], dwk[BWD ? 2 * E : 1];
+  // (lanes that pad the row read its first blocks and are left out)
+  const int e0 = !have ? 0 : l < turned ? (INTER ? 2 * E * l : E * l) : p.R + 2 * E * (l - turned);
+  const int e1 = have && l < turned && !INTER ? E * l + half : e0 + E;
+  float dwq[BWD ? 2 * E : 1], dwk[BWD ? 2 * E : 1];
 #pragma unroll
-  for (int e = 0; e < 2 * E; ++e) {
-    const int at = e < E ? e0 + e : e1 + e - E;
-    wq[e] = have && p.qw ? p.qw[at] : 1.0f;
-    wk[e] = have && p.kw ? p.kw[at] : 1.0f;
-    if (BWD) dwq[e] = dwk[e] = 0.0f;
-  }
+  for (int e = 0; e < (BWD ? 2 * E : 1); ++e) dwq[e] = dwk[e] = 0.0f;
   const float mean = 1.0f / static_cast<float>(p.D);
   // (blockIdx.y: a range of heads, where there are few tokens)
   const int h0 = blockIdx.y * head_step, h1 = h0 + head_step < heads ? h0 + head_step : heads;
@@ -225,19 +224,8 @@ __global__ void __launch_bounds__(64 * kRotWaves) rotate_kernel(RotArgs<TA> p, i
     const int64_t tok = g * S + slot;
     const bool on = have && tok < p.tokens;
     const int64_t tk = tok < p.tokens ? tok : p.tokens - 1;
-    const TA* const q = p.q + tk * p.qs;
-    const TA* const k = p.k + tk * p.ks;
-    const auto row = [&](int h) { return h < p.Hq ? q + h * p.D : k + (h - p.Hq) * p.D; };
-    const auto place = [&](int h) { return h < p.Hq ? (tk * p.Hq + h) * p.D : (tk * p.Hk + h - p.Hq) * p.D; };
     float sn[E], cs[E];
     const int32_t pos = p.pos ? p.pos[tk] : static_cast<int32_t>(tk % p.L);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      sn[e] = 0.0f;
-      cs[e] = 1.0f;
-      if (l < turned) turn_f32(pos, p.freq[E * l + e], sn[e], cs[e]);
-      if (BWD) sn[e] = -sn[e];
-    }
     // pair i of the lane: values (i, i + E), or (2i, 2i + 1) when interleaved
     const auto rotate = [&](float (&v)[2 * E]) {
 #pragma unroll
@@ -248,19 +236,10 @@ __global__ void __launch_bounds__(64 * kRotWaves) rotate_kernel(RotArgs<TA> p, i
         v[b] = __builtin_fmaf(x, sn[i], y * cs[i]);
       }
     };
-    const auto fetch = [&](const TA* r, float (&v)[2 * E]) {
-      float lo[E], hi[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) lo[e] = hi[e] = 0.0f;
-      if (have) {
-        IO::load(r + e0, lo);
-        IO::load(r + e1, hi);
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        v[e] = lo[e];
-        v[e + E] = hi[e];
-      }
+    typedef typename IO::vec_t vec_t;
+    const auto fetch = [&](const TA* r, vec_t (&v)[2]) {
+      v[0] = *reinterpret_cast<const vec_t*>(r + e0);
+      v[1] = *reinterpret_cast<const vec_t*>(r + e1);
     };
     const auto put = [&](TA* r, const float (&v)[2 * E]) {
       float lo[E], hi[E];
@@ -274,47 +253,80 @@ __global__ void __launch_bounds__(64 * kRotWaves) rotate_kernel(RotArgs<TA> p, i
         IO::store(r + e1, hi);
       }
     };
-    float next[2 * E], nextd[BWD ? 2 * E : 1];
-    fetch(row(h0), next);
-    if constexpr (BWD) fetch((h0 < p.Hq ? p.dqo : p.dko) + place(h0), nextd);
-    for (int h = h0; h < h1; ++h) {
-      const bool isq = h < p.Hq;
-      float v[2 * E], d[BWD ? 2 * E : 1], ss = 0.0f;
+    // One tensor's heads [b, e), kAhead rows on their way while one is worked
+    // on.  Nothing in here depends on a condition but the remainder: behind a
+    // branch the wait for a row would be a wait for all of them.
+    constexpr int kAhead = BWD ? kRotAhead / 2 : kRotAhead;
+    bool turns = false;
+    const auto tensor = [&](const TA* in, const TA* dy, TA* to, const float* w, float* dw, int b, int e) {
+      if (b >= e) return;
+      vec_t vr[kAhead][2], dr[BWD ? kAhead : 1][2];
+      const auto ahead = [&](int u, int h) {
+        h = h < e ? h : e - 1;
+        fetch(in + h * p.D, vr[u]);
+        if constexpr (BWD) fetch(dy + h * p.D, dr[u]);
+      };
 #pragma unroll
-      for (int e = 0; e < 2 * E; ++e) {
-        v[e] = next[e];
-        if (BWD) d[e] = nextd[e];
-      }
-      if (h + 1 < h1) {  // the next head's row while this one is worked on
-        fetch(row(h + 1), next);
-        if constexpr (BWD) fetch((h + 1 < p.Hq ? p.dqo : p.dko) + place(h + 1), nextd);
-      }
+      for (int u = 0; u < kAhead; ++u) ahead(u, b + u);
+      if (!turns) {  // the first rows are on their way
+        turns = true;
 #pragma unroll
-      for (int e = 0; e < 2 * E; ++e) ss = __builtin_fmaf(v[e], v[e], ss);
-      const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum<N>(ss), mean, p.eps));
-      TA* const out = (isq ? p.qo : p.ko) + place(h);
-      if constexpr (!BWD) {
-#pragma unroll
-        for (int e = 0; e < 2 * E; ++e) v[e] = v[e] * rstd * (isq ? wq[e] : wk[e]);
-        rotate(v);
-        put(out, v);
-      } else {
-        rotate(d);
-        float dot = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 2 * E; ++e) {
-          v[e] *= rstd;  // vhat
-          if (isq) dwq[e] += on ? d[e] * v[e] : 0.0f;
-          else dwk[e] += on ? d[e] * v[e] : 0.0f;
-          d[e] *= isq ? wq[e] : wk[e];
-          dot = __builtin_fmaf(d[e], v[e], dot);
+        for (int i = 0; i < E; ++i) {
+          sn[i] = 0.0f;
+          cs[i] = 1.0f;
+          if (l < turned) turn_f32(pos, p.freq[E * l + i], sn[i], cs[i]);
+          if (BWD) sn[i] = -sn[i];
         }
-        dot = row_sum<N>(dot) * mean;
-#pragma unroll
-        for (int e = 0; e < 2 * E; ++e) d[e] = rstd * (d[e] - v[e] * dot);
-        put(out, d);
       }
-    }
+      float wt[2 * E];
+#pragma unroll
+      for (int i = 0; i < 2 * E; ++i) wt[i] = have && w ? w[i < E ? e0 + i : e1 + i - E] : 1.0f;
+      const auto work = [&](int u, int h) {
+        float v[2 * E], d[BWD ? 2 * E : 1], ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2 * E; ++i) {
+          v[i] = IO::get(vr[u][i / E], i % E);
+          if (BWD) d[i] = IO::get(dr[u][i / E], i % E);
+        }
+        ahead(u, h + kAhead);
+#pragma unroll
+        for (int i = 0; i < 2 * E; ++i) ss = __builtin_fmaf(v[i], v[i], ss);
+        const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum<N>(have ? ss : 0.0f), mean, p.eps));
+        if constexpr (!BWD) {
+#pragma unroll
+          for (int i = 0; i < 2 * E; ++i) v[i] = v[i] * rstd * wt[i];
+          rotate(v);
+          put(to + h * p.D, v);
+        } else {
+          rotate(d);
+          float dot = 0.0f;
+          const float mine = on ? rstd : 0.0f;  // (a token that is not there adds nothing to the weights' sums)
+#pragma unroll
+          for (int i = 0; i < 2 * E; ++i) {
+            v[i] *= mine;  // vhat
+            dw[i] = __builtin_fmaf(d[i], v[i], dw[i]);
+            d[i] *= wt[i];
+            dot = __builtin_fmaf(d[i], v[i], dot);
+          }
+          dot = row_sum<N>(have ? dot : 0.0f) * mean;
+#pragma unroll
+          for (int i = 0; i < 2 * E; ++i) d[i] = rstd * (d[i] - v[i] * dot);
+          put(to + h * p.D, d);
+        }
+      };
+      int h = b;
+      for (; h + kAhead <= e; h += kAhead) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) work(u, h + u);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (h + u < e) work(u, h + u);
+    };
+    tensor(p.q + tk * p.qs, BWD ? p.dqo + tk * p.Hq * p.D : nullptr, p.qo + tk * p.Hq * p.D, p.qw, dwq, h0,
+           h1 < p.Hq ? h1 : p.Hq);
+    tensor(p.k + tk * p.ks, BWD ? p.dko + tk * p.Hk * p.D : nullptr, p.ko + tk * p.Hk * p.D, p.kw, dwk,
+           h0 < p.Hq ? 0 : h0 - p.Hq, h1 - p.Hq);
   }
   if constexpr (BWD) {
     // over the wave's tokens, then over the waves, in a fixed order
@@ -345,28 +357,29 @@ __global__ void __launch_bounds__(64 * kRotWaves) rotate_kernel(RotArgs<TA> p, i
   }
 }
 
-// Sum of the partial weight gradients: a workgroup takes 64 elements of one of
-// the two, wave w every kRotSumWaves-th row, and the waves' sums are added in
-// order.
-constexpr int kRotSumWaves = 16;
+// Sum of the partial weight gradients: a workgroup takes 16 elements of one of
+// the two; wave w and lane quarter t take every 64th row from 4 w + t on, and
+// the quarters' and the waves' sums are added in order.
+constexpr int kRotSumWaves = 16, kRotSumElems = 16;
 __global__ void __launch_bounds__(64 * kRotSumWaves) rotate_sum_kernel(const float* part, int n, int D, float* dqw,
                                                                        float* dkw) {
-  __shared__ float s_part[kRotSumWaves][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int e = blockIdx.x * 64 + lane;
+  constexpr int M = kRotSumElems, Q = 64 / M;  // elements, lane quarters
+  __shared__ float s_part[kRotSumWaves * Q][M];
+  const int m = threadIdx.x % M, t = threadIdx.x / M;
+  const int e = blockIdx.x * M + m;
   float* to = blockIdx.y == 0 ? dqw : dkw;
   if (!to) return;
   float v = 0.0f;
   if (e < D) {
     const float* from = part + blockIdx.y * D + e;
-#pragma unroll 16
-    for (int k = w; k < n; k += kRotSumWaves) v += from[static_cast<int64_t>(k) * 2 * D];
+#pragma unroll 8
+    for (int k = t; k < n; k += kRotSumWaves * Q) v += from[static_cast<int64_t>(k) * 2 * D];
   }
-  s_part[w][lane] = v;
+  s_part[t][m] = v;
   __syncthreads();
-  if (w == 0 && e < D) {
+  if (t == 0 && e < D) {
 #pragma unroll
-    for (int k = 1; k < kRotSumWaves; ++k) v += s_part[k][lane];
+    for (int k = 1; k < kRotSumWaves * Q; ++k) v += s_part[k][m];
     to[e] = v;
   }
 }
@@ -385,6 +398,9 @@ bool rot_sizes_ok(int64_t batch, int64_t L, int64_t Hq, int64_t Hk, int64_t D) {
 // there are waves (any layout) or workgroups (vectors), bounded so that their
 // sum stays short.
 constexpr int64_t kRotMaxParts = 512;
+// Workgroups of a forward up to which its heads are spread over more of them
+// (twice as many measured 5% slower: the sines are formed once more).
+constexpr int64_t kRotFwdBlocks = 512;
 int64_t rot_parts(int64_t rows) {
   const int64_t want = (rows + kRotWaves - 1) / kRotWaves * kRotWaves;
   return want < kRotWaves ? kRotWaves : want > kRotMaxParts ? kRotMaxParts : want;
@@ -420,7 +436,8 @@ void rot_launch_vec(const RotCall& c, const RotArgs<TA>& a, int64_t* parts) {
   x = x < 1 ? 1 : x;
   int step = heads;
   const int64_t most = c.bwd ? rot_parts(a.tokens * heads) : int64_t{1} << 20;
-  while (step > 1 && x * ((heads + step - 1) / step) * 2 <= (most < kRotMaxParts ? most : kRotMaxParts)) step = (step + 1) / 2;
+  const int64_t enough = c.bwd ? most : kRotFwdBlocks;
+  while (step > 1 && x * ((heads + step - 1) / step) * 2 <= enough) step = (step + 1) / 2;
   const int64_t y = (heads + step - 1) / step;
   x = x * y > most ? (most / y < 1 ? 1 : most / y) : x;
   const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(y)), block(64 * kRotWaves);
@@ -463,8 +480,9 @@ int rot_launch(const RotCall& c) {
                 static_cast<TA*>(c.ko), static_cast<float*>(c.ws), c.eps, c.batch * c.L, c.L, c.qs,
                 c.ks, static_cast<int>(c.Hq), static_cast<int>(c.Hk), static_cast<int>(c.D),
                 static_cast<int>(c.R)};
-  // the widest access that the head size, the strides and the addresses allow
-  constexpr int E = 16 / sizeof(TA);
+  // four values an access where the head size, the strides and the addresses
+  // allow it (8 measured 10-20% slower for bf16: fewer waves), or two
+  constexpr int E = 4;
   int64_t parts = 0;
   if (!rot_try<TA, E>(c, a, &parts) && !rot_try<TA, E / 2>(c, a, &parts)) {
     const int64_t rows = c.batch * c.L * (c.Hq + c.Hk);
@@ -482,7 +500,7 @@ int rot_launch(const RotCall& c) {
 #undef SSM_ROT_CASE
   }
   if (c.bwd && (c.dqw || c.dkw))
-    hipLaunchKernelGGL(rotate_sum_kernel, dim3((a.D + 63) / 64, 2), dim3(64 * kRotSumWaves), 0, c.stream, a.part,
+    hipLaunchKernelGGL(rotate_sum_kernel, dim3((a.D + kRotSumElems - 1) / kRotSumElems, 2), dim3(64 * kRotSumWaves), 0, c.stream, a.part,
                        static_cast<int>(parts), a.D, c.dqw, c.dkw);
   return launch_status(c.fn);
 }

@@ -13,7 +13,7 @@ import ctypes
 import torch
 
 from . import ops
-from .ops import _DTYPES, _check, _ptr, _raise
+from .ops import _DTYPES, _check, _raise
 
 SSM_GATED_CHUNK = 16
 
@@ -59,51 +59,73 @@ def _load():
     return lib
 
 
+# the current stream's handle of a device index, without building a Stream object where torch lets one
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_F32 = torch.float32
+
+
 def _act(x, name="x"):
     if not isinstance(x, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if x.dtype not in _DTYPES:
         raise TypeError("activations must be float32 or bfloat16, got %s" % x.dtype)
-    return x.device, x.dtype
+    return x.get_device(), x.dtype
 
 
-def _buf(t, name, shape, dtype, dev, new):
+def _in(t, name, shape, dtype, like):
+    """The address of input ``t``, which has to have this shape and type and
+    be contiguous on ``like``'s device (``ops._check`` says what is wrong)."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape
+            and t.get_device() == like.get_device() and t.is_contiguous()):
+        _check(t, name, shape, dtype, like.device)
+    return t.data_ptr()
+
+
+def _opt(t, name, shape, dtype, like):
+    return None if t is None else _in(t, name, shape, dtype, like)
+
+
+def _out(t, name, shape, dtype, like, new):
     """The output buffer ``t``, checked, or a new one (noted in ``new``)."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=dev)
+        t = torch.empty(shape, dtype=dtype, device=like.device)
         new.append(t)
-        return t
-    _check(t, name, shape, dtype, dev)
+    else:
+        _in(t, name, shape, dtype, like)
     return t
 
 
-def _space(workspace, need, dev, new):
+def _space(workspace, need, like, new):
+    """(address, bytes) of the caller's workspace or of a new one."""
     if workspace is None:
         if need == 0:
             return None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
         new.append(workspace)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous and on %s" % dev)
-    return workspace, workspace.numel() * workspace.element_size()
+        return workspace.data_ptr(), need
+    if workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on %s" % like.device)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _call(fn, dev, stream, new, *args):
-    """fn(*args, stream) with ``dev`` current; ``new`` are the tensors
-    allocated for the call."""
-    if dev.type != "cuda":
-        raise ValueError("tensors must be on a HIP device, got %s" % dev)
-    current = torch.cuda.current_stream(dev).cuda_stream
+def _call(fn, like, stream, new, *args):
+    """fn(*args, stream) with ``like``'s device current; ``new`` are the
+    tensors allocated for the call."""
+    index = like.get_device()
+    if index < 0 or not like.is_cuda:
+        raise ValueError("tensors must be on a HIP device, got %s" % like.device)
+    current = _raw_stream(index)
     if stream is None:
         stream = current
     elif stream != current:
-        ext = torch.cuda.ExternalStream(stream, device=dev)
+        ext = torch.cuda.ExternalStream(stream, device=like.device)
         for t in new:
             t.record_stream(ext)
-    if torch.cuda.current_device() == dev.index:
+    if torch.cuda.current_device() == index:
         rc = fn(*args, stream)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             rc = fn(*args, stream)
     if rc != 0:
         _raise(rc)
@@ -134,9 +156,12 @@ def ssm_gated_scan_bwd_varlen_workspace_bytes(nseq, total_len, dim, dtype=torch.
                                                                  int(bool(with_chunk_states))))
 
 
-def _gated_check(x, rgate, igate, A, z, rgate_bias, igate_bias, initial_state, cu_seqlens):
-    """Shapes of a gated scan's inputs: (packed, sequences, row length, dim)."""
-    dev, dt = _act(x)
+def _gated_inputs(x, rgate, igate, A, z, rgate_bias, igate_bias, normalize, initial_state, cu_seqlens):
+    """Sizes and addresses of a gated scan's inputs: (type, sequences, row
+    length, dim, shape of the chunk states, the C call's first arguments, the
+    initial state, the offsets)."""
+    _, dt = _act(x)
+    cu = None
     if cu_seqlens is None:
         if x.dim() != 3:
             raise ValueError("x must be (batch, seqlen, dim)")
@@ -148,45 +173,35 @@ def _gated_check(x, rgate, igate, A, z, rgate_bias, igate_bias, initial_state, c
             raise ValueError("cu_seqlens must be (nseq + 1,) with nseq >= 1")
         L, dim = x.shape
         n = cu_seqlens.numel() - 1
-        _check(cu_seqlens, "cu_seqlens", (n + 1,), torch.int32, dev)
-    f32 = torch.float32
-    for t, name in ((x, "x"), (rgate, "rgate"), (igate, "igate")):
-        _check(t, name, x.shape, dt, dev)
-    _check(z, "z", x.shape, dt, dev, optional=True)
-    _check(A, "A", (dim,), f32, dev)
-    _check(rgate_bias, "rgate_bias", (dim,), f32, dev, optional=True)
-    _check(igate_bias, "igate_bias", (dim,), f32, dev, optional=True)
-    _check(initial_state, "initial_state", (n, dim), f32, dev, optional=True)
+        cu = _in(cu_seqlens, "cu_seqlens", (n + 1,), torch.int32, x)
+    head = (_in(x, "x", x.shape, dt, x), _in(rgate, "rgate", x.shape, dt, x), _in(igate, "igate", x.shape, dt, x),
+            _in(A, "A", (dim,), _F32, x), _opt(rgate_bias, "rgate_bias", (dim,), _F32, x),
+            _opt(igate_bias, "igate_bias", (dim,), _F32, x), int(bool(normalize)), _opt(z, "z", x.shape, dt, x))
+    h0 = _opt(initial_state, "initial_state", (n, dim), _F32, x)
     chunks = (L + SSM_GATED_CHUNK - 1) // SSM_GATED_CHUNK
-    mid = (n, chunks, dim) if cu_seqlens is None else (chunks, dim)
-    return dev, dt, n, L, dim, mid
+    return dt, n, L, dim, (n, chunks, dim) if cu_seqlens is None else (chunks, dim), head, h0, cu
 
 
 def _gated_fwd(x, rgate, igate, A, cu_seqlens, z, rgate_bias, igate_bias, normalize, initial_state,
                return_last_state, return_chunk_states, out, last_state, chunk_states, workspace,
                stream):
     lib = _load()
-    dev, dt, n, L, dim, mid = _gated_check(x, rgate, igate, A, z, rgate_bias, igate_bias,
-                                           initial_state, cu_seqlens)
-    new = []
-    out = _buf(out, "out", x.shape, dt, dev, new)
+    dt, n, L, dim, mid, head, h0, cu = _gated_inputs(x, rgate, igate, A, z, rgate_bias, igate_bias, normalize,
+                                                     initial_state, cu_seqlens)
+    new, code = [], _DTYPES[dt]
+    out = _out(out, "out", x.shape, dt, x, new)
     if return_last_state or last_state is not None:
-        last_state = _buf(last_state, "last_state", (n, dim), torch.float32, dev, new)
+        last_state = _out(last_state, "last_state", (n, dim), _F32, x, new)
     if return_chunk_states or chunk_states is not None:
-        chunk_states = _buf(chunk_states, "chunk_states", mid, torch.float32, dev, new)
-    head = (_ptr(x), _ptr(rgate), _ptr(igate), _ptr(A), _ptr(rgate_bias), _ptr(igate_bias),
-            int(bool(normalize)), _ptr(z), _ptr(out), _ptr(last_state), _ptr(initial_state),
-            _ptr(chunk_states))
-    if cu_seqlens is None:
-        need = lib.ssm_gated_scan_fwd_workspace_bytes(n, L, dim, _DTYPES[dt])
-        ws, nbytes = _space(workspace, need, dev, new)
-        _call(lib.ssm_gated_scan_fwd, dev, stream, new, *head, n, L, dim, _DTYPES[dt], _ptr(ws),
-              nbytes)
+        chunk_states = _out(chunk_states, "chunk_states", mid, _F32, x, new)
+    args = head + (out.data_ptr(), None if last_state is None else last_state.data_ptr(), h0,
+                   None if chunk_states is None else chunk_states.data_ptr())
+    if cu is None:
+        ws, nbytes = _space(workspace, lib.ssm_gated_scan_fwd_workspace_bytes(n, L, dim, code), x, new)
+        _call(lib.ssm_gated_scan_fwd, x, stream, new, *args, n, L, dim, code, ws, nbytes)
     else:
-        need = lib.ssm_gated_scan_fwd_varlen_workspace_bytes(n, L, dim, _DTYPES[dt])
-        ws, nbytes = _space(workspace, need, dev, new)
-        _call(lib.ssm_gated_scan_fwd_varlen, dev, stream, new, *head, _ptr(cu_seqlens), n, L, dim,
-              _DTYPES[dt], _ptr(ws), nbytes)
+        ws, nbytes = _space(workspace, lib.ssm_gated_scan_fwd_varlen_workspace_bytes(n, L, dim, code), x, new)
+        _call(lib.ssm_gated_scan_fwd_varlen, x, stream, new, *args, cu, n, L, dim, code, ws, nbytes)
     res = (out,) + tuple(t for t in (last_state, chunk_states) if t is not None)
     return res if len(res) > 1 else out
 
@@ -222,33 +237,26 @@ def ssm_gated_scan_fwd_varlen(x, rgate, igate, A, cu_seqlens, z=None, rgate_bias
 def _gated_bwd(x, rgate, igate, A, cu_seqlens, dout, z, rgate_bias, igate_bias, normalize,
                initial_state, dlast_state, chunk_states, grads, workspace, stream):
     lib = _load()
-    dev, dt, n, L, dim, mid = _gated_check(x, rgate, igate, A, z, rgate_bias, igate_bias,
-                                           initial_state, cu_seqlens)
-    f32, new = torch.float32, []
-    _check(dout, "dout", x.shape, dt, dev)
-    _check(dlast_state, "dlast_state", (n, dim), f32, dev, optional=True)
-    _check(chunk_states, "chunk_states", mid, f32, dev, optional=True)
+    dt, n, L, dim, mid, head, h0, cu = _gated_inputs(x, rgate, igate, A, z, rgate_bias, igate_bias, normalize,
+                                                     initial_state, cu_seqlens)
+    new, code = [], _DTYPES[dt]
+    args = head + (h0, _opt(chunk_states, "chunk_states", mid, _F32, x), _in(dout, "dout", x.shape, dt, x),
+                   _opt(dlast_state, "dlast_state", (n, dim), _F32, x))
     g = dict(grads or {})
     for k in ("dx", "drgate", "digate", "dz"):
-        g[k] = None if k == "dz" and z is None else _buf(g.get(k), k, x.shape, dt, dev, new)
+        g[k] = None if k == "dz" and z is None else _out(g.get(k), k, x.shape, dt, x, new)
     for k in ("dA", "drgate_bias", "digate_bias"):
-        g[k] = _buf(g.get(k), k, (dim,), f32, dev, new)
-    g["dinitial_state"] = _buf(g.get("dinitial_state"), "dinitial_state", (n, dim), f32, dev, new)
-    head = (_ptr(x), _ptr(rgate), _ptr(igate), _ptr(A), _ptr(rgate_bias), _ptr(igate_bias),
-            int(bool(normalize)), _ptr(z), _ptr(initial_state), _ptr(chunk_states), _ptr(dout),
-            _ptr(dlast_state), _ptr(g["dx"]), _ptr(g["drgate"]), _ptr(g["digate"]), _ptr(g["dz"]),
-            _ptr(g["dA"]), _ptr(g["drgate_bias"]), _ptr(g["digate_bias"]), _ptr(g["dinitial_state"]))
+        g[k] = _out(g.get(k), k, (dim,), _F32, x, new)
+    g["dinitial_state"] = _out(g.get("dinitial_state"), "dinitial_state", (n, dim), _F32, x, new)
+    args += tuple(None if g[k] is None else g[k].data_ptr()
+                  for k in ("dx", "drgate", "digate", "dz", "dA", "drgate_bias", "digate_bias", "dinitial_state"))
     have = int(chunk_states is not None)
-    if cu_seqlens is None:
-        need = lib.ssm_gated_scan_bwd_workspace_bytes(n, L, dim, _DTYPES[dt], have)
-        ws, nbytes = _space(workspace, need, dev, new)
-        _call(lib.ssm_gated_scan_bwd, dev, stream, new, *head, n, L, dim, _DTYPES[dt], _ptr(ws),
-              nbytes)
+    if cu is None:
+        ws, nbytes = _space(workspace, lib.ssm_gated_scan_bwd_workspace_bytes(n, L, dim, code, have), x, new)
+        _call(lib.ssm_gated_scan_bwd, x, stream, new, *args, n, L, dim, code, ws, nbytes)
     else:
-        need = lib.ssm_gated_scan_bwd_varlen_workspace_bytes(n, L, dim, _DTYPES[dt], have)
-        ws, nbytes = _space(workspace, need, dev, new)
-        _call(lib.ssm_gated_scan_bwd_varlen, dev, stream, new, *head, _ptr(cu_seqlens), n, L, dim,
-              _DTYPES[dt], _ptr(ws), nbytes)
+        ws, nbytes = _space(workspace, lib.ssm_gated_scan_bwd_varlen_workspace_bytes(n, L, dim, code, have), x, new)
+        _call(lib.ssm_gated_scan_bwd_varlen, x, stream, new, *args, cu, n, L, dim, code, ws, nbytes)
     return g
 
 
@@ -283,38 +291,33 @@ def ssm_gated_state_update(state, x, rgate, igate, A, z=None, rgate_bias=None, i
     """One decode step of the gated recurrence: ``state`` (batch, dim) float32
     is updated in place; returns ``out`` (batch, dim) in x's dtype."""
     lib = _load()
-    dev, dt = _act(x)
+    _, dt = _act(x)
     if x.dim() != 2:
         raise ValueError("x must be (batch, dim)")
-    batch, dim = x.shape
-    f32, new = torch.float32, []
-    _check(state, "state", (batch, dim), f32, dev)
-    for t, name in ((x, "x"), (rgate, "rgate"), (igate, "igate")):
-        _check(t, name, x.shape, dt, dev)
-    _check(z, "z", x.shape, dt, dev, optional=True)
-    _check(A, "A", (dim,), f32, dev)
-    _check(rgate_bias, "rgate_bias", (dim,), f32, dev, optional=True)
-    _check(igate_bias, "igate_bias", (dim,), f32, dev, optional=True)
-    out = _buf(out, "out", x.shape, dt, dev, new)
-    _call(lib.ssm_gated_state_update, dev, stream, new, _ptr(state), _ptr(x), _ptr(rgate),
-          _ptr(igate), _ptr(A), _ptr(rgate_bias), _ptr(igate_bias), int(bool(normalize)), _ptr(z),
-          _ptr(out), batch, dim, _DTYPES[dt])
+    shape, new = x.shape, []
+    batch, dim = shape
+    args = (_in(state, "state", shape, _F32, x), _in(x, "x", shape, dt, x), _in(rgate, "rgate", shape, dt, x),
+            _in(igate, "igate", shape, dt, x), _in(A, "A", (dim,), _F32, x),
+            _opt(rgate_bias, "rgate_bias", (dim,), _F32, x), _opt(igate_bias, "igate_bias", (dim,), _F32, x),
+            int(bool(normalize)), _opt(z, "z", shape, dt, x))
+    out = _out(out, "out", shape, dt, x, new)
+    _call(lib.ssm_gated_state_update, x, stream, new, *args, out.data_ptr(), batch, dim, _DTYPES[dt])
     return out
 
 
 # ---------------------------------------------------------------------------
 # norm and rotation of queries and keys
 # ---------------------------------------------------------------------------
-def _heads(t, name, batch, L, D, dt, dev):
+def _heads(t, name, batch, L, D, like):
     """(heads, token stride) of a (batch, seqlen, heads, headdim) tensor whose
     tokens may lie apart (a slice of wider rows) but nothing else."""
     if t.dim() != 4 or t.shape[0] != batch or t.shape[1] != L or t.shape[3] != D:
         raise ValueError("%s has shape %s, expected (%d, %d, heads, %d)"
                          % (name, tuple(t.shape), batch, L, D))
-    if t.dtype != dt:
-        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dt))
-    if t.device != dev:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+    if t.dtype != like.dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, like.dtype))
+    if t.get_device() != like.get_device():
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, like.device))
     H = t.shape[2]
     sb, sl, sh, sd = t.stride()
     if L > 1:
@@ -328,24 +331,23 @@ def _heads(t, name, batch, L, D, dt, dev):
     return H, step
 
 
-def _rot_check(q, k, inv_freq, q_weight, k_weight, positions):
-    dev, dt = _act(q, "q")
+def _rot_inputs(q, k, inv_freq, q_weight, k_weight, positions, eps, interleaved):
+    """Sizes and the C call's first arguments."""
+    _act(q, "q")
     if q.dim() != 4:
         raise ValueError("q must be (batch, seqlen, heads, headdim)")
     batch, L, Hq, D = q.shape
-    Hq, qs = _heads(q, "q", batch, L, D, dt, dev)
-    Hk, ks = _heads(k, "k", batch, L, D, dt, dev) if k is not None else (0, 0)
+    Hq, qs = _heads(q, "q", batch, L, D, q)
+    Hk, ks = _heads(k, "k", batch, L, D, q) if k is not None else (0, 0)
     if k is not None and Hk == 0:
         raise ValueError("k has no heads: pass None")
-    f32 = torch.float32
     if inv_freq is not None and (not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1):
         raise ValueError("inv_freq must be (rotary_dim / 2,)")
     R = 0 if inv_freq is None else 2 * inv_freq.numel()
-    _check(inv_freq, "inv_freq", (R // 2,), f32, dev, optional=True)
-    _check(q_weight, "q_weight", (D,), f32, dev, optional=True)
-    _check(k_weight, "k_weight", (D,), f32, dev, optional=True)
-    _check(positions, "positions", (batch, L), torch.int32, dev, optional=True)
-    return dev, dt, batch, L, Hq, Hk, D, R, qs, ks
+    head = (q.data_ptr(), None if k is None else k.data_ptr(), _opt(q_weight, "q_weight", (D,), _F32, q),
+            _opt(k_weight, "k_weight", (D,), _F32, q), _opt(inv_freq, "inv_freq", (R // 2,), _F32, q),
+            _opt(positions, "positions", (batch, L), torch.int32, q), eps, int(bool(interleaved)))
+    return head, (batch, L, Hq, Hk, D, R, qs, ks, _DTYPES[q.dtype])
 
 
 def ssm_qk_norm_rotate_fwd(q, k, inv_freq, q_weight=None, k_weight=None, positions=None, eps=1e-6,
@@ -358,16 +360,15 @@ def ssm_qk_norm_rotate_fwd(q, k, inv_freq, q_weight=None, k_weight=None, positio
 
     Returns ``(q_out, k_out)``, contiguous (k_out None without k)."""
     lib = _load()
-    dev, dt, batch, L, Hq, Hk, D, R, qs, ks = _rot_check(q, k, inv_freq, q_weight, k_weight, positions)
+    head, sizes = _rot_inputs(q, k, inv_freq, q_weight, k_weight, positions, eps, interleaved)
     new = []
-    q_out = _buf(q_out, "q_out", (batch, L, Hq, D), dt, dev, new)
+    q_out = _out(q_out, "q_out", q.shape, q.dtype, q, new)
     if k is not None:
-        k_out = _buf(k_out, "k_out", (batch, L, Hk, D), dt, dev, new)
+        k_out = _out(k_out, "k_out", k.shape, q.dtype, q, new)
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out or k_weight given without k")
-    _call(lib.ssm_qk_norm_rotate_fwd, dev, stream, new, _ptr(q), _ptr(k), _ptr(q_weight),
-          _ptr(k_weight), _ptr(inv_freq), _ptr(positions), eps, int(bool(interleaved)), _ptr(q_out),
-          _ptr(k_out), batch, L, Hq, Hk, D, R, qs, ks, _DTYPES[dt])
+    _call(lib.ssm_qk_norm_rotate_fwd, q, stream, new, *head, q_out.data_ptr(),
+          None if k is None else k_out.data_ptr(), *sizes)
     return q_out, k_out
 
 
@@ -383,24 +384,21 @@ def ssm_qk_norm_rotate_bwd(q, k, inv_freq, dq_out, dk_out, q_weight=None, k_weig
     + sum(dk_out*k_out): a dict of dq, dk (contiguous, q's dtype; dk None
     without k) and dq_weight, dk_weight (float32; None without the weight)."""
     lib = _load()
-    dev, dt, batch, L, Hq, Hk, D, R, qs, ks = _rot_check(q, k, inv_freq, q_weight, k_weight, positions)
-    f32, new = torch.float32, []
+    head, sizes = _rot_inputs(q, k, inv_freq, q_weight, k_weight, positions, eps, interleaved)
+    batch, L, Hq, Hk, D = sizes[:5]
     if k is None and (dk_out is not None or k_weight is not None):
         raise ValueError("dk_out or k_weight given without k")
-    _check(dq_out, "dq_out", (batch, L, Hq, D), dt, dev)
-    if k is not None:
-        _check(dk_out, "dk_out", (batch, L, Hk, D), dt, dev)
+    new = []
+    head += (_in(dq_out, "dq_out", q.shape, q.dtype, q),
+             None if k is None else _in(dk_out, "dk_out", k.shape, q.dtype, q))
     g = dict(grads or {})
-    g["dq"] = _buf(g.get("dq"), "dq", (batch, L, Hq, D), dt, dev, new)
-    g["dk"] = None if k is None else _buf(g.get("dk"), "dk", (batch, L, Hk, D), dt, dev, new)
+    g["dq"] = _out(g.get("dq"), "dq", q.shape, q.dtype, q, new)
+    g["dk"] = None if k is None else _out(g.get("dk"), "dk", k.shape, q.dtype, q, new)
     for n, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
-        g[n] = None if w is None else _buf(g.get(n), n, (D,), f32, dev, new)
-    need = lib.ssm_qk_norm_rotate_bwd_workspace_bytes(batch, L, Hq, Hk, D)
-    ws, nbytes = _space(workspace, need, dev, new)
-    _call(lib.ssm_qk_norm_rotate_bwd, dev, stream, new, _ptr(q), _ptr(k), _ptr(q_weight),
-          _ptr(k_weight), _ptr(inv_freq), _ptr(positions), eps, int(bool(interleaved)), _ptr(dq_out),
-          _ptr(dk_out), _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dq_weight"]), _ptr(g["dk_weight"]),
-          batch, L, Hq, Hk, D, R, qs, ks, _DTYPES[dt], _ptr(ws), nbytes)
+        g[n] = None if w is None else _out(g.get(n), n, (D,), _F32, q, new)
+    head += tuple(None if g[n] is None else g[n].data_ptr() for n in ("dq", "dk", "dq_weight", "dk_weight"))
+    ws, nbytes = _space(workspace, lib.ssm_qk_norm_rotate_bwd_workspace_bytes(batch, L, Hq, Hk, D), q, new)
+    _call(lib.ssm_qk_norm_rotate_bwd, q, stream, new, *head, *sizes, ws, nbytes)
     return g
 
 
@@ -420,30 +418,24 @@ def ssm_causal_conv1d_bwd(x, weight, dout, bias=None, initial_conv_state=None,
     ``initial_conv_state``), dweight and dbias (float32; None without
     ``bias``).  ``grads`` may supply preallocated outputs."""
     lib = _load()
-    dev, dt = _act(x)
+    _, dt = _act(x)
     if x.dim() != 3:
         raise ValueError("x must be (batch, seqlen, dim)")
     batch, L, dim = x.shape
     if weight.dim() != 2:
         raise ValueError("weight must be (dim, width)")
     W = weight.shape[1]
-    f32, new, st = torch.float32, [], (batch, dim, W - 1)
-    _check(x, "x", x.shape, dt, dev)
-    _check(dout, "dout", x.shape, dt, dev)
-    _check(weight, "weight", (dim, W), f32, dev)
-    _check(bias, "bias", (dim,), f32, dev, optional=True)
-    _check(initial_conv_state, "initial_conv_state", st, dt, dev, optional=True)
-    _check(dfinal_conv_state, "dfinal_conv_state", st, dt, dev, optional=True)
+    new, st = [], (batch, dim, W - 1)
+    args = (_in(x, "x", x.shape, dt, x), _in(weight, "weight", (dim, W), _F32, x), _opt(bias, "bias", (dim,), _F32, x),
+            _opt(initial_conv_state, "initial_conv_state", st, dt, x), _in(dout, "dout", x.shape, dt, x),
+            _opt(dfinal_conv_state, "dfinal_conv_state", st, dt, x))
     g = dict(grads or {})
-    g["dx"] = _buf(g.get("dx"), "dx", x.shape, dt, dev, new)
-    g["dweight"] = _buf(g.get("dweight"), "dweight", (dim, W), f32, dev, new)
-    g["dbias"] = None if bias is None else _buf(g.get("dbias"), "dbias", (dim,), f32, dev, new)
+    g["dx"] = _out(g.get("dx"), "dx", x.shape, dt, x, new)
+    g["dweight"] = _out(g.get("dweight"), "dweight", (dim, W), _F32, x, new)
+    g["dbias"] = None if bias is None else _out(g.get("dbias"), "dbias", (dim,), _F32, x, new)
     g["dinitial_conv_state"] = None if initial_conv_state is None else \
-        _buf(g.get("dinitial_conv_state"), "dinitial_conv_state", st, dt, dev, new)
-    need = lib.ssm_causal_conv1d_bwd_workspace_bytes(batch, L, dim, W)
-    ws, nbytes = _space(workspace, need, dev, new)
-    _call(lib.ssm_causal_conv1d_bwd, dev, stream, new, _ptr(x), _ptr(weight), _ptr(bias),
-          _ptr(initial_conv_state), _ptr(dout), _ptr(dfinal_conv_state), _ptr(g["dx"]),
-          _ptr(g["dweight"]), _ptr(g["dbias"]), _ptr(g["dinitial_conv_state"]), batch, L, dim, W,
-          int(bool(silu)), _DTYPES[dt], _ptr(ws), nbytes)
+        _out(g.get("dinitial_conv_state"), "dinitial_conv_state", st, dt, x, new)
+    args += tuple(None if g[k] is None else g[k].data_ptr() for k in ("dx", "dweight", "dbias", "dinitial_conv_state"))
+    ws, nbytes = _space(workspace, lib.ssm_causal_conv1d_bwd_workspace_bytes(batch, L, dim, W), x, new)
+    _call(lib.ssm_causal_conv1d_bwd, x, stream, new, *args, batch, L, dim, W, int(bool(silu)), _DTYPES[dt], ws, nbytes)
     return g

@@ -254,7 +254,7 @@ def test_head_strides_are_read_right():
     """What the C call gets for slices of wider rows."""
     rows = torch.zeros(2, 3, 100)
     q = rows[..., 4:36].unflatten(-1, (4, 8))
-    assert recurrent._heads(q, "q", 2, 3, 8, torch.float32, q.device) == (4, 100)
+    assert recurrent._heads(q, "q", 2, 3, 8, q) == (4, 100)
     one = torch.zeros(5, 1, 100)[..., 4:36].unflatten(-1, (4, 8))
-    assert recurrent._heads(one, "q", 5, 1, 8, torch.float32, q.device) == (4, 100)
-    assert recurrent._heads(one[:1], "q", 1, 1, 8, torch.float32, q.device) == (4, 32)
+    assert recurrent._heads(one, "q", 5, 1, 8, q) == (4, 100)
+    assert recurrent._heads(one[:1], "q", 1, 1, 8, q) == (4, 32)
