@@ -39,11 +39,15 @@ int launch_gated_init(void* ws, size_t bytes, const int32_t* cu, int64_t nseq, i
   return launch_status(fn);
 }
 
-// Tokens of a lane; rows of the inputs a wave has in flight (a ring of
-// registers, filled again as it is used up); rows of z in flight.
-constexpr int kFwdT = 64, kFwdBatch = 4, kFwdRing = 2, kFwdZ = 16;
-constexpr int kFwdWaves = 4;
-constexpr int kFwdChunk = kFwdT * kFwdWaves;  // 256 tokens
+// Tokens of a lane, waves of a workgroup, rows of the inputs a wave has in
+// flight (a ring of registers, filled again as it is used up), waves a SIMD
+// holds.
+struct FwdLong {  // few folds per token, the whole device resident: throughput
+  static constexpr int T = 64, W = 4, batch = 4, ring = 2, occupancy = 3;
+};
+struct FwdShort {  // every load issued at once: the latency of few workgroups
+  static constexpr int T = 16, W = 8, batch = 4, ring = 4, occupancy = 4;
+};
 
 // One pass over the data: a workgroup loads its tokens once, turns them into
 // (a, b) in registers and composes its chunk's map; publishes that; waits for
@@ -55,9 +59,10 @@ constexpr int kFwdChunk = kFwdT * kFwdWaves;  // 256 tokens
 // folds have a fixed order, so results repeat bit for bit.
 // Units are handed out by a counter, earlier chunks first: a workgroup waits
 // only for ones that are running or done.
-template <typename TA, bool NORM, bool GATE, bool VL>
-__global__ void __launch_bounds__(64 * kFwdWaves, 3) gated_fwd_kernel(GatedFwdArgs<TA> p, GatedPlan pl) {
-  constexpr int T = kFwdT, W = kFwdWaves, C = kGatedC, NB = kFwdBatch, kPolls = kGatedGroup / W;
+template <typename TA, typename CF, bool NORM, bool GATE, bool VL>
+__global__ void __launch_bounds__(64 * CF::W, CF::occupancy) gated_fwd_kernel(GatedFwdArgs<TA> p, GatedPlan pl) {
+  constexpr int T = CF::T, W = CF::W, C = kGatedC, NB = CF::batch, R = CF::ring, kPolls = kGatedGroup / W;
+  constexpr int kZ = 16;  // rows of z in flight
   using IO = Cell<TA>;
   __shared__ float2 s_agg[W][C];
   __shared__ float2 s_in[kGatedGroup][C];
@@ -79,7 +84,7 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 3) gated_fwd_kernel(GatedFwdAr
   const uint32_t row = line / pl.tiles, tile = line % pl.tiles;
   const int col0 = static_cast<int>(tile) * C, col = col0 + lane;
   const bool have = col < dim;
-  const int64_t t0 = static_cast<int64_t>(c) * kFwdChunk + w * T;
+  const int64_t t0 = static_cast<int64_t>(c) * (T * W) + w * T;
   int64_t end = p.L;
   if (VL) {
     const int64_t e = p.cu[p.nseq];
@@ -99,11 +104,11 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 3) gated_fwd_kernel(GatedFwdAr
   float a[T], b[T], y = 0.0f, H = 0.0f;  // y: first the sum of the tokens' v
   Marks mk{0, 0, 0};
   if (n > 0) {
-    typename IO::raw_t xr[kFwdRing][NB], rr[kFwdRing][NB], ir[kFwdRing][NB];
+    typename IO::raw_t xr[R][NB], rr[R][NB], ir[R][NB];
     const rsrc_t rx = make_rsrc(p.x + base, span), rg = make_rsrc(p.r + base, span),
                  ri = make_rsrc(p.i + base, span);
 #pragma unroll
-    for (int j = 0; j < kFwdRing * NB; ++j) {
+    for (int j = 0; j < R * NB; ++j) {
       rr[j / NB][j % NB] = IO::load(rg, voff, at(j));
       ir[j / NB][j % NB] = IO::load(ri, voff, at(j));
       xr[j / NB][j % NB] = IO::load(rx, voff, at(j));
@@ -114,7 +119,6 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 3) gated_fwd_kernel(GatedFwdAr
     // over the n that are
 #pragma unroll
     for (int k = 0; k < T / NB; ++k) {
-      constexpr int R = kFwdRing;
 #pragma unroll
       for (int jj = 0; jj < NB; ++jj) {
         const int j = k * NB + jj;
@@ -202,10 +206,10 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 3) gated_fwd_kernel(GatedFwdAr
     const rsrc_t ro = make_rsrc(p.out + base, p.out ? span : 0);
     const uint32_t outb = p.out ? rowb : 0;
     const rsrc_t rz = make_rsrc(GATE ? p.z + base : p.z, GATE ? span : 0);
-    typename IO::raw_t zr[GATE ? kFwdZ : 1];
+    typename IO::raw_t zr[GATE ? kZ : 1];
     if (GATE) {
 #pragma unroll
-      for (int j = 0; j < kFwdZ; ++j) zr[j] = IO::load(rz, voff, at(j));
+      for (int j = 0; j < kZ; ++j) zr[j] = IO::load(rz, voff, at(j));
     }
     float* const states =
         p.chunk_states && have
@@ -215,8 +219,8 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 3) gated_fwd_kernel(GatedFwdAr
       if (j % SSM_GATED_CHUNK == 0 && states) states[static_cast<int64_t>(j / SSM_GATED_CHUNK) * dim] = h;
     };
     const auto emit = [&](int j) {
-      const float o = GATE ? h * silu_f32(IO::get(zr[GATE ? j % kFwdZ : 0])) : h;
-      if (GATE && j + kFwdZ < T) zr[j % kFwdZ] = IO::load(rz, voff, at(j + kFwdZ));
+      const float o = GATE ? h * silu_f32(IO::get(zr[GATE ? j % kZ : 0])) : h;
+      if (GATE && j + kZ < T) zr[j % kZ] = IO::load(rz, voff, at(j + kZ));
       IO::store(ro, o, voff, static_cast<uint32_t>(j) * outb);
       if ((j & 3) == 3) __builtin_amdgcn_sched_barrier(0);
     };
@@ -244,16 +248,21 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 3) gated_fwd_kernel(GatedFwdAr
   if (!VL && p.last && c + 1 == pl.chunks && w == W - 1 && have) p.last[static_cast<int64_t>(row) * dim + col] = h;
 }
 
-template <typename TA>
+template <typename CF>
+GatedPlan fwd_plan(int64_t rows, int64_t L, int64_t dim) {
+  return gated_plan(rows, L, dim, CF::T * CF::W);
+}
+
+template <typename TA, typename CF>
 int launch_gated_fwd(const GatedFwdArgs<TA>& a, bool norm, const char* fn, hipStream_t s) {
-  const GatedPlan pl = gated_plan(a.rows, a.L, a.dim, kFwdChunk);
+  const GatedPlan pl = fwd_plan<CF>(a.rows, a.L, a.dim);
   const int rc = launch_gated_init(a.ws, pl.bytes, a.cu, a.cu ? a.nseq : a.rows, a.L, a.dim, a.h0, a.last,
                                    fn, s);
   if (rc != SSM_OK || a.L == 0) return rc;
-  const dim3 grid(pl.units), block(64 * kFwdWaves);
+  const dim3 grid(pl.units), block(64 * CF::W);
 #define SSM_GATED_CASE(N, G, VLN)                                                              \
   if (norm == N && (a.z != nullptr) == G && (a.cu != nullptr) == VLN)                          \
-    hipLaunchKernelGGL((gated_fwd_kernel<TA, N, G, VLN>), grid, block, 0, s, a, pl);
+    hipLaunchKernelGGL((gated_fwd_kernel<TA, CF, N, G, VLN>), grid, block, 0, s, a, pl);
   SSM_GATED_CASE(true, true, false)
   SSM_GATED_CASE(true, false, false)
   SSM_GATED_CASE(false, true, false)
@@ -304,7 +313,8 @@ bool gated_sizes_ok(int64_t rows, int64_t L, int64_t nseq, int64_t dim, bool pac
 }
 
 size_t gated_fwd_bytes(int64_t rows, int64_t L, int64_t dim) {
-  return gated_plan(rows, L, dim, kFwdChunk).bytes;
+  const size_t a = fwd_plan<FwdLong>(rows, L, dim).bytes, b = fwd_plan<FwdShort>(rows, L, dim).bytes;
+  return a > b ? a : b;
 }
 
 template <typename TA>
@@ -312,11 +322,16 @@ int run_gated_fwd(const char* fn, const void* x, const void* r, const void* i, c
                   const float* rb, const float* ib, bool norm, const void* z, void* out, float* last,
                   const float* h0, float* states, const int32_t* cu, int64_t nseq, int64_t rows,
                   int64_t L, int dim, void* ws, hipStream_t stream) {
-  return launch_gated_fwd<TA>(
-      GatedFwdArgs<TA>{static_cast<const TA*>(x), static_cast<const TA*>(r), static_cast<const TA*>(i),
-                       static_cast<const TA*>(z), A, rb, ib, static_cast<TA*>(out), last, h0, states, cu,
-                       rows, L, nseq, dim, ws},
-      norm, fn, stream);
+  const GatedFwdArgs<TA> a{static_cast<const TA*>(x), static_cast<const TA*>(r), static_cast<const TA*>(i),
+                           static_cast<const TA*>(z), A, rb, ib, static_cast<TA*>(out), last, h0, states, cu,
+                           rows, L, nseq, dim, ws};
+  // Long stretches where they give every CU more than two workgroups (768 of
+  // them: 36 against 45 us); below, a lane that goes through its tokens in
+  // rounds of loads takes longer than the device is kept busy by them (512:
+  // 54 against 46 us; 108: 25 against 13 us).
+  return fwd_plan<FwdLong>(rows, L, dim).units > 2u * static_cast<unsigned>(device_cus())
+             ? launch_gated_fwd<TA, FwdLong>(a, norm, fn, stream)
+             : launch_gated_fwd<TA, FwdShort>(a, norm, fn, stream);
 }
 
 int gated_states(const char* fn, const void* x, const void* r, const void* i, const float* A,

@@ -83,13 +83,17 @@ def _in(t, name, shape, dtype, like):
 
 
 def _opt(t, name, shape, dtype, like):
-    return None if t is None else _in(t, name, shape, dtype, like)
+    if t is None:
+        return None
+    return _in(t, name, shape, dtype, like)
 
 
 def _out(t, name, shape, dtype, like, new):
     """The output buffer ``t``, checked, or a new one (noted in ``new``)."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=like.device)
+        # (empty_like is the quickest; it would keep the strides of a slice)
+        t = torch.empty_like(like) if dtype is like.dtype and shape == like.shape and like.is_contiguous() \
+            else like.new_empty(shape, dtype=dtype)
         new.append(t)
     else:
         _in(t, name, shape, dtype, like)
@@ -101,7 +105,7 @@ def _space(workspace, need, like, new):
     if workspace is None:
         if need == 0:
             return None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        workspace = like.new_empty(need, dtype=torch.uint8)
         new.append(workspace)
         return workspace.data_ptr(), need
     if workspace.device != like.device or not workspace.is_contiguous():

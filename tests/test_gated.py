@@ -361,3 +361,39 @@ def test_stream_argument():
         junk = torch.full((1 << 20,), 3.0, device=DEV)  # would take a workspace that was given back too early
     torch.cuda.synchronize()
     assert torch.equal(out, want) and (junk == 3.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("b,L,d", [(3, 1100, 2500), (9, 700, 1283)])
+def test_many_workgroups(b, L, d, dtype):
+    """Calls that fill the device and take the long stretches; the oracle on a
+    few channels (they are independent) and every row."""
+    p = Gated((b, L), b, d, dtype, DEV, 21)
+    out, last, mid = pkg.ssm_gated_scan_fwd(*p.args(), return_last_state=True, return_chunk_states=True, **p.kw())
+    g = pkg.ssm_gated_scan_bwd(*p.args(), p.dout, dlast_state=p.dlast, chunk_states=mid, **p.kw())
+    sel = torch.tensor([0, 1, 63, 64, d // 2, d - 2, d - 1], device=DEV)
+    pick = lambda t: None if t is None else t[..., sel].contiguous()
+    for k in ("x", "r", "i", "z", "dout", "A", "rb", "ib", "h0", "dlast"):
+        setattr(p, k, pick(getattr(p, k)))
+    forward_ok(p, pick(out), pick(last), pick(mid))
+    backward_ok(p, {k: pick(v) for k, v in g.items()})
+    lens = [500, 0, 1, L * b - 700, 150]
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device=DEV)
+    q = Gated((L * b,), 5, d, dtype, DEV, 22)
+    out, last = pkg.ssm_gated_scan_fwd_varlen(*q.args(), cu, return_last_state=True, **q.kw())
+    g = pkg.ssm_gated_scan_bwd_varlen(*q.args(), cu, q.dout, dlast_state=q.dlast, **q.kw())
+    for k in ("x", "r", "i", "z", "dout", "A", "rb", "ib", "h0", "dlast"):
+        setattr(q, k, pick(getattr(q, k)))
+    t0 = 0
+    for s, n in enumerate(lens):
+        if n <= 700:
+            h, dout, dl = q.host(s, t0, t0 + n)
+            ref, rl, _ = og.gated_scan(**h)
+            bo, bl, _, _ = gb.forward(**h, dtype=dtype)
+            within(pick(out)[None, t0:t0 + n], ref, bo, "out %d" % s)
+            within(pick(last)[s:s + 1], rl, bl, "last %d" % s)
+            rg, bd = og.gated_scan_bwd(dout=dout, dlast=dl, **h), gb.backward(dout=dout, dlast=dl, dtype=dtype, **h)
+            for k in ("dx", "drgate", "digate", "dz"):
+                within(pick(g[k])[None, t0:t0 + n], rg[k], bd[k], "%s %d" % (k, s))
+            within(pick(g["dinitial_state"])[s:s + 1], rg["dinitial_state"], bd["dinitial_state"], "dh0 %d" % s)
+        t0 += n
