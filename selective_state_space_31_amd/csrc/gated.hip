@@ -46,7 +46,7 @@ struct FwdLong {  // few folds per token, the whole device resident: throughput
   static constexpr int T = 64, W = 4, batch = 4, ring = 2, occupancy = 3;
 };
 struct FwdShort {  // every load issued at once: the latency of few workgroups
-  static constexpr int T = 16, W = 8, batch = 4, ring = 4, occupancy = 4;
+  static constexpr int T = 16, W = 16, batch = 4, ring = 4, occupancy = 4;
 };
 
 // One pass over the data: a workgroup loads its tokens once, turns them into
@@ -62,7 +62,10 @@ struct FwdShort {  // every load issued at once: the latency of few workgroups
 template <typename TA, typename CF, bool NORM, bool GATE, bool VL>
 __global__ void __launch_bounds__(64 * CF::W, CF::occupancy) gated_fwd_kernel(GatedFwdArgs<TA> p, GatedPlan pl) {
   constexpr int T = CF::T, W = CF::W, C = kGatedC, NB = CF::batch, R = CF::ring, kPolls = kGatedGroup / W;
-  constexpr int kZ = 16;  // rows of z in flight
+  // rows of z in flight; before the wait for the entering state where the
+  // registers have room for them
+  constexpr int kZ = 16;
+  constexpr bool kZEarly = T == kZ;
   using IO = Cell<TA>;
   __shared__ float2 s_agg[W][C];
   __shared__ float2 s_in[kGatedGroup][C];
@@ -157,6 +160,12 @@ __global__ void __launch_bounds__(64 * CF::W, CF::occupancy) gated_fwd_kernel(Ga
       }
     }
   }
+  const rsrc_t rz = make_rsrc(GATE && n > 0 ? p.z + base : p.z, GATE ? span : 0);
+  typename IO::raw_t zr[GATE ? kZ : 1];
+  if (GATE && kZEarly && n > 0) {
+#pragma unroll
+    for (int j = 0; j < kZ; ++j) zr[j] = IO::load(rz, voff, at(j));
+  }
   y = VL && mk.starts ? kCut : keep_of(y);
   s_agg[w][lane] = make_float2(y, H);
   __syncthreads();
@@ -205,9 +214,7 @@ __global__ void __launch_bounds__(64 * CF::W, CF::occupancy) gated_fwd_kernel(Ga
     // without out (the chunks' states alone) every store is out of range
     const rsrc_t ro = make_rsrc(p.out + base, p.out ? span : 0);
     const uint32_t outb = p.out ? rowb : 0;
-    const rsrc_t rz = make_rsrc(GATE ? p.z + base : p.z, GATE ? span : 0);
-    typename IO::raw_t zr[GATE ? kZ : 1];
-    if (GATE) {
+    if (GATE && !kZEarly) {
 #pragma unroll
       for (int j = 0; j < kZ; ++j) zr[j] = IO::load(rz, voff, at(j));
     }

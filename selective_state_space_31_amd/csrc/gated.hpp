@@ -183,7 +183,7 @@ __device__ __forceinline__ void publish(uint64_t* at, float lo, float hi) {
 // later one, so it ends.  Should the words be overwritten meanwhile (a
 // workspace given to two calls at once), the wait still ends, after a second,
 // and gives NaN.
-constexpr int kWaitLimit = 1 << 20;
+constexpr int kWaitLimit = 1 << 18;
 // K words a lane at once: at + k * stride for k < n (n <= K, uniform).  While
 // some are missing the wave polls one of them alone.
 template <int K>
