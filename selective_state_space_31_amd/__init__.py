@@ -36,5 +36,6 @@ def __getattr__(name):
         return getattr(ops, name)
     if name in _RECURRENT_OPS:
         from . import recurrent
-        return getattr(recurrent, name)
+        value = globals()[name] = getattr(recurrent, name)  # (looked up once)
+        return value
     raise AttributeError(name)

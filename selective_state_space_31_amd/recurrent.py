@@ -5,8 +5,9 @@ names, every step runs in the HIP kernels of libssm_scan.so, PyTorch supplies
 device memory and the current HIP stream, and a missing library fails loudly.
 Tensors are on one HIP device, which need not be the current one.  ``stream``
 is a raw HIP stream handle (the tensors' device's current stream by default);
-what is allocated here for a call on another stream is kept until that stream
-is done with it.
+what is allocated here for a call on another stream comes from that stream's
+memory, so the caller orders the two streams for the inputs and the results
+alone.
 """
 import ctypes
 
@@ -88,44 +89,56 @@ def _opt(t, name, shape, dtype, like):
     return _in(t, name, shape, dtype, like)
 
 
-def _out(t, name, shape, dtype, like, new):
-    """The output buffer ``t``, checked, or a new one (noted in ``new``)."""
-    if t is None:
+def _new(like, shape, dtype, stream):
+    """A new tensor for a call on ``stream`` (None: the current one)."""
+    if stream is None:
         # (empty_like is the quickest; it would keep the strides of a slice)
-        t = torch.empty_like(like) if dtype is like.dtype and shape == like.shape and like.is_contiguous() \
-            else like.new_empty(shape, dtype=dtype)
-        new.append(t)
-    else:
-        _in(t, name, shape, dtype, like)
+        if dtype is like.dtype and shape == like.shape and like.is_contiguous():
+            return torch.empty_like(like)
+        return like.new_empty(shape, dtype=dtype)
+    # On another stream the memory has to come from that stream's pool: a block
+    # of the current stream may still be in use by work queued there.  The
+    # caller will read it from the current stream, which the pool has to know.
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=like.device)):
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(torch.cuda.current_stream(like.device))
     return t
 
 
-def _space(workspace, need, like, new):
-    """(address, bytes) of the caller's workspace or of a new one."""
+def _out(t, name, shape, dtype, like, stream):
+    """The output buffer ``t``, checked, or a new one."""
+    if t is None:
+        return _new(like, shape, dtype, stream)
+    _in(t, name, shape, dtype, like)
+    return t
+
+
+def _space(workspace, need, like, stream):
+    """(the caller's workspace or a new one, its address, its bytes)."""
     if workspace is None:
         if need == 0:
-            return None, 0
-        workspace = like.new_empty(need, dtype=torch.uint8)
-        new.append(workspace)
-        return workspace.data_ptr(), need
+            return None, None, 0
+        workspace = _new(like, (need,), torch.uint8, stream)
+        return workspace, workspace.data_ptr(), need
     if workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on %s" % like.device)
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _call(fn, like, stream, new, *args):
-    """fn(*args, stream) with ``like``'s device current; ``new`` are the
-    tensors allocated for the call."""
+def _other(stream, like):
+    """``stream`` where it is another one than ``like``'s device's current
+    stream, else None."""
     index = like.get_device()
     if index < 0 or not like.is_cuda:
         raise ValueError("tensors must be on a HIP device, got %s" % like.device)
-    current = _raw_stream(index)
+    return None if stream is None or stream == _raw_stream(index) else stream
+
+
+def _call(fn, like, stream, *args):
+    """fn(*args, stream) with ``like``'s device current."""
+    index = like.get_device()
     if stream is None:
-        stream = current
-    elif stream != current:
-        ext = torch.cuda.ExternalStream(stream, device=like.device)
-        for t in new:
-            t.record_stream(ext)
+        stream = _raw_stream(index)
     if torch.cuda.current_device() == index:
         rc = fn(*args, stream)
     else:
@@ -192,20 +205,20 @@ def _gated_fwd(x, rgate, igate, A, cu_seqlens, z, rgate_bias, igate_bias, normal
     lib = _load()
     dt, n, L, dim, mid, head, h0, cu = _gated_inputs(x, rgate, igate, A, z, rgate_bias, igate_bias, normalize,
                                                      initial_state, cu_seqlens)
-    new, code = [], _DTYPES[dt]
-    out = _out(out, "out", x.shape, dt, x, new)
+    stream, code = _other(stream, x), _DTYPES[dt]
+    out = _out(out, "out", x.shape, dt, x, stream)
     if return_last_state or last_state is not None:
-        last_state = _out(last_state, "last_state", (n, dim), _F32, x, new)
+        last_state = _out(last_state, "last_state", (n, dim), _F32, x, stream)
     if return_chunk_states or chunk_states is not None:
-        chunk_states = _out(chunk_states, "chunk_states", mid, _F32, x, new)
+        chunk_states = _out(chunk_states, "chunk_states", mid, _F32, x, stream)
     args = head + (out.data_ptr(), None if last_state is None else last_state.data_ptr(), h0,
                    None if chunk_states is None else chunk_states.data_ptr())
     if cu is None:
-        ws, nbytes = _space(workspace, lib.ssm_gated_scan_fwd_workspace_bytes(n, L, dim, code), x, new)
-        _call(lib.ssm_gated_scan_fwd, x, stream, new, *args, n, L, dim, code, ws, nbytes)
+        keep, ws, nbytes = _space(workspace, lib.ssm_gated_scan_fwd_workspace_bytes(n, L, dim, code), x, stream)
+        _call(lib.ssm_gated_scan_fwd, x, stream, *args, n, L, dim, code, ws, nbytes)
     else:
-        ws, nbytes = _space(workspace, lib.ssm_gated_scan_fwd_varlen_workspace_bytes(n, L, dim, code), x, new)
-        _call(lib.ssm_gated_scan_fwd_varlen, x, stream, new, *args, cu, n, L, dim, code, ws, nbytes)
+        keep, ws, nbytes = _space(workspace, lib.ssm_gated_scan_fwd_varlen_workspace_bytes(n, L, dim, code), x, stream)
+        _call(lib.ssm_gated_scan_fwd_varlen, x, stream, *args, cu, n, L, dim, code, ws, nbytes)
     res = (out,) + tuple(t for t in (last_state, chunk_states) if t is not None)
     return res if len(res) > 1 else out
 
@@ -243,24 +256,24 @@ def _gated_bwd(x, rgate, igate, A, cu_seqlens, dout, z, rgate_bias, igate_bias, 
     lib = _load()
     dt, n, L, dim, mid, head, h0, cu = _gated_inputs(x, rgate, igate, A, z, rgate_bias, igate_bias, normalize,
                                                      initial_state, cu_seqlens)
-    new, code = [], _DTYPES[dt]
+    stream, code = _other(stream, x), _DTYPES[dt]
     args = head + (h0, _opt(chunk_states, "chunk_states", mid, _F32, x), _in(dout, "dout", x.shape, dt, x),
                    _opt(dlast_state, "dlast_state", (n, dim), _F32, x))
     g = dict(grads or {})
     for k in ("dx", "drgate", "digate", "dz"):
-        g[k] = None if k == "dz" and z is None else _out(g.get(k), k, x.shape, dt, x, new)
+        g[k] = None if k == "dz" and z is None else _out(g.get(k), k, x.shape, dt, x, stream)
     for k in ("dA", "drgate_bias", "digate_bias"):
-        g[k] = _out(g.get(k), k, (dim,), _F32, x, new)
-    g["dinitial_state"] = _out(g.get("dinitial_state"), "dinitial_state", (n, dim), _F32, x, new)
+        g[k] = _out(g.get(k), k, (dim,), _F32, x, stream)
+    g["dinitial_state"] = _out(g.get("dinitial_state"), "dinitial_state", (n, dim), _F32, x, stream)
     args += tuple(None if g[k] is None else g[k].data_ptr()
                   for k in ("dx", "drgate", "digate", "dz", "dA", "drgate_bias", "digate_bias", "dinitial_state"))
     have = int(chunk_states is not None)
     if cu is None:
-        ws, nbytes = _space(workspace, lib.ssm_gated_scan_bwd_workspace_bytes(n, L, dim, code, have), x, new)
-        _call(lib.ssm_gated_scan_bwd, x, stream, new, *args, n, L, dim, code, ws, nbytes)
+        keep, ws, nbytes = _space(workspace, lib.ssm_gated_scan_bwd_workspace_bytes(n, L, dim, code, have), x, stream)
+        _call(lib.ssm_gated_scan_bwd, x, stream, *args, n, L, dim, code, ws, nbytes)
     else:
-        ws, nbytes = _space(workspace, lib.ssm_gated_scan_bwd_varlen_workspace_bytes(n, L, dim, code, have), x, new)
-        _call(lib.ssm_gated_scan_bwd_varlen, x, stream, new, *args, cu, n, L, dim, code, ws, nbytes)
+        keep, ws, nbytes = _space(workspace, lib.ssm_gated_scan_bwd_varlen_workspace_bytes(n, L, dim, code, have), x, stream)
+        _call(lib.ssm_gated_scan_bwd_varlen, x, stream, *args, cu, n, L, dim, code, ws, nbytes)
     return g
 
 
@@ -298,14 +311,15 @@ def ssm_gated_state_update(state, x, rgate, igate, A, z=None, rgate_bias=None, i
     _, dt = _act(x)
     if x.dim() != 2:
         raise ValueError("x must be (batch, dim)")
-    shape, new = x.shape, []
+    shape = x.shape
     batch, dim = shape
     args = (_in(state, "state", shape, _F32, x), _in(x, "x", shape, dt, x), _in(rgate, "rgate", shape, dt, x),
             _in(igate, "igate", shape, dt, x), _in(A, "A", (dim,), _F32, x),
             _opt(rgate_bias, "rgate_bias", (dim,), _F32, x), _opt(igate_bias, "igate_bias", (dim,), _F32, x),
             int(bool(normalize)), _opt(z, "z", shape, dt, x))
-    out = _out(out, "out", shape, dt, x, new)
-    _call(lib.ssm_gated_state_update, x, stream, new, *args, out.data_ptr(), batch, dim, _DTYPES[dt])
+    stream = _other(stream, x)
+    out = _out(out, "out", shape, dt, x, stream)
+    _call(lib.ssm_gated_state_update, x, stream, *args, out.data_ptr(), batch, dim, _DTYPES[dt])
     return out
 
 
@@ -365,13 +379,13 @@ def ssm_qk_norm_rotate_fwd(q, k, inv_freq, q_weight=None, k_weight=None, positio
     Returns ``(q_out, k_out)``, contiguous (k_out None without k)."""
     lib = _load()
     head, sizes = _rot_inputs(q, k, inv_freq, q_weight, k_weight, positions, eps, interleaved)
-    new = []
-    q_out = _out(q_out, "q_out", q.shape, q.dtype, q, new)
-    if k is not None:
-        k_out = _out(k_out, "k_out", k.shape, q.dtype, q, new)
-    elif k_out is not None or k_weight is not None:
+    if k is None and (k_out is not None or k_weight is not None):
         raise ValueError("k_out or k_weight given without k")
-    _call(lib.ssm_qk_norm_rotate_fwd, q, stream, new, *head, q_out.data_ptr(),
+    stream = _other(stream, q)
+    q_out = _out(q_out, "q_out", q.shape, q.dtype, q, stream)
+    if k is not None:
+        k_out = _out(k_out, "k_out", k.shape, q.dtype, q, stream)
+    _call(lib.ssm_qk_norm_rotate_fwd, q, stream, *head, q_out.data_ptr(),
           None if k is None else k_out.data_ptr(), *sizes)
     return q_out, k_out
 
@@ -392,17 +406,17 @@ def ssm_qk_norm_rotate_bwd(q, k, inv_freq, dq_out, dk_out, q_weight=None, k_weig
     batch, L, Hq, Hk, D = sizes[:5]
     if k is None and (dk_out is not None or k_weight is not None):
         raise ValueError("dk_out or k_weight given without k")
-    new = []
     head += (_in(dq_out, "dq_out", q.shape, q.dtype, q),
              None if k is None else _in(dk_out, "dk_out", k.shape, q.dtype, q))
+    stream = _other(stream, q)
     g = dict(grads or {})
-    g["dq"] = _out(g.get("dq"), "dq", q.shape, q.dtype, q, new)
-    g["dk"] = None if k is None else _out(g.get("dk"), "dk", k.shape, q.dtype, q, new)
+    g["dq"] = _out(g.get("dq"), "dq", q.shape, q.dtype, q, stream)
+    g["dk"] = None if k is None else _out(g.get("dk"), "dk", k.shape, q.dtype, q, stream)
     for n, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
-        g[n] = None if w is None else _out(g.get(n), n, (D,), _F32, q, new)
+        g[n] = None if w is None else _out(g.get(n), n, (D,), _F32, q, stream)
     head += tuple(None if g[n] is None else g[n].data_ptr() for n in ("dq", "dk", "dq_weight", "dk_weight"))
-    ws, nbytes = _space(workspace, lib.ssm_qk_norm_rotate_bwd_workspace_bytes(batch, L, Hq, Hk, D), q, new)
-    _call(lib.ssm_qk_norm_rotate_bwd, q, stream, new, *head, *sizes, ws, nbytes)
+    keep, ws, nbytes = _space(workspace, lib.ssm_qk_norm_rotate_bwd_workspace_bytes(batch, L, Hq, Hk, D), q, stream)
+    _call(lib.ssm_qk_norm_rotate_bwd, q, stream, *head, *sizes, ws, nbytes)
     return g
 
 
@@ -429,17 +443,18 @@ def ssm_causal_conv1d_bwd(x, weight, dout, bias=None, initial_conv_state=None,
     if weight.dim() != 2:
         raise ValueError("weight must be (dim, width)")
     W = weight.shape[1]
-    new, st = [], (batch, dim, W - 1)
+    st = (batch, dim, W - 1)
     args = (_in(x, "x", x.shape, dt, x), _in(weight, "weight", (dim, W), _F32, x), _opt(bias, "bias", (dim,), _F32, x),
             _opt(initial_conv_state, "initial_conv_state", st, dt, x), _in(dout, "dout", x.shape, dt, x),
             _opt(dfinal_conv_state, "dfinal_conv_state", st, dt, x))
+    stream = _other(stream, x)
     g = dict(grads or {})
-    g["dx"] = _out(g.get("dx"), "dx", x.shape, dt, x, new)
-    g["dweight"] = _out(g.get("dweight"), "dweight", (dim, W), _F32, x, new)
-    g["dbias"] = None if bias is None else _out(g.get("dbias"), "dbias", (dim,), _F32, x, new)
+    g["dx"] = _out(g.get("dx"), "dx", x.shape, dt, x, stream)
+    g["dweight"] = _out(g.get("dweight"), "dweight", (dim, W), _F32, x, stream)
+    g["dbias"] = None if bias is None else _out(g.get("dbias"), "dbias", (dim,), _F32, x, stream)
     g["dinitial_conv_state"] = None if initial_conv_state is None else \
-        _out(g.get("dinitial_conv_state"), "dinitial_conv_state", st, dt, x, new)
+        _out(g.get("dinitial_conv_state"), "dinitial_conv_state", st, dt, x, stream)
     args += tuple(None if g[k] is None else g[k].data_ptr() for k in ("dx", "dweight", "dbias", "dinitial_conv_state"))
-    ws, nbytes = _space(workspace, lib.ssm_causal_conv1d_bwd_workspace_bytes(batch, L, dim, W), x, new)
-    _call(lib.ssm_causal_conv1d_bwd, x, stream, new, *args, batch, L, dim, W, int(bool(silu)), _DTYPES[dt], ws, nbytes)
+    keep, ws, nbytes = _space(workspace, lib.ssm_causal_conv1d_bwd_workspace_bytes(batch, L, dim, W), x, stream)
+    _call(lib.ssm_causal_conv1d_bwd, x, stream, *args, batch, L, dim, W, int(bool(silu)), _DTYPES[dt], ws, nbytes)
     return g

@@ -127,8 +127,8 @@ def test_nan_reaches_what_depends_on_it_only():
     assert torch.equal(out[~bad], base[~bad])
 
 
-LENGTHS = [[1], [0, 5, 0], [3, 1, 0, 0, 130, 17], [128, 128, 1], [1] * 40, [500, 0, 77, 300, 0],
-           [127, 2, 255, 1, 64, 900]]
+LENGTHS = [[0], [1], [0, 5, 0], [3, 1, 0, 0, 130, 17], [128, 128, 1], [1] * 40, [500, 0, 77, 300, 0],
+           [127, 2, 255, 1, 64, 900], [k * 7 % 4 for k in range(300)]]
 
 
 @pytest.mark.parametrize("pad", [0, 9, 300])
@@ -351,16 +351,23 @@ def test_two_streams_at_once():
 
 
 def test_stream_argument():
-    """The raw handle of another stream than the current one."""
+    """The raw handle of another stream than the current one, while the
+    current one has work queued in memory that was given back."""
     p = Gated((1, 3000), 1, 256, "fp32", DEV, 20)
     want = pkg.ssm_gated_scan_fwd(*p.args(), **p.kw())
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
     for _ in range(3):
+        big = torch.full((1 << 26,), 2.0, device=DEV)
+        for _ in range(4):
+            big = big * 1.0  # blocks of the current stream that are free and still written to
+        del big
         out = pkg.ssm_gated_scan_fwd(*p.args(), stream=s.cuda_stream, **p.kw())
-        junk = torch.full((1 << 20,), 3.0, device=DEV)  # would take a workspace that was given back too early
-    torch.cuda.synchronize()
-    assert torch.equal(out, want) and (junk == 3.0).all()
+        junk = torch.full((1 << 20,), 3.0, device=DEV)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and (junk == 3.0).all()
+    same = pkg.ssm_gated_scan_fwd(*p.args(), stream=torch.cuda.current_stream().cuda_stream, **p.kw())
+    assert torch.equal(same, want)
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
