@@ -84,8 +84,8 @@ size_t ssm_gated_scan_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t
  *                      not overlap initial_state.
  *   chunk_states     : (ceil(total_len / SSM_GATED_CHUNK), dim) float32 or
  *                      NULL; receives the state that enters token
- *                      SSM_GATED_CHUNK c from
- *                      the one before it (zero for c = 0)
+ *                      SSM_GATED_CHUNK c from the one before it (zero for
+ *                      c = 0)
  *   1 <= nseq < 2^24; total_len >= 0.
  * Nothing passes from one sequence into another, a NaN or an infinity neither.
  */
@@ -106,7 +106,8 @@ size_t ssm_gated_scan_fwd_varlen_workspace_bytes(int64_t nseq, int64_t total_len
  * not kept but walked again from chunk_states.
  *   inputs as ssm_gated_scan_fwd, plus
  *     chunk_states : what the forward left for the same inputs, or NULL: then
- *                    they are computed here first (a third more traffic)
+ *                    they are computed here first (three more reads of
+ *                    activations)
  *     dout         : (batch, seqlen, dim) act
  *     dlast_state  : (batch, dim) float32 or NULL (= 0)
  *   outputs (all overwritten, none accumulated into):
@@ -116,9 +117,9 @@ size_t ssm_gated_scan_fwd_varlen_workspace_bytes(int64_t nseq, int64_t total_len
  *     dA           : (dim) float32
  *     drgate_bias, digate_bias : (dim) float32 or NULL
  *     dinitial_state : (batch, dim) float32 or NULL
- * Where m_t is 0 (normalize, and a decay that rounds to 1: a gate closed by
- * less than 2^-149, or A = 0) the term of the gradients that divides by m_t is
- * taken as 0, its limit for a closing gate.
+ * Where 1 - a_t^2 is below 2^-126 (normalize, and a gate closed that far, or
+ * A >= 0) the gradients take m_t as 0, and the term that divides by m_t too,
+ * its limit for a closing gate.  A decay of 0 (A = -infinity) has no slope.
  * Sums over tokens and sequences are formed in a fixed order from float32
  * partials: bitwise reproducible run to run on one device.
  */
@@ -173,8 +174,8 @@ int ssm_gated_state_update(float* state, const void* x, const void* rgate, const
  *   pairs: (i, i + rotary_dim/2) with interleaved = 0, (2i, 2i+1) with 1
  *   q               : (batch, seqlen, nheads_q, headdim) act, a token's heads
  *                     together, tokens q_token_stride values apart (at least
- *                     nheads_q * headdim: rows of a fused projection are read
- *                     where they are); batch rows follow each other at seqlen
+ *                     nheads_q * headdim, at most 2^30: rows of a fused
+ *                     projection are read where they are); batch rows follow each other at seqlen
  *                     token strides.  k likewise with nheads_k.
  *   q_out, k_out    : (batch, seqlen, heads, headdim) act, contiguous.  q_out
  *                     may be q (and k_out k) where its rows are contiguous.
@@ -183,7 +184,10 @@ int ssm_gated_state_update(float* state, const void* x, const void* rgate, const
  *   positions       : (batch, seqlen) int32 DEVICE array or NULL (= the token's
  *                     index in its sequence)
  *   nheads_q >= 1; nheads_k >= 0 (0: k, k_weight and k_out NULL); headdim even,
- *   2..256; rotary_dim even, 0..headdim; eps >= 0.
+ *   2..256; rotary_dim even, 0..headdim; eps >= 0; batch * seqlen < 2^31;
+ *   at most 65536 heads each.
+ * mean(v^2) + eps is a float32: rows where it is below 2^-126 (eps = 0 alone
+ * allows it) or where a sum of squares overflows give unspecified values.
  * The angle is formed and reduced in float64, so far positions lose nothing;
  * its sine and cosine are float32 (within 2^-23).
  */

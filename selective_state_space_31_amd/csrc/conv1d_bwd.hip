@@ -27,8 +27,11 @@ struct ConvBwdArgs {
   float* part;  // (batch * chunks, W + 1, dim)
   int64_t batch, L;
   int dim;
-  uint32_t tiles, chunks;  // of 64 V channels, of kConvBwdChunk tokens
+  uint32_t tiles, chunks, units;  // of 64 V channels, of kConvBwdChunk tokens; workgroups
 };
+
+// Workgroups of a grid's row: neither extent times the threads passes 32 bits.
+constexpr uint32_t kConvGridX = 1u << 22;
 
 constexpr int kConvBwdT = 32;     // tokens of a wave
 constexpr int kConvBwdWaves = 4;  // waves of a workgroup, one stretch after the other
@@ -92,7 +95,9 @@ __global__ void __launch_bounds__(64 * kConvBwdWaves) conv_bwd_kernel(ConvBwdArg
   using IO = ConvCell<TA, V>;
   __shared__ float s_sum[kConvBwdWaves][W + 1][C];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t tile = blockIdx.x % a.tiles, rest = blockIdx.x / a.tiles;
+  const uint32_t unit = blockIdx.y * kConvGridX + blockIdx.x;
+  if (unit >= a.units) return;
+  const uint32_t tile = unit % a.tiles, rest = unit / a.tiles;
   const uint32_t chunk = rest % a.chunks, b = rest / a.chunks;
   const int dim = a.dim, col0 = static_cast<int>(tile) * C, col = col0 + lane * V;
   const bool have = col < dim;
@@ -268,7 +273,8 @@ int conv_bwd_launch(ConvBwdArgs<TA> a, int W, bool silu, float* dweight, float* 
   a.tiles = static_cast<uint32_t>((a.dim + 64 * V - 1) / (64 * V));
   a.chunks = static_cast<uint32_t>(conv_bwd_chunks(a.L));
   const int64_t n = a.batch * a.chunks;
-  const dim3 grid(static_cast<unsigned>(n * a.tiles)), block(64 * kConvBwdWaves);
+  a.units = static_cast<uint32_t>(n * a.tiles);  // (65535 * 65536 at most, of empty sequences)
+  const dim3 grid(a.units < kConvGridX ? a.units : kConvGridX, (a.units + (kConvGridX - 1ull)) / kConvGridX), block(64 * kConvBwdWaves);
 #define SSM_CONV_BWD_CASE(WW)                                                            \
   case WW:                                                                               \
     if (silu)                                                                            \
@@ -358,7 +364,7 @@ int ssm_causal_conv1d_bwd(const void* x, const float* weight, const float* bias,
                       static_cast<const TA*>(initial_conv_state), static_cast<const TA*>(dout),
                       static_cast<const TA*>(dfinal_conv_state), static_cast<TA*>(dx),
                       static_cast<TA*>(dinitial_conv_state), static_cast<float*>(workspace), batch,
-                      seqlen, static_cast<int>(dim), 0, 0};
+                      seqlen, static_cast<int>(dim), 0, 0, 0};
     if constexpr (sizeof(TA) == 2) {
       // two channels a lane where every row starts on four bytes
       if (dim % 2 == 0 && aligned(x, 4) && aligned(dout, 4) && aligned(dx, 4))

@@ -76,13 +76,13 @@ __global__ void __launch_bounds__(64 * CF::W, CF::occupancy) gated_fwd_kernel(Ga
   const int dim = p.dim;
   uint64_t* const agg = static_cast<uint64_t*>(p.ws);
   uint64_t* const carries = agg + pl.chunks * pl.cells;
-  uint32_t unit = blockIdx.x;
+  uint32_t unit = blockIdx.y * kGatedGridX + blockIdx.x;
   if (pl.chunks > 1) {
     if (threadIdx.x == 0) s_turn = atomicAdd(reinterpret_cast<uint32_t*>(carries + pl.groups * pl.cells), 1u);
     __syncthreads();
     unit = __builtin_amdgcn_readfirstlane(s_turn);
-    if (unit >= pl.units) return;  // (a workspace that another call uses at the same time)
   }
+  if (unit >= pl.units) return;  // (the grid's surplus, or a workspace that another call uses at the same time)
   const uint32_t c = unit / pl.lines, line = unit % pl.lines;
   const uint32_t row = line / pl.tiles, tile = line % pl.tiles;
   const int col0 = static_cast<int>(tile) * C, col = col0 + lane;
@@ -166,6 +166,15 @@ __global__ void __launch_bounds__(64 * CF::W, CF::occupancy) gated_fwd_kernel(Ga
 #pragma unroll
     for (int j = 0; j < kZ; ++j) zr[j] = IO::load(rz, voff, at(j));
   }
+  // The state that the first group folds from.  last_state may be its buffer,
+  // written by the row's last chunk behind the words of every chunk before it:
+  // with h0 here (the pin waits for the load) ahead of this chunk's word, nobody
+  // still reads it by then.
+  float h0 = 0.0f;
+  if (!VL && p.h0 && c < kGatedGroup) {
+    if (have) h0 = p.h0[static_cast<int64_t>(row) * dim + col];
+    asm volatile("" : "+v"(h0));
+  }
   y = VL && mk.starts ? kCut : keep_of(y);
   s_agg[w][lane] = make_float2(y, H);
   __syncthreads();
@@ -183,7 +192,6 @@ __global__ void __launch_bounds__(64 * CF::W, CF::occupancy) gated_fwd_kernel(Ga
     if (c + 1 < pl.chunks) publish(agg + c * pl.cells + cell, yt, Ht);
   }
   // the state that enters the chunk
-  const float h0 = !VL && p.h0 && have ? p.h0[static_cast<int64_t>(row) * dim + col] : 0.0f;
   if (c == 0) {
     h = h0;
   } else {
@@ -266,7 +274,7 @@ int launch_gated_fwd(const GatedFwdArgs<TA>& a, bool norm, const char* fn, hipSt
   const int rc = launch_gated_init(a.ws, pl.bytes, a.cu, a.cu ? a.nseq : a.rows, a.L, a.dim, a.h0, a.last,
                                    fn, s);
   if (rc != SSM_OK || a.L == 0) return rc;
-  const dim3 grid(pl.units), block(64 * CF::W);
+  const dim3 grid = gated_grid(pl.units), block(64 * CF::W);
 #define SSM_GATED_CASE(N, G, VLN)                                                              \
   if (norm == N && (a.z != nullptr) == G && (a.cu != nullptr) == VLN)                          \
     hipLaunchKernelGGL((gated_fwd_kernel<TA, CF, N, G, VLN>), grid, block, 0, s, a, pl);

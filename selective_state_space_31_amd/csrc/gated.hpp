@@ -181,8 +181,8 @@ __device__ __forceinline__ void publish(uint64_t* at, float lo, float hi) {
 // The lane's V words, once they are all there.  Every wait is for a
 // workgroup that took its turn earlier and publishes without waiting for a
 // later one, so it ends.  Should the words be overwritten meanwhile (a
-// workspace given to two calls at once), the wait still ends, after a second,
-// and gives NaN.
+// workspace given to two calls at once), the wait still ends, after a quarter
+// of a second, and gives NaN.
 constexpr int kWaitLimit = 1 << 18;
 // K words a lane at once: at + k * stride for k < n (n <= K, uniform).  While
 // some are missing the wave polls one of them alone.
@@ -229,6 +229,12 @@ struct GatedPlan {
   int64_t cells;
   size_t bytes;  // 0: one chunk per row, no workspace
 };
+// A grid of `units` workgroups: rows of kGatedGridX, so that neither extent
+// times the workgroup's threads passes 32 bits; the last row's surplus returns.
+constexpr uint32_t kGatedGridX = 1u << 22;
+inline dim3 gated_grid(uint32_t units) {
+  return dim3(units < kGatedGridX ? units : kGatedGridX, (units + kGatedGridX - 1) / kGatedGridX);
+}
 inline GatedPlan gated_plan(int64_t rows, int64_t L, int64_t dim, int chunk) {
   const int64_t chunks = L > 0 ? (L + chunk - 1) / chunk : 1;
   const int64_t groups = (chunks + kGatedGroup - 1) / kGatedGroup;

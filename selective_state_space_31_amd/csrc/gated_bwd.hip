@@ -38,13 +38,13 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 4) gated_bwd_kernel(GatedBwdAr
   const int dim = p.dim;
   uint64_t* const maps = static_cast<uint64_t*>(p.ws);
   uint64_t* const carries = maps + pl.chunks * pl.cells;
-  uint32_t unit = blockIdx.x;
+  uint32_t unit = blockIdx.y * kGatedGridX + blockIdx.x;
   if (pl.chunks > 1) {
     if (threadIdx.x == 0) s_turn = atomicAdd(reinterpret_cast<uint32_t*>(carries + pl.groups * pl.cells), 1u);
     __syncthreads();
     unit = __builtin_amdgcn_readfirstlane(s_turn);
-    if (unit >= pl.units) return;  // (a workspace that another call uses at the same time)
   }
+  if (unit >= pl.units) return;  // (the grid's surplus, or a workspace that another call uses at the same time)
   const uint32_t chunks = pl.chunks;
   const uint32_t c = chunks - 1 - unit / pl.lines, line = unit % pl.lines;
   const uint32_t row = line / pl.tiles, tile = line % pl.tiles;
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 4) gated_bwd_kernel(GatedBwdAr
         float m = 1.0f, sub = 0.0f;
         if (NORM) {
           const float M = input_scale2(E);
-          const float inv = M > 0.0f ? __builtin_amdgcn_rsqf(M) : 0.0f;
+          const float inv = M >= 0x1p-126f ? __builtin_amdgcn_rsqf(M) : 0.0f;  // (subnormals have no rsq)
           m = M * inv;
           sub = u * x * (a[j] * a[j] * inv);
         }
@@ -205,7 +205,8 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 4) gated_bwd_kernel(GatedBwdAr
   if (n > 0) {
     const rsrc_t rdx = make_rsrc(p.dx + base, span), rdr = make_rsrc(p.dr + base, span),
                  rdi = make_rsrc(p.di + base, span);
-    const float A = have ? p.A[col] : 0.0f;
+    float A = have ? p.A[col] : 0.0f;
+    if (A < -1e30f) A = -1e30f;  // (finite, as in A2: a decay of 0 has no slope)
 #pragma unroll
     for (int j = T - 1; j >= 0; --j) {
       if (VL && (mk.ends >> j & 1))
@@ -275,7 +276,7 @@ int launch_gated_bwd(const GatedBwdArgs<TA>& a, const GatedPlan& pl, bool norm, 
   int rc = launch_gated_init(a.ws, pl.bytes, a.cu, a.cu ? a.nseq : a.rows, a.L, a.dim, a.dlast, a.dh0, fn, s);
   if (rc != SSM_OK) return rc;
   if (a.L > 0) {
-    const dim3 grid(static_cast<unsigned>(pl.units)), block(64 * kBwdWaves);
+    const dim3 grid = gated_grid(pl.units), block(64 * kBwdWaves);
 #define SSM_GATED_CASE(N, G, VLN)                                                              \
   if (norm == N && (a.z != nullptr) == G && (a.cu != nullptr) == VLN)                          \
     hipLaunchKernelGGL((gated_bwd_kernel<TA, N, G, VLN>), grid, block, 0, s, a, pl);

@@ -519,9 +519,9 @@ int rot_call(const RotCall& c) {
   if (!rot_sizes_ok(c.batch, c.L, c.Hq, c.Hk, c.D))
     return fail(SSM_ERR_SHAPE, "%s: bad sizes batch %lld, seqlen %lld, heads %lld and %lld", c.fn,
                 (long long)c.batch, (long long)c.L, (long long)c.Hq, (long long)c.Hk);
-  constexpr int64_t kMaxStride = int64_t{1} << 31;
+  constexpr int64_t kMaxStride = int64_t{1} << 30;
   if (c.qs < c.Hq * c.D || c.qs > kMaxStride || (c.Hk > 0 && (c.ks < c.Hk * c.D || c.ks > kMaxStride)))
-    return fail(SSM_ERR_SHAPE, "%s: a token stride (%lld, %lld) is shorter than its heads", c.fn,
+    return fail(SSM_ERR_SHAPE, "%s: a token stride (%lld, %lld) is shorter than its heads or beyond 2^30", c.fn,
                 (long long)c.qs, (long long)c.ks);
   const int64_t tokens = c.batch * c.L;
   const bool any = tokens > 0;

@@ -171,3 +171,18 @@ def test_repeats_bit_for_bit_and_captured():
         run()
         torch.cuda.synchronize()
     assert got[-1].dtype == DT["bf16"] or got[-1].dtype == torch.float32
+
+
+def test_more_workgroups_than_a_grid_row():
+    """65535 one-token sequences of so many channels that the threads of one
+    grid row would pass 32 bits; every sequence has the same inputs."""
+    d = 16447
+    c = Case(1, 1, d, 2, "bf16", 31)
+    want = pkg.ssm_causal_conv1d_bwd(*c.args(), **c.kw())
+    many = lambda t: t.expand((65535,) + t.shape[1:]).contiguous()
+    g = pkg.ssm_causal_conv1d_bwd(many(c.x), c.w, many(c.dout), bias=c.bias, initial_conv_state=many(c.state),
+                                  dfinal_conv_state=many(c.dfinal), silu=c.silu)
+    assert bool((g["dx"] == want["dx"]).all())
+    assert bool((g["dinitial_conv_state"] == want["dinitial_conv_state"]).all())
+    for k in ("dweight", "dbias"):  # sums of equal values: a relative 65535 2^-24 at most
+        torch.testing.assert_close(g[k], want[k] * 65535.0, rtol=65535 * 2.0 ** -24, atol=0)

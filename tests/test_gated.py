@@ -241,6 +241,55 @@ def test_empty_sequence():
     assert not g["dA"].any() and not g["drgate_bias"].any()
 
 
+@pytest.mark.parametrize("b,L,d", [(1, 3000, 66), (16, 3000, 130), (200, 600, 200)])
+def test_resume_in_place_over_many_chunks(b, L, d):
+    """last_state in the initial state's buffer, with a row's last chunk done
+    long before or after the others read the state."""
+    p = Gated((b, L), b, d, "fp32", DEV, 23)
+    out, last = pkg.ssm_gated_scan_fwd(*p.args(), return_last_state=True, **p.kw())
+    for _ in range(3):
+        state = p.h0.clone()
+        out2, _ = pkg.ssm_gated_scan_fwd(*p.args(), last_state=state, **dict(p.kw(), initial_state=state))
+        assert torch.equal(out, out2) and torch.equal(last, state)
+
+
+def test_more_workgroups_than_a_grid_row():
+    """65535 one-token sequences of so many channels that the threads of one
+    grid row would pass 32 bits; every sequence has the same inputs."""
+    for d, bwd in ((16448, False), (8256, True)):
+        p = Gated((1, 1), 1, d, "bf16", DEV, 24)
+        out = pkg.ssm_gated_scan_fwd(*p.args(), **p.kw())
+        many = lambda t, *s: t.reshape((1,) + s).expand((65535,) + s).contiguous()
+        x, r, i, z, h0 = many(p.x, 1, d), many(p.r, 1, d), many(p.i, 1, d), many(p.z, 1, d), many(p.h0, d)
+        kw = dict(p.kw(), z=z, initial_state=h0)
+        if bwd:
+            want = pkg.ssm_gated_scan_bwd(*p.args(), p.dout, dlast_state=p.dlast, **p.kw())
+            g = pkg.ssm_gated_scan_bwd(x, r, i, p.A, many(p.dout, 1, d), dlast_state=many(p.dlast, d), **kw)
+            for k in ("dx", "drgate", "digate", "dz", "dinitial_state"):
+                assert bool((g[k] == want[k]).all()), k
+            for k in ("dA", "drgate_bias", "digate_bias"):  # sums of equal values: a relative 65535 2^-24 at most
+                torch.testing.assert_close(g[k], want[k] * 65535.0, rtol=65535 * 2.0 ** -24, atol=0)
+        else:
+            assert bool((pkg.ssm_gated_scan_fwd(x, r, i, p.A, **kw) == out).all())
+        del x, r, i, z, h0, kw
+
+
+def test_gates_closed_beyond_float32():
+    """Decays whose 1 - a^2 is subnormal or 0, and ones that are exactly 0:
+    everything stays finite, and m_t (2e-19 at most there) is taken as 0."""
+    p = Gated((1, 40), 1, 64, "fp32", DEV, 25)
+    A, r = torch.full_like(p.A, -1e-3), torch.full_like(p.r, -84.0)
+    r[:, ::3] = -200.0
+    kw = {k: v for k, v in p.kw().items() if k != "rgate_bias"}
+    g = pkg.ssm_gated_scan_bwd(p.x, r, p.i, A, p.dout, dlast_state=p.dlast, **kw)
+    assert all(torch.isfinite(v).all() for v in g.values()) and not g["digate"].abs().gt(1e-15).any()
+    A, r = torch.full_like(p.A, -float("inf")), p.r
+    out = pkg.ssm_gated_scan_fwd(p.x, r, p.i, A, **kw)
+    g = pkg.ssm_gated_scan_bwd(p.x, r, p.i, A, p.dout, dlast_state=p.dlast, **kw)
+    assert torch.isfinite(out).all() and all(torch.isfinite(v).all() for v in g.values())
+    assert not g["drgate"].any() and not g["dA"].any() and not g["dinitial_state"].any()
+
+
 def test_resume_in_place():
     p = Gated((3, 500), 3, 130, "bf16", DEV, 13)
     out, last = pkg.ssm_gated_scan_fwd(*p.args(), return_last_state=True, **p.kw())
