@@ -33,8 +33,8 @@ struct ConvBwdArgs {
 // Workgroups of a grid's row: neither extent times the threads passes 32 bits.
 constexpr uint32_t kConvGridX = 1u << 22;
 
-constexpr int kConvBwdT = 32;     // tokens of a wave
-constexpr int kConvBwdWaves = 4;  // waves of a workgroup, one stretch after the other
+constexpr int kConvBwdT = 16;     // tokens of a wave
+constexpr int kConvBwdWaves = 8;  // waves of a workgroup, one stretch after the other
 constexpr int kConvBwdChunk = kConvBwdT * kConvBwdWaves;
 
 // V channels of one token: raw bits as loaded, widened at use (as in the

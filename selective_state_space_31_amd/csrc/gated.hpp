@@ -56,11 +56,14 @@ __device__ __forceinline__ void decay(float v, float& a, float& m) {
 struct Params {
   float A2, rb2, ib2;
 };
+__device__ __forceinline__ Params params_of(float A, float rb, float ib) {
+  float A2 = A * -kLog2e;
+  if (A2 > 1e30f) A2 = 1e30f;  // (finite: a token that is masked takes it times 0)
+  return Params{A2, rb * -kLog2e, ib * -kLog2e};
+}
 __device__ __forceinline__ Params load_params(const float* A, const float* rb, const float* ib, int c,
                                               bool have) {
-  float A2 = have ? A[c] * -kLog2e : 0.0f;
-  if (A2 > 1e30f) A2 = 1e30f;  // (finite: a token that is masked takes it times 0)
-  return Params{A2, have && rb ? rb[c] * -kLog2e : 0.0f, have && ib ? ib[c] * -kLog2e : 0.0f};
+  return params_of(have ? A[c] : 0.0f, have && rb ? rb[c] : 0.0f, have && ib ? ib[c] : 0.0f);
 }
 
 // ----------------------------------------------------------------------------
@@ -148,13 +151,33 @@ struct Marks {
   uint64_t starts, ends;
   int seq;
 };
-__device__ __forceinline__ Marks find_marks(const int32_t* cu, int nseq, int64_t t0, int n) {
+// The offsets, read through the scalar cache: nothing writes them meanwhile,
+// and a scalar load waits for no row that is on its way.
+typedef const int32_t __attribute__((address_space(4)))* scalar_i32;
+__device__ __forceinline__ scalar_i32 scalar_of(const int32_t* p) {
+  return (scalar_i32)(reinterpret_cast<uintptr_t>(p));
+}
+__device__ __forceinline__ Marks find_marks(const int32_t* cu, int nseq, int64_t from, int n) {
+  const scalar_i32 cs = scalar_of(cu);
+  const int t0 = static_cast<int>(from);  // (n > 0: the tokens are below cu[nseq])
+  // one search for the whole stretch, until an offset falls inside of it: the
+  // sequence of each of its tokens is in [lo, hi), the last s with cu[s] <= t
+  // (empty sequences are passed over)
+  int lo = 0, hi = nseq;
+  while (hi - lo > 1) {
+    const int mid = lo + ((hi - lo) >> 1), v = cs[mid];
+    if (v <= t0) lo = mid;
+    else if (v >= t0 + n) hi = mid;
+    else break;
+  }
+  if (hi - lo == 1)
+    return Marks{cs[lo] == t0 ? uint64_t{1} : 0, cs[lo + 1] == t0 + n ? uint64_t{1} << (n - 1) : 0, lo};
+  // a lane searches for its token
   const int lane = threadIdx.x & 63;
   Marks m{0, 0, 0};
   bool st = false, en = false;
   if (lane < n) {
-    const int64_t t = t0 + lane;
-    int lo = 0, hi = nseq;  // the last s < nseq with cu[s] <= t: empty sequences are passed over
+    const int t = t0 + lane;
     while (hi - lo > 1) {
       const int mid = lo + ((hi - lo) >> 1);
       if (cu[mid] <= t) lo = mid; else hi = mid;

@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 4) gated_bwd_kernel(GatedBwdAr
   const int64_t t0 = static_cast<int64_t>(c) * kBwdChunk + w * T;
   int64_t end = p.L;
   if (VL) {
-    const int64_t e = p.cu[p.nseq];
+    const int64_t e = scalar_of(p.cu)[p.nseq];
     end = e < 0 ? 0 : (e < end ? e : end);
   }
   const int n = end <= t0 ? 0 : (end - t0 < T ? static_cast<int>(end - t0) : T);  // the wave's tokens

@@ -217,6 +217,27 @@ def test_step(batch, dim, dtype, gate):
     within(state, rl, bl, "state")
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("which", range(6))
+def test_step_at_odd_addresses(dtype, which):
+    """One array after the other starts one element into its allocation."""
+    p = Gated((5,), 5, 66, dtype, DEV, 40)
+    kw = {k: v for k, v in p.kw().items() if k not in ("initial_state", "z")}
+    want_state = p.h0.clone()
+    want = pkg.ssm_gated_state_update(want_state, *p.args(), z=p.z, **kw)
+
+    def off(t, k):
+        b = torch.full((t.numel() + 2,), 7.0, device=DEV, dtype=t.dtype)
+        v = b[1:-1].view(t.shape) if k == which else b[:-2].view(t.shape)
+        return v.copy_(t), b
+
+    (state, sb), (x, _), (r, _), (i, _), (z, _) = (off(t, k) for k, t in enumerate((p.h0, p.x, p.r, p.i, p.z)))
+    out, ob = off(torch.zeros_like(p.x), 5)
+    pkg.ssm_gated_state_update(state, x, r, i, p.A, z=z, out=out, **kw)
+    assert torch.equal(out, want) and torch.equal(state, want_state)
+    assert sb[-1] == 7.0 and ob[-1] == 7.0 and (which == 0) == (sb[0] == 7.0) and (which == 5) == (ob[0] == 7.0)
+
+
 def test_steps_continue_a_scan():
     p = Gated((2, 40), 2, 100, "fp32", DEV, 11)
     kw = {k: v for k, v in p.kw().items() if k not in ("initial_state", "z")}
