@@ -90,7 +90,8 @@ def _opt(t, name, shape, dtype, like):
 
 
 def _new(like, shape, dtype, stream):
-    """A new tensor for a call on ``stream`` (None: the current one)."""
+    """A new tensor for a call on ``stream`` (None: the current one).  ``like``
+    is on the device, and where there is one it has this shape and type."""
     if stream is None:
         # (empty_like is the quickest; it would keep the strides of a slice)
         if dtype is like.dtype and shape == like.shape and like.is_contiguous():
@@ -208,7 +209,8 @@ def _gated_fwd(x, rgate, igate, A, cu_seqlens, z, rgate_bias, igate_bias, normal
     stream, code = _other(stream, x), _DTYPES[dt]
     out = _out(out, "out", x.shape, dt, x, stream)
     if return_last_state or last_state is not None:
-        last_state = _out(last_state, "last_state", (n, dim), _F32, x, stream)
+        last_state = _out(last_state, "last_state", (n, dim), _F32, x if initial_state is None else initial_state,
+                          stream)
     if return_chunk_states or chunk_states is not None:
         chunk_states = _out(chunk_states, "chunk_states", mid, _F32, x, stream)
     args = head + (out.data_ptr(), None if last_state is None else last_state.data_ptr(), h0,
@@ -263,8 +265,9 @@ def _gated_bwd(x, rgate, igate, A, cu_seqlens, dout, z, rgate_bias, igate_bias, 
     for k in ("dx", "drgate", "digate", "dz"):
         g[k] = None if k == "dz" and z is None else _out(g.get(k), k, x.shape, dt, x, stream)
     for k in ("dA", "drgate_bias", "digate_bias"):
-        g[k] = _out(g.get(k), k, (dim,), _F32, x, stream)
-    g["dinitial_state"] = _out(g.get("dinitial_state"), "dinitial_state", (n, dim), _F32, x, stream)
+        g[k] = _out(g.get(k), k, (dim,), _F32, A, stream)
+    g["dinitial_state"] = _out(g.get("dinitial_state"), "dinitial_state", (n, dim), _F32,
+                               x if initial_state is None else initial_state, stream)
     args += tuple(None if g[k] is None else g[k].data_ptr()
                   for k in ("dx", "drgate", "digate", "dz", "dA", "drgate_bias", "digate_bias", "dinitial_state"))
     have = int(chunk_states is not None)
@@ -413,7 +416,7 @@ def ssm_qk_norm_rotate_bwd(q, k, inv_freq, dq_out, dk_out, q_weight=None, k_weig
     g["dq"] = _out(g.get("dq"), "dq", q.shape, q.dtype, q, stream)
     g["dk"] = None if k is None else _out(g.get("dk"), "dk", k.shape, q.dtype, q, stream)
     for n, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
-        g[n] = None if w is None else _out(g.get(n), n, (D,), _F32, q, stream)
+        g[n] = None if w is None else _out(g.get(n), n, (D,), _F32, w, stream)
     head += tuple(None if g[n] is None else g[n].data_ptr() for n in ("dq", "dk", "dq_weight", "dk_weight"))
     keep, ws, nbytes = _space(workspace, lib.ssm_qk_norm_rotate_bwd_workspace_bytes(batch, L, Hq, Hk, D), q, stream)
     _call(lib.ssm_qk_norm_rotate_bwd, q, stream, *head, *sizes, ws, nbytes)
@@ -450,10 +453,10 @@ def ssm_causal_conv1d_bwd(x, weight, dout, bias=None, initial_conv_state=None,
     stream = _other(stream, x)
     g = dict(grads or {})
     g["dx"] = _out(g.get("dx"), "dx", x.shape, dt, x, stream)
-    g["dweight"] = _out(g.get("dweight"), "dweight", (dim, W), _F32, x, stream)
-    g["dbias"] = None if bias is None else _out(g.get("dbias"), "dbias", (dim,), _F32, x, stream)
+    g["dweight"] = _out(g.get("dweight"), "dweight", (dim, W), _F32, weight, stream)
+    g["dbias"] = None if bias is None else _out(g.get("dbias"), "dbias", (dim,), _F32, bias, stream)
     g["dinitial_conv_state"] = None if initial_conv_state is None else \
-        _out(g.get("dinitial_conv_state"), "dinitial_conv_state", st, dt, x, stream)
+        _out(g.get("dinitial_conv_state"), "dinitial_conv_state", st, dt, initial_conv_state, stream)
     args += tuple(None if g[k] is None else g[k].data_ptr() for k in ("dx", "dweight", "dbias", "dinitial_conv_state"))
     keep, ws, nbytes = _space(workspace, lib.ssm_causal_conv1d_bwd_workspace_bytes(batch, L, dim, W), x, stream)
     _call(lib.ssm_causal_conv1d_bwd, x, stream, *args, batch, L, dim, W, int(bool(silu)), _DTYPES[dt], ws, nbytes)
