@@ -33,8 +33,11 @@ struct ConvBwdArgs {
 // Workgroups of a grid's row: neither extent times the threads passes 32 bits.
 constexpr uint32_t kConvGridX = 1u << 22;
 
-constexpr int kConvBwdT = 16;     // tokens of a wave
-constexpr int kConvBwdWaves = 8;  // waves of a workgroup, one stretch after the other
+// Tokens of a wave and waves of a workgroup, one stretch after the other.  The
+// layer of 4 x 2048 x 1536 bf16 and 3 x 1001 x 515 float32 (3 taps): 16 x 8 20.3
+// and 8.3 us, 32 x 4 21.4 and 10.1, 8 x 16 23.7 and 7.9, 16 x 16 26.8 and 9.2.
+constexpr int kConvBwdT = 16;
+constexpr int kConvBwdWaves = 8;
 constexpr int kConvBwdChunk = kConvBwdT * kConvBwdWaves;
 
 // V channels of one token: raw bits as loaded, widened at use (as in the
@@ -89,6 +92,9 @@ constexpr uint32_t kConvNoColumn = 0x7fffff00u;
 // waves' (found in cache).  All loads are issued before the first use.  The
 // sums over tokens stay in registers, are added over the workgroup's waves in
 // LDS and leave one row of partials per workgroup.
+// Two reads and one write of the activations bound it, with 69 vector
+// instructions per token and two channels (70% of the time) next to them:
+// 4 x 2048 x 1536 bf16, 4 taps, 20.3 us, 3.7 TB/s; 3 x 1001 x 515 float32 8.3 us.
 template <typename TA, int V, int W, bool SILU>
 __global__ void __launch_bounds__(64 * kConvBwdWaves) conv_bwd_kernel(ConvBwdArgs<TA> a) {
   constexpr int T = kConvBwdT, C = 64 * V, K = W - 1;
@@ -231,6 +237,7 @@ __global__ void __launch_bounds__(64 * kConvBwdWaves) conv_bwd_kernel(ConvBwdArg
 // Sums of the workgroups' partials: a workgroup takes 64 channels of one tap
 // (the last one the bias), wave w every kConvSumWaves-th row, and the waves'
 // sums are added in order.
+// 2 MB for 4 x 2048 x 1536: its launch and one round trip, 3.9 us.
 constexpr int kConvSumWaves = 8;
 __global__ void __launch_bounds__(64 * kConvSumWaves) conv_bwd_sum_kernel(const float* part, int64_t n, int dim,
                                                                           int W, float* dweight, float* dbias) {
@@ -366,7 +373,8 @@ int ssm_causal_conv1d_bwd(const void* x, const float* weight, const float* bias,
                       static_cast<TA*>(dinitial_conv_state), static_cast<float*>(workspace), batch,
                       seqlen, static_cast<int>(dim), 0, 0, 0};
     if constexpr (sizeof(TA) == 2) {
-      // two channels a lane where every row starts on four bytes
+      // two channels a lane where every row starts on four bytes (8 x 4096 x
+      // 5120: 197 us, one channel 212; 4 x 2048 x 1536: 20.3 and 19.6)
       if (dim % 2 == 0 && aligned(x, 4) && aligned(dout, 4) && aligned(dx, 4))
         return conv_bwd_launch<TA, 2>(a, static_cast<int>(width), silu != 0, dweight, dbias, stream);
     }

@@ -4,13 +4,18 @@
 //   a_t = e^(A sigma(r_t + rb)),  h_t = a_t h_{t-1} + m_t sigma(i_t + ib) x_t
 //   out_t = h_t silu(z_t)
 //
+// About 36 vector instructions per token and channel stand against 8 to 20
+// bytes, so memory bounds a long run (vector ALU busy 68% of the time at 131072
+// tokens) and latency a short one.
+//
 #include "gated.hpp"
 #include "host_util.hpp"
 
 namespace ssm {
 
 // Ones into the published words, zero into the counter; empty sequences'
-// states.  A grid-stride loop over each.
+// states.  A grid-stride loop over each; a launch (2 to 5 us) more than work
+// (0.4 MB for 4 x 2048 x 1536).
 __global__ void __launch_bounds__(256) gated_init_kernel(uint64_t* words, int64_t nwords,
                                                          uint32_t* turn, const int32_t* cu,
                                                          int64_t nstates, int dim,
@@ -40,12 +45,14 @@ int launch_gated_init(void* ws, size_t bytes, const int32_t* cu, int64_t nseq, i
 }
 
 // Tokens of a lane, waves of a workgroup, rows of the inputs a wave has in
-// flight (a ring of registers, filled again as it is used up), waves a SIMD
-// holds.
-struct FwdLong {  // few folds per token, the whole device resident: throughput
+// flight (batch * ring: a ring of registers, filled again as it is used up),
+// waves a SIMD holds.
+struct FwdLong {  // few folds per token, 3 workgroups to a CU: throughput
+  // (4 x 2048 x 1536 bf16: 36 us; T 32 with z fetched before the wait 45)
   static constexpr int T = 64, W = 4, batch = 4, ring = 2, occupancy = 3;
 };
 struct FwdShort {  // every load issued at once: the latency of few workgroups
+  // (8192 x 1001 float32: 41 us; half as many waves 46, T 8 47)
   static constexpr int T = 16, W = 16, batch = 4, ring = 4, occupancy = 4;
 };
 
@@ -59,6 +66,13 @@ struct FwdShort {  // every load issued at once: the latency of few workgroups
 // folds have a fixed order, so results repeat bit for bit.
 // Units are handed out by a counter, earlier chunks first: a workgroup waits
 // only for ones that are running or done.
+// Reading the data once is what the split is for: chunk maps in a launch of
+// their own would read x and both gates twice (7 units of traffic for 5).
+// Measured (kernel alone): 1 x 131072 x 2048 bf16 447 us, 4.8 TB/s of the
+// algorithm's bytes (copies of the same size reach 4.9 to 6.1); 4 x 2048 x 1536
+// bf16 with z 36 us, 3.4 TB/s; packed 8192 x 1001 float32 with z 41 us, 4.0
+// TB/s; packed 3001 x 515 float32 16 us, the chain ticket -> loads -> publish ->
+// wait -> stores of one round of workgroups.
 template <typename TA, typename CF, bool NORM, bool GATE, bool VL>
 __global__ void __launch_bounds__(64 * CF::W, CF::occupancy) gated_fwd_kernel(GatedFwdArgs<TA> p, GatedPlan pl) {
   constexpr int T = CF::T, W = CF::W, C = kGatedC, NB = CF::batch, R = CF::ring, kPolls = kGatedGroup / W;
@@ -300,8 +314,10 @@ struct GatedStepArgs {
   int dim;
 };
 
-// V neighbouring channels of one sequence per lane, each array moved as one
-// access.
+// One step: h <- a h + m u x, out = h silu(z).  V neighbouring channels of one
+// sequence per lane, each array moved as one access.  Bound by memory where
+// there is enough of it (256 x 5120 float32: 36.7 MB in 8.0 us, 4.6 TB/s),
+// otherwise by its launch (1 x 2048 bf16: 2.5 us).
 template <typename T, int V>
 struct alignas(V * sizeof(T)) Pack {
   T v[V];
@@ -364,9 +380,10 @@ int run_gated_fwd(const char* fn, const void* x, const void* r, const void* i, c
                            static_cast<const TA*>(z), A, rb, ib, static_cast<TA*>(out), last, h0, states, cu,
                            rows, L, nseq, dim, ws};
   // Long stretches where they give every CU more than two workgroups (768 of
-  // them: 36 against 45 us); below, a lane that goes through its tokens in
-  // rounds of loads takes longer than the device is kept busy by them (512:
-  // 54 against 46 us; 108: 25 against 13 us).
+  // them, 4 x 2048 x 1536 bf16: 36 against 45 us); below, a lane that goes
+  // through its tokens in rounds of loads takes longer than the device is kept
+  // busy by them (512, 8192 x 1001 float32: 54 against 41 us; 108, 3001 x 515
+  // float32: 25 against 16 us).
   return fwd_plan<FwdLong>(rows, L, dim).units > 2u * static_cast<unsigned>(device_cus())
              ? launch_gated_fwd<TA, FwdLong>(a, norm, fn, stream)
              : launch_gated_fwd<TA, FwdShort>(a, norm, fn, stream);

@@ -5,6 +5,8 @@
 //   n = v rstd w, rstd = 1 / sqrt(mean(v^2) + eps); pairs (p, q) of n turn by
 //   theta = position * inv_freq.  Backward, with g the gradient turned back:
 //   dv = rstd (g w - vhat mean(g w vhat)), vhat = v rstd;  dw = sum g vhat.
+// One read and one write of every value: memory bounds it, then the latency of
+// a head's sums.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -65,7 +67,9 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // Head sizes and alignments that no vector access fits: one wave per row
-// (token, head); lane l holds elements l, l + 64, ...
+// (token, head); lane l holds elements l, l + 64, ...  Every lane forms its own
+// sines, for every head again (16 heads of 128, 8192 tokens, bf16: 62 us where
+// the vector kernel takes 12.5): alignment's slow path, not a choice.
 template <typename TA, bool INTER, bool BWD>
 __global__ void __launch_bounds__(64 * kRotWaves) rotate_any_kernel(RotArgs<TA> p) {
   const int lane = threadIdx.x & 63;
@@ -142,7 +146,7 @@ __global__ void __launch_bounds__(64 * kRotWaves) rotate_any_kernel(RotArgs<TA> 
   }
 }
 
-// E values moved as one access of 4, 8 or 16 bytes.
+// E values moved as one access of 4 (bf16), 8 or 16 bytes.
 template <typename TA, int E>
 struct RotVec;
 template <int E>
@@ -200,6 +204,10 @@ __device__ __forceinline__ float row_sum(float v) {
 // So a rotation needs no other lane, and a row takes N = D / (2 E) lanes,
 // rounded up to a power of two; a wave holds 64 / N tokens and goes through
 // their heads, forming the sines and cosines once per token.
+// Measured (kernel alone): 8192 tokens of 8 + 8 heads of 128 bf16 12.5 us, 5.4
+// TB/s; 256 tokens of 1 + 1 heads of 64 3.3 us, a launch and three round trips.
+// Gradients: 4002 tokens of 16 + 4 heads of 128 bf16 13.4 us, 4.6 TB/s (rows in
+// flight: 2 here; 4 14.1 us).
 template <typename TA, int E, int N, bool INTER, bool BWD>
 __global__ void __launch_bounds__(64 * kRotWaves) rotate_kernel(RotArgs<TA> p, int head_step) {
   using IO = RotVec<TA, E>;
@@ -360,6 +368,7 @@ __global__ void __launch_bounds__(64 * kRotWaves) rotate_kernel(RotArgs<TA> p, i
 // Sum of the partial weight gradients: a workgroup takes 16 elements of one of
 // the two; wave w and lane quarter t take every 64th row from 4 w + t on, and
 // the quarters' and the waves' sums are added in order.
+// At most 1024 rows of 1 KB (heads of 128): its launch and two round trips, 4.9 us.
 constexpr int kRotSumWaves = 16, kRotSumElems = 16;
 __global__ void __launch_bounds__(64 * kRotSumWaves) rotate_sum_kernel(const float* part, int n, int D, float* dqw,
                                                                        float* dkw) {
@@ -396,8 +405,11 @@ bool rot_sizes_ok(int64_t batch, int64_t L, int64_t Hq, int64_t Hk, int64_t D) {
 
 // Rows of partial weight gradients the backward may leave at most: as many as
 // there are waves (any layout) or workgroups (vectors), bounded so that their
-// sum stays short.
-constexpr int64_t kRotMaxParts = 512;
+// sum stays short (2048: 14.8 + 6.0 us for the 4002 tokens where 1024 take 13.4
+// + 4.9).  Half as many workgroups with four values an access, whose waves hold
+// twice the rows (8192 tokens of 16 + 16 heads of 128 float32: 70 us, with all
+// of them 74).
+constexpr int64_t kRotMaxParts = 1024;
 // Workgroups of a forward up to which its heads are spread over more of them
 // (twice as many measured 5% slower: the sines are formed once more).
 constexpr int64_t kRotFwdBlocks = 512;
@@ -435,7 +447,7 @@ void rot_launch_vec(const RotCall& c, const RotArgs<TA>& a, int64_t* parts) {
   int64_t x = (groups + kRotWaves - 1) / kRotWaves;
   x = x < 1 ? 1 : x;
   int step = heads;
-  const int64_t most = c.bwd ? rot_parts(a.tokens * heads) : int64_t{1} << 20;
+  const int64_t most = c.bwd ? (rot_parts(a.tokens * heads) + E / 2 - 1) / (E / 2) : int64_t{1} << 20;
   const int64_t enough = c.bwd ? most : kRotFwdBlocks;
   while (step > 1 && x * ((heads + step - 1) / step) * 2 <= enough) step = (step + 1) / 2;
   const int64_t y = (heads + step - 1) / step;
@@ -456,7 +468,7 @@ void rot_launch_vec(const RotCall& c, const RotArgs<TA>& a, int64_t* parts) {
 template <typename TA>
 bool rot_fits(const RotCall& c, int E) {
   const size_t bytes = E * sizeof(TA);
-  if (c.D % (2 * E) || c.R % (2 * E) || c.D / (2 * E) > 64) return false;
+  if (c.D % (2 * E) || c.R % (2 * E)) return false;
   if (c.qs % E || !aligned(c.q, bytes) || !aligned(c.qo, bytes) || (c.bwd && !aligned(c.dqo, bytes))) return false;
   return !c.Hk || (c.ks % E == 0 && aligned(c.k, bytes) && aligned(c.ko, bytes) && (!c.bwd || aligned(c.dko, bytes)));
 }
@@ -468,8 +480,10 @@ bool rot_try(const RotCall& c, const RotArgs<TA>& a, int64_t* parts) {
   if (lanes <= 4) rot_launch_vec<TA, E, 4>(c, a, parts);
   else if (lanes <= 8) rot_launch_vec<TA, E, 8>(c, a, parts);
   else if (lanes <= 16) rot_launch_vec<TA, E, 16>(c, a, parts);
-  else if (lanes <= 32) rot_launch_vec<TA, E, 32>(c, a, parts);
-  else rot_launch_vec<TA, E, 64>(c, a, parts);
+  if constexpr (E == 2) {
+    if (lanes > 32) rot_launch_vec<TA, E, 64>(c, a, parts);
+    else if (lanes > 16) rot_launch_vec<TA, E, 32>(c, a, parts);
+  }
   return true;
 }
 
@@ -480,11 +494,14 @@ int rot_launch(const RotCall& c) {
                 static_cast<TA*>(c.ko), static_cast<float*>(c.ws), c.eps, c.batch * c.L, c.L, c.qs,
                 c.ks, static_cast<int>(c.Hq), static_cast<int>(c.Hk), static_cast<int>(c.D),
                 static_cast<int>(c.R)};
-  // four values an access where the head size, the strides and the addresses
-  // allow it (8 measured 10-20% slower for bf16: fewer waves), or two
-  constexpr int E = 4;
+  // Two values an access where the head size, the strides and the addresses
+  // allow it, four of float32 up to 128 of them in a head.  8192 tokens,
+  // gradients with two | four: 16 + 16 heads of 128 float32 75 | 70 us, 8 + 8 of
+  // 256 68 | 78, 4002 tokens of 16 + 4 of 128 bf16 13.4 | 16.8 (half the waves);
+  // forward 47 | 45, 40 | 43, 12.5 | 13.8 (8 + 8 of 128 bf16).
   int64_t parts = 0;
-  if (!rot_try<TA, E>(c, a, &parts) && !rot_try<TA, E / 2>(c, a, &parts)) {
+  const bool four = sizeof(TA) == 4 && c.D <= 128;
+  if (!(four && rot_try<TA, 4>(c, a, &parts)) && !rot_try<TA, 2>(c, a, &parts)) {
     const int64_t rows = c.batch * c.L * (c.Hq + c.Hk);
     const int64_t want = (rows + kRotWaves - 1) / kRotWaves;
     const int64_t blocks = c.bwd ? rot_parts(rows) / kRotWaves : want > (1 << 20) ? (1 << 20) : want;
@@ -500,8 +517,8 @@ int rot_launch(const RotCall& c) {
 #undef SSM_ROT_CASE
   }
   if (c.bwd && (c.dqw || c.dkw))
-    hipLaunchKernelGGL(rotate_sum_kernel, dim3((a.D + kRotSumElems - 1) / kRotSumElems, 2), dim3(64 * kRotSumWaves), 0, c.stream, a.part,
-                       static_cast<int>(parts), a.D, c.dqw, c.dkw);
+    hipLaunchKernelGGL(rotate_sum_kernel, dim3((a.D + kRotSumElems - 1) / kRotSumElems, 2), dim3(64 * kRotSumWaves),
+                       0, c.stream, a.part, static_cast<int>(parts), a.D, c.dqw, c.dkw);
   return launch_status(c.fn);
 }
 
