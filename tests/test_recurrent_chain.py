@@ -116,3 +116,29 @@ def test_rotated_keys_and_queries_feed_the_ssd():
         acc = acc * np.exp(dt[:, t] * s.A.cpu().numpy())[..., None] + dt[:, t][..., None] * x[:, t]
         lim[:, t] = acc
     within(a, c, 2 * (2 * u * np.abs(ref) + 2 * u * (E1 + E2) * gate) + 2 * u * w * lim * gate + 1e-6, "moved")
+
+
+def test_one_tensor_as_several_inputs():
+    """Inputs may be the same tensor: the results are those of copies."""
+    g = torch.Generator(device=DEV).manual_seed(77)
+    x = torch.randn(2, 300, 70, generator=g, device=DEV)
+    A, b, h = -torch.rand(70, generator=g, device=DEV), x[0, 0].clone(), x[:, 0].contiguous()
+    one = lambda t: t
+    two = lambda t: t.clone()
+    res = []
+    for c in (one, two):
+        out, last, mid = pkg.ssm_gated_scan_fwd(c(x), c(x), c(x), A, z=c(x), rgate_bias=c(b), igate_bias=c(b),
+                                                initial_state=c(h), return_last_state=True, return_chunk_states=True)
+        grads = pkg.ssm_gated_scan_bwd(c(x), c(x), c(x), A, c(x), z=c(x), rgate_bias=c(b), igate_bias=c(b),
+                                       initial_state=c(h), dlast_state=c(h), chunk_states=mid)
+        state = h.clone()
+        y = pkg.ssm_gated_state_update(state, c(h), c(h), c(h), A, z=c(h), rgate_bias=c(b), igate_bias=c(b))
+        q = x.view(2, 300, 5, 14)
+        qo, ko = pkg.ssm_qk_norm_rotate_fwd(c(q), c(q), b[:7].abs(), b[:14], b[:14])
+        rg = pkg.ssm_qk_norm_rotate_bwd(c(q), c(q), b[:7].abs(), c(q), c(q), b[:14], b[:14])
+        cw = x.reshape(-1)[:280].view(70, 4)
+        cs = x.reshape(-1)[:420].view(2, 70, 3)
+        cg = pkg.ssm_causal_conv1d_bwd(c(x), cw, c(x), bias=c(b), initial_conv_state=c(cs), dfinal_conv_state=c(cs))
+        res.append([out, last, mid, state, y, qo, ko] + [d[k] for d in (grads, rg, cg) for k in sorted(d)])
+    assert all(torch.equal(u, v) for u, v in zip(*res))
+    assert torch.equal(res[0][5], res[0][6])
