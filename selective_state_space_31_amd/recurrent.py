@@ -63,7 +63,8 @@ def _load():
 # the current stream's handle of a device index, without building a Stream object where torch lets one
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
-_F32 = torch.float32
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_F32, _Tensor, _empty_like = torch.float32, torch.Tensor, torch.empty_like
 
 
 def _act(x, name="x"):
@@ -77,7 +78,7 @@ def _act(x, name="x"):
 def _in(t, name, shape, dtype, like):
     """The address of input ``t``, which has to have this shape and type and
     be contiguous on ``like``'s device (``ops._check`` says what is wrong)."""
-    if not (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape
+    if not (type(t) is _Tensor and t.dtype is dtype and t.shape == shape
             and t.get_device() == like.get_device() and t.is_contiguous()):
         _check(t, name, shape, dtype, like.device)
     return t.data_ptr()
@@ -90,18 +91,20 @@ def _opt(t, name, shape, dtype, like):
 
 
 def _new(like, shape, dtype, stream):
-    """A new tensor for a call on ``stream`` (None: the current one).  ``like``
-    is on the device, and where there is one it has this shape and type."""
+    """A new tensor for a call on ``stream`` (None: the current one), on
+    ``like``'s device; ``shape`` may be ``like`` itself (its shape and type)."""
     if stream is None:
         # (empty_like is the quickest; it would keep the strides of a slice)
-        if dtype is like.dtype and shape == like.shape and like.is_contiguous():
-            return torch.empty_like(like)
+        if (shape is like or (dtype is like.dtype and shape == like.shape)) and like.is_contiguous():
+            return _empty_like(like)
+        if shape is like:
+            shape = like.shape
         return like.new_empty(shape, dtype=dtype)
     # On another stream the memory has to come from that stream's pool: a block
     # of the current stream may still be in use by work queued there.  The
     # caller will read it from the current stream, which the pool has to know.
     with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=like.device)):
-        t = like.new_empty(shape, dtype=dtype)
+        t = like.new_empty(like.shape if shape is like else shape, dtype=dtype)
     t.record_stream(torch.cuda.current_stream(like.device))
     return t
 
@@ -110,7 +113,7 @@ def _out(t, name, shape, dtype, like, stream):
     """The output buffer ``t``, checked, or a new one."""
     if t is None:
         return _new(like, shape, dtype, stream)
-    _in(t, name, shape, dtype, like)
+    _in(t, name, like.shape if shape is like else shape, dtype, like)
     return t
 
 
@@ -140,7 +143,7 @@ def _call(fn, like, stream, *args):
     index = like.get_device()
     if stream is None:
         stream = _raw_stream(index)
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         rc = fn(*args, stream)
     else:
         with torch.cuda.device(index):
@@ -207,7 +210,7 @@ def _gated_fwd(x, rgate, igate, A, cu_seqlens, z, rgate_bias, igate_bias, normal
     dt, n, L, dim, mid, head, h0, cu = _gated_inputs(x, rgate, igate, A, z, rgate_bias, igate_bias, normalize,
                                                      initial_state, cu_seqlens)
     stream, code = _other(stream, x), _DTYPES[dt]
-    out = _out(out, "out", x.shape, dt, x, stream)
+    out = _out(out, "out", x, dt, x, stream)
     if return_last_state or last_state is not None:
         last_state = _out(last_state, "last_state", (n, dim), _F32, x if initial_state is None else initial_state,
                           stream)
@@ -263,7 +266,7 @@ def _gated_bwd(x, rgate, igate, A, cu_seqlens, dout, z, rgate_bias, igate_bias, 
                    _opt(dlast_state, "dlast_state", (n, dim), _F32, x))
     g = dict(grads or {})
     for k in ("dx", "drgate", "digate", "dz"):
-        g[k] = None if k == "dz" and z is None else _out(g.get(k), k, x.shape, dt, x, stream)
+        g[k] = None if k == "dz" and z is None else _out(g.get(k), k, x, dt, x, stream)
     for k in ("dA", "drgate_bias", "digate_bias"):
         g[k] = _out(g.get(k), k, (dim,), _F32, A, stream)
     g["dinitial_state"] = _out(g.get("dinitial_state"), "dinitial_state", (n, dim), _F32,
@@ -321,7 +324,7 @@ def ssm_gated_state_update(state, x, rgate, igate, A, z=None, rgate_bias=None, i
             _opt(rgate_bias, "rgate_bias", (dim,), _F32, x), _opt(igate_bias, "igate_bias", (dim,), _F32, x),
             int(bool(normalize)), _opt(z, "z", shape, dt, x))
     stream = _other(stream, x)
-    out = _out(out, "out", shape, dt, x, stream)
+    out = _out(out, "out", x, dt, x, stream)
     _call(lib.ssm_gated_state_update, x, stream, *args, out.data_ptr(), batch, dim, _DTYPES[dt])
     return out
 
@@ -340,6 +343,8 @@ def _heads(t, name, batch, L, D, like):
     if t.get_device() != like.get_device():
         raise ValueError("%s is on %s, expected %s" % (name, t.device, like.device))
     H = t.shape[2]
+    if t.is_contiguous():
+        return H, H * D
     sb, sl, sh, sd = t.stride()
     if L > 1:
         step = sl
@@ -385,9 +390,9 @@ def ssm_qk_norm_rotate_fwd(q, k, inv_freq, q_weight=None, k_weight=None, positio
     if k is None and (k_out is not None or k_weight is not None):
         raise ValueError("k_out or k_weight given without k")
     stream = _other(stream, q)
-    q_out = _out(q_out, "q_out", q.shape, q.dtype, q, stream)
+    q_out = _out(q_out, "q_out", q, q.dtype, q, stream)
     if k is not None:
-        k_out = _out(k_out, "k_out", k.shape, q.dtype, q, stream)
+        k_out = _out(k_out, "k_out", k, q.dtype, k, stream)
     _call(lib.ssm_qk_norm_rotate_fwd, q, stream, *head, q_out.data_ptr(),
           None if k is None else k_out.data_ptr(), *sizes)
     return q_out, k_out
@@ -413,8 +418,8 @@ def ssm_qk_norm_rotate_bwd(q, k, inv_freq, dq_out, dk_out, q_weight=None, k_weig
              None if k is None else _in(dk_out, "dk_out", k.shape, q.dtype, q))
     stream = _other(stream, q)
     g = dict(grads or {})
-    g["dq"] = _out(g.get("dq"), "dq", q.shape, q.dtype, q, stream)
-    g["dk"] = None if k is None else _out(g.get("dk"), "dk", k.shape, q.dtype, q, stream)
+    g["dq"] = _out(g.get("dq"), "dq", q, q.dtype, q, stream)
+    g["dk"] = None if k is None else _out(g.get("dk"), "dk", k, q.dtype, k, stream)
     for n, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
         g[n] = None if w is None else _out(g.get(n), n, (D,), _F32, w, stream)
     head += tuple(None if g[n] is None else g[n].data_ptr() for n in ("dq", "dk", "dq_weight", "dk_weight"))
@@ -452,7 +457,7 @@ def ssm_causal_conv1d_bwd(x, weight, dout, bias=None, initial_conv_state=None,
             _opt(dfinal_conv_state, "dfinal_conv_state", st, dt, x))
     stream = _other(stream, x)
     g = dict(grads or {})
-    g["dx"] = _out(g.get("dx"), "dx", x.shape, dt, x, stream)
+    g["dx"] = _out(g.get("dx"), "dx", x, dt, x, stream)
     g["dweight"] = _out(g.get("dweight"), "dweight", (dim, W), _F32, weight, stream)
     g["dbias"] = None if bias is None else _out(g.get("dbias"), "dbias", (dim,), _F32, bias, stream)
     g["dinitial_conv_state"] = None if initial_conv_state is None else \
