@@ -76,3 +76,61 @@ def test_conv1d_gradients_past_32_bits():
     g2 = pkg.ssm_causal_conv1d_bwd(x[:, t0:].contiguous(), w, dout[:, t0:].contiguous(), bias=bias,
                                    initial_conv_state=before)
     assert torch.equal(g["dx"][:, t0:], g2["dx"])
+
+
+def test_largest_dim():
+    """dim = 2^22: a wave's rows span the most bytes that are allowed.  Each
+    end of the channels against a call on those channels alone."""
+    dim, n, tok = 1 << 22, 70, 100
+    g = torch.Generator(device=DEV).manual_seed(8)
+    new = lambda *s: torch.empty(s, device=DEV).normal_(generator=g)
+    x, r, i, dout = (new(1, tok, dim) for _ in range(4))
+    A, h0 = -torch.rand(dim, device=DEV, generator=g), new(1, dim)
+    out, last = pkg.ssm_gated_scan_fwd(x, r, i, A, z=dout, initial_state=h0, return_last_state=True)
+    grads = pkg.ssm_gated_scan_bwd(x, r, i, A, dout, z=r, initial_state=h0)
+    w = new(dim, 4)
+    conv = pkg.ssm_causal_conv1d_bwd(x, w, dout, bias=A)
+    for s in (slice(0, n), slice(dim - n, dim)):
+        c = lambda t: t[..., s].contiguous()
+        o2, l2 = pkg.ssm_gated_scan_fwd(c(x), c(r), c(i), c(A), z=c(dout), initial_state=c(h0), return_last_state=True)
+        g2 = pkg.ssm_gated_scan_bwd(c(x), c(r), c(i), c(A), c(dout), z=c(r), initial_state=c(h0))
+        c2 = pkg.ssm_causal_conv1d_bwd(c(x), w[s].contiguous(), c(dout), bias=c(A))
+        # two foldings of 100 tokens: each value within 100 roundings of the largest there
+        close = lambda a, b: torch.testing.assert_close(a, b, rtol=0, atol=200 * 2.0 ** -24 * float(b.abs().max()))
+        close(out[..., s], o2)
+        close(last[..., s], l2)
+        for k in g2:
+            close(grads[k][..., s], g2[k])
+        assert torch.equal(conv["dx"][..., s], c2["dx"])
+        assert torch.equal(conv["dweight"][s], c2["dweight"]) and torch.equal(conv["dbias"][s], c2["dbias"])
+
+
+def test_largest_step():
+    batch, dim = 1023, 1 << 21  # just below the limit of 2^31 - 2048
+    x, r, i = (act(9 + k, batch, dim) for k in range(3))
+    A = -torch.linspace(0.05, 3.0, dim, device=DEV)
+    state = torch.ones(batch, dim, device=DEV)
+    row = state[-1:].clone()
+    out = pkg.ssm_gated_state_update(state, x, r, i, A)
+    ref = pkg.ssm_gated_state_update(row, x[-1:].contiguous(), r[-1:].contiguous(), i[-1:].contiguous(), A)
+    assert torch.equal(out[-1:], ref) and torch.equal(state[-1:], row)
+
+
+def test_packed_offsets_up_to_int32():
+    """One channel, sequences that end just below the largest offset."""
+    total, cut = 2 ** 31 - 1000, 2 ** 31 - 7001
+    x, r, i = (act(20 + k, total, 1) for k in range(3))
+    A = torch.full((1,), -0.5, device=DEV)
+    cu = torch.tensor([0, 5, cut, cut, total], dtype=torch.int32, device=DEV)
+    out, last = pkg.ssm_gated_scan_fwd_varlen(x, r, i, A, cu, return_last_state=True)
+    end = [v[cut:].contiguous() for v in (x, r, i)]
+    o2, l2 = pkg.ssm_gated_scan_fwd_varlen(*end, A, torch.tensor([0, total - cut], dtype=torch.int32, device=DEV),
+                                           return_last_state=True)
+    near(out[cut:], o2)
+    torch.testing.assert_close(last[3], l2[0], rtol=1e-5, atol=1e-5)
+    assert last[2] == 0 and bool(torch.isfinite(last).all()) and bool(torch.isfinite(out[cut - 100:]).all())
+    # the long sequence's end: decays around 0.78 leave nothing of what is 3000 tokens back
+    o3, l3 = pkg.ssm_gated_scan_fwd_varlen(*(v[cut - 5000:cut].contiguous() for v in (x, r, i)), A,
+                                           torch.tensor([0, 5000], dtype=torch.int32, device=DEV), return_last_state=True)
+    near(out[cut - 2000:cut], o3[-2000:])
+    torch.testing.assert_close(last[1], l3[0], rtol=1e-5, atol=1e-5)
