@@ -59,6 +59,9 @@ extern "C" {
  *   < 2^31 (SSM_ERR_SHAPE beyond).
  *   workspace         : at least ssm_gated_scan_fwd_workspace_bytes(...) bytes
  * Bitwise reproducible run to run on one device.
+ * An infinite state or input gives an infinite state from there on (NaN where
+ * infinities of both signs meet; where a decay rounds to 0, below about
+ * 2^-126, infinite or NaN).
  */
 int ssm_gated_scan_fwd(const void* x, const void* rgate, const void* igate, const float* A,
                        const float* rgate_bias, const float* igate_bias, int normalize,
@@ -120,6 +123,10 @@ size_t ssm_gated_scan_fwd_varlen_workspace_bytes(int64_t nseq, int64_t total_len
  * Where 1 - a_t^2 is below 2^-126 (normalize, and a gate closed that far, or
  * A >= 0) the gradients take m_t as 0, and the term that divides by m_t too,
  * its limit for a closing gate.  A decay of 0 (A = -infinity) has no slope.
+ * An infinite dout or dlast_state gives infinite gradients at the tokens before
+ * it, as infinite states do behind it.  Where a state is infinite, drgate and
+ * dz (and the sums over such tokens) are not finite; dx, digate and
+ * dinitial_state do not depend on the states.
  * Sums over tokens and sequences are formed in a fixed order from float32
  * partials: bitwise reproducible run to run on one device.
  */

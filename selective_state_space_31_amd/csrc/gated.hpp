@@ -125,9 +125,13 @@ __device__ __forceinline__ float keep_of(float S) {
   const float E = decay_parts(S, a);
   return E < 0.5f && E >= 0.0f ? -__builtin_fabsf(E) : a;
 }
+// An infinite h stays infinite (no decay is 0 in exact arithmetic), also where
+// P is the identity or underflows, whose products with it would be NaN: looked
+// at only where the result is not finite.
 template <bool VL>
 __device__ __forceinline__ float pass(float y, float H, float h) {
-  const float r = __builtin_fmaf(y, h, below_one(y) ? h : 0.0f) + H;
+  float r = __builtin_fmaf(y, h, below_one(y) ? h : 0.0f) + H;
+  if (!__builtin_isfinite(r) && __builtin_isinf(h)) r = h + H;
   if constexpr (VL) return y == kCut ? H : r;
   return r;
 }
