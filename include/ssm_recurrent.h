@@ -46,7 +46,9 @@ extern "C" {
  * variance whatever the gate) and m_t = 1 when it is 0.
  *   x, rgate, igate, z, out : (batch, seqlen, dim) act; z may be NULL
  *   A                 : (dim) float32, A <= 0: the log of the smallest decay.
- *                       (A > 0 grows; with normalize its m_t is 0.)
+ *                       (A > 0, up to 88, grows; with normalize its m_t is 0.
+ *                       A state that passes float32's range is infinite or
+ *                       NaN from there on.)
  *   rgate_bias, igate_bias : (dim) float32 or NULL (= 0)
  *   initial_state     : (batch, dim) float32 or NULL (= zeros)
  *   last_state        : (batch, dim) float32 or NULL; h after the last token.

@@ -113,17 +113,28 @@ constexpr uint32_t kNoColumn = 0x7fffff00u;
 // to 1 loses the same way at every factor when it is rounded (1 - p)(1 - e) ->
 // 1 - p - e, which a memory of thousands of tokens shows (1.1e-5 at 6000
 // tokens with decays of 1 - 1e-5 to 1 - 1e-3, against 1e-6 in this form).
+// y below kCut is -P^(1/4), for P from 2^64 on (a growing state, A > 0; P <= 1
+// otherwise): a product beyond float32 acts on a state factor by factor, so
+// that only states that are themselves beyond float32 overflow.  Past 2^508,
+// where any state but 0 does, it stays at the largest float, and 0 stays 0.
 // kCut: a sequence starts inside the stretch, nothing of the incoming state
 // passes; it is left out rather than multiplied by zero, so that a NaN or an
 // infinity stays in its own sequence.
 constexpr float kCut = -2.0f;
 __device__ __forceinline__ bool below_one(float y) { return __float_as_int(y) < 0; }
 
+constexpr float kMaxRoot = 0x1.fffffep127f;
+
 // y of a stretch whose v add up to S (the identity for 0).
 __device__ __forceinline__ float keep_of(float S) {
   float a;
   const float E = decay_parts(S, a);
-  return E < 0.5f && E >= 0.0f ? -__builtin_fabsf(E) : a;
+  const float y = E < 0.5f && E >= 0.0f ? -__builtin_fabsf(E) : a;
+  return S < -64.0f ? -__builtin_fminf(__builtin_amdgcn_exp2f(-0.25f * S), kMaxRoot) : y;
+}
+// P^(1/4) of a y that is no cut.
+__device__ __forceinline__ float root_of(float y) {
+  return y < kCut ? -y : __builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(below_one(y) ? 1.0f + y : y));
 }
 // An infinite h stays infinite (no decay is 0 in exact arithmetic), also where
 // P is the identity or underflows, whose products with it would be NaN: looked
@@ -131,7 +142,10 @@ __device__ __forceinline__ float keep_of(float S) {
 template <bool VL>
 __device__ __forceinline__ float pass(float y, float H, float h) {
   float r = __builtin_fmaf(y, h, below_one(y) ? h : 0.0f) + H;
-  if (!__builtin_isfinite(r) && __builtin_isinf(h)) r = h + H;
+  if (y < kCut)
+    r = h * -y * -y * -y * -y + H;
+  else if (!__builtin_isfinite(r) && __builtin_isinf(h))
+    r = h + H;
   if constexpr (VL) return y == kCut ? H : r;
   return r;
 }
@@ -143,6 +157,7 @@ __device__ __forceinline__ void compose(float& y1, float& H1, float y2, float H2
   const float both = __builtin_fmaf(y1, y2, y1) + y2;  // (1 + y1)(1 + y2) - 1
   float y = n1 ? (n2 ? (both >= -0.5f ? -__builtin_fabsf(both) : 1.0f + both) : __builtin_fmaf(y1, y2, y2))
                : __builtin_fmaf(y1, y2, n2 ? y1 : 0.0f);
+  if (y > 0x1p64f || y1 < kCut || y2 < kCut) y = -__builtin_fminf(root_of(y1) * root_of(y2), kMaxRoot);
   if constexpr (VL) {
     if (y1 == kCut || y2 == kCut) y = kCut;
   }

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 4) gated_bwd_kernel(GatedBwdAr
           const float M = input_scale2(E);
           const float inv = M >= 0x1p-126f ? __builtin_amdgcn_rsqf(M) : 0.0f;  // (subnormals have no rsq)
           m = M * inv;
-          sub = u * x * (a[j] * a[j] * inv);
+          sub = u * x * (a[j] * inv * a[j]);  // (a^2 alone may overflow where A > 0)
         }
         if (VL && (mk.starts >> j & 1))
           h = p.h0 && have ? p.h0[static_cast<int64_t>(__builtin_amdgcn_readlane(mk.seq, j)) * dim + col] : 0.0f;
