@@ -26,13 +26,14 @@ __device__ __forceinline__ float sigmoid_f32(float v) { return sigmoid2(v * -kLo
 // rounds low on average, which a memory of thousands of tokens adds up), and
 // m = sqrt(1 - a^2) = sqrt(E (2 - E)) loses nothing to cancellation.  q(v) =
 // (1 - 2^-v) / v as a cubic fitted at Chebyshev points of [0, 3/16], within
-// 4.1e-8 of it.  Beyond, a <= 0.879 and E = 1 - a is exact enough.
+// 4.1e-8 of it there and nowhere else (7e-6 at -3/16).  Above, a <= 0.879 and
+// E = 1 - a is exact enough; below 0 (growing states) m is 0 and only a counts.
 __device__ __forceinline__ float decay_parts(float v, float& a) {
   const float ex = __builtin_amdgcn_exp2f(-v);
   float q = __builtin_fmaf(v, -0.009133012033998966f, 0.055447835475206375f);
   q = __builtin_fmaf(v, q, -0.24022440612316132f);
   q = __builtin_fmaf(v, q, 0.6931471824645996f);
-  const bool near = __builtin_fabsf(v) < 0.1875f;
+  const bool near = __float_as_uint(v) < __float_as_uint(0.1875f);  // (0 <= v < 3/16: a sign or a NaN compares above)
   // both sides are computed and one is selected: left to itself the compiler
   // branches around each side, and the tokens no longer overlap
   float En = v * q, Ef = 1.0f - ex, an = 1.0f - En;
