@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(64 * CF::W, CF::occupancy) gated_fwd_kernel(Ga
           a[j] = 1.0f;
           b[j] = 0.0f;
         }
-        if (start && p.h0 && have) b[j] = __builtin_fmaf(a[j], p.h0[s * dim + col], b[j]);
+        // (without an initial state a * 0, so that a NaN gate counts as it does in a whole sequence)
+        if (start) b[j] = __builtin_fmaf(a[j], p.h0 && have ? p.h0[s * dim + col] : 0.0f, b[j]);
         H = start ? b[j] : __builtin_fmaf(a[j], H, b[j]);
       }
     }
