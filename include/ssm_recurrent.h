@@ -197,8 +197,8 @@ int ssm_gated_state_update(float* state, const void* x, const void* rgate, const
  *   at most 65536 heads each.
  * mean(v^2) + eps is a float32: rows where it is below 2^-126 (eps = 0 alone
  * allows it) or where a sum of squares overflows give unspecified values.
- * The angle is formed and reduced in float64, so far positions lose nothing;
- * its sine and cosine are float32 (within 2^-23).
+ * The angle is formed and reduced in two parts of float64, so no position loses
+ * anything; its sine and cosine are float32 (within 2^-23).
  */
 int ssm_qk_norm_rotate_fwd(const void* q, const void* k, const float* q_weight,
                            const float* k_weight, const float* inv_freq, const int32_t* positions,

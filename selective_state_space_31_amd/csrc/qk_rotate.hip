@@ -18,13 +18,19 @@
 
 namespace ssm {
 
-// sin and cos of pos * freq.  The product is exact to 2^-53 in float64 (31 and
-// 24 bits), is reduced there to a quarter turn, and what is left (|r| <= 1/8
-// turn) goes through float32 Taylor polynomials: sin to x^9, cos to x^10 at
-// |x| <= pi/4 (next terms 1.8e-9 and 1.2e-10).
+// sin and cos of pos * freq.  The angle in turns is formed in two float64 parts:
+// the product of 31 and 24 bits and its rounding, times 1/(2 pi) in two parts;
+// at 2^31 the first part alone is off by 4e-7.  It is reduced there to a quarter
+// turn, and what is left (|r| <= 1/8 turn) goes through float32 Taylor
+// polynomials: sin to x^9, cos to x^10 at |x| <= pi/4 (next terms 1.8e-9 and
+// 1.2e-10; with their roundings within 2^-23).
 __device__ __forceinline__ void turn_f32(int32_t pos, float freq, float& sn, float& cs) {
-  double t = static_cast<double>(pos) * static_cast<double>(freq) * 0.15915494309189535;
-  t -= __builtin_rint(t);  // turns, [-1/2, 1/2]
+#pragma clang fp contract(off)  // (t is the rounded product: fused into the difference below, its rounding would count twice)
+  constexpr double kInv = 0.15915494309189535, kInvLow = -9.839338337591243e-18;  // 1/(2 pi)
+  const double p = static_cast<double>(pos), f = static_cast<double>(freq), a = p * f;
+  double t = a * kInv;
+  const double low = __builtin_fma(a, kInv, -t) + __builtin_fma(a, kInvLow, __builtin_fma(p, f, -a) * kInv);
+  t = (t - __builtin_rint(t)) + low;  // turns, [-1/2, 1/2]
   const double q = __builtin_rint(t * 4.0);
   const float x = static_cast<float>((t - q * 0.25) * 6.283185307179586);
   const float x2 = x * x;
