@@ -194,11 +194,8 @@ __global__ void __launch_bounds__(64 * CF::W, CF::occupancy) gated_fwd_kernel(Ga
   s_agg[w][lane] = make_float2(y, H);
   __syncthreads();
   // the map of the waves before this one; the last wave also the chunk's
-  float yw = -0.0f, Hw = 0.0f, yt = 0.0f, Ht = 0.0f, h;
-  for (int k = 0; k < w; ++k) {
-    const float2 f = s_agg[k][lane];
-    compose<VL>(yw, Hw, f.x, f.y);
-  }
+  float yw, Hw, yt = 0.0f, Ht = 0.0f, h;
+  fold_maps<VL, false>(s_agg, w, lane, yw, Hw);
   const int64_t cell = static_cast<int64_t>(line) * C + lane;
   if (w == W - 1) {
     yt = yw;
@@ -224,11 +221,7 @@ __global__ void __launch_bounds__(64 * CF::W, CF::occupancy) gated_fwd_kernel(Ga
       s_carry[lane] = state[0];
     }
     __syncthreads();
-    h = s_carry[lane];
-    for (int j = 0; j < there; ++j) {
-      const float2 f = s_in[j][lane];
-      h = pass<VL>(f.x, f.y, h);
-    }
+    h = fold_state<VL, false>(s_in, there, lane, s_carry[lane]);
   }
   if (w == W - 1 && (c + 1) % kGatedGroup == 0 && c + 1 < pl.chunks)
     publish(carries + (c + 1) / kGatedGroup * pl.cells + cell, 0.0f, pass<VL>(yt, Ht, h));

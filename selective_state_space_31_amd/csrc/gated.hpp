@@ -137,32 +137,79 @@ __device__ __forceinline__ float keep_of(float S) {
 __device__ __forceinline__ float root_of(float y) {
   return y < kCut ? -y : __builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(below_one(y) ? 1.0f + y : y));
 }
+// The state behind a stretch with h before it.  PLAIN: without what follows,
+// for a caller that looks at the result.
 // An infinite h stays infinite (no decay is 0 in exact arithmetic), also where
-// P is the identity or underflows, whose products with it would be NaN: looked
-// at only where the result is not finite.
-template <bool VL>
+// P is the identity or underflows, whose products with it would be NaN.
+template <bool VL, bool PLAIN = false>
 __device__ __forceinline__ float pass(float y, float H, float h) {
   float r = __builtin_fmaf(y, h, below_one(y) ? h : 0.0f) + H;
-  if (y < kCut)
-    r = h * -y * -y * -y * -y + H;
-  else if (!__builtin_isfinite(r) && __builtin_isinf(h))
-    r = h + H;
+  if (!PLAIN) {
+    if (y < kCut)
+      r = h * -y * -y * -y * -y + H;
+    else if (!__builtin_isfinite(r) && __builtin_isinf(h))
+      r = h + H;
+  }
   if constexpr (VL) return y == kCut ? H : r;
   return r;
 }
 // (y1, H1) followed by (y2, H2).
-template <bool VL>
+template <bool VL, bool PLAIN = false>
 __device__ __forceinline__ void compose(float& y1, float& H1, float y2, float H2) {
-  H1 = pass<VL>(y2, H2, H1);
+  H1 = pass<VL, PLAIN>(y2, H2, H1);
   const bool n1 = below_one(y1), n2 = below_one(y2);
   const float both = __builtin_fmaf(y1, y2, y1) + y2;  // (1 + y1)(1 + y2) - 1
   float y = n1 ? (n2 ? (both >= -0.5f ? -__builtin_fabsf(both) : 1.0f + both) : __builtin_fmaf(y1, y2, y2))
                : __builtin_fmaf(y1, y2, n2 ? y1 : 0.0f);
-  if (y > 0x1p64f || y1 < kCut || y2 < kCut) y = -__builtin_fminf(root_of(y1) * root_of(y2), kMaxRoot);
+  if (!PLAIN && (y > 0x1p64f || y1 < kCut || y2 < kCut))
+    y = -__builtin_fminf(root_of(y1) * root_of(y2), kMaxRoot);
   if constexpr (VL) {
     if (y1 == kCut || y2 == kCut) y = kCut;
   }
   y1 = y;
+}
+
+// n maps of the lane's channel, in LDS, composed or applied to a state one
+// after the other (BACK: from the last to the first).  The plain forms go
+// wrong only where a root is among the maps, or in a way that stays visible in
+// the result: an infinity or NaN ends at a cut at most, and P never falls from
+// above 2^64 (an overflowed one with the identity behind it is NaN).  Then the fold is done once more with care (with a look at every
+// step packed 8192 x 1001 float32 takes 46 us, so 43).
+template <bool VL, bool BACK>
+__device__ __forceinline__ void fold_maps(const float2 (*maps)[kGatedC], int n, int lane, float& y, float& H) {
+  y = -0.0f;
+  H = 0.0f;
+  float least = 0.0f;
+  for (int k = 0; k < n; ++k) {
+    const float2 f = maps[BACK ? n - 1 - k : k][lane];
+    least = __builtin_fminf(least, f.x);
+    compose<VL, true>(y, H, f.x, f.y);
+  }
+  if (least < kCut || !(y <= 0x1p64f) || !__builtin_isfinite(H)) {
+    y = -0.0f;
+    H = 0.0f;
+    for (int k = 0; k < n; ++k) {
+      const float2 f = maps[BACK ? n - 1 - k : k][lane];
+      compose<VL>(y, H, f.x, f.y);
+    }
+  }
+}
+template <bool VL, bool BACK>
+__device__ __forceinline__ float fold_state(const float2 (*maps)[kGatedC], int n, int lane, float h0) {
+  float h = h0, least = 0.0f;
+  for (int k = 0; k < n; ++k) {
+    const float2 f = maps[BACK ? n - 1 - k : k][lane];
+    least = __builtin_fminf(least, f.x);
+    h = pass<VL, true>(f.x, f.y, h);
+  }
+  if (least < kCut || !__builtin_isfinite(h)) {
+    h = h0;
+    for (int k = 0; k < n; ++k) {
+      const float2 f = maps[BACK ? n - 1 - k : k][lane];
+      h = pass<VL>(f.x, f.y, h);
+    }
+  }
+  return h;
 }
 
 // Which of a wave's tokens (64 at most) start and end their sequence, a bit

@@ -170,11 +170,8 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 4) gated_bwd_kernel(GatedBwdAr
   y = VL && (mk.starts | mk.ends) ? kCut : keep_of(y);
   s_rev[w][lane] = make_float2(y, Q);
   __syncthreads();
-  float yw = -0.0f, Qw = 0.0f, yt = 0.0f, Qt = 0.0f;
-  for (int q = W - 1; q > w; --q) {
-    const float2 f = s_rev[q][lane];
-    compose<VL>(yw, Qw, f.x, f.y);
-  }
+  float yw, Qw, yt = 0.0f, Qt = 0.0f;
+  fold_maps<VL, true>(s_rev + w + 1, W - 1 - w, lane, yw, Qw);
   const int64_t cell = static_cast<int64_t>(line) * C + lane;
   if (w == 0) {
     yt = yw;
@@ -200,11 +197,7 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 4) gated_bwd_kernel(GatedBwdAr
     s_carry[lane] = from[0];
   }
   __syncthreads();
-  float k = s_carry[lane];
-  for (int j = there - 1; j >= 0; --j) {
-    const float2 f = s_in[j][lane];
-    k = pass<VL>(f.x, f.y, k);
-  }
+  float k = fold_state<VL, true>(s_in, there, lane, s_carry[lane]);
   if (w == 0 && c == first && c > 0)
     publish(carries + c / kGatedGroup * pl.cells + cell, 0.0f, pass<VL>(yt, Qt, k));
   k = pass<VL>(yw, Qw, k);
