@@ -129,6 +129,19 @@ def _space(workspace, need, like, stream):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+def _buffers(grads, names, absent):
+    """A copy of ``grads``, whose keys have to be among ``names``; buffers for
+    outputs that this call does not have (``absent``) are refused."""
+    if not grads:
+        return {}
+    for k, t in grads.items():
+        if k not in names:
+            raise ValueError("grads: %r is none of %s" % (k, ", ".join(names)))
+        if t is not None and k in absent:
+            raise ValueError("grads: %s is given, but this call has no such output" % k)
+    return dict(grads)
+
+
 def _other(stream, like):
     """``stream`` where it is another one than ``like``'s device's current
     stream, else None."""
@@ -256,23 +269,25 @@ def ssm_gated_scan_fwd_varlen(x, rgate, igate, A, cu_seqlens, z=None, rgate_bias
                       chunk_states, workspace, stream)
 
 
+_GATED_GRADS = ("dx", "drgate", "digate", "dz", "dA", "drgate_bias", "digate_bias", "dinitial_state")
+
+
 def _gated_bwd(x, rgate, igate, A, cu_seqlens, dout, z, rgate_bias, igate_bias, normalize,
                initial_state, dlast_state, chunk_states, grads, workspace, stream):
     lib = _load()
     dt, n, L, dim, mid, head, h0, cu = _gated_inputs(x, rgate, igate, A, z, rgate_bias, igate_bias, normalize,
                                                      initial_state, cu_seqlens)
+    g = _buffers(grads, _GATED_GRADS, ("dz",) if z is None else ())
     stream, code = _other(stream, x), _DTYPES[dt]
     args = head + (h0, _opt(chunk_states, "chunk_states", mid, _F32, x), _in(dout, "dout", x.shape, dt, x),
                    _opt(dlast_state, "dlast_state", (n, dim), _F32, x))
-    g = dict(grads or {})
-    for k in ("dx", "drgate", "digate", "dz"):
+    for k in _GATED_GRADS[:4]:
         g[k] = None if k == "dz" and z is None else _out(g.get(k), k, x, dt, x, stream)
     for k in ("dA", "drgate_bias", "digate_bias"):
         g[k] = _out(g.get(k), k, (dim,), _F32, A, stream)
     g["dinitial_state"] = _out(g.get("dinitial_state"), "dinitial_state", (n, dim), _F32,
                                x if initial_state is None else initial_state, stream)
-    args += tuple(None if g[k] is None else g[k].data_ptr()
-                  for k in ("dx", "drgate", "digate", "dz", "dA", "drgate_bias", "digate_bias", "dinitial_state"))
+    args += tuple(None if g[k] is None else g[k].data_ptr() for k in _GATED_GRADS)
     have = int(chunk_states is not None)
     if cu is None:
         keep, ws, nbytes = _space(workspace, lib.ssm_gated_scan_bwd_workspace_bytes(n, L, dim, code, have), x, stream)
@@ -291,7 +306,7 @@ def ssm_gated_scan_bwd(x, rgate, igate, A, dout, z=None, rgate_bias=None, igate_
     for the same inputs (computed again without it).  Returns a dict: dx,
     drgate, digate, dz (None without z) in x's dtype; dA, drgate_bias,
     digate_bias, dinitial_state in float32.  ``grads`` may supply preallocated
-    outputs under the same keys."""
+    outputs under the same keys (other keys, or a dz without z, are refused)."""
     return _gated_bwd(x, rgate, igate, A, None, dout, z, rgate_bias, igate_bias, normalize,
                       initial_state, dlast_state, chunk_states, grads, workspace, stream)
 
@@ -408,7 +423,9 @@ def ssm_qk_norm_rotate_bwd(q, k, inv_freq, dq_out, dk_out, q_weight=None, k_weig
                            stream=None):
     """Gradients of ``ssm_qk_norm_rotate_fwd`` for the loss sum(dq_out*q_out)
     + sum(dk_out*k_out): a dict of dq, dk (contiguous, q's dtype; dk None
-    without k) and dq_weight, dk_weight (float32; None without the weight)."""
+    without k) and dq_weight, dk_weight (float32; None without the weight).
+    ``grads`` may supply preallocated outputs; keys that are no output of the
+    call are refused."""
     lib = _load()
     head, sizes = _rot_inputs(q, k, inv_freq, q_weight, k_weight, positions, eps, interleaved)
     batch, L, Hq, Hk, D = sizes[:5]
@@ -416,8 +433,9 @@ def ssm_qk_norm_rotate_bwd(q, k, inv_freq, dq_out, dk_out, q_weight=None, k_weig
         raise ValueError("dk_out or k_weight given without k")
     head += (_in(dq_out, "dq_out", q.shape, q.dtype, q),
              None if k is None else _in(dk_out, "dk_out", k.shape, q.dtype, q))
+    g = _buffers(grads, ("dq", "dk", "dq_weight", "dk_weight"),
+                 [n for n, t in (("dk", k), ("dq_weight", q_weight), ("dk_weight", k_weight)) if t is None])
     stream = _other(stream, q)
-    g = dict(grads or {})
     g["dq"] = _out(g.get("dq"), "dq", q, q.dtype, q, stream)
     g["dk"] = None if k is None else _out(g.get("dk"), "dk", k, q.dtype, k, stream)
     for n, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
@@ -442,7 +460,8 @@ def ssm_causal_conv1d_bwd(x, weight, dout, bias=None, initial_conv_state=None,
     sum(dfinal_conv_state*final_conv_state): a dict of dx and
     dinitial_conv_state (x's dtype; the latter None without
     ``initial_conv_state``), dweight and dbias (float32; None without
-    ``bias``).  ``grads`` may supply preallocated outputs."""
+    ``bias``).  ``grads`` may supply preallocated outputs; keys that are no
+    output of the call are refused."""
     lib = _load()
     _, dt = _act(x)
     if x.dim() != 3:
@@ -455,8 +474,9 @@ def ssm_causal_conv1d_bwd(x, weight, dout, bias=None, initial_conv_state=None,
     args = (_in(x, "x", x.shape, dt, x), _in(weight, "weight", (dim, W), _F32, x), _opt(bias, "bias", (dim,), _F32, x),
             _opt(initial_conv_state, "initial_conv_state", st, dt, x), _in(dout, "dout", x.shape, dt, x),
             _opt(dfinal_conv_state, "dfinal_conv_state", st, dt, x))
+    g = _buffers(grads, ("dx", "dweight", "dbias", "dinitial_conv_state"),
+                 [n for n, t in (("dbias", bias), ("dinitial_conv_state", initial_conv_state)) if t is None])
     stream = _other(stream, x)
-    g = dict(grads or {})
     g["dx"] = _out(g.get("dx"), "dx", x, dt, x, stream)
     g["dweight"] = _out(g.get("dweight"), "dweight", (dim, W), _F32, weight, stream)
     g["dbias"] = None if bias is None else _out(g.get("dbias"), "dbias", (dim,), _F32, bias, stream)
