@@ -4,8 +4,8 @@
 //   a_t = e^(A sigma(r_t + rb)),  h_t = a_t h_{t-1} + m_t sigma(i_t + ib) x_t
 //   out_t = h_t silu(z_t)
 //
-// About 36 vector instructions per token and channel stand against 8 to 20
-// bytes, so memory bounds a long run (vector ALU busy 68% of the time at 131072
+// 37 vector instructions per token and channel, 44 with z, stand against 8 to 20
+// bytes, so memory bounds a long run (vector ALU busy 70% of the time at 131072
 // tokens) and latency a short one.
 //
 #include "gated.hpp"
@@ -48,11 +48,11 @@ int launch_gated_init(void* ws, size_t bytes, const int32_t* cu, int64_t nseq, i
 // flight (batch * ring: a ring of registers, filled again as it is used up),
 // waves a SIMD holds.
 struct FwdLong {  // few folds per token, 3 workgroups to a CU: throughput
-  // (4 x 2048 x 1536 bf16: 36 us; T 32 with z fetched before the wait 45)
+  // (4 x 2048 x 1536 bf16: 37 us; T 32 with z fetched before the wait 45)
   static constexpr int T = 64, W = 4, batch = 4, ring = 2, occupancy = 3;
 };
 struct FwdShort {  // every load issued at once: the latency of few workgroups
-  // (8192 x 1001 float32: 41 us; half as many waves 46, T 8 47)
+  // (8192 x 1001 float32: 43 us; half as many waves and T 8 each 5 more)
   static constexpr int T = 16, W = 16, batch = 4, ring = 4, occupancy = 4;
 };
 
@@ -68,10 +68,10 @@ struct FwdShort {  // every load issued at once: the latency of few workgroups
 // only for ones that are running or done.
 // Reading the data once is what the split is for: chunk maps in a launch of
 // their own would read x and both gates twice (7 units of traffic for 5).
-// Measured (kernel alone): 1 x 131072 x 2048 bf16 447 us, 4.8 TB/s of the
+// Measured (kernel alone): 1 x 131072 x 2048 bf16 450 us, 4.8 TB/s of the
 // algorithm's bytes (copies of the same size reach 4.9 to 6.1); 4 x 2048 x 1536
-// bf16 with z 36 us, 3.4 TB/s; packed 8192 x 1001 float32 with z 41 us, 4.0
-// TB/s; packed 3001 x 515 float32 16 us, the chain ticket -> loads -> publish ->
+// with z bf16 37 us, 3.4 TB/s, float32 54 us, 4.6 TB/s; packed 8192 x 1001 with
+// z float32 43 us, 3.8 TB/s, bf16 35 us; packed 3001 x 515 of either type 16 us, the chain ticket -> loads -> publish ->
 // wait -> stores of one round of workgroups.
 template <typename TA, typename CF, bool NORM, bool GATE, bool VL>
 __global__ void __launch_bounds__(64 * CF::W, CF::occupancy) gated_fwd_kernel(GatedFwdArgs<TA> p, GatedPlan pl) {
@@ -374,10 +374,14 @@ int run_gated_fwd(const char* fn, const void* x, const void* r, const void* i, c
                            static_cast<const TA*>(z), A, rb, ib, static_cast<TA*>(out), last, h0, states, cu,
                            rows, L, nseq, dim, ws};
   // Long stretches where they give every CU more than two workgroups (768 of
-  // them, 4 x 2048 x 1536 bf16: 36 against 45 us); below, a lane that goes
+  // them, 4 x 2048 x 1536 bf16: 37 against 42 us); below, a lane that goes
   // through its tokens in rounds of loads takes longer than the device is kept
   // busy by them (512, 8192 x 1001 float32: 54 against 41 us; 108, 3001 x 515
-  // float32: 25 against 16 us).
+  // float32: 25 against 16 us).  The length needs no rule of its own: rows that
+  // fill neither stretch cost what their workgroups' starts and whole stretches
+  // cost, and the long ones still less (512 x 4 x 2048 bf16 189 against 241 us,
+  // 256 x 16 x 2048 104 against 123, 16 x 64 x 5120 21 against 28; float32 the
+  // same within 8%, in the same order).
   return fwd_plan<FwdLong>(rows, L, dim).units > 2u * static_cast<unsigned>(device_cus())
              ? launch_gated_fwd<TA, FwdLong>(a, norm, fn, stream)
              : launch_gated_fwd<TA, FwdShort>(a, norm, fn, stream);

@@ -28,10 +28,11 @@ static_assert(SSM_GATED_CHUNK == kBwdT, "a wave starts where the forward kept th
 // 16 of them are 96 of the 128 registers that let four waves share a SIMD; the
 // ring holds four tokens on the way (all sixteen at two waves a SIMD: 70 us
 // against 58 for the layer, 22.5 against 23 for few workgroups; no variant is
-// kept for that).  85 vector instructions a token keep the vector ALU busy for
+// kept for that).  88 vector instructions a token keep the vector ALU busy for
 // 57% of the time; the rest waits on memory.
-// Measured (kernel alone): 4 x 2048 x 1536 bf16 with z 58 us for 9 activation
-// tensors, 3.9 TB/s; packed 3001 x 515 float32 23 us.
+// Measured (kernel alone): 4 x 2048 x 1536 with z, 9 activation tensors, bf16 59
+// us, 3.8 TB/s, float32 97 us, 4.7 TB/s; packed 8192 x 1001 float32 96 us, bf16
+// 65 us; packed 3001 x 515 float32 23 us, bf16 21 us.
 template <typename TA, bool NORM, bool GATE, bool VL>
 __global__ void __launch_bounds__(64 * kBwdWaves, 4) gated_bwd_kernel(GatedBwdArgs<TA> p, GatedPlan pl) {
   constexpr int T = kBwdT, W = kBwdWaves, C = kGatedC, NB = kBwdBatch, kPolls = (kGatedGroup + W - 1) / W;

@@ -374,6 +374,8 @@ __global__ void __launch_bounds__(64 * kRotWaves) rotate_kernel(RotArgs<TA> p, i
 // Sum of the partial weight gradients: a workgroup takes 16 elements of one of
 // the two; wave w and lane quarter t take every 64th row from 4 w + t on, and
 // the quarters' and the waves' sums are added in order.
+// A launch of its own: the rows are there in no fixed order, and atomics would
+// add them in that one, differently from run to run.
 // At most 1024 rows of 1 KB (heads of 128): its launch and two round trips, 4.9 us.
 constexpr int kRotSumWaves = 16, kRotSumElems = 16;
 __global__ void __launch_bounds__(64 * kRotSumWaves) rotate_sum_kernel(const float* part, int n, int D, float* dqw,
