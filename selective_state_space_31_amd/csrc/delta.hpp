@@ -73,4 +73,157 @@ inline size_t strided_bytes(int64_t rows, int64_t width, int64_t stride, size_t 
   return rows > 0 ? (static_cast<size_t>(rows - 1) * stride + width) * es : 0;
 }
 
+// ---------------------------------------------------------------------------
+// matrix products in float32's precision on the bf16 matrix cores
+// ---------------------------------------------------------------------------
+// A float32 value is the sum of three bf16 ones (8 significant bits each, the
+// later parts round what the earlier ones left).  A product of two such values
+// keeps the partial products whose parts' indices add up to less than three:
+// six of nine, the dropped ones below 2^-26 of it.  A bf16 input is its own first
+// part, exactly.  (The float32 matrix instruction has the precision too, at 1/16
+// of the bf16 rate: six products are 2.7 times as fast, three 5.3.)
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+
+template <int N>
+struct Parts {
+  static constexpr int value = N;
+};
+template <typename TA>
+struct ActParts;
+template <>
+struct ActParts<float> {
+  static constexpr int in = 3, out = 3;  // of an input; of what reaches act outputs alone
+};
+template <>
+struct ActParts<bf16_t> {
+  static constexpr int in = 1, out = 2;
+};
+
+__device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                 0);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const bf16x2 v = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};
+  return __builtin_bit_cast(uint32_t, v);
+}
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+// Two values into N parts each, packed
+template <int N>
+__device__ __forceinline__ void split2(float a, float b, uint32_t (&p)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    p[i] = pack_bf16(a, b);
+    a -= bf_lo(p[i]);
+    b -= bf_hi(p[i]);
+  }
+}
+
+// c += a b over the parts, up to `LIM` of their indices' sum
+template <int LIM, int NA, int NB>
+__device__ __forceinline__ f32x4 mul_parts(const u32x4 (&a)[NA], const u32x4 (&b)[NB], f32x4 c) {
+#pragma unroll
+  for (int s = LIM - 1; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i <= s; ++i)
+      if (i < NA && s - i < NB) c = mfma16(a[i], b[s - i], c);
+  return c;
+}
+
+// Matrix fragments.  A product's left operand: lane l holds row l % 16, columns
+// 8 (l / 16) .. + 7 of a 16 x 32 block; the right one likewise with rows and
+// columns exchanged; the result has column l % 16, rows 4 (l / 16) + 0..3.  In
+// memory a fragment is 64 times 16 bytes, lane after lane.
+//
+// Four results of a lane (rows 4 (l / 16) .. + 3 of row block t of 16) go into
+// right operands over those rows: 8 bytes at this offset of 32-row block t / 2.
+__device__ __forceinline__ int frag_put(int lane, int t) {
+  const int q = lane >> 4;
+  return (((t & 1) * 2 + (q >> 1)) * 16 + (lane & 15)) * 16 + (q & 1) * 8;
+}
+
+// Lower triangle of 64 x 64 in 16 x 32 blocks: row blocks 0 and 1 have one,
+// 2 and 3 have two.
+constexpr int kTri = 6;
+__device__ __forceinline__ int tri_at(int rowblock, int kb) { return rowblock < 2 ? rowblock : 2 * rowblock - 2 + kb; }
+
+// The sequence that chunk place `slot` of a packed call lies in: the largest s
+// in [0, nseq) with cu[s] / C + s <= slot, found by a 64-way search.  Probes stay
+// inside cu[0, nseq), so unsorted offsets still give an index in range.  slot is
+// wave-uniform and all 64 lanes must be active.
+__device__ __forceinline__ int delta_owner(const int32_t* cu, int nseq, int64_t slot) {
+  const int lane = static_cast<int>(threadIdx.x & 63);
+  int lo = 0, cnt = nseq;
+  for (;;) {
+    const int stride = (cnt + 63) >> 6;
+    const int i = lane * stride;
+    const bool p = i < cnt && int64_t{cu[lo + i]} / kDeltaC + lo + i <= slot;
+    const unsigned long long m = __ballot(p);
+    const int k = m ? 63 - __builtin_clzll(m) : 0;
+    lo = __builtin_amdgcn_readfirstlane(lo + k * stride);
+    if (stride == 1) return lo;
+    cnt = (cnt - k * stride < stride) ? cnt - k * stride : stride;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// chunks
+// ---------------------------------------------------------------------------
+// What does not depend on the state, per chunk (delta_prep.hip).  K and Q are
+// the chunk's rows, gamma_i = e^{G_i} with G the running sum of g, D_ij =
+// e^{G_i - G_j}, A_ij = beta_i D_ij k_i.k_j below the diagonal, T = (I + A)^-1,
+// P_ij = D_ij q_i.k_j on and below it.
+struct ChunkSpace {
+  // per place and key head, parts in turn: fragments of K and Q (4 row blocks x
+  // KT of 32 columns) and of K^T (2 KT row blocks x 2 of 32 tokens)
+  u32x4 *kf, *qf, *ktf;
+  // per place and value head: fragments of T diag(beta) in three parts, of P
+  u32x4 *tf, *pf;
+  float* vec;  // gamma (64), e^{G_63 - G_i} (64)
+};
+
+template <typename TA>
+struct PrepArgs {
+  const TA *q, *k;
+  const float *beta, *g;
+  const int32_t* cu;
+  int64_t nseq, L, qs, ks;
+  int hk, hv, K;
+  ChunkSpace c;
+};
+
+inline int delta_kt(int K) { return K <= 32 ? 1 : K <= 64 ? 2 : K <= 128 ? 4 : 8; }  // columns in blocks of 32
+
+inline size_t chunk_space(const DeltaDims& d, int dtype, void* base, ChunkSpace* c) {
+  const size_t in = dtype == SSM_DTYPE_F32 ? 3 : 1, out = dtype == SSM_DTYPE_F32 ? 3 : 2, kt = delta_kt(d.K);
+  const size_t n = static_cast<size_t>(d.chunks()), frag = 64 * sizeof(u32x4);
+  const size_t rows = n * d.hk * in * 4 * kt * frag, tri = n * d.hv * kTri * frag;
+  char* p = static_cast<char*>(base);
+  size_t at = 0;
+  const auto take = [&](size_t bytes) {
+    char* const r = p ? p + at : nullptr;
+    at += bytes;
+    return r;
+  };
+  ChunkSpace s;
+  s.kf = reinterpret_cast<u32x4*>(take(rows));
+  s.qf = reinterpret_cast<u32x4*>(take(rows));
+  s.ktf = reinterpret_cast<u32x4*>(take(rows));
+  s.tf = reinterpret_cast<u32x4*>(take(3 * tri));
+  s.pf = reinterpret_cast<u32x4*>(take(out * tri));
+  s.vec = reinterpret_cast<float*>(take(n * d.hv * 2 * kDeltaC * 4));
+  if (c) *c = s;
+  return at;
+}
+
+// Launches the preparation of every chunk.
+void delta_prep(int dtype, const void* q, const void* k, const float* beta, const float* g, const int32_t* cu,
+                const DeltaDims& d, const ChunkSpace& c, hipStream_t stream);
+
 }  // namespace ssm

@@ -5,11 +5,269 @@
 namespace ssm {
 namespace {
 
-size_t fwd_bytes(const DeltaDims& d, int dtype) {
-  (void)d;
-  (void)dtype;
-  return 0;
+template <typename TA>
+struct RecArgs {
+  const TA* v;
+  TA* out;
+  const float* first;
+  float *last, *mids;
+  const int32_t* cu;
+  ChunkSpace c;
+  float scale;
+  int64_t nseq, L, vs;
+  int hk, hv, K, V, slices;
+};
+
+// The chunks one after another.  With S0 the state before a chunk, per column
+// block of 16 NC values:
+//   X = V - gamma (K S0);  U = T diag(beta) X;  out = scale (gamma (Q S0) + P U)
+//   S1 = gamma_C S0 + K^T (d U)
+// A workgroup of four waves takes one column block of a head (columns do not
+// meet): wave w the tokens 16 w .. + 15 of X, U and out, and every fourth row
+// block of S, which stays in its registers.  S, X, U and d U pass through LDS as
+// right operands in bf16 parts; the left operands come from memory as fragments,
+// each needed by one wave alone, the next chunk's while this one is worked on.
+template <typename TA, int KT, int NC, bool MIDS>
+__global__ void __launch_bounds__(256) delta_rec_kernel(const RecArgs<TA> p) {
+  constexpr int IN = ActParts<TA>::in, OUT = ActParts<TA>::out, TW = (KT + 1) / 2;
+  __shared__ u32x4 sS[3][KT][NC][64], sX[3][2][NC][64], sU[OUT][2][NC][64], sD[3][2][NC][64];
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // The workgroups of a head read the same fragments: they go to the same XCD
+  // (workgroups are dealt to the eight XCDs in turn).
+  const unsigned group = blockIdx.x / (8u * static_cast<unsigned>(p.slices)), in = blockIdx.x % (8u * static_cast<unsigned>(p.slices));
+  const int64_t pair = int64_t{group} * 8 + (in & 7);
+  if (pair >= p.nseq * p.hv) return;
+  const int slice = static_cast<int>(in >> 3), c0 = slice * 16 * NC;
+  const int64_t b = pair / p.hv;
+  const int h = static_cast<int>(pair - b * p.hv), j = h / (p.hv / p.hk);
+  const DeltaSeq q = delta_seq(p.cu, b, p.L);
+  const int nc = static_cast<int>((q.hi - q.lo + kDeltaC - 1) / kDeltaC);
+  const size_t sv = static_cast<size_t>(p.K) * p.V;
+  const bool tiles = TW > 1 || w < 2 * KT;  // (with 32 rows two waves hold none)
+
+  // state values of this lane: row block t, column block nb
+  const auto state_io = [&](auto&& f) {
+#pragma unroll
+    for (int i = 0; i < TW; ++i)
+#pragma unroll
+      for (int nb = 0; nb < NC; ++nb)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * (w + 4 * i) + 4 * g + r, col = c0 + 16 * nb + n;
+          if (tiles && row < p.K && col < p.V) f(i, nb, r, static_cast<size_t>(row) * p.V + col);
+        }
+  };
+  f32x4 S[TW][NC];
+#pragma unroll
+  for (int i = 0; i < TW; ++i)
+#pragma unroll
+    for (int nb = 0; nb < NC; ++nb) S[i][nb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  if (p.first) {
+    const float* const src = p.first + pair * sv;
+    state_io([&](int i, int nb, int r, size_t at) { S[i][nb][r] = src[at]; });
+  }
+  const auto put = [&](u32x4* base, int blocks, int t, int nb, f32x4 x, auto parts) {
+    constexpr int N = decltype(parts)::value;
+    uint32_t lo[N], hi[N];
+    split2(x[0], x[1], lo);
+    split2(x[2], x[3], hi);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      *reinterpret_cast<u32x2*>(reinterpret_cast<char*>(base + ((i * blocks + (t >> 1)) * NC + nb) * 64) +
+                                frag_put(lane, t)) = u32x2{lo[i], hi[i]};
+  };
+  const auto put_state = [&]() {
+    if (tiles)
+#pragma unroll
+      for (int i = 0; i < TW; ++i)
+#pragma unroll
+        for (int nb = 0; nb < NC; ++nb) put(&sS[0][0][0][0], KT, w + 4 * i, nb, S[i][nb], Parts<3>{});
+  };
+  if (nc > 0) put_state();
+
+  // left operands of one chunk
+  u32x4 fk[KT][IN], fq[KT][IN], ft[2][3], fp[2][OUT], fkt[TW][2][IN];
+  float ga[4], de[4], gC;
+  TA rv[NC][4];
+  const int kbs = w < 2 ? 1 : 2;
+  const auto load_kq = [&](int64_t slot) {
+    const size_t at = static_cast<size_t>(slot * p.hk + j) * IN * 4 * KT * 64 + lane;
+#pragma unroll
+    for (int kb = 0; kb < KT; ++kb)
+#pragma unroll
+      for (int i = 0; i < IN; ++i) {
+        fk[kb][i] = p.c.kf[at + ((i * 4 + w) * KT + kb) * 64];
+        fq[kb][i] = p.c.qf[at + ((i * 4 + w) * KT + kb) * 64];
+      }
+  };
+  const auto load_v = [&](int64_t slot, int64_t t0) {
+    const float* const vec = p.c.vec + (slot * p.hv + h) * 2 * kDeltaC;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      ga[r] = vec[16 * w + 4 * g + r];
+      de[r] = vec[kDeltaC + 16 * w + 4 * g + r];
+      const int64_t t = t0 + 16 * w + 4 * g + r;
+#pragma unroll
+      for (int nb = 0; nb < NC; ++nb) {
+        const int col = c0 + 16 * nb + n;
+        rv[nb][r] = TA{};
+        if (t < q.hi && col < p.V) rv[nb][r] = p.v[t * p.vs + h * p.V + col];
+      }
+    }
+    gC = vec[kDeltaC - 1];
+  };
+  const auto load_t = [&](int64_t slot) {
+    const size_t at = static_cast<size_t>(slot * p.hv + h) * 3 * kTri * 64 + lane;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (kb < kbs) ft[kb][i] = p.c.tf[at + (i * kTri + tri_at(w, kb)) * 64];
+  };
+  const auto load_pkt = [&](int64_t slot) {
+    const size_t at = static_cast<size_t>(slot * p.hv + h) * OUT * kTri * 64 + lane;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int i = 0; i < OUT; ++i)
+        if (kb < kbs) fp[kb][i] = p.c.pf[at + (i * kTri + tri_at(w, kb)) * 64];
+    const size_t kt = static_cast<size_t>(slot * p.hk + j) * IN * 2 * KT * 2 * 64 + lane;
+    if (tiles)
+#pragma unroll
+      for (int x = 0; x < TW; ++x)
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int i = 0; i < IN; ++i) fkt[x][kb][i] = p.c.ktf[kt + ((i * 2 * KT + w + 4 * x) * 2 + kb) * 64];
+  };
+  if (nc > 0) {
+    load_kq(q.slot);
+    load_v(q.slot, q.lo);
+    load_t(q.slot);
+    load_pkt(q.slot);
+  }
+  __syncthreads();
+  for (int c = 0; c < nc; ++c) {
+    const int64_t slot = q.slot + c, t0 = q.lo + int64_t{c} * kDeltaC;
+    const int more = c + 1 < nc ? 1 : 0;  // (the last chunk's loads ahead are its own again)
+    if constexpr (MIDS) {
+      float* const dst = p.mids + (slot * p.hv + h) * sv;
+      state_io([&](int i, int nb, int r, size_t at) { dst[at] = S[i][nb][r]; });
+    }
+    // ---- X and Q S0 ----
+    f32x4 o[NC];
+#pragma unroll
+    for (int nb = 0; nb < NC; ++nb) {
+      f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
+#pragma unroll
+      for (int kb = 0; kb < KT; ++kb) {
+        u32x4 s[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) s[i] = sS[i][kb][nb][lane];
+        x = mul_parts<3>(fk[kb], s, x);
+        y = mul_parts<OUT>(fq[kb], s, y);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        o[nb][r] = ga[r] * y[r];
+        x[r] = to_f32(rv[nb][r]) - ga[r] * x[r];
+      }
+      put(&sX[0][0][0][0], 2, w, nb, x, Parts<3>{});
+    }
+    load_kq(slot + more);
+    float dl[4];
+    const float decay = gC;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) dl[r] = de[r];
+    load_v(slot + more, t0 + more * kDeltaC);
+    __syncthreads();
+    // ---- U ----
+#pragma unroll
+    for (int nb = 0; nb < NC; ++nb) {
+      f32x4 u = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        if (kb >= kbs) break;
+        u32x4 x[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) x[i] = sX[i][kb][nb][lane];
+        u = mul_parts<3>(ft[kb], x, u);
+      }
+      put(&sU[0][0][0][0], 2, w, nb, u, Parts<OUT>{});
+#pragma unroll
+      for (int r = 0; r < 4; ++r) u[r] *= dl[r];
+      put(&sD[0][0][0][0], 2, w, nb, u, Parts<3>{});
+    }
+    load_t(slot + more);
+    __syncthreads();
+    // ---- S1, then out ----
+    if (tiles) {
+#pragma unroll
+      for (int nb = 0; nb < NC; ++nb)
+#pragma unroll
+        for (int i = 0; i < TW; ++i) S[i][nb] *= decay;
+#pragma unroll
+      for (int nb = 0; nb < NC; ++nb)
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          u32x4 u[3];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) u[i] = sD[i][kb][nb][lane];
+#pragma unroll
+          for (int i = 0; i < TW; ++i) S[i][nb] = mul_parts<3>(fkt[i][kb], u, S[i][nb]);
+        }
+      put_state();
+    }
+#pragma unroll
+    for (int nb = 0; nb < NC; ++nb) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        if (kb >= kbs) break;
+        u32x4 u[OUT];
+#pragma unroll
+        for (int i = 0; i < OUT; ++i) u[i] = sU[i][kb][nb][lane];
+        o[nb] = mul_parts<OUT>(fp[kb], u, o[nb]);
+      }
+      const int col = c0 + 16 * nb + n;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int64_t t = t0 + 16 * w + 4 * g + r;
+        if (t < q.hi && col < p.V) store_act(p.out + (t * p.hv + h) * p.V + col, p.scale * o[nb][r]);
+      }
+    }
+    load_pkt(slot + more);
+    __syncthreads();
+  }
+  if (p.last) {
+    float* const dst = p.last + pair * sv;
+    state_io([&](int i, int nb, int r, size_t at) { dst[at] = S[i][nb][r]; });
+  }
 }
+
+template <typename TA, int KT, int NC>
+void launch_rec(const RecArgs<TA>& a, hipStream_t stream) {
+  const int64_t pairs = a.nseq * a.hv;
+  const dim3 grid(static_cast<unsigned>((pairs + 7) / 8 * 8 * a.slices)), block(256);
+  if (a.mids) hipLaunchKernelGGL((delta_rec_kernel<TA, KT, NC, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((delta_rec_kernel<TA, KT, NC, false>), grid, block, 0, stream, a);
+}
+
+template <typename TA>
+int run_chunks(const char* fn, const void* v, float scale, void* out, float* last, const float* first, float* mids,
+               const int32_t* cu, const DeltaDims& d, const ChunkSpace& c, hipStream_t stream) {
+  RecArgs<TA> a{static_cast<const TA*>(v), static_cast<TA*>(out), first, last, mids, cu, c, scale, d.nseq, d.L, d.vs,
+                d.hk, d.hv, d.K, d.V, (d.V + 15) / 16};
+  switch (delta_kt(d.K)) {
+    case 1: launch_rec<TA, 1, 1>(a, stream); break;
+    case 2: launch_rec<TA, 2, 1>(a, stream); break;
+    case 4: launch_rec<TA, 4, 1>(a, stream); break;
+    default: launch_rec<TA, 8, 1>(a, stream); break;
+  }
+  return launch_status(fn);
+}
+
+size_t fwd_bytes(const DeltaDims& d, int dtype) { return chunk_space(d, dtype, nullptr, nullptr); }
 
 int delta_fwd(const char* fn, const void* q, const void* k, const void* v, const float* beta, const float* g,
               float scale, void* out, float* last, const float* first, float* mids, const int32_t* cu, bool packed,
@@ -61,7 +319,12 @@ int delta_fwd(const char* fn, const void* q, const void* k, const void* v, const
   if (need > 0 && !aligned(ws, 256))
     return fail(SSM_ERR_ALIGN, "%s: workspace is not 256-byte aligned", fn);
   if (L == 0 && !last) return SSM_OK;
-  return delta_walk(fn, dtype, q, k, v, beta, g, scale, out, last, first, mids, packed ? cu : nullptr, d, stream);
+  if (!packed) cu = nullptr;
+  ChunkSpace c;
+  chunk_space(d, dtype, ws, &c);
+  if (L > 0) delta_prep(dtype, q, k, beta, g, cu, d, c, stream);
+  return dtype == SSM_DTYPE_F32 ? run_chunks<float>(fn, v, scale, out, last, first, mids, cu, d, c, stream)
+                                : run_chunks<bf16_t>(fn, v, scale, out, last, first, mids, cu, d, c, stream);
 }
 
 size_t query(int64_t nseq, int64_t L, int64_t hk, int64_t hv, int64_t K, int64_t V, bool packed, int dtype) {

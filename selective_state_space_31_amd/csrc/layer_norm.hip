@@ -22,6 +22,7 @@ namespace ssm {
 namespace {
 
 constexpr int64_t kNormMaxDim = 16384;
+constexpr int kNormWavesPerCu = 32;   // forward: more rows than that go round
 constexpr int kNormMaxParts = 512;  // workgroups that leave partial weight gradients
 
 // 16 bytes of a row; rows may start anywhere, so the compiler is told of no
@@ -93,8 +94,8 @@ __device__ __forceinline__ float wave_sum(float x) {
   return x;
 }
 
-// Sum over the WPR waves of a row (a fixed order); `slot` alternates so that
-// one barrier a sum is enough.
+// Sum over the WPR waves of a row (a fixed order).  A slot is written again
+// only behind the barrier of another one, so one barrier a sum is enough.
 template <int WPR>
 __device__ __forceinline__ float row_sum(float x, float* red, int slot) {
   x = wave_sum(x);
@@ -114,12 +115,19 @@ template <int NV, int VEC>
 __device__ __forceinline__ void load_param(float (&w)[NV][VEC], const float* p, float fill, int first,
                                            int step, int dim) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    const int c = first + i * step;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const int c = first + i * step + j;
-      w[i][j] = p && c < dim ? p[c] : fill;
+    for (int j = 0; j < VEC; ++j) w[i][j] = fill;
+    if (!p) continue;
+    if (c + VEC <= dim) {
+      __builtin_memcpy(&w[i], p + c, sizeof(w[i]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if (c + j < dim) w[i][j] = p[c + j];
     }
+  }
 }
 
 template <typename TA>
@@ -156,37 +164,45 @@ __device__ __forceinline__ float centre(NormRow<TA, NV>& s, float* red, int firs
   return 1.0f / sqrtf(__builtin_fmaf(row_sum<WPR>(t, red, 1), inv, eps));
 }
 
-template <typename TA, int NV, int WPR>
+// Each row group (a wave, or WPR of them) goes through every gridDim-th row
+// with its columns' weights in registers.
+template <typename TA, int NV, int WPR, bool RES>
 __global__ void __launch_bounds__(WPR > 4 ? 64 * WPR : 256)
     norm_fwd_kernel(const NormArgs<TA> p) {
-  constexpr int VEC = Piece<TA>::n, step = 64 * WPR * VEC;
+  constexpr int VEC = Piece<TA>::n, step = 64 * WPR * VEC, GROUPS = WPR == 1 ? 4 : 1;
   __shared__ float red[2 * WPR];
   const int tid = static_cast<int>(threadIdx.x);
-  const int lane = WPR == 1 ? tid & 63 : tid;
-  const int64_t row = WPR == 1 ? int64_t{blockIdx.x} * 4 + (tid >> 6) : int64_t{blockIdx.x};
-  if (row >= p.rows) return;  // (whole waves, and no barrier with one wave a row)
+  const int lane = WPR == 1 ? tid & 63 : tid, group = WPR == 1 ? tid >> 6 : 0;
   const int first = lane * VEC, dim = p.dim;
-  NormRow<TA, NV> s;
+  const int64_t hop = int64_t{gridDim.x} * GROUPS;
+  int64_t row = int64_t{blockIdx.x} * GROUPS + group;
+  if (row >= p.rows) return;  // (whole waves, and no barrier with one wave a row)
+  NormRow<TA, NV> s, r;
   s.load(p.x + row * p.xs, first, step, dim);
-  if (p.res) {
-    NormRow<TA, NV> r;
-    r.load(p.res + row * p.rs, first, step, dim);
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) s.v[i][j] += r.v[i][j];
-    s.round();
-    if (p.sum) s.store(p.sum + row * dim, first, step, dim);
-  }
+  if constexpr (RES) r.load(p.res + row * p.rs, first, step, dim);
   float w[NV][VEC], b[NV][VEC];
   load_param(w, p.w, 1.0f, first, step, dim);
   load_param(b, p.b, 0.0f, first, step, dim);
-  const float rstd = centre<WPR>(s, red, first, step, dim, p.eps);
+  for (;;) {
+    if constexpr (RES) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) s.v[i][j] = __builtin_fmaf(s.v[i][j] * rstd, w[i][j], b[i][j]);
-  s.store(p.out + row * dim, first, step, dim);
+        for (int j = 0; j < VEC; ++j) s.v[i][j] += r.v[i][j];
+      s.round();
+      if (p.sum) s.store(p.sum + row * dim, first, step, dim);
+    }
+    const float rstd = centre<WPR>(s, red, first, step, dim, p.eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) s.v[i][j] = __builtin_fmaf(s.v[i][j] * rstd, w[i][j], b[i][j]);
+    s.store(p.out + row * dim, first, step, dim);
+    row += hop;
+    if (row >= p.rows) return;
+    s.load(p.x + row * p.xs, first, step, dim);
+    if constexpr (RES) r.load(p.res + row * p.rs, first, step, dim);
+  }
 }
 
 // Gradients: each row group (a wave, or WPR of them) goes through every
@@ -242,7 +258,6 @@ __global__ void __launch_bounds__(WPR > 4 ? 64 * WPR : 256)
         for (int j = 0; j < VEC; ++j) y.v[i][j] += s.v[i][j];
     }
     y.store(p.out + row * dim, first, step, dim);
-    if constexpr (WPR > 1) __syncthreads();  // (red is written again)
   }
   if (!p.part) return;
   if constexpr (GROUPS > 1) {
@@ -345,8 +360,10 @@ int launch_norm_fwd(const char* fn, const void* x, const void* res, const float*
                        static_cast<TA*>(out), static_cast<TA*>(sum), nullptr, eps, rows, xs, rs, dim};
   norm_choose<TA>(rows, dim, [&](auto nv, auto wpr) {
     constexpr int NV = decltype(nv)::value, W = decltype(wpr)::value;
-    const unsigned grid = static_cast<unsigned>(W == 1 ? (rows + 3) / 4 : rows);
-    hipLaunchKernelGGL((norm_fwd_kernel<TA, NV, W>), dim3(grid), dim3(W == 1 ? 256 : 64 * W), 0, stream, a);
+    const int64_t units = W == 1 ? (rows + 3) / 4 : rows, most = int64_t{device_cus()} * kNormWavesPerCu / (W == 1 ? 4 : W);
+    const dim3 grid(static_cast<unsigned>(units < most ? units : most)), block(W == 1 ? 256 : 64 * W);
+    if (res) hipLaunchKernelGGL((norm_fwd_kernel<TA, NV, W, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((norm_fwd_kernel<TA, NV, W, false>), grid, block, 0, stream, a);
   });
   return launch_status(fn);
 }
