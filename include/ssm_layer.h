@@ -63,9 +63,10 @@ extern "C" {
  *   last_state      : the same shape or NULL; S after the last token.  May be
  *                     the initial_state buffer (resume in place).
  *   chunk_states    : (batch, ceil(seqlen / SSM_DELTA_CHUNK), nheads_v,
- *                     headdim_k, headdim_v) float32 or NULL; receives the state
- *                     before every SSM_DELTA_CHUNK-th token, for
- *                     ssm_delta_rule_bwd
+ *                     headdim_k + SSM_DELTA_CHUNK, headdim_v) float32 or NULL;
+ *                     receives for every chunk of SSM_DELTA_CHUNK tokens the
+ *                     state before it (headdim_k rows), then u of its tokens
+ *                     (zeros behind the last one), for ssm_delta_rule_bwd
  *   1 <= headdim_k, headdim_v <= 256; nheads_v a multiple of nheads_k, at most
  *   65535; 1 <= batch <= 65535; seqlen >= 0 (0 only copies the initial state);
  *   batch * seqlen < 2^31; batch * ceil(seqlen / SSM_DELTA_CHUNK) * nheads_v <
@@ -105,11 +106,10 @@ size_t ssm_delta_rule_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t
  *   initial_state, last_state : (nseq, nheads_v, headdim_k, headdim_v) float32
  *                      or NULL.  last_state may be the initial_state buffer.
  *   chunk_states     : (total_len / SSM_DELTA_CHUNK + nseq, nheads_v,
- *                      headdim_k, headdim_v) float32 or NULL (the division
- *                      rounds down); receives the state before token
- *                      SSM_DELTA_CHUNK c of sequence s at cu[s] /
- *                      SSM_DELTA_CHUNK + s + c.  Places that no chunk has keep
- *                      what they held.
+ *                      headdim_k + SSM_DELTA_CHUNK, headdim_v) float32 or NULL
+ *                      (the division rounds down); receives what belongs to
+ *                      chunk c of sequence s at cu[s] / SSM_DELTA_CHUNK + s + c.
+ *                      Places that no chunk has keep what they held.
  *   1 <= nseq < 2^20; 0 <= total_len < 2^31; (total_len / SSM_DELTA_CHUNK +
  *   nseq) * nheads_v < 2^26.
  * Nothing passes from one sequence into another, a NaN or an infinity neither.

@@ -31,6 +31,8 @@ struct DeltaDims {
     return packed ? L / kDeltaC + nseq : nseq * ((L + kDeltaC - 1) / kDeltaC);
   }
   size_t state_values() const { return static_cast<size_t>(hv) * K * V; }
+  // of chunk_states: the state and the chunk's u per place and head
+  size_t mid_values() const { return static_cast<size_t>(chunks()) * hv * (K + kDeltaC) * V; }
 };
 
 inline bool delta_sizes_ok(int64_t nseq, int64_t L, int64_t hk, int64_t hv, int64_t K, int64_t V, bool packed) {
@@ -148,10 +150,24 @@ __device__ __forceinline__ int frag_put(int lane, int t) {
   return (((t & 1) * 2 + (q >> 1)) * 16 + (lane & 15)) * 16 + (q & 1) * 8;
 }
 
-// Lower triangle of 64 x 64 in 16 x 32 blocks: row blocks 0 and 1 have one,
-// 2 and 3 have two.
+// base: [N][blocks][NC][64]; x goes into the parts' fragments of column block nb.
+template <int N, int NC>
+__device__ __forceinline__ void put_parts(u32x4* base, int blocks, int t, int nb, int lane, f32x4 x) {
+  uint32_t lo[N], hi[N];
+  split2(x[0], x[1], lo);
+  split2(x[2], x[3], hi);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    *reinterpret_cast<u32x2*>(reinterpret_cast<char*>(base + ((i * blocks + (t >> 1)) * NC + nb) * 64) +
+                              frag_put(lane, t)) = u32x2{lo[i], hi[i]};
+}
+
+// Triangles of 64 x 64 in 16 x 32 blocks.  Lower: row blocks 0 and 1 have one,
+// 2 and 3 have two.  Upper (a lower one transposed): 0 and 1 have two, 2 and 3
+// the second alone.
 constexpr int kTri = 6;
 __device__ __forceinline__ int tri_at(int rowblock, int kb) { return rowblock < 2 ? rowblock : 2 * rowblock - 2 + kb; }
+__device__ __forceinline__ int tri_up(int rowblock, int kb) { return rowblock < 2 ? 2 * rowblock + kb : 2 + rowblock; }
 
 // The sequence that chunk place `slot` of a packed call lies in: the largest s
 // in [0, nseq) with cu[s] / C + s <= slot, found by a 64-way search.  Probes stay
@@ -181,9 +197,10 @@ __device__ __forceinline__ int delta_owner(const int32_t* cu, int nseq, int64_t 
 // P_ij = D_ij q_i.k_j on and below it.
 struct ChunkSpace {
   // per place and key head, parts in turn: fragments of K and Q (4 row blocks x
-  // KT of 32 columns) and of K^T (2 KT row blocks x 2 of 32 tokens)
-  u32x4 *kf, *qf, *ktf;
-  // per place and value head: fragments of T diag(beta) in three parts, of P
+  // KT of 32 columns) and of K^T and Q^T (2 KT row blocks x 2 of 32 tokens)
+  u32x4 *kf, *qf, *ktf, *qtf;
+  // per place and value head: fragments of T diag(beta) in three parts and of P
+  // (forward), of T^T and P^T in three parts each (backward)
   u32x4 *tf, *pf;
   float* vec;  // gamma (64), e^{G_63 - G_i} (64)
 };
@@ -200,21 +217,23 @@ struct PrepArgs {
 
 inline int delta_kt(int K) { return K <= 32 ? 1 : K <= 64 ? 2 : K <= 128 ? 4 : 8; }  // columns in blocks of 32
 
-inline size_t chunk_space(const DeltaDims& d, int dtype, void* base, ChunkSpace* c) {
-  const size_t in = dtype == SSM_DTYPE_F32 ? 3 : 1, out = dtype == SSM_DTYPE_F32 ? 3 : 2, kt = delta_kt(d.K);
+// Carves the forward's or the backward's space from `base` (NULL: counts only);
+// returns the bytes.
+inline size_t chunk_space(const DeltaDims& d, int dtype, bool back, char* base, ChunkSpace* c) {
+  const size_t in = dtype == SSM_DTYPE_F32 ? 3 : 1, out = dtype == SSM_DTYPE_F32 || back ? 3 : 2, kt = delta_kt(d.K);
   const size_t n = static_cast<size_t>(d.chunks()), frag = 64 * sizeof(u32x4);
   const size_t rows = n * d.hk * in * 4 * kt * frag, tri = n * d.hv * kTri * frag;
-  char* p = static_cast<char*>(base);
   size_t at = 0;
   const auto take = [&](size_t bytes) {
-    char* const r = p ? p + at : nullptr;
+    char* const r = base ? base + at : nullptr;
     at += bytes;
     return r;
   };
   ChunkSpace s;
   s.kf = reinterpret_cast<u32x4*>(take(rows));
-  s.qf = reinterpret_cast<u32x4*>(take(rows));
+  s.qf = reinterpret_cast<u32x4*>(take(back ? 0 : rows));
   s.ktf = reinterpret_cast<u32x4*>(take(rows));
+  s.qtf = reinterpret_cast<u32x4*>(take(back ? rows : 0));
   s.tf = reinterpret_cast<u32x4*>(take(3 * tri));
   s.pf = reinterpret_cast<u32x4*>(take(out * tri));
   s.vec = reinterpret_cast<float*>(take(n * d.hv * 2 * kDeltaC * 4));
@@ -222,8 +241,12 @@ inline size_t chunk_space(const DeltaDims& d, int dtype, void* base, ChunkSpace*
   return at;
 }
 
-// Launches the preparation of every chunk.
-void delta_prep(int dtype, const void* q, const void* k, const float* beta, const float* g, const int32_t* cu,
-                const DeltaDims& d, const ChunkSpace& c, hipStream_t stream);
+// Launches the preparation of every chunk, the forward's or the backward's.
+void delta_prep(int dtype, bool back, const void* q, const void* k, const float* beta, const float* g,
+                const int32_t* cu, const DeltaDims& d, const ChunkSpace& c, hipStream_t stream);
+
+// The forward over chunks; out, last and mids may be NULL (delta_fwd.hip).
+void delta_chunks(int dtype, const void* v, float scale, void* out, float* last, const float* first, float* mids,
+                  const int32_t* cu, const DeltaDims& d, const ChunkSpace& c, hipStream_t stream);
 
 }  // namespace ssm

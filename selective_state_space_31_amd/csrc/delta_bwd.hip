@@ -5,11 +5,665 @@
 namespace ssm {
 namespace {
 
-size_t bwd_bytes(const DeltaDims& d, int dtype, bool have) {
-  (void)d;
-  (void)dtype;
-  (void)have;
-  return 0;
+// ---------------------------------------------------------------------------
+// the states' gradients, chunk after chunk from the last one
+// ---------------------------------------------------------------------------
+template <typename TA>
+struct BackArgs {
+  const TA* dout;
+  TA* dv;
+  const float *dlast, *beta;
+  float *dfirst, *dmid, *y;  // dmid: the gradient of the state behind every chunk; y: T^T dU of its tokens
+  const int32_t* cu;
+  ChunkSpace c;
+  float scale;
+  int64_t nseq, L;
+  int hk, hv, K, V, slices;
+};
+
+// With dS1 the gradient of the state behind a chunk, per block of 16 NC columns:
+//   dU = d (K dS1) + scale P^T dO;  Y = T^T dU;  dV = beta Y
+//   dS0 = gamma_C dS1 + scale Q^T (gamma dO) - K^T (gamma beta Y)
+// The forward's layout: wave w has the tokens 16 w .. + 15 and every fourth row
+// block of dS.
+template <typename TA, int KT, int NC>
+__global__ void __launch_bounds__(256) delta_back_kernel(const BackArgs<TA> p) {
+  constexpr int IN = ActParts<TA>::in, TW = (KT + 1) / 2;
+  __shared__ u32x4 sS[3][KT][NC][64], sU[3][2][NC][64], sZ[3][2][NC][64], sG[3][2][NC][64], sO[IN][2][NC][64];
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // (a head's workgroups on one XCD, as in the forward)
+  const unsigned wide = 8u * static_cast<unsigned>(p.slices);
+  const int64_t pair = int64_t{blockIdx.x / wide} * 8 + (blockIdx.x % wide & 7);
+  if (pair >= p.nseq * p.hv) return;
+  const int c0 = static_cast<int>(blockIdx.x % wide >> 3) * 16 * NC;
+  const int64_t b = pair / p.hv;
+  const int h = static_cast<int>(pair - b * p.hv), j = h / (p.hv / p.hk);
+  const DeltaSeq q = delta_seq(p.cu, b, p.L);
+  const int nc = static_cast<int>((q.hi - q.lo + kDeltaC - 1) / kDeltaC);
+  const size_t sv = static_cast<size_t>(p.K) * p.V;
+  const bool tiles = TW > 1 || w < 2 * KT;
+
+  const auto state_io = [&](auto&& f) {
+#pragma unroll
+    for (int i = 0; i < TW; ++i)
+#pragma unroll
+      for (int nb = 0; nb < NC; ++nb)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * (w + 4 * i) + 4 * g + r, col = c0 + 16 * nb + n;
+          if (tiles && row < p.K && col < p.V) f(i, nb, r, static_cast<size_t>(row) * p.V + col);
+        }
+  };
+  f32x4 S[TW][NC];
+#pragma unroll
+  for (int i = 0; i < TW; ++i)
+#pragma unroll
+    for (int nb = 0; nb < NC; ++nb) S[i][nb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  if (p.dlast) {
+    const float* const src = p.dlast + pair * sv;
+    state_io([&](int i, int nb, int r, size_t at) { S[i][nb][r] = src[at]; });
+  }
+  const auto put_state = [&]() {
+    if (tiles)
+#pragma unroll
+      for (int i = 0; i < TW; ++i)
+#pragma unroll
+        for (int nb = 0; nb < NC; ++nb) put_parts<3, NC>(&sS[0][0][0][0], KT, w + 4 * i, nb, lane, S[i][nb]);
+  };
+
+  // left operands of one chunk, and its gradients of out
+  u32x4 fk[KT][IN], ft[2][3], fp[2][3], fqt[TW][2][IN], fkt[TW][2][IN];
+  float ga[4], de[4], be[4], gC, nga[4], nde[4], nbe[4], ngC;
+  f32x4 dO[NC], ndO[NC];
+  const int kb0 = w >> 1;  // the triangles' rows w have the blocks kb0 .. 1
+  const auto load_k = [&](int64_t slot) {
+    const size_t at = static_cast<size_t>(slot * p.hk + j) * IN * 4 * KT * 64 + lane;
+#pragma unroll
+    for (int kb = 0; kb < KT; ++kb)
+#pragma unroll
+      for (int i = 0; i < IN; ++i) fk[kb][i] = p.c.kf[at + ((i * 4 + w) * KT + kb) * 64];
+  };
+  const auto load_tri = [&](int64_t slot, const u32x4* src, u32x4 (&f)[2][3]) {
+    const size_t at = static_cast<size_t>(slot * p.hv + h) * 3 * kTri * 64 + lane;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (kb >= kb0) f[kb][i] = src[at + (i * kTri + tri_up(w, kb)) * 64];
+  };
+  const auto load_cols = [&](int64_t slot) {
+    const size_t at = static_cast<size_t>(slot * p.hk + j) * IN * 2 * KT * 2 * 64 + lane;
+    if (tiles)
+#pragma unroll
+      for (int x = 0; x < TW; ++x)
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int i = 0; i < IN; ++i) {
+            fqt[x][kb][i] = p.c.qtf[at + ((i * 2 * KT + w + 4 * x) * 2 + kb) * 64];
+            fkt[x][kb][i] = p.c.ktf[at + ((i * 2 * KT + w + 4 * x) * 2 + kb) * 64];
+          }
+  };
+  const auto load_o = [&](int64_t slot, int64_t t0) {
+    const float* const vec = p.c.vec + (slot * p.hv + h) * 2 * kDeltaC;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      nga[r] = vec[16 * w + 4 * g + r];
+      nde[r] = vec[kDeltaC + 16 * w + 4 * g + r];
+      const int64_t t = t0 + 16 * w + 4 * g + r;
+      nbe[r] = t < q.hi ? p.beta[t * p.hv + h] : 0.0f;
+#pragma unroll
+      for (int nb = 0; nb < NC; ++nb) {
+        const int col = c0 + 16 * nb + n;
+        ndO[nb][r] = t < q.hi && col < p.V ? to_f32(p.dout[(t * p.hv + h) * p.V + col]) : 0.0f;
+      }
+    }
+    ngC = vec[kDeltaC - 1];
+  };
+  const auto take_o = [&]() {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      ga[r] = nga[r];
+      de[r] = nde[r];
+      be[r] = nbe[r];
+    }
+    gC = ngC;
+#pragma unroll
+    for (int nb = 0; nb < NC; ++nb) {
+      dO[nb] = ndO[nb];
+      put_parts<IN, NC>(&sO[0][0][0][0], 2, w, nb, lane, dO[nb]);
+    }
+  };
+  if (nc > 0) {
+    const int64_t slot = q.slot + nc - 1;
+    load_k(slot);
+    load_o(slot, q.lo + int64_t{nc - 1} * kDeltaC);
+    load_tri(slot, p.c.pf, fp);
+    load_tri(slot, p.c.tf, ft);
+    load_cols(slot);
+    put_state();
+    take_o();
+  }
+  __syncthreads();
+  for (int c = nc - 1; c >= 0; --c) {
+    const int64_t slot = q.slot + c, t0 = q.lo + int64_t{c} * kDeltaC;
+    const int more = c > 0 ? 1 : 0;  // (the first chunk's loads ahead are its own again)
+    {
+      float* const dst = p.dmid + (slot * p.hv + h) * sv;
+      state_io([&](int i, int nb, int r, size_t at) { dst[at] = S[i][nb][r]; });
+    }
+    load_o(slot - more, t0 - more * kDeltaC);
+    // ---- dU ----
+#pragma unroll
+    for (int nb = 0; nb < NC; ++nb) {
+      f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
+#pragma unroll
+      for (int kb = 0; kb < KT; ++kb) {
+        u32x4 s[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) s[i] = sS[i][kb][nb][lane];
+        x = mul_parts<3>(fk[kb], s, x);
+      }
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        if (kb < kb0) continue;
+        u32x4 o[IN];
+#pragma unroll
+        for (int i = 0; i < IN; ++i) o[i] = sO[i][kb][nb][lane];
+        y = mul_parts<3>(fp[kb], o, y);
+      }
+      f32x4 z;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        x[r] = de[r] * x[r] + p.scale * y[r];
+        z[r] = p.scale * ga[r] * dO[nb][r];
+      }
+      put_parts<3, NC>(&sU[0][0][0][0], 2, w, nb, lane, x);
+      put_parts<3, NC>(&sG[0][0][0][0], 2, w, nb, lane, z);
+    }
+    load_k(slot - more);
+    load_tri(slot - more, p.c.pf, fp);
+    __syncthreads();
+    // ---- Y, dV ----
+    const float decay = gC;
+#pragma unroll
+    for (int nb = 0; nb < NC; ++nb) {
+      f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        if (kb < kb0) continue;
+        u32x4 u[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) u[i] = sU[i][kb][nb][lane];
+        y = mul_parts<3>(ft[kb], u, y);
+      }
+      const int col = c0 + 16 * nb + n;
+      float* const dst = p.y + ((slot * p.hv + h) * kDeltaC + 16 * w + 4 * g) * p.V + col;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int64_t t = t0 + 16 * w + 4 * g + r;
+        if (col < p.V) dst[static_cast<size_t>(r) * p.V] = y[r];
+        y[r] *= be[r];
+        if (t < q.hi && col < p.V) store_act(p.dv + (t * p.hv + h) * p.V + col, y[r]);
+        y[r] *= -ga[r];
+      }
+      put_parts<3, NC>(&sZ[0][0][0][0], 2, w, nb, lane, y);
+    }
+    load_tri(slot - more, p.c.tf, ft);
+    take_o();
+    __syncthreads();
+    // ---- dS0 ----
+    if (tiles) {
+#pragma unroll
+      for (int nb = 0; nb < NC; ++nb) {
+#pragma unroll
+        for (int i = 0; i < TW; ++i) S[i][nb] *= decay;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          u32x4 o[3], z[3];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            o[i] = sG[i][kb][nb][lane];
+            z[i] = sZ[i][kb][nb][lane];
+          }
+#pragma unroll
+          for (int i = 0; i < TW; ++i) {
+            S[i][nb] = mul_parts<3>(fqt[i][kb], o, S[i][nb]);
+            S[i][nb] = mul_parts<3>(fkt[i][kb], z, S[i][nb]);
+          }
+        }
+      }
+      put_state();
+    }
+    load_cols(slot - more);
+    __syncthreads();
+  }
+  if (p.dfirst) {
+    float* const dst = p.dfirst + pair * sv;
+    state_io([&](int i, int nb, int r, size_t at) { dst[at] = S[i][nb][r]; });
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the inputs' gradients, every chunk by itself
+// ---------------------------------------------------------------------------
+template <typename TA>
+struct GradArgs {
+  const TA *q, *k, *v, *dout;
+  const float *beta, *g, *mids, *dmid, *y;
+  TA *dq, *dk;
+  float *dbeta, *dg;
+  const int32_t* cu;
+  ChunkSpace c;
+  float scale;
+  int64_t nseq, L, qs, ks, vs;
+  int hk, hv, K, V;
+};
+
+constexpr int kGradRow = kDeltaC + 4;
+
+// Eight float32 values of row r from column c (zeros behind `width` and for
+// rows that are not there), with 4-byte alignment
+__device__ __forceinline__ void load8(float (&x)[8], const float* row, bool there, int c, int width) {
+  if (there && c + 8 <= width) {
+    __builtin_memcpy(x, row + c, sizeof(x));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = there && c + e < width ? row[c + e] : 0.0f;
+  }
+}
+template <int N>
+__device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&f)[N]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    uint32_t part[N];
+    split2(x[2 * e], x[2 * e + 1], part);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i][e] = part[i];
+  }
+}
+template <typename TA>
+__device__ __forceinline__ void load8_act(float (&x)[8], const TA* row, bool there, int c, int width) {
+  TA raw[8];
+  if (there && c + 8 <= width) {
+    __builtin_memcpy(raw, row + c, sizeof(raw));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = to_f32(raw[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = there && c + e < width ? to_f32(row[c + e]) : 0.0f;
+  }
+}
+
+// Per value head, with S0 and U from the forward, dS1 and Y from the pass back
+// (G1 = dO U^T, G2 = Y U^T on and below, and below, the diagonal):
+//   F = scale D G1;  E = -beta D G2
+//   dQ = scale gamma (dO S0^T) + F K
+//   dK = [E K - gamma beta (Y S0^T)] + [d (U dS1^T) + E^T K + F^T Q] = read + write
+//   dbeta_i = v_i.y_i - gamma_i k_i.(Y S0^T)_i - sum_j (G2 D K K^T)_ij
+//   dG_i = q_i.dq_i + k_i.(read - write)_i  (e^{G_i} goes with what reads, e^{-G_i}
+//   with what writes), and <S1, dS1> for the last one; dg is their sum from behind
+// One workgroup a chunk and key head, over its value heads in turn.  Wave w has
+// the triangles' rows 16 w .. + 15 and the column blocks w, w + 4, .. of dQ and dK.
+template <typename TA, int KT>
+__global__ void __launch_bounds__(256) delta_grad_kernel(const GradArgs<TA> p) {
+  constexpr int IN = ActParts<TA>::in, CT = (KT + 1) / 2;
+  typedef float Mat[kDeltaC][kGradRow];
+  __shared__ u32x4 sF[12][3][64];  // dO, Y, U: 4 row blocks of 32 columns; then two triangles' 6 blocks
+  __shared__ Mat sE, sP;
+  __shared__ double sG[kDeltaC];
+  __shared__ float sga[kDeltaC], sde[kDeltaC], sbe[kDeltaC], sdb[kDeltaC], sdot[2][4][kDeltaC], sone[4];
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t slot = blockIdx.x / static_cast<unsigned>(p.hk);
+  const int j = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.hk)), rep = p.hv / p.hk;
+  const int64_t per = (p.L + kDeltaC - 1) / kDeltaC;
+  const int64_t b = p.cu ? delta_owner(p.cu, static_cast<int>(p.nseq), slot) : slot / per;
+  const DeltaSeq q = delta_seq(p.cu, b, p.L);
+  const int64_t t0 = q.lo + (slot - q.slot) * kDeltaC;
+  if (slot < q.slot || t0 >= q.hi) return;  // (a place that no chunk has)
+  const int valid = static_cast<int>(q.hi - t0 < kDeltaC ? q.hi - t0 : kDeltaC);
+  const size_t sv = static_cast<size_t>(p.K) * p.V, mv = sv + static_cast<size_t>(kDeltaC) * p.V;
+  const bool cols = CT > 1 || w < 2 * KT;  // (with 32 columns two waves hold none)
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+
+  f32x4 dq[4][CT], dk[4][CT];
+#pragma unroll
+  for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) dq[rt][ct] = dk[rt][ct] = zero;
+
+  for (int h = j * rep; h < (j + 1) * rep; ++h) {
+    const int64_t at = slot * p.hv + h;
+    const float *const S0 = p.mids + at * mv, *const U = S0 + sv, *const dS = p.dmid + at * sv,
+                *const Y = p.y + at * kDeltaC * p.V;
+    if (w == 0) {  // as in the preparation
+      const bool in = lane < valid;
+      const float x = in && p.g ? p.g[(t0 + lane) * p.hv + h] : 0.0f;
+      double G = x < -1e4f ? -1e4 : static_cast<double>(x);
+#pragma unroll
+      for (int m = 1; m < 64; m <<= 1) {
+        const double up = __shfl_up(G, m);
+        if (lane >= m) G += up;
+      }
+      sG[lane] = G;
+      sga[lane] = expf(static_cast<float>(G));
+      sde[lane] = expf(static_cast<float>(__shfl(G, 63) - G));
+      sbe[lane] = in ? p.beta[(t0 + lane) * p.hv + h] : 0.0f;
+    }
+    f32x4 r1[4][CT], r2[4][CT], r3[4][CT], g1[4], g2[4];
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) {
+      g1[rt] = g2[rt] = zero;
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) r1[rt][ct] = r2[rt][ct] = r3[rt][ct] = zero;
+    }
+    float vy = 0.0f, ss = 0.0f;
+    const int row = 16 * w + n;
+    for (int vb = 0; vb < p.V; vb += 32) {
+      const int c = vb + 8 * g;
+      float xo[8], xy[8], xu[8], xv[8];
+      const int64_t tok = (t0 + row) * p.hv + h;
+      load8_act(xo, p.dout + tok * p.V, row < valid, c, p.V);
+      load8_act(xv, p.v + (t0 + row) * p.vs + h * p.V, row < valid, c, p.V);
+      load8(xy, Y + static_cast<size_t>(row) * p.V, true, c, p.V);
+      load8(xu, U + static_cast<size_t>(row) * p.V, true, c, p.V);
+      u32x4 fo[IN], fy[3], fu[3];
+      split8(xo, fo);
+      split8(xy, fy);
+      split8(xu, fu);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) vy = __builtin_fmaf(xv[e], xy[e], vy);
+      __syncthreads();  // (what was in LDS has been used)
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        if (i < IN) sF[w][i][lane] = fo[i < IN ? i : 0];
+        sF[4 + w][i][lane] = fy[i];
+        sF[8 + w][i][lane] = fu[i];
+      }
+      __syncthreads();
+      if (cols) {
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          const int d = 16 * (w + 4 * ct) + n;
+          float xs[8], xd[8];
+          load8(xs, S0 + static_cast<size_t>(d) * p.V, d < p.K, c, p.V);
+          load8(xd, dS + static_cast<size_t>(d) * p.V, d < p.K, c, p.V);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(xs[e], xd[e], ss);
+          u32x4 fs[3], fd[3];
+          split8(xs, fs);
+          split8(xd, fd);
+#pragma unroll
+          for (int rt = 0; rt < 4; ++rt) {
+            u32x4 a[IN], y[3], u[3];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+              if (i < IN) a[i < IN ? i : 0] = sF[rt][i][lane];
+              y[i] = sF[4 + rt][i][lane];
+              u[i] = sF[8 + rt][i][lane];
+            }
+            r1[rt][ct] = mul_parts<3>(a, fs, r1[rt][ct]);
+            r2[rt][ct] = mul_parts<3>(y, fs, r2[rt][ct]);
+            r3[rt][ct] = mul_parts<3>(u, fd, r3[rt][ct]);
+          }
+        }
+      }
+#pragma unroll
+      for (int jt = 0; jt < 4; ++jt) {
+        if (jt > w) continue;
+        u32x4 u[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) u[i] = sF[8 + jt][i][lane];
+        g1[jt] = mul_parts<3>(fo, u, g1[jt]);
+        g2[jt] = mul_parts<3>(fy, u, g2[jt]);
+      }
+    }
+    __syncthreads();
+    // ---- E, F, and what dbeta takes from A ----
+    f32x4 db = zero;
+    const size_t kat = static_cast<size_t>(slot * p.hk + j) * IN * 4 * KT * 64 + lane;
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) {
+      if (jt > w) continue;
+      f32x4 kk = zero;
+#pragma unroll
+      for (int kb = 0; kb < KT; ++kb) {
+        u32x4 a[IN], c[IN];
+#pragma unroll
+        for (int i = 0; i < IN; ++i) {
+          a[i] = p.c.kf[kat + ((i * 4 + w) * KT + kb) * 64];
+          c[i] = p.c.kf[kat + ((i * 4 + jt) * KT + kb) * 64];
+        }
+        kk = mul_parts<3>(a, c, kk);
+      }
+      const int col = 16 * jt + n;
+      const double Gc = sG[col];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = 16 * w + 4 * g + e;
+        const float D = i >= col ? expf(static_cast<float>(sG[i] - Gc)) : 0.0f;
+        const float m = i > col ? -D * g2[jt][e] : 0.0f;
+        sE[i][col] = sbe[i] * m;
+        sP[i][col] = i >= col ? p.scale * D * g1[jt][e] : 0.0f;
+        db[e] = __builtin_fmaf(m, kk[e], db[e]);
+      }
+    }
+    if (w % 2 == 0) {  // the block right of the diagonal completes a fragment's 32 columns
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sE[16 * w + 4 * g + e][16 * w + 16 + n] = sP[16 * w + 4 * g + e][16 * w + 16 + n] = 0.0f;
+    }
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) db[e] += __shfl_xor(db[e], m);
+    vy += __shfl_xor(vy, 16);
+    vy += __shfl_xor(vy, 32);
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) ss += __shfl_xor(ss, m);
+    if (n == 0)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sdb[16 * w + 4 * g + e] = db[e];
+    if (lane == 0) sone[w] = ss;
+    __syncthreads();
+    if (lane < 16) sdb[16 * w + lane] += vy;  // (row 16 w + n: lanes of this wave alone)
+    // ---- the triangles as left operands: E and F, then E^T and F^T ----
+    const size_t cat = static_cast<size_t>(slot * p.hk + j) * IN * 2 * KT * 2 * 64 + lane;
+    float dots[4][4], bdot[4][4], cross = 0.0f;
+    // rows' scales, the part of dG and of dbeta that stands before the triangles' products
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * rt + 4 * g + r;
+        const float ga = sga[i], de = sde[i], be = sbe[i];
+        dots[rt][r] = bdot[rt][r] = 0.0f;
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          const int d = 16 * (w + 4 * ct) + n;
+          const float kx = cols && i < valid && d < p.K ? to_f32(p.k[(t0 + i) * p.ks + j * p.K + d]) : 0.0f;
+          bdot[rt][r] = __builtin_fmaf(kx, r2[rt][ct][r], bdot[rt][r]);
+          r1[rt][ct][r] *= p.scale * ga;
+          r2[rt][ct][r] *= -ga * be;
+          r3[rt][ct][r] *= de;
+          cross = __builtin_fmaf(kx, r3[rt][ct][r], cross);
+        }
+        bdot[rt][r] *= -ga;
+      }
+#pragma unroll
+    for (int turn = 0; turn < 2; ++turn) {
+      __syncthreads();
+      for (int kb = turn ? w >> 1 : 0; kb <= (turn ? 1 : w >> 1); ++kb) {
+        const int c = 32 * kb + 8 * g, f = turn ? tri_up(w, kb) : tri_at(w, kb);
+        float xe[8], xf[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          xe[e] = turn ? sE[c + e][row] : sE[row][c + e];
+          xf[e] = turn ? sP[c + e][row] : sP[row][c + e];
+        }
+        u32x4 fe[3], ff[3];
+        split8(xe, fe);
+        split8(xf, ff);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          sF[f][i][lane] = fe[i];
+          sF[6 + f][i][lane] = ff[i];
+        }
+      }
+      __syncthreads();
+      if (cols) {
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb) {
+            u32x4 kt[IN], qt[IN];
+#pragma unroll
+            for (int i = 0; i < IN; ++i) {
+              kt[i] = p.c.ktf[cat + ((i * 2 * KT + w + 4 * ct) * 2 + kb) * 64];
+              if (turn) qt[i] = p.c.qtf[cat + ((i * 2 * KT + w + 4 * ct) * 2 + kb) * 64];
+            }
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+              if (turn ? kb < rt >> 1 : kb > rt >> 1) continue;
+              const int f = turn ? tri_up(rt, kb) : tri_at(rt, kb);
+              u32x4 e[3], x[3];
+#pragma unroll
+              for (int i = 0; i < 3; ++i) {
+                e[i] = sF[f][i][lane];
+                x[i] = sF[6 + f][i][lane];
+              }
+              if (turn) {
+                r3[rt][ct] = mul_parts<3>(e, kt, r3[rt][ct]);
+                r3[rt][ct] = mul_parts<3>(x, qt, r3[rt][ct]);
+              } else {
+                r2[rt][ct] = mul_parts<3>(e, kt, r2[rt][ct]);
+                r1[rt][ct] = mul_parts<3>(x, kt, r1[rt][ct]);
+              }
+            }
+          }
+      }
+    }
+    // ---- dG, dbeta: sums over the rows ----
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * rt + 4 * g + r;
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          const int d = 16 * (w + 4 * ct) + n;
+          const bool there = cols && i < valid && d < p.K;
+          const float kx = there ? to_f32(p.k[(t0 + i) * p.ks + j * p.K + d]) : 0.0f;
+          const float qx = there ? to_f32(p.q[(t0 + i) * p.qs + j * p.K + d]) : 0.0f;
+          dots[rt][r] = __builtin_fmaf(qx, r1[rt][ct][r], dots[rt][r]);
+          dots[rt][r] = __builtin_fmaf(kx, r2[rt][ct][r] - r3[rt][ct][r], dots[rt][r]);
+          dq[rt][ct][r] += r1[rt][ct][r];
+          dk[rt][ct][r] += r2[rt][ct][r] + r3[rt][ct][r];
+        }
+#pragma unroll
+        for (int m = 1; m < 16; m <<= 1) {
+          dots[rt][r] += __shfl_xor(dots[rt][r], m);
+          bdot[rt][r] += __shfl_xor(bdot[rt][r], m);
+        }
+        if (n == 0) {
+          sdot[0][w][i] = dots[rt][r];
+          sdot[1][w][i] = bdot[rt][r];
+        }
+      }
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) cross += __shfl_xor(cross, m);
+    if (lane == 0) sone[w] = __builtin_fmaf(sga[kDeltaC - 1], sone[w], cross);
+    __syncthreads();
+    if (w == 0) {
+      const float last = (sone[0] + sone[1]) + (sone[2] + sone[3]);
+      float d = (sdot[0][0][lane] + sdot[0][1][lane]) + (sdot[0][2][lane] + sdot[0][3][lane]);
+      const float e = (sdot[1][0][lane] + sdot[1][1][lane]) + (sdot[1][2][lane] + sdot[1][3][lane]);
+#pragma unroll
+      for (int m = 1; m < 64; m <<= 1) {  // the sum from behind
+        const float up = __shfl_down(d, m);
+        if (lane + m < 64) d += up;
+      }
+      if (lane < valid) {
+        p.dbeta[(t0 + lane) * p.hv + h] = sdb[lane] + e;
+        if (p.dg) p.dg[(t0 + lane) * p.hv + h] = d + last;
+      }
+    }
+    __syncthreads();
+  }
+  if (!cols) return;
+#pragma unroll
+  for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int i = 16 * rt + 4 * g + r;
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        const int d = 16 * (w + 4 * ct) + n;
+        if (i < valid && d < p.K) {
+          store_act(p.dq + ((t0 + i) * p.hk + j) * p.K + d, dq[rt][ct][r]);
+          store_act(p.dk + ((t0 + i) * p.hk + j) * p.K + d, dk[rt][ct][r]);
+        }
+      }
+    }
+}
+
+// The gradients' own space: the backward's chunk parts, the state gradients, Y,
+// and without chunk_states those and the forward's chunk parts.
+struct BackSpace {
+  ChunkSpace back, fwd;
+  float *dmid, *y, *mids;
+};
+
+size_t back_space(const DeltaDims& d, int dtype, bool have, char* base, BackSpace* s) {
+  BackSpace x{};
+  size_t at = chunk_space(d, dtype, true, base, &x.back);
+  const auto take = [&](size_t bytes) {
+    char* const r = base ? base + at : nullptr;
+    at += (bytes + 255) / 256 * 256;
+    return reinterpret_cast<float*>(r);
+  };
+  x.dmid = take(static_cast<size_t>(d.chunks()) * d.state_values() * 4);
+  x.y = take(static_cast<size_t>(d.chunks()) * d.hv * kDeltaC * d.V * 4);
+  x.mids = nullptr;
+  if (!have) {
+    x.mids = take(d.mid_values() * 4);
+    at += chunk_space(d, dtype, false, base ? base + at : nullptr, &x.fwd);
+  }
+  if (s) *s = x;
+  return at;
+}
+
+size_t bwd_bytes(const DeltaDims& d, int dtype, bool have) { return back_space(d, dtype, have, nullptr, nullptr); }
+
+template <typename TA, int KT>
+void launch_bwd(const BackArgs<TA>& a, const GradArgs<TA>& e, int64_t chunks, hipStream_t stream) {
+  const int64_t pairs = a.nseq * a.hv;
+  hipLaunchKernelGGL((delta_back_kernel<TA, KT, 1>), dim3(static_cast<unsigned>((pairs + 7) / 8 * 8 * a.slices)),
+                     dim3(256), 0, stream, a);
+  if (a.L > 0)
+    hipLaunchKernelGGL((delta_grad_kernel<TA, KT>), dim3(static_cast<unsigned>(chunks * a.hk)), dim3(256), 0, stream,
+                       e);
+}
+
+template <typename TA>
+int run_bwd(const char* fn, const void* q, const void* k, const void* v, const float* beta, const float* g,
+            float scale, const float* mids, const void* dout, const float* dlast, void* dq, void* dk, void* dv,
+            float* dbeta, float* dg, float* dfirst, const int32_t* cu, const DeltaDims& d, const BackSpace& s,
+            hipStream_t stream) {
+  const BackArgs<TA> a{static_cast<const TA*>(dout), static_cast<TA*>(dv), dlast, beta, dfirst, s.dmid, s.y, cu,
+                       s.back, scale, d.nseq, d.L, d.hk, d.hv, d.K, d.V, (d.V + 15) / 16};
+  const GradArgs<TA> e{static_cast<const TA*>(q), static_cast<const TA*>(k), static_cast<const TA*>(v),
+                       static_cast<const TA*>(dout), beta, g, mids, s.dmid, s.y, static_cast<TA*>(dq),
+                       static_cast<TA*>(dk), dbeta, dg, cu, s.back, scale, d.nseq, d.L, d.qs, d.ks, d.vs, d.hk, d.hv,
+                       d.K, d.V};
+  switch (delta_kt(d.K)) {
+    case 1: launch_bwd<TA, 1>(a, e, d.chunks(), stream); break;
+    case 2: launch_bwd<TA, 2>(a, e, d.chunks(), stream); break;
+    case 4: launch_bwd<TA, 4>(a, e, d.chunks(), stream); break;
+    default: launch_bwd<TA, 8>(a, e, d.chunks(), stream); break;
+  }
+  return launch_status(fn);
 }
 
 int delta_bwd(const char* fn, const void* q, const void* k, const void* v, const float* beta, const float* g,
@@ -49,7 +703,7 @@ int delta_bwd(const char* fn, const void* q, const void* k, const void* v, const
                       {beta, gate, "beta"},
                       {g, g ? gate : 0, "g"},
                       {first, first ? st : 0, "initial_state"},
-                      {mids, mids ? d.chunks() * d.state_values() * 4 : 0, "chunk_states"},
+                      {mids, mids ? d.mid_values() * 4 : 0, "chunk_states"},
                       {dout, val, "dout"},
                       {dlast, dlast ? st : 0, "dlast_state"},
                       {cu, packed ? static_cast<size_t>(nseq + 1) * 4 : 0, "cu_seqlens"}};
@@ -69,9 +723,18 @@ int delta_bwd(const char* fn, const void* q, const void* k, const void* v, const
   if (need > 0 && !aligned(ws, 256))
     return fail(SSM_ERR_ALIGN, "%s: workspace is not 256-byte aligned", fn);
   if (L == 0 && !dfirst) return SSM_OK;
-  (void)scale;
-  (void)stream;
-  return fail(SSM_ERR_UNSUPPORTED, "%s: not built yet", fn);
+  if (!packed) cu = nullptr;
+  BackSpace x;
+  back_space(d, dtype, mids != nullptr, static_cast<char*>(ws), &x);
+  if (L > 0) {
+    if (!mids) {
+      delta_prep(dtype, false, q, k, beta, g, cu, d, x.fwd, stream);
+      delta_chunks(dtype, v, scale, nullptr, nullptr, first, x.mids, cu, d, x.fwd, stream);
+    }
+    delta_prep(dtype, true, q, k, beta, g, cu, d, x.back, stream);
+  }
+  return (dtype == SSM_DTYPE_F32 ? run_bwd<float> : run_bwd<bf16_t>)(
+      fn, q, k, v, beta, g, scale, mids ? mids : x.mids, dout, dlast, dq, dk, dv, dbeta, dg, dfirst, cu, d, x, stream);
 }
 
 size_t query(int64_t nseq, int64_t L, int64_t hk, int64_t hv, int64_t K, int64_t V, bool packed, int dtype, int have) {

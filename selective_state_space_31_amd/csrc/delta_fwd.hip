@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(256) delta_rec_kernel(const RecArgs<TA> p) {
   const int h = static_cast<int>(pair - b * p.hv), j = h / (p.hv / p.hk);
   const DeltaSeq q = delta_seq(p.cu, b, p.L);
   const int nc = static_cast<int>((q.hi - q.lo + kDeltaC - 1) / kDeltaC);
-  const size_t sv = static_cast<size_t>(p.K) * p.V;
+  const size_t sv = static_cast<size_t>(p.K) * p.V, mv = sv + static_cast<size_t>(kDeltaC) * p.V;
   const bool tiles = TW > 1 || w < 2 * KT;  // (with 32 rows two waves hold none)
 
   // state values of this lane: row block t, column block nb
@@ -67,22 +67,12 @@ __global__ void __launch_bounds__(256) delta_rec_kernel(const RecArgs<TA> p) {
     const float* const src = p.first + pair * sv;
     state_io([&](int i, int nb, int r, size_t at) { S[i][nb][r] = src[at]; });
   }
-  const auto put = [&](u32x4* base, int blocks, int t, int nb, f32x4 x, auto parts) {
-    constexpr int N = decltype(parts)::value;
-    uint32_t lo[N], hi[N];
-    split2(x[0], x[1], lo);
-    split2(x[2], x[3], hi);
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      *reinterpret_cast<u32x2*>(reinterpret_cast<char*>(base + ((i * blocks + (t >> 1)) * NC + nb) * 64) +
-                                frag_put(lane, t)) = u32x2{lo[i], hi[i]};
-  };
   const auto put_state = [&]() {
     if (tiles)
 #pragma unroll
       for (int i = 0; i < TW; ++i)
 #pragma unroll
-        for (int nb = 0; nb < NC; ++nb) put(&sS[0][0][0][0], KT, w + 4 * i, nb, S[i][nb], Parts<3>{});
+        for (int nb = 0; nb < NC; ++nb) put_parts<3, NC>(&sS[0][0][0][0], KT, w + 4 * i, nb, lane, S[i][nb]);
   };
   if (nc > 0) put_state();
 
@@ -152,7 +142,7 @@ __global__ void __launch_bounds__(256) delta_rec_kernel(const RecArgs<TA> p) {
     const int64_t slot = q.slot + c, t0 = q.lo + int64_t{c} * kDeltaC;
     const int more = c + 1 < nc ? 1 : 0;  // (the last chunk's loads ahead are its own again)
     if constexpr (MIDS) {
-      float* const dst = p.mids + (slot * p.hv + h) * sv;
+      float* const dst = p.mids + (slot * p.hv + h) * mv;
       state_io([&](int i, int nb, int r, size_t at) { dst[at] = S[i][nb][r]; });
     }
     // ---- X and Q S0 ----
@@ -173,7 +163,7 @@ __global__ void __launch_bounds__(256) delta_rec_kernel(const RecArgs<TA> p) {
         o[nb][r] = ga[r] * y[r];
         x[r] = to_f32(rv[nb][r]) - ga[r] * x[r];
       }
-      put(&sX[0][0][0][0], 2, w, nb, x, Parts<3>{});
+      put_parts<3, NC>(&sX[0][0][0][0], 2, w, nb, lane, x);
     }
     load_kq(slot + more);
     float dl[4];
@@ -194,10 +184,17 @@ __global__ void __launch_bounds__(256) delta_rec_kernel(const RecArgs<TA> p) {
         for (int i = 0; i < 3; ++i) x[i] = sX[i][kb][nb][lane];
         u = mul_parts<3>(ft[kb], x, u);
       }
-      put(&sU[0][0][0][0], 2, w, nb, u, Parts<OUT>{});
+      put_parts<OUT, NC>(&sU[0][0][0][0], 2, w, nb, lane, u);
+      if constexpr (MIDS) {
+        const int col = c0 + 16 * nb + n;
+        float* const dst = p.mids + (slot * p.hv + h) * mv + sv + col;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (col < p.V) dst[static_cast<size_t>(16 * w + 4 * g + r) * p.V] = u[r];
+      }
 #pragma unroll
       for (int r = 0; r < 4; ++r) u[r] *= dl[r];
-      put(&sD[0][0][0][0], 2, w, nb, u, Parts<3>{});
+      put_parts<3, NC>(&sD[0][0][0][0], 2, w, nb, lane, u);
     }
     load_t(slot + more);
     __syncthreads();
@@ -233,7 +230,7 @@ __global__ void __launch_bounds__(256) delta_rec_kernel(const RecArgs<TA> p) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int64_t t = t0 + 16 * w + 4 * g + r;
-        if (t < q.hi && col < p.V) store_act(p.out + (t * p.hv + h) * p.V + col, p.scale * o[nb][r]);
+        if (p.out && t < q.hi && col < p.V) store_act(p.out + (t * p.hv + h) * p.V + col, p.scale * o[nb][r]);
       }
     }
     load_pkt(slot + more);
@@ -254,8 +251,8 @@ void launch_rec(const RecArgs<TA>& a, hipStream_t stream) {
 }
 
 template <typename TA>
-int run_chunks(const char* fn, const void* v, float scale, void* out, float* last, const float* first, float* mids,
-               const int32_t* cu, const DeltaDims& d, const ChunkSpace& c, hipStream_t stream) {
+void run_chunks(const void* v, float scale, void* out, float* last, const float* first, float* mids,
+                const int32_t* cu, const DeltaDims& d, const ChunkSpace& c, hipStream_t stream) {
   RecArgs<TA> a{static_cast<const TA*>(v), static_cast<TA*>(out), first, last, mids, cu, c, scale, d.nseq, d.L, d.vs,
                 d.hk, d.hv, d.K, d.V, (d.V + 15) / 16};
   switch (delta_kt(d.K)) {
@@ -264,10 +261,9 @@ int run_chunks(const char* fn, const void* v, float scale, void* out, float* las
     case 4: launch_rec<TA, 4, 1>(a, stream); break;
     default: launch_rec<TA, 8, 1>(a, stream); break;
   }
-  return launch_status(fn);
 }
 
-size_t fwd_bytes(const DeltaDims& d, int dtype) { return chunk_space(d, dtype, nullptr, nullptr); }
+size_t fwd_bytes(const DeltaDims& d, int dtype) { return chunk_space(d, dtype, false, nullptr, nullptr); }
 
 int delta_fwd(const char* fn, const void* q, const void* k, const void* v, const float* beta, const float* g,
               float scale, void* out, float* last, const float* first, float* mids, const int32_t* cu, bool packed,
@@ -304,7 +300,7 @@ int delta_fwd(const char* fn, const void* q, const void* k, const void* v, const
                       {cu, packed ? static_cast<size_t>(nseq + 1) * 4 : 0, "cu_seqlens"}};
   const Span outs[] = {{out, static_cast<size_t>(d.tokens()) * hv * V * es, "out"},
                        {last, last ? st : 0, "last_state"},
-                       {mids, mids ? d.chunks() * d.state_values() * 4 : 0, "chunk_states"},
+                       {mids, mids ? d.mid_values() * 4 : 0, "chunk_states"},
                        {ws, ws ? need : 0, "workspace"}};
   for (const auto& o : outs)
     for (const auto& n : ins)
@@ -321,10 +317,10 @@ int delta_fwd(const char* fn, const void* q, const void* k, const void* v, const
   if (L == 0 && !last) return SSM_OK;
   if (!packed) cu = nullptr;
   ChunkSpace c;
-  chunk_space(d, dtype, ws, &c);
-  if (L > 0) delta_prep(dtype, q, k, beta, g, cu, d, c, stream);
-  return dtype == SSM_DTYPE_F32 ? run_chunks<float>(fn, v, scale, out, last, first, mids, cu, d, c, stream)
-                                : run_chunks<bf16_t>(fn, v, scale, out, last, first, mids, cu, d, c, stream);
+  chunk_space(d, dtype, false, static_cast<char*>(ws), &c);
+  if (L > 0) delta_prep(dtype, false, q, k, beta, g, cu, d, c, stream);
+  delta_chunks(dtype, v, scale, out, last, first, mids, cu, d, c, stream);
+  return launch_status(fn);
 }
 
 size_t query(int64_t nseq, int64_t L, int64_t hk, int64_t hv, int64_t K, int64_t V, bool packed, int dtype) {
@@ -335,6 +331,13 @@ size_t query(int64_t nseq, int64_t L, int64_t hk, int64_t hv, int64_t K, int64_t
 }
 
 }  // namespace
+
+void delta_chunks(int dtype, const void* v, float scale, void* out, float* last, const float* first, float* mids,
+                  const int32_t* cu, const DeltaDims& d, const ChunkSpace& c, hipStream_t stream) {
+  if (dtype == SSM_DTYPE_F32) run_chunks<float>(v, scale, out, last, first, mids, cu, d, c, stream);
+  else run_chunks<bf16_t>(v, scale, out, last, first, mids, cu, d, c, stream);
+}
+
 }  // namespace ssm
 
 using namespace ssm;

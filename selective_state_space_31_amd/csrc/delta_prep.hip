@@ -27,9 +27,9 @@ __device__ __forceinline__ void put16(Mat& m, int i, int j, f32x4 c, float sign)
 }
 
 // One workgroup a chunk and value head; wave w has rows 16 w .. + 15.
-template <typename TA, int KT>
+template <typename TA, int KT, bool BACK>
 __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
-  constexpr int IN = ActParts<TA>::in, OUT = ActParts<TA>::out;
+  constexpr int IN = ActParts<TA>::in, OUT = BACK ? 3 : ActParts<TA>::out;
   __shared__ u32x4 sk[IN][4][KT][64];
   __shared__ Mat sA, sP, sT;
   __shared__ double sG[kDeltaC];
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
       for (int i = 0; i < IN; ++i) {
         if (which) qa[kb][i] = f[i];
         else sk[i][w][kb][lane] = f[i];
-        if (h % r == 0)
+        if (h % r == 0 && !(BACK && which))
           (which ? p.c.qf : p.c.kf)[((((slot * p.hk + j) * IN + i) * 4 + w) * KT + kb) * 64 + lane] = f[i];
       }
     }
@@ -168,32 +168,40 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
   }
   __syncthreads();
 
-  // ---- fragments of T diag(beta) and P; wave w its row block ----
-  for (int kb = 0; kb <= w >> 1; ++kb) {
+  // ---- fragments of T diag(beta) and P, or of T^T and P^T; wave w its row block ----
+  for (int kb = BACK ? w >> 1 : 0; kb <= (BACK ? 1 : w >> 1); ++kb) {
     const int c = 32 * kb + 8 * g;
     u32x4 ft[3], fp[OUT];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       uint32_t part[3], op[OUT];
-      split2(sT[row][c + 2 * e] * sbeta[c + 2 * e], sT[row][c + 2 * e + 1] * sbeta[c + 2 * e + 1], part);
-      split2(sP[row][c + 2 * e], sP[row][c + 2 * e + 1], op);
+      const int x = c + 2 * e;
+      if constexpr (BACK) {
+        split2(sT[x][row], sT[x + 1][row], part);
+        split2(sP[x][row], sP[x + 1][row], op);
+      } else {
+        split2(sT[row][x] * sbeta[x], sT[row][x + 1] * sbeta[x + 1], part);
+        split2(sP[row][x], sP[row][x + 1], op);
+      }
 #pragma unroll
       for (int i = 0; i < 3; ++i) ft[i][e] = part[i];
 #pragma unroll
       for (int i = 0; i < OUT; ++i) fp[i][e] = op[i];
     }
     const int64_t at = slot * p.hv + h;
+    const int f = BACK ? tri_up(w, kb) : tri_at(w, kb);
 #pragma unroll
-    for (int i = 0; i < 3; ++i) p.c.tf[((at * 3 + i) * kTri + tri_at(w, kb)) * 64 + lane] = ft[i];
+    for (int i = 0; i < 3; ++i) p.c.tf[((at * 3 + i) * kTri + f) * 64 + lane] = ft[i];
 #pragma unroll
-    for (int i = 0; i < OUT; ++i) p.c.pf[((at * OUT + i) * kTri + tri_at(w, kb)) * 64 + lane] = fp[i];
+    for (int i = 0; i < OUT; ++i) p.c.pf[((at * OUT + i) * kTri + f) * 64 + lane] = fp[i];
   }
-  // ---- fragments of K^T ----
-  if (h % r == 0) {
+  // ---- fragments of K^T (and Q^T) ----
+  if (h % r != 0) return;
+  const auto transposed = [&](u32x4* dst) {
     const uint16_t* const flat = reinterpret_cast<const uint16_t*>(&sk[0][0][0][0]);
     for (int f = w; f < IN * 2 * KT * 2; f += 4) {
       const int i = f / (4 * KT), t = f / 2 % (2 * KT), kb = f & 1;
-      const int d = 16 * t + n;  // the row of K^T
+      const int d = 16 * t + n;  // the row of the transposed matrix
       u32x4 v;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -206,31 +214,41 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
         }
         v[e] = two;
       }
-      p.c.ktf[((((slot * p.hk + j) * IN + i) * 2 * KT + t) * 2 + kb) * 64 + lane] = v;
+      dst[((((slot * p.hk + j) * IN + i) * 2 * KT + t) * 2 + kb) * 64 + lane] = v;
     }
+  };
+  transposed(p.c.ktf);
+  if constexpr (BACK) {
+    __syncthreads();
+#pragma unroll
+    for (int kb = 0; kb < KT; ++kb)
+#pragma unroll
+      for (int i = 0; i < IN; ++i) sk[i][w][kb][lane] = qa[kb][i];
+    __syncthreads();
+    transposed(p.c.qtf);
   }
 }
 
-template <typename TA>
+template <typename TA, bool BACK>
 void launch(const void* q, const void* k, const float* beta, const float* g, const int32_t* cu, const DeltaDims& d,
             const ChunkSpace& c, hipStream_t stream) {
   const PrepArgs<TA> a{static_cast<const TA*>(q), static_cast<const TA*>(k), beta, g, cu, d.nseq, d.L, d.qs, d.ks,
                        d.hk, d.hv, d.K, c};
   const dim3 grid(static_cast<unsigned>(d.chunks() * d.hv)), block(256);
   switch (delta_kt(d.K)) {
-    case 1: hipLaunchKernelGGL((delta_prep_kernel<TA, 1>), grid, block, 0, stream, a); break;
-    case 2: hipLaunchKernelGGL((delta_prep_kernel<TA, 2>), grid, block, 0, stream, a); break;
-    case 4: hipLaunchKernelGGL((delta_prep_kernel<TA, 4>), grid, block, 0, stream, a); break;
-    default: hipLaunchKernelGGL((delta_prep_kernel<TA, 8>), grid, block, 0, stream, a); break;
+    case 1: hipLaunchKernelGGL((delta_prep_kernel<TA, 1, BACK>), grid, block, 0, stream, a); break;
+    case 2: hipLaunchKernelGGL((delta_prep_kernel<TA, 2, BACK>), grid, block, 0, stream, a); break;
+    case 4: hipLaunchKernelGGL((delta_prep_kernel<TA, 4, BACK>), grid, block, 0, stream, a); break;
+    default: hipLaunchKernelGGL((delta_prep_kernel<TA, 8, BACK>), grid, block, 0, stream, a); break;
   }
 }
 
 }  // namespace
 
-void delta_prep(int dtype, const void* q, const void* k, const float* beta, const float* g, const int32_t* cu,
-                const DeltaDims& d, const ChunkSpace& c, hipStream_t stream) {
-  if (dtype == SSM_DTYPE_F32) launch<float>(q, k, beta, g, cu, d, c, stream);
-  else launch<bf16_t>(q, k, beta, g, cu, d, c, stream);
+void delta_prep(int dtype, bool back, const void* q, const void* k, const float* beta, const float* g,
+                const int32_t* cu, const DeltaDims& d, const ChunkSpace& c, hipStream_t stream) {
+  if (dtype == SSM_DTYPE_F32) (back ? launch<float, true> : launch<float, false>)(q, k, beta, g, cu, d, c, stream);
+  else (back ? launch<bf16_t, true> : launch<bf16_t, false>)(q, k, beta, g, cu, d, c, stream);
 }
 
 }  // namespace ssm

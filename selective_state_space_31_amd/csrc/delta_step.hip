@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(256) delta_walk_kernel(const WalkArgs<TA> p) {
   const bool mine = c0 < p.V;  // (V is a multiple of VEC)
   const DeltaSeq q = delta_seq(p.cu, b, p.L);
   const size_t sv = static_cast<size_t>(p.K) * p.V, at = static_cast<size_t>(row) * p.V + c0;
-  const size_t hop = static_cast<size_t>(ROWS) * p.V;
+  const size_t hop = static_cast<size_t>(ROWS) * p.V, mv = sv + static_cast<size_t>(kDeltaC) * p.V;
   Cols s[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(256) delta_walk_kernel(const WalkArgs<TA> p) {
   }
   for (int64_t t = q.lo; t < q.hi; ++t) {
     if (p.mids && (t - q.lo) % kDeltaC == 0 && mine) {
-      float* const m = p.mids + ((q.slot + (t - q.lo) / kDeltaC) * p.hv + h) * sv + at;
+      float* const m = p.mids + ((q.slot + (t - q.lo) / kDeltaC) * p.hv + h) * mv + at;
 #pragma unroll
       for (int i = 0; i < R; ++i)
         if (row + i * ROWS < p.K) *reinterpret_cast<Cols*>(m + i * hop) = s[i];
@@ -113,6 +113,12 @@ __global__ void __launch_bounds__(256) delta_walk_kernel(const WalkArgs<TA> p) {
       const float kr = sk[row + i * ROWS];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) s[i].x[e] = __builtin_fmaf(kr, u[e], decay * s[i].x[e]);
+    }
+    if (p.mids && row == 0 && mine) {  // (behind the last token zeros complete its chunk)
+      float* const m = p.mids + ((q.slot + (t - q.lo) / kDeltaC) * p.hv + h) * mv + sv + c0;
+      for (int64_t i = (t - q.lo) % kDeltaC; i < (t + 1 < q.hi ? (t - q.lo) % kDeltaC + 1 : kDeltaC); ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) m[i * p.V + e] = i == (t - q.lo) % kDeltaC ? u[e] : 0.0f;
     }
     if (row == 0 && mine) {
       TA* const o = p.out + (static_cast<size_t>(t) * p.hv + h) * p.V + c0;

@@ -117,7 +117,7 @@ class _Delta:
             raise ValueError("q has %d heads, k %d" % (Hk, Hkk))
         self.lead, self.like, self.gate = lead, q, lead + (Hv,)
         self.out, self.key = lead + (Hv, V), lead + (Hk, K)
-        self.state, self.mids = (self.n, Hv, K, V), chunks + (Hv, K, V)
+        self.state, self.mids = (self.n, Hv, K, V), chunks + (Hv, K + SSM_DELTA_CHUNK, V)
         self.scale = K ** -0.5 if scale is None else float(scale)
         self.head = (q.data_ptr(), k.data_ptr(), v.data_ptr(), _in(beta, "beta", self.gate, _F32, q),
                      _opt(g, "g", self.gate, _F32, q), self.scale)
@@ -157,8 +157,9 @@ def ssm_delta_rule_fwd(q, k, v, beta, g=None, scale=None, initial_state=None, re
     headdim_k, headdim_v) float32; ``scale`` defaults to headdim_k ** -0.5.
 
     Returns ``out`` (contiguous), followed by ``last_state`` and by
-    ``chunk_states`` where they are asked for or passed (``chunk_states`` is
-    for the gradients).
+    ``chunk_states`` where they are asked for or passed (for the gradients:
+    per chunk of 64 tokens the state before it and the tokens' u, (batch,
+    chunks, heads_v, headdim_k + 64, headdim_v) float32).
     """
     return _delta_fwd(q, k, v, beta, None, g, scale, initial_state, return_last_state, return_chunk_states, out,
                       last_state, chunk_states, workspace, stream)

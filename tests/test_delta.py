@@ -95,7 +95,7 @@ def test_packed(lengths, dtype):
         t[int(cu[-1]):] = float("nan")  # (padding reaches nothing)
     off = torch.tensor(cu, dtype=torch.int32, device=DEV)
     out = torch.full((T, 4, 77), 5.0, dtype=p.v.dtype, device=DEV)
-    mids = torch.full((T // 64 + n, 4, 64, 77), 7.0, device=DEV)
+    mids = torch.full((T // 64 + n, 4, 64 + 64, 77), 7.0, device=DEV)
     _, last, _ = pkg.ssm_delta_rule_fwd_varlen(*p.args(), off, return_last_state=True, out=out, chunk_states=mids, **p.kw())
     torch.cuda.synchronize()
     assert (out[int(cu[-1]):] == 5.0).all()
@@ -245,7 +245,7 @@ def test_captured_and_replayed():
 def test_nothing_written_outside():
     b, L, hv, K, V, guard = 2, 70, 3, 33, 19, 1000
     p = Delta((b, L), b, 1, hv, K, V, "bf16", DEV, seed=19)
-    n, m, c = b * L * hv * V, b * hv * K * V, b * 2 * hv * K * V
+    n, m, c = b * L * hv * V, b * hv * K * V, b * 2 * hv * (K + 64) * V
     ob = torch.full((n + 2 * guard,), 3.0, dtype=torch.bfloat16, device=DEV)
     sb = torch.full((m + 2 * guard,), 3.0, device=DEV)
     cb = torch.full((c + 2 * guard,), 3.0, device=DEV)
@@ -253,7 +253,7 @@ def test_nothing_written_outside():
     wb = torch.full((need + 2 * 4096,), 9, dtype=torch.uint8, device=DEV)
     ws = wb[4096:4096 + need] if need else None
     pkg.ssm_delta_rule_fwd(*p.args(), out=ob[guard:-guard].view(b, L, hv, V), last_state=sb[guard:-guard].view(b, hv, K, V),
-                           chunk_states=cb[guard:-guard].view(b, 2, hv, K, V), workspace=ws, **p.kw())
+                           chunk_states=cb[guard:-guard].view(b, 2, hv, K + 64, V), workspace=ws, **p.kw())
     torch.cuda.synchronize()
     for t in (ob, sb, cb):
         assert (t[:guard] == 3.0).all() and (t[-guard:] == 3.0).all()
