@@ -47,7 +47,7 @@ extern "C" {
  *   out[b,t,h,:] = scale S^T q[b,t,j,:]
  *   q, k            : (batch, seqlen, nheads_k, headdim_k) act; a token's heads
  *                     together, tokens q_token_stride (k_token_stride) values
- *                     apart (at least nheads_k * headdim_k, at most 2^30: rows
+ *                     apart (at least nheads_k * headdim_k, at most 2^22: rows
  *                     of a fused projection are read where they are); batch
  *                     rows follow each other at seqlen token strides
  *   v               : (batch, seqlen, nheads_v, headdim_v) act, tokens

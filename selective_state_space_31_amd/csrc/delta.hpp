@@ -45,7 +45,7 @@ inline bool delta_sizes_ok(int64_t nseq, int64_t L, int64_t hk, int64_t hv, int6
 }
 
 inline bool delta_strides_ok(const DeltaDims& d) {
-  const int64_t most = int64_t{1} << 30;
+  const int64_t most = int64_t{1} << 22;  // (64 rows stay within 32-bit byte offsets)
   return d.qs >= int64_t{d.hk} * d.K && d.qs <= most && d.ks >= int64_t{d.hk} * d.K && d.ks <= most &&
          d.vs >= int64_t{d.hv} * d.V && d.vs <= most;
 }
@@ -122,6 +122,7 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t (&p)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     p[i] = pack_bf16(a, b);
+    asm("" : "+v"(p[i]));  // (or the compiler converts a second time for each half)
     a -= bf_lo(p[i]);
     b -= bf_hi(p[i]);
   }
@@ -138,28 +139,43 @@ __device__ __forceinline__ f32x4 mul_parts(const u32x4 (&a)[NA], const u32x4 (&b
   return c;
 }
 
-// Matrix fragments.  A product's left operand: lane l holds row l % 16, columns
-// 8 (l / 16) .. + 7 of a 16 x 32 block; the right one likewise with rows and
-// columns exchanged; the result has column l % 16, rows 4 (l / 16) + 0..3.  In
-// memory a fragment is 64 times 16 bytes, lane after lane.
-//
-// Four results of a lane (rows 4 (l / 16) .. + 3 of row block t of 16) go into
-// right operands over those rows: 8 bytes at this offset of 32-row block t / 2.
-__device__ __forceinline__ int frag_put(int lane, int t) {
-  const int q = lane >> 4;
-  return (((t & 1) * 2 + (q >> 1)) * 16 + (lane & 15)) * 16 + (q & 1) * 8;
-}
+// Matrix fragments.  A product's left operand: lane l holds row l % 16 and eight
+// of 32 columns; the right one likewise with rows and columns exchanged; the
+// result has column l % 16, rows 4 (l / 16) + 0..3.  Which eight is free as long
+// as both operands agree.  Sums over headdim_k take 8 (l / 16) .. + 7, which lie
+// together in a row of K or Q.  Sums over tokens take 4 q .. + 3 and 16 + 4 q
+// .. + 3 with q = l / 16: then two results below each other are, value by value,
+// the right operand of a product over their rows, and two results of the
+// transposed product side by side a left one.  In memory a fragment is 64 times
+// 16 bytes, lane after lane.
+__device__ __forceinline__ int frag_tok(int q, int e) { return (e < 4 ? 4 * q : 12 + 4 * q) + e; }
 
-// base: [N][blocks][NC][64]; x goes into the parts' fragments of column block nb.
-template <int N, int NC>
-__device__ __forceinline__ void put_parts(u32x4* base, int blocks, int t, int nb, int lane, f32x4 x) {
+template <int N>
+__device__ __forceinline__ void split4(f32x4 x, u32x2 (&p)[N]) {
   uint32_t lo[N], hi[N];
   split2(x[0], x[1], lo);
   split2(x[2], x[3], hi);
 #pragma unroll
+  for (int i = 0; i < N; ++i) p[i] = u32x2{lo[i], hi[i]};
+}
+// A result over row block t goes into the parts' right operands in LDS, base:
+// [N][blocks][NC][64], column block nb: for sums over tokens, over headdim_k.
+template <int N, int NC>
+__device__ __forceinline__ void put_tok(u32x4* base, int blocks, int t, int nb, int lane, f32x4 x) {
+  u32x2 p[N];
+  split4(x, p);
+#pragma unroll
   for (int i = 0; i < N; ++i)
-    *reinterpret_cast<u32x2*>(reinterpret_cast<char*>(base + ((i * blocks + (t >> 1)) * NC + nb) * 64) +
-                              frag_put(lane, t)) = u32x2{lo[i], hi[i]};
+    reinterpret_cast<u32x2*>(base + ((i * blocks + (t >> 1)) * NC + nb) * 64 + lane)[t & 1] = p[i];
+}
+template <int N, int NC>
+__device__ __forceinline__ void put_key(u32x4* base, int blocks, int t, int nb, int lane, f32x4 x) {
+  u32x2 p[N];
+  split4(x, p);
+  const int q = lane >> 4, at = ((t & 1) * 2 + (q >> 1)) * 16 + (lane & 15);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    reinterpret_cast<u32x2*>(base + ((i * blocks + (t >> 1)) * NC + nb) * 64 + at)[q & 1] = p[i];
 }
 
 // Triangles of 64 x 64 in 16 x 32 blocks.  Lower: row blocks 0 and 1 have one,
@@ -186,6 +202,15 @@ __device__ __forceinline__ int delta_owner(const int32_t* cu, int nseq, int64_t 
     if (stride == 1) return lo;
     cnt = (cnt - k * stride < stride) ? cnt - k * stride : stride;
   }
+}
+
+// (Several workgroups write a line of an output: it stays in L2 for them.)
+template <typename TA>
+__device__ __forceinline__ void buffer_store_act(float v, rsrc_t r, uint32_t off) {
+  TA t;
+  store_act(&t, v);
+  if constexpr (sizeof(TA) == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, off, 0, 0);
+  else __builtin_amdgcn_raw_buffer_store_b16(t.bits, r, off, 0, 0);
 }
 
 // ---------------------------------------------------------------------------

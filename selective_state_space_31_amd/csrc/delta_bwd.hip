@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(256) delta_back_kernel(const BackArgs<TA> p) {
 #pragma unroll
       for (int i = 0; i < TW; ++i)
 #pragma unroll
-        for (int nb = 0; nb < NC; ++nb) put_parts<3, NC>(&sS[0][0][0][0], KT, w + 4 * i, nb, lane, S[i][nb]);
+        for (int nb = 0; nb < NC; ++nb) put_key<3, NC>(&sS[0][0][0][0], KT, w + 4 * i, nb, lane, S[i][nb]);
   };
 
   // left operands of one chunk, and its gradients of out
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(256) delta_back_kernel(const BackArgs<TA> p) {
 #pragma unroll
     for (int nb = 0; nb < NC; ++nb) {
       dO[nb] = ndO[nb];
-      put_parts<IN, NC>(&sO[0][0][0][0], 2, w, nb, lane, dO[nb]);
+      put_tok<IN, NC>(&sO[0][0][0][0], 2, w, nb, lane, dO[nb]);
     }
   };
   if (nc > 0) {
@@ -179,8 +179,8 @@ __global__ void __launch_bounds__(256) delta_back_kernel(const BackArgs<TA> p) {
         x[r] = de[r] * x[r] + p.scale * y[r];
         z[r] = p.scale * ga[r] * dO[nb][r];
       }
-      put_parts<3, NC>(&sU[0][0][0][0], 2, w, nb, lane, x);
-      put_parts<3, NC>(&sG[0][0][0][0], 2, w, nb, lane, z);
+      put_tok<3, NC>(&sU[0][0][0][0], 2, w, nb, lane, x);
+      put_tok<3, NC>(&sG[0][0][0][0], 2, w, nb, lane, z);
     }
     load_k(slot - more);
     load_tri(slot - more, p.c.pf, fp);
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(256) delta_back_kernel(const BackArgs<TA> p) {
         if (t < q.hi && col < p.V) store_act(p.dv + (t * p.hv + h) * p.V + col, y[r]);
         y[r] *= -ga[r];
       }
-      put_parts<3, NC>(&sZ[0][0][0][0], 2, w, nb, lane, y);
+      put_tok<3, NC>(&sZ[0][0][0][0], 2, w, nb, lane, y);
     }
     load_tri(slot - more, p.c.tf, ft);
     take_o();
@@ -495,12 +495,13 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const GradArgs<TA> p) {
     for (int turn = 0; turn < 2; ++turn) {
       __syncthreads();
       for (int kb = turn ? w >> 1 : 0; kb <= (turn ? 1 : w >> 1); ++kb) {
-        const int c = 32 * kb + 8 * g, f = turn ? tri_up(w, kb) : tri_at(w, kb);
+        const int f = turn ? tri_up(w, kb) : tri_at(w, kb);
         float xe[8], xf[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          xe[e] = turn ? sE[c + e][row] : sE[row][c + e];
-          xf[e] = turn ? sP[c + e][row] : sP[row][c + e];
+          const int c = 32 * kb + frag_tok(g, e);
+          xe[e] = turn ? sE[c][row] : sE[row][c];
+          xf[e] = turn ? sP[c][row] : sP[row][c];
         }
         u32x4 fe[3], ff[3];
         split8(xe, fe);

@@ -20,232 +20,335 @@ struct RecArgs {
 
 // The chunks one after another.  With S0 the state before a chunk, per column
 // block of 16 NC values:
-//   X = V - gamma (K S0);  U = T diag(beta) X;  out = scale (gamma (Q S0) + P U)
-//   S1 = gamma_C S0 + K^T (d U)
-// A workgroup of four waves takes one column block of a head (columns do not
-// meet): wave w the tokens 16 w .. + 15 of X, U and out, and every fourth row
-// block of S, which stays in its registers.  S, X, U and d U pass through LDS as
-// right operands in bf16 parts; the left operands come from memory as fragments,
-// each needed by one wave alone, the next chunk's while this one is worked on.
+//   X = V - gamma (K S0);  U = T diag(beta) X;  S1 = gamma_C S0 + K^T (d U)
+//   out = scale (gamma (Q S0) + P U)
+// A workgroup takes one column block of a head (columns do not meet).  Its first
+// four waves carry the chain X, U, S1: wave w has the tokens 16 w .. + 15 and
+// every fourth row block of S, in registers.  The other four form the outputs, 16
+// tokens each, in the time that the chain leaves.  S, X and d U pass through LDS
+// as right operands in bf16 parts; the left operands come from memory as
+// fragments, each needed by one wave alone, the next chunk's while this one is
+// worked on.  What bounds it is the chain through a chunk: three products, three
+// splits and three barriers, one after another.
 template <typename TA, int KT, int NC, bool MIDS>
-__global__ void __launch_bounds__(256) delta_rec_kernel(const RecArgs<TA> p) {
+__global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const RecArgs<TA> p) {
   constexpr int IN = ActParts<TA>::in, OUT = ActParts<TA>::out, TW = (KT + 1) / 2;
-  __shared__ u32x4 sS[3][KT][NC][64], sX[3][2][NC][64], sU[OUT][2][NC][64], sD[3][2][NC][64];
+  __shared__ u32x4 sS[3][KT][NC][64], sX[3][2][NC][64], sD[3][2][NC][64];
+  __shared__ f32x4 sU[4][NC][64];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave & 3;
   // The workgroups of a head read the same fragments: they go to the same XCD
   // (workgroups are dealt to the eight XCDs in turn).
-  const unsigned group = blockIdx.x / (8u * static_cast<unsigned>(p.slices)), in = blockIdx.x % (8u * static_cast<unsigned>(p.slices));
-  const int64_t pair = int64_t{group} * 8 + (in & 7);
+  const unsigned wide = 8u * static_cast<unsigned>(p.slices);
+  const int64_t pair = int64_t{blockIdx.x / wide} * 8 + (blockIdx.x % wide & 7);
   if (pair >= p.nseq * p.hv) return;
-  const int slice = static_cast<int>(in >> 3), c0 = slice * 16 * NC;
+  const int c0 = static_cast<int>(blockIdx.x % wide >> 3) * 16 * NC;
   const int64_t b = pair / p.hv;
   const int h = static_cast<int>(pair - b * p.hv), j = h / (p.hv / p.hk);
   const DeltaSeq q = delta_seq(p.cu, b, p.L);
   const int nc = static_cast<int>((q.hi - q.lo + kDeltaC - 1) / kDeltaC);
   const size_t sv = static_cast<size_t>(p.K) * p.V, mv = sv + static_cast<size_t>(kDeltaC) * p.V;
-  const bool tiles = TW > 1 || w < 2 * KT;  // (with 32 rows two waves hold none)
+  // Buffer accesses outside the range read zeros and write nothing: rows behind
+  // the sequence or the state, and by this offset columns behind the last one.
+  constexpr uint32_t es = sizeof(TA), kNone = 0x80000000u;
+  const auto rows_of = [&](int64_t t0) {
+    return static_cast<uint32_t>(q.hi - t0 < kDeltaC ? q.hi - t0 : kDeltaC);
+  };
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  const bool two = w >= 2;  // the triangles' rows w have two blocks
 
-  // state values of this lane: row block t, column block nb
-  const auto state_io = [&](auto&& f) {
+  // the wave's rows of K or Q as fragments
+  u32x4 fr[KT][IN];
+  const auto load_rows = [&](int64_t slot) {
+    const u32x4* const src = (wave < 4 ? p.c.kf : p.c.qf) + ((slot * p.hk + j) * (IN * 4 * KT) + w * KT) * 64;
+#pragma unroll
+    for (int kb = 0; kb < KT; ++kb)
+#pragma unroll
+      for (int i = 0; i < IN; ++i) fr[kb][i] = (src + (i * 4 * KT + kb) * 64)[lane];
+  };
+
+  if (wave >= 4) {
+    // ---- outputs ----
+    const uint32_t orow = static_cast<uint32_t>(p.hv * p.V) * es;
+    uint32_t oat[NC][4];
+#pragma unroll
+    for (int nb = 0; nb < NC; ++nb)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        oat[nb][r] = c0 + 16 * nb + n < p.V ? (16u * w + 4u * g + r) * orow + (16 * nb + n) * es : kNone;
+    u32x4 fp[2][OUT];
+    f32x4 nga;
+    const auto load_p = [&](int64_t slot) {
+      nga = reinterpret_cast<const f32x4*>(p.c.vec + (slot * p.hv + h) * 2 * kDeltaC)[4 * w + g];
+      const u32x4* const src = p.c.pf + ((slot * p.hv + h) * (OUT * kTri) + tri_at(w, 0)) * 64;
+#pragma unroll
+      for (int i = 0; i < OUT; ++i) {
+        fp[0][i] = (src + i * kTri * 64)[lane];
+        if (two) fp[1][i] = (src + (i * kTri + 1) * 64)[lane];
+      }
+    };
+    // The next chunks' operands into L2, two chunks before they are asked for:
+    // lines 128 bytes apart, a share for each of the head's workgroups.
+    uint32_t touched = 0;
+    const auto touch = [&](int64_t slot) {
+      const char* src;
+      int bytes;
+      if (w < 3) {
+        src = reinterpret_cast<const char*>((w == 0 ? p.c.kf : w == 1 ? p.c.qf : p.c.ktf) + (slot * p.hk + j) * (IN * 4 * KT * 64));
+        bytes = IN * 4 * KT * 1024;
+      } else {
+        src = reinterpret_cast<const char*>(p.c.tf + (slot * p.hv + h) * (3 * kTri * 64));
+        bytes = 3 * kTri * 1024;
+      }
+      const int at = (lane * p.slices + c0 / (16 * NC)) * 128;
+      if (at < bytes) touched = *reinterpret_cast<const uint32_t*>(src + at);
+      if (w == 3 && at < OUT * kTri * 1024)
+        touched ^= *reinterpret_cast<const uint32_t*>(
+            reinterpret_cast<const char*>(p.c.pf + (slot * p.hv + h) * (OUT * kTri * 64)) + at);
+    };
+    if (nc > 0) {
+      load_rows(q.slot);
+      load_p(q.slot);
+    }
+    f32x4 y[NC];
+    u32x4 up[NC][2][OUT];
+    __syncthreads();
+    if (nc == 0) return;  // (the chain waits at no further barrier either)
+    for (int c = 0;; ++c) {
+      const int64_t slot = q.slot + c;
+      const int more = c + 1 < nc ? 1 : 0;  // (the last chunk's loads ahead are its own again)
+      if (c > 0) {  // the chunk before: its u came behind the last barrier but one
+#pragma unroll
+        for (int nb = 0; nb < NC; ++nb) {
+          y[nb] = mul_parts<OUT>(fp[0], up[nb][0], y[nb]);
+          if (two) y[nb] = mul_parts<OUT>(fp[1], up[nb][1], y[nb]);
+        }
+        if (c < nc) load_p(slot);
+        if (p.out) {
+          const int64_t t0 = q.lo + int64_t{c - 1} * kDeltaC;
+          const rsrc_t rs = make_rsrc(p.out + (t0 * p.hv + h) * p.V + c0,
+                                      (rows_of(t0) - 1) * orow + static_cast<uint32_t>(p.V - c0) * es);
+#pragma unroll
+          for (int nb = 0; nb < NC; ++nb)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) buffer_store_act<TA>(p.scale * y[nb][r], rs, oat[nb][r]);
+        }
+        if (c == nc) break;
+      }
+      __syncthreads();
+      asm volatile("" ::"v"(touched));
+      touch(q.slot + (c + 3 < nc ? c + 3 : nc - 1));
+#pragma unroll
+      for (int nb = 0; nb < NC; ++nb) {
+        y[nb] = zero;
+#pragma unroll
+        for (int kb = 0; kb < KT; ++kb) {
+          u32x4 s[OUT];
+#pragma unroll
+          for (int i = 0; i < OUT; ++i) s[i] = sS[i][kb][nb][lane];
+          y[nb] = mul_parts<OUT>(fr[kb], s, y[nb]);
+        }
+        y[nb] *= nga;
+      }
+      load_rows(slot + more);
+      __syncthreads();
+#pragma unroll
+      for (int nb = 0; nb < NC; ++nb)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          u32x2 part[OUT];
+          split4(sU[t][nb][lane], part);
+#pragma unroll
+          for (int i = 0; i < OUT; ++i) {
+            up[nb][t >> 1][i][2 * (t & 1)] = part[i][0];
+            up[nb][t >> 1][i][2 * (t & 1) + 1] = part[i][1];
+          }
+        }
+      __syncthreads();
+    }
+    return;
+  }
+
+  // ---- chain ----
+  const bool tiles = TW > 1 || w < 2 * KT;  // (with 32 rows two waves hold none)
+  const uint32_t sbytes = static_cast<uint32_t>(sv * 4), srow = static_cast<uint32_t>(p.V) * 4;
+  const uint32_t vrow = static_cast<uint32_t>(p.vs) * es;
+  uint32_t sat[NC], vat[NC][4];
+#pragma unroll
+  for (int nb = 0; nb < NC; ++nb) {
+    const bool mine = c0 + 16 * nb + n < p.V;
+    sat[nb] = mine ? (16u * w + 4u * g) * srow + (c0 + 16 * nb + n) * 4u : kNone;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) vat[nb][r] = mine ? (16u * w + 4u * g + r) * vrow + (16 * nb + n) * es : kNone;
+  }
+  f32x4 S[TW][NC];
+#pragma unroll
+  for (int i = 0; i < TW; ++i)
+#pragma unroll
+    for (int nb = 0; nb < NC; ++nb) S[i][nb] = zero;
+  if (p.first && tiles) {
+    const rsrc_t rs = make_rsrc(p.first + pair * sv, sbytes);
 #pragma unroll
     for (int i = 0; i < TW; ++i)
 #pragma unroll
       for (int nb = 0; nb < NC; ++nb)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 16 * (w + 4 * i) + 4 * g + r, col = c0 + 16 * nb + n;
-          if (tiles && row < p.K && col < p.V) f(i, nb, r, static_cast<size_t>(row) * p.V + col);
-        }
-  };
-  f32x4 S[TW][NC];
-#pragma unroll
-  for (int i = 0; i < TW; ++i)
-#pragma unroll
-    for (int nb = 0; nb < NC; ++nb) S[i][nb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  if (p.first) {
-    const float* const src = p.first + pair * sv;
-    state_io([&](int i, int nb, int r, size_t at) { S[i][nb][r] = src[at]; });
+        for (int r = 0; r < 4; ++r)
+          S[i][nb][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, sat[nb] + (64 * i + r) * srow, 0, 0));
   }
+  const auto state_store = [&](float* dst) {
+    const rsrc_t rs = make_rsrc(dst, sbytes);
+#pragma unroll
+    for (int i = 0; i < TW; ++i)
+#pragma unroll
+      for (int nb = 0; nb < NC; ++nb)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][nb][r]), rs, sat[nb] + (64 * i + r) * srow, 0, 0);
+  };
   const auto put_state = [&]() {
     if (tiles)
 #pragma unroll
       for (int i = 0; i < TW; ++i)
 #pragma unroll
-        for (int nb = 0; nb < NC; ++nb) put_parts<3, NC>(&sS[0][0][0][0], KT, w + 4 * i, nb, lane, S[i][nb]);
+        for (int nb = 0; nb < NC; ++nb) put_key<3, NC>(&sS[0][0][0][0], KT, w + 4 * i, nb, lane, S[i][nb]);
   };
-  if (nc > 0) put_state();
-
-  // left operands of one chunk
-  u32x4 fk[KT][IN], fq[KT][IN], ft[2][3], fp[2][OUT], fkt[TW][2][IN];
-  float ga[4], de[4], gC;
-  TA rv[NC][4];
-  const int kbs = w < 2 ? 1 : 2;
-  const auto load_kq = [&](int64_t slot) {
-    const size_t at = static_cast<size_t>(slot * p.hk + j) * IN * 4 * KT * 64 + lane;
-#pragma unroll
-    for (int kb = 0; kb < KT; ++kb)
-#pragma unroll
-      for (int i = 0; i < IN; ++i) {
-        fk[kb][i] = p.c.kf[at + ((i * 4 + w) * KT + kb) * 64];
-        fq[kb][i] = p.c.qf[at + ((i * 4 + w) * KT + kb) * 64];
-      }
-  };
+  u32x4 ft[2][3], fkt[TW][2][IN];
+  f32x4 nga, nde;
+  float ngC;
+  typename Io<TA>::raw_t rv[NC][4];
   const auto load_v = [&](int64_t slot, int64_t t0) {
     const float* const vec = p.c.vec + (slot * p.hv + h) * 2 * kDeltaC;
+    nga = reinterpret_cast<const f32x4*>(vec)[4 * w + g];
+    nde = reinterpret_cast<const f32x4*>(vec + kDeltaC)[4 * w + g];
+    ngC = vec[kDeltaC - 1 + (tid >> 9)];  // (by a vector load: a scalar one would be waited for at the barrier)
+    const rsrc_t rs = make_rsrc(p.v + t0 * p.vs + h * p.V + c0,
+                                (rows_of(t0) - 1) * vrow + static_cast<uint32_t>(p.V - c0) * es);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      ga[r] = vec[16 * w + 4 * g + r];
-      de[r] = vec[kDeltaC + 16 * w + 4 * g + r];
-      const int64_t t = t0 + 16 * w + 4 * g + r;
+    for (int nb = 0; nb < NC; ++nb)
 #pragma unroll
-      for (int nb = 0; nb < NC; ++nb) {
-        const int col = c0 + 16 * nb + n;
-        rv[nb][r] = TA{};
-        if (t < q.hi && col < p.V) rv[nb][r] = p.v[t * p.vs + h * p.V + col];
-      }
-    }
-    gC = vec[kDeltaC - 1];
+      for (int r = 0; r < 4; ++r) rv[nb][r] = Io<TA>::load(rs, vat[nb][r], 0);
   };
   const auto load_t = [&](int64_t slot) {
-    const size_t at = static_cast<size_t>(slot * p.hv + h) * 3 * kTri * 64 + lane;
+    const u32x4* const src = p.c.tf + ((slot * p.hv + h) * (3 * kTri) + tri_at(w, 0)) * 64;
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int i = 0; i < 3; ++i)
-        if (kb < kbs) ft[kb][i] = p.c.tf[at + (i * kTri + tri_at(w, kb)) * 64];
+    for (int i = 0; i < 3; ++i) {
+      ft[0][i] = (src + i * kTri * 64)[lane];
+      if (two) ft[1][i] = (src + (i * kTri + 1) * 64)[lane];
+    }
   };
-  const auto load_pkt = [&](int64_t slot) {
-    const size_t at = static_cast<size_t>(slot * p.hv + h) * OUT * kTri * 64 + lane;
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int i = 0; i < OUT; ++i)
-        if (kb < kbs) fp[kb][i] = p.c.pf[at + (i * kTri + tri_at(w, kb)) * 64];
-    const size_t kt = static_cast<size_t>(slot * p.hk + j) * IN * 2 * KT * 2 * 64 + lane;
+  const auto load_kt = [&](int64_t slot) {
+    const u32x4* const kt = p.c.ktf + ((slot * p.hk + j) * (IN * 4 * KT) + 2 * w) * 64;
     if (tiles)
 #pragma unroll
       for (int x = 0; x < TW; ++x)
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-          for (int i = 0; i < IN; ++i) fkt[x][kb][i] = p.c.ktf[kt + ((i * 2 * KT + w + 4 * x) * 2 + kb) * 64];
+          for (int i = 0; i < IN; ++i) fkt[x][kb][i] = (kt + (i * 4 * KT + 8 * x + kb) * 64)[lane];
   };
   if (nc > 0) {
-    load_kq(q.slot);
+    load_rows(q.slot);
     load_v(q.slot, q.lo);
     load_t(q.slot);
-    load_pkt(q.slot);
+    load_kt(q.slot);
+    put_state();
   }
   __syncthreads();
   for (int c = 0; c < nc; ++c) {
     const int64_t slot = q.slot + c, t0 = q.lo + int64_t{c} * kDeltaC;
-    const int more = c + 1 < nc ? 1 : 0;  // (the last chunk's loads ahead are its own again)
-    if constexpr (MIDS) {
-      float* const dst = p.mids + (slot * p.hv + h) * mv;
-      state_io([&](int i, int nb, int r, size_t at) { dst[at] = S[i][nb][r]; });
-    }
-    // ---- X and Q S0 ----
-    f32x4 o[NC];
+    const int more = c + 1 < nc ? 1 : 0;
+    // ---- X ----
+    const f32x4 de = nde;
+    f32x4 x[NC];
+    if constexpr (MIDS)
+      if (tiles) state_store(p.mids + (slot * p.hv + h) * mv);
 #pragma unroll
     for (int nb = 0; nb < NC; ++nb) {
-      f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
+      x[nb] = zero;
 #pragma unroll
       for (int kb = 0; kb < KT; ++kb) {
         u32x4 s[3];
 #pragma unroll
         for (int i = 0; i < 3; ++i) s[i] = sS[i][kb][nb][lane];
-        x = mul_parts<3>(fk[kb], s, x);
-        y = mul_parts<OUT>(fq[kb], s, y);
+        x[nb] = mul_parts<3>(fr[kb], s, x[nb]);
       }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        o[nb][r] = ga[r] * y[r];
-        x[r] = to_f32(rv[nb][r]) - ga[r] * x[r];
-      }
-      put_parts<3, NC>(&sX[0][0][0][0], 2, w, nb, lane, x);
     }
-    load_kq(slot + more);
-    float dl[4];
-    const float decay = gC;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) dl[r] = de[r];
-    load_v(slot + more, t0 + more * kDeltaC);
+    for (int i = 0; i < TW; ++i)
+#pragma unroll
+      for (int nb = 0; nb < NC; ++nb) S[i][nb] *= ngC;
+#pragma unroll
+    for (int nb = 0; nb < NC; ++nb) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[nb][r] = Io<TA>::f32(rv[nb][r]) - nga[r] * x[nb][r];
+      put_tok<3, NC>(&sX[0][0][0][0], 2, w, nb, lane, x[nb]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    load_rows(slot + more);
     __syncthreads();
     // ---- U ----
+    u32x4 xp[2][NC][3];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int nb = 0; nb < NC; ++nb)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) xp[kb][nb][i] = sX[i][kb][nb][lane];
+    load_v(slot + more, t0 + more * kDeltaC);
+    f32x4 u[NC];
+#pragma unroll
+    for (int nb = 0; nb < NC; ++nb) u[nb] = mul_parts<3>(ft[0], xp[0][nb], zero);
+    if (two)
+#pragma unroll
+      for (int nb = 0; nb < NC; ++nb) u[nb] = mul_parts<3>(ft[1], xp[1][nb], u[nb]);
 #pragma unroll
     for (int nb = 0; nb < NC; ++nb) {
-      f32x4 u = {0.0f, 0.0f, 0.0f, 0.0f};
+      sU[w][nb][lane] = u[nb];
+      put_tok<3, NC>(&sD[0][0][0][0], 2, w, nb, lane, u[nb] * de);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (MIDS) {
+      const rsrc_t rs = make_rsrc(p.mids + (slot * p.hv + h) * mv + sv, kDeltaC * srow);
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        if (kb >= kbs) break;
-        u32x4 x[3];
-#pragma unroll
-        for (int i = 0; i < 3; ++i) x[i] = sX[i][kb][nb][lane];
-        u = mul_parts<3>(ft[kb], x, u);
-      }
-      put_parts<OUT, NC>(&sU[0][0][0][0], 2, w, nb, lane, u);
-      if constexpr (MIDS) {
-        const int col = c0 + 16 * nb + n;
-        float* const dst = p.mids + (slot * p.hv + h) * mv + sv + col;
+      for (int nb = 0; nb < NC; ++nb)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (col < p.V) dst[static_cast<size_t>(16 * w + 4 * g + r) * p.V] = u[r];
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) u[r] *= dl[r];
-      put_parts<3, NC>(&sD[0][0][0][0], 2, w, nb, lane, u);
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(u[nb][r]), rs, sat[nb] + r * srow, 0, 0);
     }
-    load_t(slot + more);
     __syncthreads();
-    // ---- S1, then out ----
+    // ---- S1 ----
     if (tiles) {
+      u32x4 d[2][NC][3];
 #pragma unroll
-      for (int nb = 0; nb < NC; ++nb)
+      for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int i = 0; i < TW; ++i) S[i][nb] *= decay;
+        for (int nb = 0; nb < NC; ++nb)
 #pragma unroll
-      for (int nb = 0; nb < NC; ++nb)
+          for (int i = 0; i < 3; ++i) d[kb][nb][i] = sD[i][kb][nb][lane];
+      load_t(slot + more);
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          u32x4 u[3];
+      for (int i = 0; i < TW; ++i)
 #pragma unroll
-          for (int i = 0; i < 3; ++i) u[i] = sD[i][kb][nb][lane];
+        for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-          for (int i = 0; i < TW; ++i) S[i][nb] = mul_parts<3>(fkt[i][kb], u, S[i][nb]);
-        }
+          for (int nb = 0; nb < NC; ++nb) S[i][nb] = mul_parts<3>(fkt[i][kb], d[kb][nb], S[i][nb]);
       put_state();
+    } else {
+      load_t(slot + more);
     }
-#pragma unroll
-    for (int nb = 0; nb < NC; ++nb) {
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        if (kb >= kbs) break;
-        u32x4 u[OUT];
-#pragma unroll
-        for (int i = 0; i < OUT; ++i) u[i] = sU[i][kb][nb][lane];
-        o[nb] = mul_parts<OUT>(fp[kb], u, o[nb]);
-      }
-      const int col = c0 + 16 * nb + n;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t t = t0 + 16 * w + 4 * g + r;
-        if (p.out && t < q.hi && col < p.V) store_act(p.out + (t * p.hv + h) * p.V + col, p.scale * o[nb][r]);
-      }
-    }
-    load_pkt(slot + more);
+    __builtin_amdgcn_sched_barrier(0);
+    load_kt(slot + more);
     __syncthreads();
   }
-  if (p.last) {
-    float* const dst = p.last + pair * sv;
-    state_io([&](int i, int nb, int r, size_t at) { dst[at] = S[i][nb][r]; });
-  }
+  if (p.last && tiles) state_store(p.last + pair * sv);
 }
 
 template <typename TA, int KT, int NC>
-void launch_rec(const RecArgs<TA>& a, hipStream_t stream) {
+void launch_rec(RecArgs<TA> a, hipStream_t stream) {
   const int64_t pairs = a.nseq * a.hv;
-  const dim3 grid(static_cast<unsigned>((pairs + 7) / 8 * 8 * a.slices)), block(256);
+  a.slices = (a.V + 16 * NC - 1) / (16 * NC);
+  const dim3 grid(static_cast<unsigned>((pairs + 7) / 8 * 8 * a.slices)), block(512);
   if (a.mids) hipLaunchKernelGGL((delta_rec_kernel<TA, KT, NC, true>), grid, block, 0, stream, a);
   else hipLaunchKernelGGL((delta_rec_kernel<TA, KT, NC, false>), grid, block, 0, stream, a);
 }
@@ -253,8 +356,8 @@ void launch_rec(const RecArgs<TA>& a, hipStream_t stream) {
 template <typename TA>
 void run_chunks(const void* v, float scale, void* out, float* last, const float* first, float* mids,
                 const int32_t* cu, const DeltaDims& d, const ChunkSpace& c, hipStream_t stream) {
-  RecArgs<TA> a{static_cast<const TA*>(v), static_cast<TA*>(out), first, last, mids, cu, c, scale, d.nseq, d.L, d.vs,
-                d.hk, d.hv, d.K, d.V, (d.V + 15) / 16};
+  const RecArgs<TA> a{static_cast<const TA*>(v), static_cast<TA*>(out), first, last, mids, cu, c, scale, d.nseq, d.L,
+                      d.vs, d.hk, d.hv, d.K, d.V, 1};
   switch (delta_kt(d.K)) {
     case 1: launch_rec<TA, 1, 1>(a, stream); break;
     case 2: launch_rec<TA, 2, 1>(a, stream); break;

@@ -26,15 +26,20 @@ __device__ __forceinline__ void put16(Mat& m, int i, int j, f32x4 c, float sign)
   for (int r = 0; r < 4; ++r) m[16 * i + 4 * g + r][16 * j + n] = sign * c[r];
 }
 
-// One workgroup a chunk and value head; wave w has rows 16 w .. + 15.
+// One workgroup a chunk and value head; wave w has the tokens 16 w .. + 15.
+// Products are formed transposed (K K^T and K Q^T with the wave's tokens as
+// columns): a lane then holds four neighbours of a row of A, and two results
+// side by side are a fragment of P.  K^T comes out of products with the columns
+// of the unit matrix, which are exact.
 template <typename TA, int KT, bool BACK>
 __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
   constexpr int IN = ActParts<TA>::in, OUT = BACK ? 3 : ActParts<TA>::out;
   __shared__ u32x4 sk[IN][4][KT][64];
-  __shared__ Mat sA, sP, sT;
+  __shared__ Mat sA, sT;
   __shared__ double sG[kDeltaC];
   __shared__ float sbeta[kDeltaC];
-  const int tid = static_cast<int>(threadIdx.x), w = tid >> 6, lane = tid & 63, n = lane & 15, g = lane >> 4;
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t slot = blockIdx.x / static_cast<unsigned>(p.hv);
   const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.hv)), r = p.hv / p.hk, j = h / r;
   const int64_t per = (p.L + kDeltaC - 1) / kDeltaC;
@@ -43,17 +48,17 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
   const int64_t t0 = q.lo + (slot - q.slot) * kDeltaC;
   if (slot < q.slot || t0 >= q.hi) return;  // (a place that no chunk has)
   const int valid = static_cast<int>(q.hi - t0 < kDeltaC ? q.hi - t0 : kDeltaC);
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  const bool first = h % r == 0;  // the key head's own fragments are written once
+  const int row = 16 * w + n;
 
   // ---- rows of K and Q: into fragments ----
-  u32x4 qa[KT][IN];
-  const int row = 16 * w + n;
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    const TA* const src = which ? p.q + (t0 + row) * p.qs + j * p.K : p.k + (t0 + row) * p.ks + j * p.K;
+  u32x4 fk[KT][IN], fq[KT][IN];
+  const auto load_rows = [&](const TA* src, u32x4 (&f)[KT][IN]) {
 #pragma unroll
     for (int kb = 0; kb < KT; ++kb) {
-      const int c = 32 * kb + 8 * g;
       TA raw[8];
+      const int c = 32 * kb + 8 * g;
       if (row < valid && c + 8 <= p.K) {
         __builtin_memcpy(raw, src + c, sizeof(raw));
       } else {
@@ -63,27 +68,21 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
           if (row < valid && c + e < p.K) raw[e] = src[c + e];
         }
       }
-      u32x4 f[IN];
       if constexpr (IN == 1) {
-        __builtin_memcpy(&f[0], raw, sizeof(f[0]));
+        __builtin_memcpy(&f[kb][0], raw, sizeof(f[kb][0]));
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           uint32_t part[IN];
           split2(to_f32(raw[2 * e]), to_f32(raw[2 * e + 1]), part);
 #pragma unroll
-          for (int i = 0; i < IN; ++i) f[i][e] = part[i];
+          for (int i = 0; i < IN; ++i) f[kb][i][e] = part[i];
         }
       }
-#pragma unroll
-      for (int i = 0; i < IN; ++i) {
-        if (which) qa[kb][i] = f[i];
-        else sk[i][w][kb][lane] = f[i];
-        if (h % r == 0 && !(BACK && which))
-          (which ? p.c.qf : p.c.kf)[((((slot * p.hk + j) * IN + i) * 4 + w) * KT + kb) * 64 + lane] = f[i];
-      }
     }
-  }
+  };
+  load_rows(p.k + (t0 + row) * p.ks + j * p.K, fk);
+  load_rows(p.q + (t0 + row) * p.qs + j * p.K, fq);
   if (w == 0) {
     const bool in = lane < valid;
     sbeta[lane] = in ? p.beta[(t0 + lane) * p.hv + h] : 0.0f;
@@ -101,36 +100,70 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
     vec[lane] = expf(static_cast<float>(G));
     vec[kDeltaC + lane] = expf(static_cast<float>(__shfl(G, 63) - G));
   }
+#pragma unroll
+  for (int kb = 0; kb < KT; ++kb)
+#pragma unroll
+    for (int i = 0; i < IN; ++i) {
+      sk[i][w][kb][lane] = fk[kb][i];
+      if (first) {
+        const int64_t at = ((((slot * p.hk + j) * IN + i) * 4 + w) * KT + kb) * 64 + lane;
+        p.c.kf[at] = fk[kb][i];
+        if constexpr (!BACK) p.c.qf[at] = fq[kb][i];
+      }
+    }
   __syncthreads();
 
-  // ---- K K^T and Q K^T, decayed: A and P ----
-  for (int jt = 0; jt <= w; ++jt) {
-    f32x4 kk = {0.0f, 0.0f, 0.0f, 0.0f}, qk = kk;
+  // ---- A (into LDS) and P: D_ij k_i.k_j and D_ij q_i.k_j, lane's i = row ----
+  const double Gr = sG[row];
+  const float br = sbeta[row];
+  const int64_t at = slot * p.hv + h;
 #pragma unroll
-    for (int kb = 0; kb < KT; ++kb) {
-      u32x4 a[IN], c[IN];
+  for (int pair = 0; pair < 2; ++pair) {
+    u32x4 fp[OUT];
 #pragma unroll
-      for (int i = 0; i < IN; ++i) {
-        a[i] = sk[i][w][kb][lane];
-        c[i] = sk[i][jt][kb][lane];
+    for (int half = 0; half < 2; ++half) {
+      const int jt = 2 * pair + half;
+      const bool below = jt <= w;
+      f32x4 kk = zero, qk = zero;
+      if (below) {
+#pragma unroll
+        for (int kb = 0; kb < KT; ++kb) {
+          u32x4 a[IN];
+#pragma unroll
+          for (int i = 0; i < IN; ++i) a[i] = sk[i][jt][kb][lane];
+          kk = mul_parts<3>(a, fk[kb], kk);
+          if constexpr (!BACK) qk = mul_parts<3>(a, fq[kb], qk);
+        }
       }
-      kk = mul_parts<3>(a, c, kk);
-      qk = mul_parts<3>(qa[kb], c, qk);
-    }
-    const int col = 16 * jt + n;
-    const double Gc = sG[col];
+      float4 a4 = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (below) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = 16 * w + 4 * g + e;
-      const float D = i >= col ? expf(static_cast<float>(sG[i] - Gc)) : 0.0f;
-      sA[i][col] = i > col ? sbeta[i] * D * kk[e] : 0.0f;
-      sP[i][col] = i >= col ? D * qk[e] : 0.0f;
-    }
-  }
-  if (w % 2 == 0) {  // the block right of the diagonal completes a fragment's 32 columns
+        for (int e = 0; e < 4; ++e) {
+          const int o = 16 * jt + 4 * g + e;
+          const float D = row >= o ? expf(static_cast<float>(Gr - sG[o])) : 0.0f;
+          qk[e] *= D;
+          reinterpret_cast<float*>(&a4)[e] = row > o ? br * D * kk[e] : 0.0f;
+        }
+        *reinterpret_cast<float4*>(&sA[row][16 * jt + 4 * g]) = a4;
+      }
+      if constexpr (!BACK) {
+        uint32_t lo[OUT], hi[OUT];
+        split2(qk[0], qk[1], lo);
+        split2(qk[2], qk[3], hi);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sP[16 * w + 4 * g + e][16 * w + 16 + n] = sT[16 * w + 4 * g + e][16 * w + 16 + n] = 0.0f;
+        for (int i = 0; i < OUT; ++i) {
+          fp[i][2 * half] = lo[i];
+          fp[i][2 * half + 1] = hi[i];
+        }
+      }
+    }
+    if constexpr (!BACK)
+      if (pair <= w >> 1)
+#pragma unroll
+        for (int i = 0; i < OUT; ++i) p.c.pf[((at * OUT + i) * kTri + tri_at(w, pair)) * 64 + lane] = fp[i];
   }
+  if (w % 2 == 0)  // the block right of the diagonal completes a fragment's 32 columns
+    *reinterpret_cast<float4*>(&sT[row][16 * w + 16 + 4 * g]) = float4{0.0f, 0.0f, 0.0f, 0.0f};
   __syncthreads();
 
   // ---- T = (I + A)^-1: the diagonal blocks of 16 by substitution, a column a
@@ -149,7 +182,6 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
       for (int i = 0; i < 16; ++i) sT[16 * w + i][16 * w + n] = t[i];
   }
   __syncthreads();
-  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
   // blocks (1, 0) and (3, 2); the inner product goes through A's own block
   if (w < 2) put16(sA, 2 * w + 1, 2 * w, mul16(sA, 2 * w + 1, 2 * w, sT, 2 * w, 2 * w, zero), 1.0f);
   __syncthreads();
@@ -168,64 +200,94 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
   }
   __syncthreads();
 
-  // ---- fragments of T diag(beta) and P, or of T^T and P^T; wave w its row block ----
+  // ---- fragments of T diag(beta), or of T^T; wave w its row block ----
   for (int kb = BACK ? w >> 1 : 0; kb <= (BACK ? 1 : w >> 1); ++kb) {
-    const int c = 32 * kb + 8 * g;
-    u32x4 ft[3], fp[OUT];
+    u32x4 ft[3];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      uint32_t part[3], op[OUT];
-      const int x = c + 2 * e;
-      if constexpr (BACK) {
-        split2(sT[x][row], sT[x + 1][row], part);
-        split2(sP[x][row], sP[x + 1][row], op);
-      } else {
-        split2(sT[row][x] * sbeta[x], sT[row][x + 1] * sbeta[x + 1], part);
-        split2(sP[row][x], sP[row][x + 1], op);
-      }
+      uint32_t part[3];
+      const int x = 32 * kb + frag_tok(g, 2 * e);
+      if constexpr (BACK) split2(sT[x][row], sT[x + 1][row], part);
+      else split2(sT[row][x] * sbeta[x], sT[row][x + 1] * sbeta[x + 1], part);
 #pragma unroll
       for (int i = 0; i < 3; ++i) ft[i][e] = part[i];
-#pragma unroll
-      for (int i = 0; i < OUT; ++i) fp[i][e] = op[i];
     }
-    const int64_t at = slot * p.hv + h;
     const int f = BACK ? tri_up(w, kb) : tri_at(w, kb);
 #pragma unroll
     for (int i = 0; i < 3; ++i) p.c.tf[((at * 3 + i) * kTri + f) * 64 + lane] = ft[i];
-#pragma unroll
-    for (int i = 0; i < OUT; ++i) p.c.pf[((at * OUT + i) * kTri + f) * 64 + lane] = fp[i];
   }
-  // ---- fragments of K^T (and Q^T) ----
-  if (h % r != 0) return;
-  const auto transposed = [&](u32x4* dst) {
-    const uint16_t* const flat = reinterpret_cast<const uint16_t*>(&sk[0][0][0][0]);
-    for (int f = w; f < IN * 2 * KT * 2; f += 4) {
-      const int i = f / (4 * KT), t = f / 2 % (2 * KT), kb = f & 1;
-      const int d = 16 * t + n;  // the row of the transposed matrix
-      u32x4 v;
+  // ---- fragments of K^T (and Q^T): products with the unit matrix's columns ----
+  u32x4 unit[2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t two = 0;
+  for (int half = 0; half < 2; ++half)
 #pragma unroll
-        for (int o = 0; o < 2; ++o) {
-          const int tok = 32 * kb + 8 * g + 2 * e + o;
-          const int unit = ((i * 4 + tok / 16) * KT + d / 32) * 64 + (d % 32 / 8) * 16 + tok % 16;
-          two |= static_cast<uint32_t>(flat[unit * 8 + d % 8]) << (16 * o);
-        }
-        v[e] = two;
-      }
-      dst[((((slot * p.hk + j) * IN + i) * 2 * KT + t) * 2 + kb) * 64 + lane] = v;
+    for (int e = 0; e < 4; ++e) {
+      const int c = 8 * g + 2 * e - 16 * half;
+      unit[half][e] = (c == n ? 0x3f80u : 0u) | (c + 1 == n ? 0x3f800000u : 0u);
     }
+  const auto transposed = [&](u32x4* dst) {
+    const u32x4 e = w & 1 ? unit[1] : unit[0];
+    for (int t = w; t < 2 * KT; t += 4)
+#pragma unroll
+      for (int i = 0; i < IN; ++i)
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          u32x4 v;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const f32x4 x = mfma16(sk[i][2 * kb + half][t >> 1][lane], e, zero);
+            v[2 * half] = pack_bf16(x[0], x[1]);
+            v[2 * half + 1] = pack_bf16(x[2], x[3]);
+          }
+          dst[((((slot * p.hk + j) * IN + i) * 2 * KT + t) * 2 + kb) * 64 + lane] = v;
+        }
   };
-  transposed(p.c.ktf);
+  if (first) transposed(p.c.ktf);
+  // ---- P^T: D_ij q_i.k_j with the lane's j = row.  Q takes K's place in LDS,
+  // whose fragments the wave still has ----
   if constexpr (BACK) {
     __syncthreads();
 #pragma unroll
     for (int kb = 0; kb < KT; ++kb)
 #pragma unroll
-      for (int i = 0; i < IN; ++i) sk[i][w][kb][lane] = qa[kb][i];
+      for (int i = 0; i < IN; ++i) sk[i][w][kb][lane] = fq[kb][i];
     __syncthreads();
-    transposed(p.c.qtf);
+    if (first) transposed(p.c.qtf);
+#pragma unroll
+    for (int pair = 0; pair < 2; ++pair) {
+      if (pair < w >> 1) continue;
+      u32x4 fp[3];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int it = 2 * pair + half;
+        f32x4 qk = zero;
+        if (it >= w) {
+#pragma unroll
+          for (int kb = 0; kb < KT; ++kb) {
+            u32x4 a[IN];
+#pragma unroll
+            for (int i = 0; i < IN; ++i) a[i] = sk[i][it][kb][lane];
+            qk = mul_parts<3>(a, fk[kb], qk);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int o = 16 * it + 4 * g + e;
+            qk[e] *= o >= row ? expf(static_cast<float>(sG[o] - Gr)) : 0.0f;
+            if (o < row) qk[e] = 0.0f;
+          }
+        }
+        uint32_t lo[3], hi[3];
+        split2(qk[0], qk[1], lo);
+        split2(qk[2], qk[3], hi);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          fp[i][2 * half] = lo[i];
+          fp[i][2 * half + 1] = hi[i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 3; ++i) p.c.pf[((at * 3 + i) * kTri + tri_up(w, pair)) * 64 + lane] = fp[i];
+    }
   }
 }
 
