@@ -263,16 +263,6 @@ struct GradArgs {
 
 constexpr int kGradRow = kDeltaC + 4;
 
-// Eight float32 values of row r from column c (zeros behind `width` and for
-// rows that are not there), with 4-byte alignment
-__device__ __forceinline__ void load8(float (&x)[8], const float* row, bool there, int c, int width) {
-  if (there && c + 8 <= width) {
-    __builtin_memcpy(x, row + c, sizeof(x));
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = there && c + e < width ? row[c + e] : 0.0f;
-  }
-}
 template <int N>
 __device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&f)[N]) {
 #pragma unroll
@@ -283,19 +273,6 @@ __device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&f)[N]) {
     for (int i = 0; i < N; ++i) f[i][e] = part[i];
   }
 }
-template <typename TA>
-__device__ __forceinline__ void load8_act(float (&x)[8], const TA* row, bool there, int c, int width) {
-  TA raw[8];
-  if (there && c + 8 <= width) {
-    __builtin_memcpy(raw, row + c, sizeof(raw));
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = to_f32(raw[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = there && c + e < width ? to_f32(row[c + e]) : 0.0f;
-  }
-}
-
 // Per value head, with S0 and U from the forward, dS1 and Y from the pass back
 // (G1 = dO U^T, G2 = Y U^T on and below, and below, the diagonal):
 //   F = scale D G1;  E = -beta D G2
@@ -304,18 +281,27 @@ __device__ __forceinline__ void load8_act(float (&x)[8], const TA* row, bool the
 //   dbeta_i = v_i.y_i - gamma_i k_i.(Y S0^T)_i - sum_j (G2 D K K^T)_ij
 //   dG_i = q_i.dq_i + k_i.(read - write)_i  (e^{G_i} goes with what reads, e^{-G_i}
 //   with what writes), and <S1, dS1> for the last one; dg is their sum from behind
-// One workgroup a chunk and key head, over its value heads in turn.  Wave w has
-// the triangles' rows 16 w .. + 15 and the column blocks w, w + 4, .. of dQ and dK.
-template <typename TA, int KT>
-__global__ void __launch_bounds__(256) delta_grad_kernel(const GradArgs<TA> p) {
-  constexpr int IN = ActParts<TA>::in, CT = (KT + 1) / 2;
+// One workgroup of eight waves a chunk and key head, over its value heads in turn.
+// dQ and dK are cut into RT row by CT column blocks a wave; waves 0-3 have G1's and
+// F's rows, waves 4-7 G2's and E's.  The row operands (dO, Y, U, then E and F) pass
+// through LDS in parts; S0 and dS1 come as rows straight from memory, where each is
+// the right operand as it lies.
+template <int KT>
+struct GradCut {
+  static constexpr int RT = KT < 4 ? KT : 4, RG = 4 / RT, CG = 8 / RG, CT = 2 * KT / CG;
+};
+
+template <typename TA, int KT, bool SHARED>
+__global__ void __launch_bounds__(512, 2) delta_grad_kernel(const GradArgs<TA> p) {
+  constexpr int IN = ActParts<TA>::in, RT = GradCut<KT>::RT, CG = GradCut<KT>::CG, CT = GradCut<KT>::CT;
   typedef float Mat[kDeltaC][kGradRow];
   __shared__ u32x4 sF[12][3][64];  // dO, Y, U: 4 row blocks of 32 columns; then two triangles' 6 blocks
   __shared__ Mat sE, sP;
   __shared__ double sG[kDeltaC];
-  __shared__ float sga[kDeltaC], sde[kDeltaC], sbe[kDeltaC], sdb[kDeltaC], sdot[2][4][kDeltaC], sone[4];
+  __shared__ float sga[kDeltaC], sde[kDeltaC], sbe[kDeltaC], sdb[2][kDeltaC], sdot[2][CG][kDeltaC], sone[2][8];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave & 3;
+  const int cg = wave % CG, rg = wave / CG;
   const int64_t slot = blockIdx.x / static_cast<unsigned>(p.hk);
   const int j = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.hk)), rep = p.hv / p.hk;
   const int64_t per = (p.L + kDeltaC - 1) / kDeltaC;
@@ -325,20 +311,29 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const GradArgs<TA> p) {
   if (slot < q.slot || t0 >= q.hi) return;  // (a place that no chunk has)
   const int valid = static_cast<int>(q.hi - t0 < kDeltaC ? q.hi - t0 : kDeltaC);
   const size_t sv = static_cast<size_t>(p.K) * p.V, mv = sv + static_cast<size_t>(kDeltaC) * p.V;
-  const bool cols = CT > 1 || w < 2 * KT;  // (with 32 columns two waves hold none)
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int row = 16 * w + n;
 
-  f32x4 dq[4][CT], dk[4][CT];
+  const auto value = [&](const u32x4 (&f)[2][IN], int rt, int r) {
+    float x = 0.0f;
+    const int e = 4 * (rt & 1) + r;
 #pragma unroll
-  for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) dq[rt][ct] = dk[rt][ct] = zero;
+    for (int i = IN - 1; i >= 0; --i) {
+      const u32x4 v = RT == 4 ? f[rt >> 1][i] : rg * RT >= 2 ? f[1][i] : f[0][i];
+      x += e & 1 ? bf_hi(v[e >> 1]) : bf_lo(v[e >> 1]);
+    }
+    return x;
+  };
 
-  for (int h = j * rep; h < (j + 1) * rep; ++h) {
+  f32x4 dq[RT][CT], dk[RT][CT];  // with several value heads: the sums over them
+#pragma unroll
+  for (int x = 0; x < RT; ++x)
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) dq[x][ct] = dk[x][ct] = zero;
+
+  for (int h = j * rep; h < (SHARED ? (j + 1) * rep : j + 1); ++h) {
     const int64_t at = slot * p.hv + h;
-    const float *const S0 = p.mids + at * mv, *const U = S0 + sv, *const dS = p.dmid + at * sv,
-                *const Y = p.y + at * kDeltaC * p.V;
-    if (w == 0) {  // as in the preparation
+    if (wave == 0) {  // as in the preparation
       const bool in = lane < valid;
       const float x = in && p.g ? p.g[(t0 + lane) * p.hv + h] : 0.0f;
       double G = x < -1e4f ? -1e4 : static_cast<double>(x);
@@ -352,258 +347,339 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const GradArgs<TA> p) {
       sde[lane] = expf(static_cast<float>(__shfl(G, 63) - G));
       sbe[lane] = in ? p.beta[(t0 + lane) * p.hv + h] : 0.0f;
     }
-    f32x4 r1[4][CT], r2[4][CT], r3[4][CT], g1[4], g2[4];
+    f32x4 r1[RT][CT], r2[RT][CT], r3[RT][CT], gg[4];
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt) {
-      g1[rt] = g2[rt] = zero;
+    for (int x = 0; x < 4; ++x) gg[x] = zero;
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) r1[rt][ct] = r2[rt][ct] = r3[rt][ct] = zero;
-    }
+    for (int x = 0; x < RT; ++x)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) r1[x][ct] = r2[x][ct] = r3[x][ct] = zero;
     float vy = 0.0f, ss = 0.0f;
-    const int row = 16 * w + n;
-    for (int vb = 0; vb < p.V; vb += 32) {
-      const int c = vb + 8 * g;
-      float xo[8], xy[8], xu[8], xv[8];
-      const int64_t tok = (t0 + row) * p.hv + h;
-      load8_act(xo, p.dout + tok * p.V, row < valid, c, p.V);
-      load8_act(xv, p.v + (t0 + row) * p.vs + h * p.V, row < valid, c, p.V);
-      load8(xy, Y + static_cast<size_t>(row) * p.V, true, c, p.V);
-      load8(xu, U + static_cast<size_t>(row) * p.V, true, c, p.V);
-      u32x4 fo[IN], fy[3], fu[3];
-      split8(xo, fo);
-      split8(xy, fy);
-      split8(xu, fu);
+    // Rows fetched a block of 32 columns ahead: waves 0-3 Y, dO and v, waves 4-7
+    // U.  Where the last block is not full, columns behind V are made zeros in
+    // the left operands and in S0 (what is multiplied with them is finite: the
+    // next row's values).
+    float xa[8], xs[CT][8], xd[CT][8];
+    TA xo[8], xv[8];
+    const uint32_t vw = static_cast<uint32_t>(p.V) * 4;
+    const rsrc_t rS = make_rsrc(p.mids + at * mv, static_cast<uint32_t>(sv * 4));
+    const rsrc_t rD = make_rsrc(p.dmid + at * sv, static_cast<uint32_t>(sv * 4));
+    const rsrc_t rA = make_rsrc(wave < 4 ? p.y + at * kDeltaC * p.V : p.mids + at * mv + sv, kDeltaC * vw);
+    const TA* const orow = p.dout + ((t0 + row) * p.hv + h) * p.V + 8 * g;
+    const TA* const vrow = p.v + (t0 + row) * p.vs + h * p.V + 8 * g;
+    const auto rows8 = [&](float (&x)[8], rsrc_t r, uint32_t off) {
+      const u32x4 lo = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+      const u32x4 hi = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off + 16, 0, 0));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) vy = __builtin_fmaf(xv[e], xy[e], vy);
-      __syncthreads();  // (what was in LDS has been used)
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        if (i < IN) sF[w][i][lane] = fo[i < IN ? i : 0];
-        sF[4 + w][i][lane] = fy[i];
-        sF[8 + w][i][lane] = fu[i];
+      for (int e = 0; e < 4; ++e) {
+        x[e] = __uint_as_float(lo[e]);
+        x[4 + e] = __uint_as_float(hi[e]);
       }
-      __syncthreads();
-      if (cols) {
+    };
+    const auto fetch = [&](int vb) {
+      const uint32_t c = static_cast<uint32_t>(vb + 8 * g) * 4;
+      rows8(xa, rA, static_cast<uint32_t>(row) * vw + c);
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          const int d = 16 * (w + 4 * ct) + n;
-          float xs[8], xd[8];
-          load8(xs, S0 + static_cast<size_t>(d) * p.V, d < p.K, c, p.V);
-          load8(xd, dS + static_cast<size_t>(d) * p.V, d < p.K, c, p.V);
+      for (int ct = 0; ct < CT; ++ct) {
+        const uint32_t d = static_cast<uint32_t>(16 * (cg + CG * ct) + n) * vw + c;
+        rows8(xs[ct], rS, d);
+        rows8(xd[ct], rD, d);
+      }
+      const bool full = vb + 32 <= p.V;
+      if (wave < 4) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(xs[e], xd[e], ss);
-          u32x4 fs[3], fd[3];
-          split8(xs, fs);
-          split8(xd, fd);
+        for (int e = 0; e < 8; ++e) xo[e] = xv[e] = TA{};
+        if (row < valid) {
+          if (full) {
+            __builtin_memcpy(xo, orow + vb, sizeof(xo));
+            __builtin_memcpy(xv, vrow + vb, sizeof(xv));
+          } else {
 #pragma unroll
-          for (int rt = 0; rt < 4; ++rt) {
-            u32x4 a[IN], y[3], u[3];
-#pragma unroll
-            for (int i = 0; i < 3; ++i) {
-              if (i < IN) a[i < IN ? i : 0] = sF[rt][i][lane];
-              y[i] = sF[4 + rt][i][lane];
-              u[i] = sF[8 + rt][i][lane];
-            }
-            r1[rt][ct] = mul_parts<3>(a, fs, r1[rt][ct]);
-            r2[rt][ct] = mul_parts<3>(y, fs, r2[rt][ct]);
-            r3[rt][ct] = mul_parts<3>(u, fd, r3[rt][ct]);
+            for (int e = 0; e < 8; ++e)
+              if (vb + 8 * g + e < p.V) {
+                xo[e] = orow[vb + e];
+                xv[e] = vrow[vb + e];
+              }
           }
         }
       }
+      if (!full)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (vb + 8 * g + e >= p.V) {
+            xa[e] = 0.0f;
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) xs[ct][e] = 0.0f;
+          }
+    };
+    fetch(0);
+    for (int vb = 0; vb < p.V; vb += 32) {
+      u32x4 fa[3], fo[IN], fs[CT][3], fd[CT][3];
+      split8(xa, fa);
+      if (wave < 4) {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          f[e] = to_f32(xo[e]);
+          vy = __builtin_fmaf(to_f32(xv[e]), xa[e], vy);
+        }
+        split8(f, fo);
+      }
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(xs[ct][e], xd[ct][e], ss);
+        split8(xs[ct], fs[ct]);
+        split8(xd[ct], fd[ct]);
+      }
+      __syncthreads();  // (what was in LDS has been used)
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        sF[(wave < 4 ? 4 : 8) + w][i][lane] = fa[i];
+        if (i < IN && wave < 4) sF[w][i][lane] = fo[i < IN ? i : 0];
+      }
+      __syncthreads();
+      if (vb + 32 < p.V) fetch(vb + 32);
+#pragma unroll
+      for (int x = 0; x < RT; ++x) {
+        const int rt = rg * RT + x;
+        u32x4 a[IN], y[3], u[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          if (i < IN) a[i < IN ? i : 0] = sF[rt][i][lane];
+          y[i] = sF[4 + rt][i][lane];
+          u[i] = sF[8 + rt][i][lane];
+        }
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          r1[x][ct] = mul_parts<3>(a, fs[ct], r1[x][ct]);
+          r2[x][ct] = mul_parts<3>(y, fs[ct], r2[x][ct]);
+          r3[x][ct] = mul_parts<3>(u, fd[ct], r3[x][ct]);
+        }
+      }
+      u32x4 fy[3];
+      if (wave >= 4)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) fy[i] = sF[4 + w][i][lane];
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
         if (jt > w) continue;
         u32x4 u[3];
 #pragma unroll
         for (int i = 0; i < 3; ++i) u[i] = sF[8 + jt][i][lane];
-        g1[jt] = mul_parts<3>(fo, u, g1[jt]);
-        g2[jt] = mul_parts<3>(fy, u, g2[jt]);
+        if (wave < 4) gg[jt] = mul_parts<3>(fo, u, gg[jt]);
+        else gg[jt] = mul_parts<3>(fy, u, gg[jt]);
       }
     }
-    __syncthreads();
-    // ---- E, F, and what dbeta takes from A ----
+    // K^T and Q^T of the wave's columns: right operands of the triangles' products,
+    // and value by value what a result's place is multiplied with in the sums
+    u32x4 kt[CT][2][IN], qt[CT][2][IN];
+    {
+      const size_t cat = static_cast<size_t>(slot * p.hk + j) * IN * 2 * KT * 2 * 64 + lane;
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int i = 0; i < IN; ++i) {
+            kt[ct][kb][i] = p.c.ktf[cat + ((i * 2 * KT + cg + CG * ct) * 2 + kb) * 64];
+            qt[ct][kb][i] = p.c.qtf[cat + ((i * 2 * KT + cg + CG * ct) * 2 + kb) * 64];
+          }
+    }
+    // ---- F (waves 0-3); E and what dbeta takes from A (waves 4-7) ----
     f32x4 db = zero;
     const size_t kat = static_cast<size_t>(slot * p.hk + j) * IN * 4 * KT * 64 + lane;
 #pragma unroll
     for (int jt = 0; jt < 4; ++jt) {
       if (jt > w) continue;
       f32x4 kk = zero;
+      if (wave >= 4)
 #pragma unroll
-      for (int kb = 0; kb < KT; ++kb) {
-        u32x4 a[IN], c[IN];
+        for (int kb = 0; kb < KT; ++kb) {
+          u32x4 a[IN], c[IN];
 #pragma unroll
-        for (int i = 0; i < IN; ++i) {
-          a[i] = p.c.kf[kat + ((i * 4 + w) * KT + kb) * 64];
-          c[i] = p.c.kf[kat + ((i * 4 + jt) * KT + kb) * 64];
+          for (int i = 0; i < IN; ++i) {
+            a[i] = p.c.kf[kat + ((i * 4 + w) * KT + kb) * 64];
+            c[i] = p.c.kf[kat + ((i * 4 + jt) * KT + kb) * 64];
+          }
+          kk = mul_parts<3>(a, c, kk);
         }
-        kk = mul_parts<3>(a, c, kk);
-      }
       const int col = 16 * jt + n;
       const double Gc = sG[col];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int i = 16 * w + 4 * g + e;
         const float D = i >= col ? expf(static_cast<float>(sG[i] - Gc)) : 0.0f;
-        const float m = i > col ? -D * g2[jt][e] : 0.0f;
-        sE[i][col] = sbe[i] * m;
-        sP[i][col] = i >= col ? p.scale * D * g1[jt][e] : 0.0f;
-        db[e] = __builtin_fmaf(m, kk[e], db[e]);
+        if (wave < 4) {
+          sP[i][col] = i >= col ? p.scale * D * gg[jt][e] : 0.0f;
+        } else {
+          const float m = i > col ? -D * gg[jt][e] : 0.0f;
+          sE[i][col] = sbe[i] * m;
+          db[e] = __builtin_fmaf(m, kk[e], db[e]);
+        }
       }
     }
-    if (w % 2 == 0) {  // the block right of the diagonal completes a fragment's 32 columns
+    if (w % 2 == 0)  // the block right of the diagonal completes a fragment's 32 columns
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sE[16 * w + 4 * g + e][16 * w + 16 + n] = sP[16 * w + 4 * g + e][16 * w + 16 + n] = 0.0f;
+      for (int e = 0; e < 4; ++e) (wave < 4 ? sP : sE)[16 * w + 4 * g + e][16 * w + 16 + n] = 0.0f;
+    if (wave >= 4) {
+#pragma unroll
+      for (int m = 1; m < 16; m <<= 1)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) db[e] += __shfl_xor(db[e], m);
+      if (n == 0)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sdb[1][16 * w + 4 * g + e] = db[e];
+    } else {
+      vy += __shfl_xor(vy, 16);
+      vy += __shfl_xor(vy, 32);
+      if (g == 0) sdb[0][row] = vy;
     }
+    // ---- the rows' scales, and what stands in dG and dbeta before the triangles' products ----
+    float dots[RT][4], bdot[RT][4], cross = 0.0f;
 #pragma unroll
-    for (int m = 1; m < 16; m <<= 1)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) db[e] += __shfl_xor(db[e], m);
-    vy += __shfl_xor(vy, 16);
-    vy += __shfl_xor(vy, 32);
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) ss += __shfl_xor(ss, m);
-    if (n == 0)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sdb[16 * w + 4 * g + e] = db[e];
-    if (lane == 0) sone[w] = ss;
-    __syncthreads();
-    if (lane < 16) sdb[16 * w + lane] += vy;  // (row 16 w + n: lanes of this wave alone)
-    // ---- the triangles as left operands: E and F, then E^T and F^T ----
-    const size_t cat = static_cast<size_t>(slot * p.hk + j) * IN * 2 * KT * 2 * 64 + lane;
-    float dots[4][4], bdot[4][4], cross = 0.0f;
-    // rows' scales, the part of dG and of dbeta that stands before the triangles' products
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt)
+    for (int x = 0; x < RT; ++x) {
+      const int rt = rg * RT + x;
+      const f32x4 ga = *reinterpret_cast<const f32x4*>(&sga[16 * rt + 4 * g]);
+      const f32x4 de = *reinterpret_cast<const f32x4*>(&sde[16 * rt + 4 * g]);
+      const f32x4 be = *reinterpret_cast<const f32x4*>(&sbe[16 * rt + 4 * g]);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int i = 16 * rt + 4 * g + r;
-        const float ga = sga[i], de = sde[i], be = sbe[i];
-        dots[rt][r] = bdot[rt][r] = 0.0f;
+        bdot[x][r] = 0.0f;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
-          const int d = 16 * (w + 4 * ct) + n;
-          const float kx = cols && i < valid && d < p.K ? to_f32(p.k[(t0 + i) * p.ks + j * p.K + d]) : 0.0f;
-          bdot[rt][r] = __builtin_fmaf(kx, r2[rt][ct][r], bdot[rt][r]);
-          r1[rt][ct][r] *= p.scale * ga;
-          r2[rt][ct][r] *= -ga * be;
-          r3[rt][ct][r] *= de;
-          cross = __builtin_fmaf(kx, r3[rt][ct][r], cross);
+          const float kx = value(kt[ct], RT == 1 ? rt : x, r);
+          bdot[x][r] = __builtin_fmaf(kx, r2[x][ct][r], bdot[x][r]);
+          r1[x][ct][r] *= p.scale * ga[r];
+          r2[x][ct][r] *= -ga[r] * be[r];
+          r3[x][ct][r] *= de[r];
+          cross = __builtin_fmaf(kx, r3[x][ct][r], cross);
         }
-        bdot[rt][r] *= -ga;
+        bdot[x][r] *= -ga[r];
       }
+    }
+    // ---- the triangles as left operands: E and F, then E^T and F^T ----
 #pragma unroll
     for (int turn = 0; turn < 2; ++turn) {
       __syncthreads();
+      const Mat& m = wave < 4 ? sE : sP;
       for (int kb = turn ? w >> 1 : 0; kb <= (turn ? 1 : w >> 1); ++kb) {
-        const int f = turn ? tri_up(w, kb) : tri_at(w, kb);
-        float xe[8], xf[8];
+        float x[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int c = 32 * kb + frag_tok(g, e);
-          xe[e] = turn ? sE[c][row] : sE[row][c];
-          xf[e] = turn ? sP[c][row] : sP[row][c];
+          x[e] = turn ? m[c][row] : m[row][c];
         }
-        u32x4 fe[3], ff[3];
-        split8(xe, fe);
-        split8(xf, ff);
+        u32x4 f[3];
+        split8(x, f);
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          sF[f][i][lane] = fe[i];
-          sF[6 + f][i][lane] = ff[i];
-        }
+        for (int i = 0; i < 3; ++i) sF[(wave < 4 ? 0 : 6) + (turn ? tri_up(w, kb) : tri_at(w, kb))][i][lane] = f[i];
       }
       __syncthreads();
-      if (cols) {
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
+      for (int x = 0; x < RT; ++x) {
+        const int rt = rg * RT + x;
 #pragma unroll
-          for (int kb = 0; kb < 2; ++kb) {
-            u32x4 kt[IN], qt[IN];
+        for (int kb = 0; kb < 2; ++kb) {
+          if (turn ? kb < rt >> 1 : kb > rt >> 1) continue;
+          const int f = turn ? tri_up(rt, kb) : tri_at(rt, kb);
+          u32x4 e[3], y[3];
 #pragma unroll
-            for (int i = 0; i < IN; ++i) {
-              kt[i] = p.c.ktf[cat + ((i * 2 * KT + w + 4 * ct) * 2 + kb) * 64];
-              if (turn) qt[i] = p.c.qtf[cat + ((i * 2 * KT + w + 4 * ct) * 2 + kb) * 64];
-            }
+          for (int i = 0; i < 3; ++i) {
+            e[i] = sF[f][i][lane];
+            y[i] = sF[6 + f][i][lane];
+          }
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt) {
-              if (turn ? kb < rt >> 1 : kb > rt >> 1) continue;
-              const int f = turn ? tri_up(rt, kb) : tri_at(rt, kb);
-              u32x4 e[3], x[3];
-#pragma unroll
-              for (int i = 0; i < 3; ++i) {
-                e[i] = sF[f][i][lane];
-                x[i] = sF[6 + f][i][lane];
-              }
-              if (turn) {
-                r3[rt][ct] = mul_parts<3>(e, kt, r3[rt][ct]);
-                r3[rt][ct] = mul_parts<3>(x, qt, r3[rt][ct]);
-              } else {
-                r2[rt][ct] = mul_parts<3>(e, kt, r2[rt][ct]);
-                r1[rt][ct] = mul_parts<3>(x, kt, r1[rt][ct]);
-              }
+          for (int ct = 0; ct < CT; ++ct) {
+            if (turn) {
+              r3[x][ct] = mul_parts<3>(e, kt[ct][kb], r3[x][ct]);
+              r3[x][ct] = mul_parts<3>(y, qt[ct][kb], r3[x][ct]);
+            } else {
+              r2[x][ct] = mul_parts<3>(e, kt[ct][kb], r2[x][ct]);
+              r1[x][ct] = mul_parts<3>(y, kt[ct][kb], r1[x][ct]);
             }
           }
+        }
       }
     }
     // ---- dG, dbeta: sums over the rows ----
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt)
+    for (int x = 0; x < RT; ++x) {
+      const int rt = rg * RT + x;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int i = 16 * rt + 4 * g + r;
+        dots[x][r] = 0.0f;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
-          const int d = 16 * (w + 4 * ct) + n;
-          const bool there = cols && i < valid && d < p.K;
-          const float kx = there ? to_f32(p.k[(t0 + i) * p.ks + j * p.K + d]) : 0.0f;
-          const float qx = there ? to_f32(p.q[(t0 + i) * p.qs + j * p.K + d]) : 0.0f;
-          dots[rt][r] = __builtin_fmaf(qx, r1[rt][ct][r], dots[rt][r]);
-          dots[rt][r] = __builtin_fmaf(kx, r2[rt][ct][r] - r3[rt][ct][r], dots[rt][r]);
-          dq[rt][ct][r] += r1[rt][ct][r];
-          dk[rt][ct][r] += r2[rt][ct][r] + r3[rt][ct][r];
+          const float kx = value(kt[ct], RT == 1 ? rt : x, r), qx = value(qt[ct], RT == 1 ? rt : x, r);
+          dots[x][r] = __builtin_fmaf(qx, r1[x][ct][r], dots[x][r]);
+          dots[x][r] = __builtin_fmaf(kx, r2[x][ct][r] - r3[x][ct][r], dots[x][r]);
+          if constexpr (SHARED) {
+            dq[x][ct][r] += r1[x][ct][r];
+            dk[x][ct][r] += r2[x][ct][r] + r3[x][ct][r];
+          } else {
+            dq[x][ct][r] = r1[x][ct][r];
+            dk[x][ct][r] = r2[x][ct][r] + r3[x][ct][r];
+          }
         }
 #pragma unroll
         for (int m = 1; m < 16; m <<= 1) {
-          dots[rt][r] += __shfl_xor(dots[rt][r], m);
-          bdot[rt][r] += __shfl_xor(bdot[rt][r], m);
+          dots[x][r] += __shfl_xor(dots[x][r], m);
+          bdot[x][r] += __shfl_xor(bdot[x][r], m);
         }
         if (n == 0) {
-          sdot[0][w][i] = dots[rt][r];
-          sdot[1][w][i] = bdot[rt][r];
+          sdot[0][cg][16 * rt + 4 * g + r] = dots[x][r];
+          sdot[1][cg][16 * rt + 4 * g + r] = bdot[x][r];
         }
       }
+    }
+    if (rg != 0) ss = 0.0f;  // (the row groups read the same states)
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) cross += __shfl_xor(cross, m);
-    if (lane == 0) sone[w] = __builtin_fmaf(sga[kDeltaC - 1], sone[w], cross);
+    for (int m = 1; m < 64; m <<= 1) {
+      ss += __shfl_xor(ss, m);
+      cross += __shfl_xor(cross, m);
+    }
+    if (lane == 0) {
+      sone[0][wave] = ss;
+      sone[1][wave] = cross;
+    }
     __syncthreads();
-    if (w == 0) {
-      const float last = (sone[0] + sone[1]) + (sone[2] + sone[3]);
-      float d = (sdot[0][0][lane] + sdot[0][1][lane]) + (sdot[0][2][lane] + sdot[0][3][lane]);
-      const float e = (sdot[1][0][lane] + sdot[1][1][lane]) + (sdot[1][2][lane] + sdot[1][3][lane]);
+    if (wave == 0) {
+      float last = 0.0f, top = 0.0f, d = 0.0f, e = sdb[0][lane] + sdb[1][lane];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        last += sone[1][i];
+        top += sone[0][i];
+      }
+#pragma unroll
+      for (int i = 0; i < CG; ++i) {
+        d += sdot[0][i][lane];
+        e += sdot[1][i][lane];
+      }
+      last = __builtin_fmaf(sga[kDeltaC - 1], top, last);
 #pragma unroll
       for (int m = 1; m < 64; m <<= 1) {  // the sum from behind
         const float up = __shfl_down(d, m);
         if (lane + m < 64) d += up;
       }
       if (lane < valid) {
-        p.dbeta[(t0 + lane) * p.hv + h] = sdb[lane] + e;
+        p.dbeta[(t0 + lane) * p.hv + h] = e;
         if (p.dg) p.dg[(t0 + lane) * p.hv + h] = d + last;
       }
     }
     __syncthreads();
   }
-  if (!cols) return;
 #pragma unroll
-  for (int rt = 0; rt < 4; ++rt)
+  for (int x = 0; x < RT; ++x)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int i = 16 * rt + 4 * g + r;
+      const int i = 16 * (rg * RT + x) + 4 * g + r;
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
-        const int d = 16 * (w + 4 * ct) + n;
+        const int d = 16 * (cg + CG * ct) + n;
         if (i < valid && d < p.K) {
-          store_act(p.dq + ((t0 + i) * p.hk + j) * p.K + d, dq[rt][ct][r]);
-          store_act(p.dk + ((t0 + i) * p.hk + j) * p.K + d, dk[rt][ct][r]);
+          store_act(p.dq + ((t0 + i) * p.hk + j) * p.K + d, dq[x][ct][r]);
+          store_act(p.dk + ((t0 + i) * p.hk + j) * p.K + d, dk[x][ct][r]);
         }
       }
     }
@@ -642,9 +718,10 @@ void launch_bwd(const BackArgs<TA>& a, const GradArgs<TA>& e, int64_t chunks, hi
   const int64_t pairs = a.nseq * a.hv;
   hipLaunchKernelGGL((delta_back_kernel<TA, KT, 1>), dim3(static_cast<unsigned>((pairs + 7) / 8 * 8 * a.slices)),
                      dim3(256), 0, stream, a);
-  if (a.L > 0)
-    hipLaunchKernelGGL((delta_grad_kernel<TA, KT>), dim3(static_cast<unsigned>(chunks * a.hk)), dim3(256), 0, stream,
-                       e);
+  if (a.L == 0) return;
+  const dim3 grid(static_cast<unsigned>(chunks * a.hk)), block(512);
+  if (a.hv > a.hk) hipLaunchKernelGGL((delta_grad_kernel<TA, KT, true>), grid, block, 0, stream, e);
+  else hipLaunchKernelGGL((delta_grad_kernel<TA, KT, false>), grid, block, 0, stream, e);
 }
 
 template <typename TA>

@@ -22,8 +22,7 @@ namespace ssm {
 namespace {
 
 constexpr int64_t kNormMaxDim = 16384;
-constexpr int kNormWavesPerCu = 32;   // forward: more rows than that go round
-constexpr int kNormMaxParts = 512;  // workgroups that leave partial weight gradients
+constexpr int kNormWavesPerCu = 32;  // forward: more rows than that go round
 
 // 16 bytes of a row; rows may start anywhere, so the compiler is told of no
 // alignment (the hardware takes unaligned vector accesses)
@@ -33,81 +32,47 @@ struct Piece {
   TA v[n];
 };
 
+// NV pieces of a lane: values first + i step .. of a row of dim values; zeros
+// behind its end, and everywhere without the row
 template <typename TA, int NV>
-struct NormRow {
+struct Raw {
   static constexpr int VEC = Piece<TA>::n;
-  float v[NV][VEC];
-
-  // values `first + i step ..` of the row p of dim values; zeros behind it
-  __device__ __forceinline__ void load(const TA* p, int first, int step, int dim) {
-    Piece<TA> raw[NV];
+  Piece<TA> v[NV];
+  __device__ __forceinline__ void load(const TA* p, int first, int step, int dim, bool there) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = first + i * step;
-      if (c + VEC <= dim) {
-        __builtin_memcpy(&raw[i], p + c, sizeof(raw[i]));
+      if (there && c + VEC <= dim) {
+        __builtin_memcpy(&v[i], p + c, sizeof(v[i]));
       } else {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          if (c + j < dim) raw[i].v[j] = p[c + j];
-          else raw[i].v[j] = TA{};
+          v[i].v[j] = TA{};
+          if (there && c + j < dim) v[i].v[j] = p[c + j];
         }
       }
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) v[i][j] = to_f32(raw[i].v[j]);
   }
-  __device__ __forceinline__ void store(TA* p, int first, int step, int dim) const {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = first + i * step;
-      Piece<TA> raw;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) store_act(&raw.v[j], v[i][j]);
-      if (c + VEC <= dim) {
-        __builtin_memcpy(p + c, &raw, sizeof(raw));
-      } else {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          if (c + j < dim) p[c + j] = raw.v[j];
-      }
-    }
-  }
-  // rounds every value to TA, as a store and a load would
-  __device__ __forceinline__ void round() {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        TA t;
-        store_act(&t, v[i][j]);
-        v[i][j] = to_f32(t);
-      }
-  }
+  __device__ __forceinline__ float at(int i, int j) const { return to_f32(v[i].v[j]); }
 };
 
-__device__ __forceinline__ float wave_sum(float x) {
+template <typename TA, int NV>
+__device__ __forceinline__ void store_row(const float (&x)[NV][Piece<TA>::n], TA* p, int first, int step, int dim) {
+  constexpr int VEC = Piece<TA>::n;
 #pragma unroll
-  for (int m = 32; m > 0; m >>= 1) x += __shfl_xor(x, m);
-  return x;
-}
-
-// Sum over the WPR waves of a row (a fixed order).  A slot is written again
-// only behind the barrier of another one, so one barrier a sum is enough.
-template <int WPR>
-__device__ __forceinline__ float row_sum(float x, float* red, int slot) {
-  x = wave_sum(x);
-  if constexpr (WPR > 1) {
-    const int w = static_cast<int>(threadIdx.x >> 6);
-    if ((threadIdx.x & 63) == 0) red[slot * WPR + w] = x;
-    __syncthreads();
-    x = 0.0f;
+  for (int i = 0; i < NV; ++i) {
+    const int c = first + i * step;
+    Piece<TA> raw;
 #pragma unroll
-    for (int i = 0; i < WPR; ++i) x += red[slot * WPR + i];
+    for (int j = 0; j < VEC; ++j) store_act(&raw.v[j], x[i][j]);
+    if (c + VEC <= dim) {
+      __builtin_memcpy(p + c, &raw, sizeof(raw));
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if (c + j < dim) p[c + j] = raw.v[j];
+    }
   }
-  return x;
 }
 
 // Weights of a lane's columns, float32 (`fill` without the array)
@@ -130,6 +95,49 @@ __device__ __forceinline__ void load_param(float (&w)[NV][VEC], const float* p, 
   }
 }
 
+// A workgroup works on GROUPS rows at a time, `waves` waves each.  Sums over a
+// row go through the lanes of its waves and, with MULTI, through LDS in a fixed
+// order; a slot is written again only behind the barrier of another one, so one
+// barrier a sum is enough (all groups meet there).
+template <bool MULTI>
+struct RowGroup {
+  int lane, group, waves, w;
+  float* red;  // [slot][group][2][waves]
+  __device__ __forceinline__ RowGroup(int wpr, float* r) {
+    const int tid = static_cast<int>(threadIdx.x), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    waves = MULTI ? wpr : 1;
+    group = wave / waves;
+    w = wave - group * waves;
+    lane = w * 64 + (tid & 63);
+    red = r;
+  }
+  __device__ __forceinline__ void sum2(float& a, float& b, int slot) const {
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) {
+      a += __shfl_xor(a, m);
+      b += __shfl_xor(b, m);
+    }
+    if constexpr (MULTI) {
+      float* const p = red + (slot * 16 + group * waves) * 2;
+      if ((lane & 63) == 0) {
+        p[2 * w] = a;
+        p[2 * w + 1] = b;
+      }
+      __syncthreads();
+      a = b = 0.0f;
+      for (int i = 0; i < waves; ++i) {
+        a += p[2 * i];
+        b += p[2 * i + 1];
+      }
+    }
+  }
+  __device__ __forceinline__ float sum(float a, int slot) const {
+    float none = 0.0f;
+    sum2(a, none, slot);
+    return a;
+  }
+};
+
 template <typename TA>
 struct NormArgs {
   const TA *x, *res;  // forward: x and residual; backward: s and dout
@@ -139,177 +147,192 @@ struct NormArgs {
   float* part;    // backward: (parts, 2, dim)
   float eps;
   int64_t rows, xs, rs;
-  int dim;
+  int dim, waves, groups;
 };
 
 // c = s - mean(s) in place, and 1 / sqrt(mean(c^2) + eps)
-template <int WPR, typename TA, int NV>
-__device__ __forceinline__ float centre(NormRow<TA, NV>& s, float* red, int first, int step, int dim,
+template <bool MULTI, int NV, int VEC>
+__device__ __forceinline__ float centre(float (&s)[NV][VEC], const RowGroup<MULTI>& rg, int first, int step, int dim,
                                         float eps) {
-  constexpr int VEC = NormRow<TA, NV>::VEC;
   float t = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) t += s.v[i][j];
-  const float inv = 1.0f / static_cast<float>(dim), mean = row_sum<WPR>(t, red, 0) * inv;
+    for (int j = 0; j < VEC; ++j) t += s[i][j];
+  const float inv = 1.0f / static_cast<float>(dim), mean = rg.sum(t, 0) * inv;
   t = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-      s.v[i][j] = first + i * step + j < dim ? s.v[i][j] - mean : 0.0f;
-      t = __builtin_fmaf(s.v[i][j], s.v[i][j], t);
+      s[i][j] = first + i * step + j < dim ? s[i][j] - mean : 0.0f;
+      t = __builtin_fmaf(s[i][j], s[i][j], t);
     }
-  return 1.0f / sqrtf(__builtin_fmaf(row_sum<WPR>(t, red, 1), inv, eps));
+  return 1.0f / sqrtf(__builtin_fmaf(rg.sum(t, 1), inv, eps));
 }
 
-// Each row group (a wave, or WPR of them) goes through every gridDim-th row
-// with its columns' weights in registers.
-template <typename TA, int NV, int WPR, bool RES>
-__global__ void __launch_bounds__(WPR > 4 ? 64 * WPR : 256)
-    norm_fwd_kernel(const NormArgs<TA> p) {
-  constexpr int VEC = Piece<TA>::n, step = 64 * WPR * VEC, GROUPS = WPR == 1 ? 4 : 1;
-  __shared__ float red[2 * WPR];
-  const int tid = static_cast<int>(threadIdx.x);
-  const int lane = WPR == 1 ? tid & 63 : tid, group = WPR == 1 ? tid >> 6 : 0;
-  const int first = lane * VEC, dim = p.dim;
-  const int64_t hop = int64_t{gridDim.x} * GROUPS;
-  int64_t row = int64_t{blockIdx.x} * GROUPS + group;
-  if (row >= p.rows) return;  // (whole waves, and no barrier with one wave a row)
-  NormRow<TA, NV> s, r;
-  s.load(p.x + row * p.xs, first, step, dim);
-  if constexpr (RES) r.load(p.res + row * p.rs, first, step, dim);
+// Every row group goes through its share of the rows with its columns' weights
+// in registers.
+template <typename TA, int NV, bool MULTI, bool RES>
+__global__ void __launch_bounds__(MULTI ? 1024 : 256) norm_fwd_kernel(const NormArgs<TA> p) {
+  constexpr int VEC = Piece<TA>::n;
+  __shared__ float red[MULTI ? 64 : 1];
+  const RowGroup<MULTI> rg(p.waves, red);
+  const int first = rg.lane * VEC, dim = p.dim, step = 64 * rg.waves * VEC;
+  const int64_t hop = int64_t{gridDim.x} * p.groups;
   float w[NV][VEC], b[NV][VEC];
   load_param(w, p.w, 1.0f, first, step, dim);
   load_param(b, p.b, 0.0f, first, step, dim);
-  for (;;) {
-    if constexpr (RES) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) s.v[i][j] += r.v[i][j];
-      s.round();
-      if (p.sum) s.store(p.sum + row * dim, first, step, dim);
-    }
-    const float rstd = centre<WPR>(s, red, first, step, dim, p.eps);
+  for (int64_t base = int64_t{blockIdx.x} * p.groups; base < p.rows; base += hop) {
+    const int64_t row = base + rg.group;
+    const bool there = row < p.rows;
+    Raw<TA, NV> s, r;
+    s.load(p.x + row * p.xs, first, step, dim, there);
+    if constexpr (RES) r.load(p.res + row * p.rs, first, step, dim, there);
+    float x[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) s.v[i][j] = __builtin_fmaf(s.v[i][j] * rstd, w[i][j], b[i][j]);
-    s.store(p.out + row * dim, first, step, dim);
-    row += hop;
-    if (row >= p.rows) return;
-    s.load(p.x + row * p.xs, first, step, dim);
-    if constexpr (RES) r.load(p.res + row * p.rs, first, step, dim);
+      for (int j = 0; j < VEC; ++j) {
+        x[i][j] = s.at(i, j);
+        if constexpr (RES) {  // rounded, as it is kept
+          TA t;
+          store_act(&t, x[i][j] + r.at(i, j));
+          x[i][j] = to_f32(t);
+        }
+      }
+    if constexpr (RES)
+      if (p.sum && there) store_row<TA, NV>(x, p.sum + row * dim, first, step, dim);
+    const float rstd = centre<MULTI>(x, rg, first, step, dim, p.eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) x[i][j] = __builtin_fmaf(x[i][j] * rstd, w[i][j], b[i][j]);
+    if (there) store_row<TA, NV>(x, p.out + row * dim, first, step, dim);
   }
 }
 
-// Gradients: each row group (a wave, or WPR of them) goes through every
-// gridDim-th row with its columns' weight gradients in registers; the
-// workgroup's groups are added through LDS, and the workgroup leaves one
+// Gradients, in the same way, with the columns' weight gradients in registers
+// too; the groups' are added through LDS in turn, and the workgroup leaves one
 // partial row.
-template <typename TA, int NV, int WPR>
-__global__ void __launch_bounds__(WPR > 4 ? 64 * WPR : 256)
-    norm_bwd_kernel(const NormArgs<TA> p) {
-  constexpr int VEC = Piece<TA>::n, step = 64 * WPR * VEC, GROUPS = WPR == 1 ? 4 : 1;
-  __shared__ float red[4 * WPR];
-  const int tid = static_cast<int>(threadIdx.x);
-  const int lane = WPR == 1 ? tid & 63 : tid, group = WPR == 1 ? tid >> 6 : 0;
-  const int first = lane * VEC, dim = p.dim;
+template <typename TA, int NV, bool MULTI>
+__global__ void __launch_bounds__(MULTI ? 1024 : 256) norm_bwd_kernel(const NormArgs<TA> p) {
+  constexpr int VEC = Piece<TA>::n;
+  __shared__ float red[MULTI ? 96 : 1];
+  extern __shared__ float fold[];  // [2][64 waves VEC], with several groups
+  const RowGroup<MULTI> rg(p.waves, red);
+  const int first = rg.lane * VEC, dim = p.dim, step = 64 * rg.waves * VEC;
+  const int64_t hop = int64_t{gridDim.x} * p.groups;
   float dw[NV][VEC], db[NV][VEC], w[NV][VEC];
   load_param(w, p.w, 1.0f, first, step, dim);
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) dw[i][j] = db[i][j] = 0.0f;
-  const int64_t hop = int64_t{gridDim.x} * GROUPS;
-  for (int64_t row = int64_t{blockIdx.x} * GROUPS + group; row < p.rows; row += hop) {
-    NormRow<TA, NV> s, y;
-    s.load(p.x + row * p.xs, first, step, dim);
-    y.load(p.res + row * dim, first, step, dim);
-    const float rstd = centre<WPR>(s, red, first, step, dim, p.eps);
+  for (int64_t base = int64_t{blockIdx.x} * p.groups; base < p.rows; base += hop) {
+    const int64_t row = base + rg.group;
+    const bool there = row < p.rows;
+    Raw<TA, NV> rs, ry, rd;
+    rs.load(p.x + row * p.xs, first, step, dim, there);
+    ry.load(p.res + row * dim, first, step, dim, there);
+    if (p.dres) rd.load(p.dres + row * dim, first, step, dim, there);
+    float s[NV][VEC], y[NV][VEC];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        s[i][j] = rs.at(i, j);
+        y[i][j] = ry.at(i, j);
+      }
+    const float rstd = centre<MULTI>(s, rg, first, step, dim, p.eps);
     float t0 = 0.0f, t1 = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        const float h = s.v[i][j] * rstd, g = y.v[i][j];
+        const float h = s[i][j] * rstd, g = y[i][j];  // (0 for a row that is not there)
         dw[i][j] = __builtin_fmaf(g, h, dw[i][j]);
         db[i][j] += g;
-        s.v[i][j] = h;
-        y.v[i][j] = g * w[i][j];
-        t0 += y.v[i][j];
-        t1 = __builtin_fmaf(y.v[i][j], h, t1);
+        s[i][j] = h;
+        y[i][j] = g * w[i][j];
+        t0 += y[i][j];
+        t1 = __builtin_fmaf(y[i][j], h, t1);
       }
+    rg.sum2(t0, t1, 2);
     const float inv = 1.0f / static_cast<float>(dim);
-    t0 = row_sum<WPR>(t0, red, 2) * inv;
-    t1 = row_sum<WPR>(t1, red, 3) * inv;
+    t0 *= inv;
+    t1 *= inv;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < VEC; ++j)
-        y.v[i][j] = rstd * (y.v[i][j] - t0 - s.v[i][j] * t1);
-    if (p.dres) {
-      s.load(p.dres + row * dim, first, step, dim);
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) y.v[i][j] += s.v[i][j];
-    }
-    y.store(p.out + row * dim, first, step, dim);
+        y[i][j] = __builtin_fmaf(rstd, y[i][j] - t0 - s[i][j] * t1, p.dres ? rd.at(i, j) : 0.0f);
+    if (there) store_row<TA, NV>(y, p.out + row * dim, first, step, dim);
   }
   if (!p.part) return;
-  if constexpr (GROUPS > 1) {
-    __shared__ float fold[2][64 * VEC];
-    for (int g = 1; g < GROUPS; ++g)
-      for (int i = 0; i < NV; ++i) {
-        __syncthreads();
-        if (group == g)
-          for (int j = 0; j < VEC; ++j) {
-            fold[0][j * 64 + lane] = dw[i][j];
-            fold[1][j * 64 + lane] = db[i][j];
-          }
-        __syncthreads();
-        if (group == 0)
-          for (int j = 0; j < VEC; ++j) {
-            dw[i][j] += fold[0][j * 64 + lane];
-            db[i][j] += fold[1][j * 64 + lane];
-          }
-      }
-    if (group != 0) return;
-  }
+  const int lanes = 64 * rg.waves;
+  for (int g = 1; g < p.groups; ++g)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      __syncthreads();
+      if (rg.group == g)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          fold[j * lanes + rg.lane] = dw[i][j];
+          fold[(VEC + j) * lanes + rg.lane] = db[i][j];
+        }
+      __syncthreads();
+      if (rg.group == 0)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          dw[i][j] += fold[j * lanes + rg.lane];
+          db[i][j] += fold[(VEC + j) * lanes + rg.lane];
+        }
+    }
+  if (rg.group != 0) return;
   float* const o = p.part + int64_t{blockIdx.x} * 2 * dim;
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    const int c = first + i * step;
+    if (c + VEC <= dim) {
+      __builtin_memcpy(o + c, dw[i], sizeof(dw[i]));
+      __builtin_memcpy(o + dim + c, db[i], sizeof(db[i]));
+    } else {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const int c = first + i * step + j;
-      if (c < dim) {
-        o[c] = dw[i][j];
-        o[dim + c] = db[i][j];
-      }
+      for (int j = 0; j < VEC; ++j)
+        if (c + j < dim) {
+          o[c + j] = dw[i][j];
+          o[dim + c + j] = db[i][j];
+        }
     }
+  }
 }
 
-// The partial rows' sum: a workgroup takes 64 of the 2 dim columns, its four
-// waves every fourth row.
-__global__ void __launch_bounds__(256)
+// The partial rows' sum: a workgroup takes 64 of the 2 dim columns, each of its
+// sixteen waves every sixteenth row, in four sums at a time.
+__global__ void __launch_bounds__(1024)
     norm_reduce_kernel(const float* part, int parts, int dim, float* dw, float* db) {
-  __shared__ float red[4][64];
+  __shared__ float red[16][64];
   const int lane = static_cast<int>(threadIdx.x & 63), g = static_cast<int>(threadIdx.x >> 6);
   const int c = static_cast<int>(blockIdx.x) * 64 + lane, n = 2 * dim;
-  float t = 0.0f;
-  if (c < n)
-    for (int i = g; i < parts; i += 4) t += part[static_cast<size_t>(i) * n + c];
-  red[g][lane] = t;
+  float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (c < n) {
+    int i = g;
+    for (; i + 48 < parts; i += 64)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) t[k] += part[static_cast<size_t>(i + 16 * k) * n + c];
+    for (; i < parts; i += 16) t[0] += part[static_cast<size_t>(i) * n + c];
+  }
+  red[g][lane] = (t[0] + t[1]) + (t[2] + t[3]);
   __syncthreads();
   if (g != 0 || c >= n) return;
-  t = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+  float x = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) x += red[k][lane];
   if (c < dim) {
-    if (dw) dw[c] = t;
+    if (dw) dw[c] = x;
   } else if (db) {
-    db[c - dim] = t;
+    db[c - dim] = x;
   }
 }
 
@@ -318,29 +341,59 @@ struct Count {
   static constexpr int value = N;
 };
 
-// Calls go(NV, WPR) for the fewest waves a row fits with four pieces a lane;
-// with few rows four waves share one.
-template <typename TA, typename Go>
-void norm_choose(int64_t rows, int dim, Go&& go) {
-  constexpr int VEC = Piece<TA>::n;
-  const int pieces = (dim + VEC - 1) / VEC;
-  const auto with = [&](auto wpr) {
-    constexpr int W = decltype(wpr)::value;
-    const int nv = (pieces + 64 * W - 1) / (64 * W);
-    if (nv <= 1) go(Count<1>{}, wpr);
-    else if (nv <= 2) go(Count<2>{}, wpr);
-    else if (nv <= 3) go(Count<3>{}, wpr);
-    else go(Count<4>{}, wpr);
-  };
+struct NormPlan {
+  bool multi;
+  int nv, waves, groups;
+};
+
+// One wave a row while its share of a row stays within `most` pieces a lane:
+// five in the forward (8192 x 2560 bf16 with the sum 27.7 us, shared by five waves
+// 30.6; 131072 x 2048 188 and 201 us), three in the backward, which keeps three
+// times as many values (8192 x 1536 bf16 26.6 us, by three waves 32.7; 3001 x 515
+// float32 9.8 and 13.1 us).  Wider rows, and rows too few to fill the device, are
+// shared by waves.
+NormPlan norm_plan(int64_t rows, int dim, int vec, int most) {
+  const int pieces = (dim + vec - 1) / vec, nv = (pieces + 63) / 64;
   const bool few = rows < 4 * device_cus();
-  if (pieces <= 64 * 4 && (!few || pieces <= 64)) with(Count<1>{});
-  else if (pieces <= 256 * 4) with(Count<4>{});
-  else with(Count<16>{});
+  if (nv <= 1 || (nv <= most && !few)) return NormPlan{false, nv, 1, 4};
+  NormPlan p{true, 1, nv, 1};
+  while (p.nv * 16 < nv) p.nv *= 2;
+  p.waves = (nv + p.nv - 1) / p.nv;
+  return p;
 }
 
-int norm_parts(int64_t rows) {
-  const int64_t n = (rows + 3) / 4;
-  return static_cast<int>(n < 1 ? 1 : n > kNormMaxParts ? kNormMaxParts : n);
+// Calls go(NV, MULTI); ONE and MANY bound what the caller's plans can hold.
+template <int ONE, int MANY, typename Go>
+void norm_go(const NormPlan& p, Go&& go) {
+  if (!p.multi) {
+    if (p.nv == 1) go(Count<1>{}, Count<0>{});
+    else if (p.nv == 2) go(Count<2>{}, Count<0>{});
+    else if (p.nv == 3) go(Count<3>{}, Count<0>{});
+    else if constexpr (ONE == 5) {
+      if (p.nv == 4) go(Count<4>{}, Count<0>{});
+      else go(Count<5>{}, Count<0>{});
+    }
+  } else if (p.nv == 1) {
+    go(Count<1>{}, Count<1>{});
+  } else if (p.nv == 2) {
+    go(Count<2>{}, Count<1>{});
+  } else if constexpr (MANY == 4) {
+    go(Count<4>{}, Count<1>{});
+  }
+}
+
+NormPlan bwd_plan(int64_t rows, int dim, int vec) {
+  NormPlan p = norm_plan(rows, dim, vec, 3);
+  if (p.multi) p.groups = p.nv == 1 ? 16 / p.waves : 1;  // (more rows to a partial row)
+  return p;
+}
+
+int norm_parts(const NormPlan& p, int64_t rows) {
+  const int64_t n = (rows + p.groups - 1) / p.groups;
+  // (two workgroups a compute unit with one wave a row: 8192 x 1536 bf16 26.6 us,
+  // one 40.8, three 33.0)
+  const int64_t most = device_cus() * (p.multi ? 1 : 2);
+  return static_cast<int>(n < 1 ? 1 : n > most ? most : n);
 }
 
 bool norm_sizes_ok(int64_t rows, int64_t dim, int64_t s0, int64_t s1) {
@@ -356,14 +409,18 @@ size_t strided(int64_t rows, int64_t dim, int64_t stride, size_t es) {
 template <typename TA>
 int launch_norm_fwd(const char* fn, const void* x, const void* res, const float* w, const float* b, float eps,
                     void* out, void* sum, int64_t rows, int dim, int64_t xs, int64_t rs, hipStream_t stream) {
-  const NormArgs<TA> a{static_cast<const TA*>(x), static_cast<const TA*>(res), nullptr, w, b,
-                       static_cast<TA*>(out), static_cast<TA*>(sum), nullptr, eps, rows, xs, rs, dim};
-  norm_choose<TA>(rows, dim, [&](auto nv, auto wpr) {
-    constexpr int NV = decltype(nv)::value, W = decltype(wpr)::value;
-    const int64_t units = W == 1 ? (rows + 3) / 4 : rows, most = int64_t{device_cus()} * kNormWavesPerCu / (W == 1 ? 4 : W);
-    const dim3 grid(static_cast<unsigned>(units < most ? units : most)), block(W == 1 ? 256 : 64 * W);
-    if (res) hipLaunchKernelGGL((norm_fwd_kernel<TA, NV, W, true>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((norm_fwd_kernel<TA, NV, W, false>), grid, block, 0, stream, a);
+  const NormPlan plan = norm_plan(rows, dim, Piece<TA>::n, 5);
+  const NormArgs<TA> a{static_cast<const TA*>(x), static_cast<const TA*>(res), nullptr, w, b, static_cast<TA*>(out),
+                       static_cast<TA*>(sum), nullptr, eps, rows, xs, rs, dim, plan.waves, plan.groups};
+  const int64_t units = (rows + plan.groups - 1) / plan.groups;
+  const int64_t most = int64_t{device_cus()} * kNormWavesPerCu / (plan.waves * plan.groups);
+  const dim3 grid(static_cast<unsigned>(units < most ? units : most)), block(64 * plan.waves * plan.groups);
+  constexpr int most_nv = kNormMaxDim / (16 * 64 * Piece<TA>::n);
+  norm_go<5, most_nv>(plan, [&](auto nv, auto multi) {
+    constexpr int NV = decltype(nv)::value;
+    constexpr bool M = decltype(multi)::value != 0;
+    if (res) hipLaunchKernelGGL((norm_fwd_kernel<TA, NV, M, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((norm_fwd_kernel<TA, NV, M, false>), grid, block, 0, stream, a);
   });
   return launch_status(fn);
 }
@@ -372,16 +429,19 @@ template <typename TA>
 int launch_norm_bwd(const char* fn, const void* s, const float* w, float eps, const void* dout, const void* dres,
                     void* dx, float* dw, float* db, int64_t rows, int dim, int64_t ss, float* part,
                     hipStream_t stream) {
-  const int parts = norm_parts(rows);
+  constexpr int VEC = Piece<TA>::n;
+  const NormPlan plan = bwd_plan(rows, dim, VEC);
+  const int parts = norm_parts(plan, rows);
   const NormArgs<TA> a{static_cast<const TA*>(s), static_cast<const TA*>(dout), static_cast<const TA*>(dres), w,
-                       nullptr, static_cast<TA*>(dx), nullptr, dw || db ? part : nullptr, eps, rows, ss, dim, dim};
-  norm_choose<TA>(rows, dim, [&](auto nv, auto wpr) {
-    constexpr int NV = decltype(nv)::value, W = decltype(wpr)::value;
-    hipLaunchKernelGGL((norm_bwd_kernel<TA, NV, W>), dim3(static_cast<unsigned>(parts)),
-                       dim3(W == 1 ? 256 : 64 * W), 0, stream, a);
+                       nullptr, static_cast<TA*>(dx), nullptr, dw || db ? part : nullptr, eps, rows, ss, dim, dim,
+                       plan.waves, plan.groups};
+  const size_t lds = plan.groups > 1 ? sizeof(float) * 2 * 64 * plan.waves * VEC : 0;
+  norm_go<3, kNormMaxDim / (16 * 64 * VEC)>(plan, [&](auto nv, auto multi) {
+    hipLaunchKernelGGL((norm_bwd_kernel<TA, decltype(nv)::value, decltype(multi)::value != 0>),
+                       dim3(static_cast<unsigned>(parts)), dim3(64 * plan.waves * plan.groups), lds, stream, a);
   });
   if (dw || db)
-    hipLaunchKernelGGL(norm_reduce_kernel, dim3(static_cast<unsigned>((2 * dim + 63) / 64)), dim3(256), 0, stream,
+    hipLaunchKernelGGL(norm_reduce_kernel, dim3(static_cast<unsigned>((2 * dim + 63) / 64)), dim3(1024), 0, stream,
                        part, parts, dim, dw, db);
   return launch_status(fn);
 }
@@ -435,7 +495,8 @@ int ssm_layer_norm_fwd(const void* x, const void* residual, const float* weight,
 
 size_t ssm_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, int dtype) {
   if ((dtype != SSM_DTYPE_F32 && dtype != SSM_DTYPE_BF16) || !norm_sizes_ok(rows, dim, dim, dim)) return 0;
-  return static_cast<size_t>(norm_parts(rows)) * 2 * dim * 4;
+  const NormPlan plan = bwd_plan(rows, static_cast<int>(dim), dtype == SSM_DTYPE_F32 ? 4 : 8);
+  return static_cast<size_t>(norm_parts(plan, rows)) * 2 * dim * 4;
 }
 
 int ssm_layer_norm_bwd(const void* s, const float* weight, float eps, const void* dout, const void* dresidual,
