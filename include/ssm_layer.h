@@ -65,8 +65,9 @@ extern "C" {
  *   chunk_states    : (batch, ceil(seqlen / SSM_DELTA_CHUNK), nheads_v,
  *                     headdim_k + SSM_DELTA_CHUNK, headdim_v) float32 or NULL;
  *                     receives for every chunk of SSM_DELTA_CHUNK tokens the
- *                     state before it (headdim_k rows), then u of its tokens
- *                     (zeros behind the last one), for ssm_delta_rule_bwd
+ *                     state before it (headdim_k rows), then v - S^T k of its
+ *                     tokens (zeros behind the last one), for
+ *                     ssm_delta_rule_bwd
  *   1 <= headdim_k, headdim_v <= 256; nheads_v a multiple of nheads_k, at most
  *   65535; 1 <= batch <= 65535; seqlen >= 0 (0 only copies the initial state);
  *   batch * seqlen < 2^31; batch * ceil(seqlen / SSM_DELTA_CHUNK) * nheads_v <

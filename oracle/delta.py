@@ -32,12 +32,12 @@ def delta_rule(q, k, v, beta, g=None, scale=None, h0=None):
     return out, S, before
 
 
-def updates(q, k, v, beta, g=None, scale=None, h0=None):
-    """u of every token (L, Hv, V)."""
+def missing(q, k, v, beta, g=None, scale=None, h0=None):
+    """v - S^T k of every token (L, Hv, V)."""
     _, last, before = delta_rule(q, k, v, beta, g, scale, h0)
     _, kh = _heads(q, k, v.shape[1])
     S = before if g is None else np.exp(g)[:, :, None, None] * before
-    return beta[:, :, None] * (v - np.einsum("thkv,thk->thv", S, kh))
+    return v - np.einsum("thkv,thk->thv", S, kh)
 
 
 def delta_rule_bwd(q, k, v, beta, dout, g=None, scale=None, h0=None, dlast=None):

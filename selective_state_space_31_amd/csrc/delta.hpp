@@ -31,7 +31,7 @@ struct DeltaDims {
     return packed ? L / kDeltaC + nseq : nseq * ((L + kDeltaC - 1) / kDeltaC);
   }
   size_t state_values() const { return static_cast<size_t>(hv) * K * V; }
-  // of chunk_states: the state and the chunk's u per place and head
+  // of chunk_states: the state and the chunk's e per place and head
   size_t mid_values() const { return static_cast<size_t>(chunks()) * hv * (K + kDeltaC) * V; }
 };
 
@@ -216,18 +216,25 @@ __device__ __forceinline__ void buffer_store_act(float v, rsrc_t r, uint32_t off
 // ---------------------------------------------------------------------------
 // chunks
 // ---------------------------------------------------------------------------
-// What does not depend on the state, per chunk (delta_prep.hip).  K and Q are
-// the chunk's rows, gamma_i = e^{G_i} with G the running sum of g, D_ij =
-// e^{G_i - G_j}, A_ij = beta_i D_ij k_i.k_j below the diagonal, T = (I + A)^-1,
-// P_ij = D_ij q_i.k_j on and below it.
+// With S0 the state before a chunk, G the running sum of g, gamma_i = e^{G_i},
+// D_ij = e^{G_i - G_j} and e_i = v_i - S^T k_i what a token finds missing (so u =
+// beta e):
+//   (I + A) e = V - gamma (K S0),  A_ij = beta_j D_ij k_i.k_j below the diagonal
+//   out = scale (gamma (Q S0) + P e),  P_ij = beta_j D_ij q_i.k_j on and below it
+//   S1 = gamma_63 S0 + K^T (d e),  d_j = beta_j e^{G_63 - G_j}
+// e rather than u, so that beta = 0 needs no division for beta's gradient, which is
+// y.e.  The backward solves with beta_i in A_ij and keeps beta out of P and d: that
+// is the transposed system of u.
+// What does not depend on the state is prepared per chunk (delta_prep.hip), T =
+// (I + A)^-1 among it.
 struct ChunkSpace {
   // per place and key head, parts in turn: fragments of K and Q (4 row blocks x
   // KT of 32 columns) and of K^T and Q^T (2 KT row blocks x 2 of 32 tokens)
   u32x4 *kf, *qf, *ktf, *qtf;
-  // per place and value head: fragments of T diag(beta) in three parts and of P
-  // (forward), of T^T and P^T in three parts each (backward)
+  // per place and value head: fragments of T in three parts and of P (forward), of
+  // T^T and P^T in three parts each (backward)
   u32x4 *tf, *pf;
-  float* vec;  // gamma (64), e^{G_63 - G_i} (64)
+  float* vec;  // gamma (64), d (64)
 };
 
 template <typename TA>

@@ -250,14 +250,14 @@ __global__ void __launch_bounds__(256) delta_back_kernel(const BackArgs<TA> p) {
 // ---------------------------------------------------------------------------
 template <typename TA>
 struct GradArgs {
-  const TA *q, *k, *v, *dout;
+  const TA* dout;
   const float *beta, *g, *mids, *dmid, *y;
   TA *dq, *dk;
   float *dbeta, *dg;
   const int32_t* cu;
   ChunkSpace c;
   float scale;
-  int64_t nseq, L, qs, ks, vs;
+  int64_t nseq, L;
   int hk, hv, K, V;
 };
 
@@ -273,17 +273,17 @@ __device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&f)[N]) {
     for (int i = 0; i < N; ++i) f[i][e] = part[i];
   }
 }
-// Per value head, with S0 and U from the forward, dS1 and Y from the pass back
-// (G1 = dO U^T, G2 = Y U^T on and below, and below, the diagonal):
-//   F = scale D G1;  E = -beta D G2
+// Per value head, with S0 and E from the forward, dS1 and Y from the pass back
+// (G1 = dO E^T on and below the diagonal, G2 = Y E^T below it):
+//   F_ij = scale beta_j D_ij G1_ij;  H_ij = -beta_i beta_j D_ij G2_ij
 //   dQ = scale gamma (dO S0^T) + F K
-//   dK = [E K - gamma beta (Y S0^T)] + [d (U dS1^T) + E^T K + F^T Q] = read + write
-//   dbeta_i = v_i.y_i - gamma_i k_i.(Y S0^T)_i - sum_j (G2 D K K^T)_ij
+//   dK = [H K - gamma beta (Y S0^T)] + [d beta (E dS1^T) + H^T K + F^T Q] = read + write
+//   dbeta_i = y_i.e_i
 //   dG_i = q_i.dq_i + k_i.(read - write)_i  (e^{G_i} goes with what reads, e^{-G_i}
 //   with what writes), and <S1, dS1> for the last one; dg is their sum from behind
 // One workgroup of eight waves a chunk and key head, over its value heads in turn.
 // dQ and dK are cut into RT row by CT column blocks a wave; waves 0-3 have G1's and
-// F's rows, waves 4-7 G2's and E's.  The row operands (dO, Y, U, then E and F) pass
+// F's rows, waves 4-7 G2's and H's.  The row operands (dO, Y, E, then H and F) pass
 // through LDS in parts; S0 and dS1 come as rows straight from memory, where each is
 // the right operand as it lies.
 template <int KT>
@@ -295,10 +295,10 @@ template <typename TA, int KT, bool SHARED>
 __global__ void __launch_bounds__(512, 2) delta_grad_kernel(const GradArgs<TA> p) {
   constexpr int IN = ActParts<TA>::in, RT = GradCut<KT>::RT, CG = GradCut<KT>::CG, CT = GradCut<KT>::CT;
   typedef float Mat[kDeltaC][kGradRow];
-  __shared__ u32x4 sF[12][3][64];  // dO, Y, U: 4 row blocks of 32 columns; then two triangles' 6 blocks
-  __shared__ Mat sE, sP;
+  __shared__ u32x4 sF[12][3][64];  // dO, Y, E: 4 row blocks of 32 columns; then two triangles' 6 blocks
+  __shared__ Mat sH, sP;
   __shared__ double sG[kDeltaC];
-  __shared__ float sga[kDeltaC], sde[kDeltaC], sbe[kDeltaC], sdb[2][kDeltaC], sdot[2][CG][kDeltaC], sone[2][8];
+  __shared__ float sga[kDeltaC], sde[kDeltaC], sbe[kDeltaC], sdb[kDeltaC], sdot[CG][kDeltaC], sone[2][8];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave & 3;
   const int cg = wave % CG, rg = wave / CG;
@@ -354,19 +354,16 @@ __global__ void __launch_bounds__(512, 2) delta_grad_kernel(const GradArgs<TA> p
     for (int x = 0; x < RT; ++x)
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) r1[x][ct] = r2[x][ct] = r3[x][ct] = zero;
-    float vy = 0.0f, ss = 0.0f;
-    // Rows fetched a block of 32 columns ahead: waves 0-3 Y, dO and v, waves 4-7
-    // U.  Where the last block is not full, columns behind V are made zeros in
-    // the left operands and in S0 (what is multiplied with them is finite: the
-    // next row's values).
-    float xa[8], xs[CT][8], xd[CT][8];
-    TA xo[8], xv[8];
+    float ye = 0.0f, ss = 0.0f;
+    // Rows of 32 columns at a time: waves 0-3 E (and Y for y.e), waves 4-7 Y and dO.
+    // Where the last block is not full, columns behind V are made zeros in the left
+    // operands and in S0 (what is multiplied with them is finite: the next row's).
     const uint32_t vw = static_cast<uint32_t>(p.V) * 4;
     const rsrc_t rS = make_rsrc(p.mids + at * mv, static_cast<uint32_t>(sv * 4));
     const rsrc_t rD = make_rsrc(p.dmid + at * sv, static_cast<uint32_t>(sv * 4));
-    const rsrc_t rA = make_rsrc(wave < 4 ? p.y + at * kDeltaC * p.V : p.mids + at * mv + sv, kDeltaC * vw);
+    const rsrc_t rE = make_rsrc(p.mids + at * mv + sv, kDeltaC * vw);
+    const rsrc_t rY = make_rsrc(p.y + at * kDeltaC * p.V, kDeltaC * vw);
     const TA* const orow = p.dout + ((t0 + row) * p.hv + h) * p.V + 8 * g;
-    const TA* const vrow = p.v + (t0 + row) * p.vs + h * p.V + 8 * g;
     const auto rows8 = [&](float (&x)[8], rsrc_t r, uint32_t off) {
       const u32x4 lo = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
       const u32x4 hi = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off + 16, 0, 0));
@@ -376,55 +373,61 @@ __global__ void __launch_bounds__(512, 2) delta_grad_kernel(const GradArgs<TA> p
         x[4 + e] = __uint_as_float(hi[e]);
       }
     };
-    const auto fetch = [&](int vb) {
+    for (int vb = 0; vb < p.V; vb += 32) {
       const uint32_t c = static_cast<uint32_t>(vb + 8 * g) * 4;
-      rows8(xa, rA, static_cast<uint32_t>(row) * vw + c);
+      const bool full = vb + 32 <= p.V;
+      float xs[CT][8], xd[CT][8];
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
         const uint32_t d = static_cast<uint32_t>(16 * (cg + CG * ct) + n) * vw + c;
         rows8(xs[ct], rS, d);
         rows8(xd[ct], rD, d);
       }
-      const bool full = vb + 32 <= p.V;
-      if (wave < 4) {
+      u32x4 fa[3], fo[IN];
+      {
+        float xa[8], xb[8];
+        rows8(xa, wave < 4 ? rE : rY, static_cast<uint32_t>(row) * vw + c);
+        if (wave < 4) {
+          rows8(xb, rY, static_cast<uint32_t>(row) * vw + c);
+        } else {
+          TA xo[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) xo[e] = xv[e] = TA{};
-        if (row < valid) {
-          if (full) {
-            __builtin_memcpy(xo, orow + vb, sizeof(xo));
-            __builtin_memcpy(xv, vrow + vb, sizeof(xv));
-          } else {
+          for (int e = 0; e < 8; ++e) xo[e] = TA{};
+          if (row < valid) {
+            if (full) {
+              __builtin_memcpy(xo, orow + vb, sizeof(xo));
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (vb + 8 * g + e < p.V) {
-                xo[e] = orow[vb + e];
-                xv[e] = vrow[vb + e];
-              }
+              for (int e = 0; e < 8; ++e)
+                if (vb + 8 * g + e < p.V) xo[e] = orow[vb + e];
+            }
           }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) xb[e] = to_f32(xo[e]);
+        }
+        if (!full)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (vb + 8 * g + e >= p.V) {
+              xa[e] = 0.0f;
+#pragma unroll
+              for (int ct = 0; ct < CT; ++ct) xs[ct][e] = 0.0f;
+            }
+        split8(xa, fa);
+        if (wave < 4) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) ye = __builtin_fmaf(xa[e], xb[e], ye);
+        } else {
+          split8(xb, fo);
         }
       }
-      if (!full)
+      __syncthreads();  // (what was in LDS has been used)
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (vb + 8 * g + e >= p.V) {
-            xa[e] = 0.0f;
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) xs[ct][e] = 0.0f;
-          }
-    };
-    fetch(0);
-    for (int vb = 0; vb < p.V; vb += 32) {
-      u32x4 fa[3], fo[IN], fs[CT][3], fd[CT][3];
-      split8(xa, fa);
-      if (wave < 4) {
-        float f[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          f[e] = to_f32(xo[e]);
-          vy = __builtin_fmaf(to_f32(xv[e]), xa[e], vy);
-        }
-        split8(f, fo);
+      for (int i = 0; i < 3; ++i) {
+        sF[(wave < 4 ? 8 : 4) + w][i][lane] = fa[i];
+        if (i < IN && wave >= 4) sF[w][i][lane] = fo[i < IN ? i : 0];
       }
+      u32x4 fs[CT][3], fd[CT][3];
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
 #pragma unroll
@@ -432,14 +435,7 @@ __global__ void __launch_bounds__(512, 2) delta_grad_kernel(const GradArgs<TA> p
         split8(xs[ct], fs[ct]);
         split8(xd[ct], fd[ct]);
       }
-      __syncthreads();  // (what was in LDS has been used)
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        sF[(wave < 4 ? 4 : 8) + w][i][lane] = fa[i];
-        if (i < IN && wave < 4) sF[w][i][lane] = fo[i < IN ? i : 0];
-      }
       __syncthreads();
-      if (vb + 32 < p.V) fetch(vb + 32);
 #pragma unroll
       for (int x = 0; x < RT; ++x) {
         const int rt = rg * RT + x;
@@ -456,11 +452,11 @@ __global__ void __launch_bounds__(512, 2) delta_grad_kernel(const GradArgs<TA> p
           r2[x][ct] = mul_parts<3>(y, fs[ct], r2[x][ct]);
           r3[x][ct] = mul_parts<3>(u, fd[ct], r3[x][ct]);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      u32x4 fy[3];
-      if (wave >= 4)
+      if (wave < 4)
 #pragma unroll
-        for (int i = 0; i < 3; ++i) fy[i] = sF[4 + w][i][lane];
+        for (int i = 0; i < IN; ++i) fo[i] = sF[w][i][lane];
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
         if (jt > w) continue;
@@ -468,7 +464,7 @@ __global__ void __launch_bounds__(512, 2) delta_grad_kernel(const GradArgs<TA> p
 #pragma unroll
         for (int i = 0; i < 3; ++i) u[i] = sF[8 + jt][i][lane];
         if (wave < 4) gg[jt] = mul_parts<3>(fo, u, gg[jt]);
-        else gg[jt] = mul_parts<3>(fy, u, gg[jt]);
+        else gg[jt] = mul_parts<3>(fa, u, gg[jt]);
       }
     }
     // K^T and Q^T of the wave's columns: right operands of the triangles' products,
@@ -486,57 +482,32 @@ __global__ void __launch_bounds__(512, 2) delta_grad_kernel(const GradArgs<TA> p
             qt[ct][kb][i] = p.c.qtf[cat + ((i * 2 * KT + cg + CG * ct) * 2 + kb) * 64];
           }
     }
-    // ---- F (waves 0-3); E and what dbeta takes from A (waves 4-7) ----
-    f32x4 db = zero;
-    const size_t kat = static_cast<size_t>(slot * p.hk + j) * IN * 4 * KT * 64 + lane;
+    // ---- F (waves 0-3) and H (waves 4-7) ----
+    Mat& mine = wave < 4 ? sP : sH;
 #pragma unroll
     for (int jt = 0; jt < 4; ++jt) {
       if (jt > w) continue;
-      f32x4 kk = zero;
-      if (wave >= 4)
-#pragma unroll
-        for (int kb = 0; kb < KT; ++kb) {
-          u32x4 a[IN], c[IN];
-#pragma unroll
-          for (int i = 0; i < IN; ++i) {
-            a[i] = p.c.kf[kat + ((i * 4 + w) * KT + kb) * 64];
-            c[i] = p.c.kf[kat + ((i * 4 + jt) * KT + kb) * 64];
-          }
-          kk = mul_parts<3>(a, c, kk);
-        }
       const int col = 16 * jt + n;
       const double Gc = sG[col];
+      const float bc = sbe[col];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int i = 16 * w + 4 * g + e;
-        const float D = i >= col ? expf(static_cast<float>(sG[i] - Gc)) : 0.0f;
-        if (wave < 4) {
-          sP[i][col] = i >= col ? p.scale * D * gg[jt][e] : 0.0f;
-        } else {
-          const float m = i > col ? -D * gg[jt][e] : 0.0f;
-          sE[i][col] = sbe[i] * m;
-          db[e] = __builtin_fmaf(m, kk[e], db[e]);
-        }
+        const float D = (wave < 4 ? i >= col : i > col) ? bc * expf(static_cast<float>(sG[i] - Gc)) : 0.0f;
+        mine[i][col] = D * gg[jt][e] * (wave < 4 ? p.scale : -sbe[i]);
+        if (i < col) mine[i][col] = 0.0f;
       }
     }
     if (w % 2 == 0)  // the block right of the diagonal completes a fragment's 32 columns
 #pragma unroll
-      for (int e = 0; e < 4; ++e) (wave < 4 ? sP : sE)[16 * w + 4 * g + e][16 * w + 16 + n] = 0.0f;
-    if (wave >= 4) {
-#pragma unroll
-      for (int m = 1; m < 16; m <<= 1)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) db[e] += __shfl_xor(db[e], m);
-      if (n == 0)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sdb[1][16 * w + 4 * g + e] = db[e];
-    } else {
-      vy += __shfl_xor(vy, 16);
-      vy += __shfl_xor(vy, 32);
-      if (g == 0) sdb[0][row] = vy;
+      for (int e = 0; e < 4; ++e) mine[16 * w + 4 * g + e][16 * w + 16 + n] = 0.0f;
+    if (wave < 4) {
+      ye += __shfl_xor(ye, 16);
+      ye += __shfl_xor(ye, 32);
+      if (g == 0) sdb[row] = ye;
     }
-    // ---- the rows' scales, and what stands in dG and dbeta before the triangles' products ----
-    float dots[RT][4], bdot[RT][4], cross = 0.0f;
+    // ---- the rows' scales, and K^T d E's part of <S1, dS1> ----
+    float cross = 0.0f;
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
       const int rt = rg * RT + x;
@@ -545,24 +516,21 @@ __global__ void __launch_bounds__(512, 2) delta_grad_kernel(const GradArgs<TA> p
       const f32x4 be = *reinterpret_cast<const f32x4*>(&sbe[16 * rt + 4 * g]);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        bdot[x][r] = 0.0f;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
           const float kx = value(kt[ct], RT == 1 ? rt : x, r);
-          bdot[x][r] = __builtin_fmaf(kx, r2[x][ct][r], bdot[x][r]);
           r1[x][ct][r] *= p.scale * ga[r];
           r2[x][ct][r] *= -ga[r] * be[r];
-          r3[x][ct][r] *= de[r];
+          r3[x][ct][r] *= de[r] * be[r];
           cross = __builtin_fmaf(kx, r3[x][ct][r], cross);
         }
-        bdot[x][r] *= -ga[r];
       }
     }
-    // ---- the triangles as left operands: E and F, then E^T and F^T ----
+    // ---- the triangles as left operands: H and F, then H^T and F^T ----
 #pragma unroll
     for (int turn = 0; turn < 2; ++turn) {
       __syncthreads();
-      const Mat& m = wave < 4 ? sE : sP;
+      const Mat& m = wave < 4 ? sH : sP;
       for (int kb = turn ? w >> 1 : 0; kb <= (turn ? 1 : w >> 1); ++kb) {
         float x[8];
 #pragma unroll
@@ -602,18 +570,18 @@ __global__ void __launch_bounds__(512, 2) delta_grad_kernel(const GradArgs<TA> p
         }
       }
     }
-    // ---- dG, dbeta: sums over the rows ----
+    // ---- dG: sums over the rows ----
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
       const int rt = rg * RT + x;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        dots[x][r] = 0.0f;
+        float dot = 0.0f;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
           const float kx = value(kt[ct], RT == 1 ? rt : x, r), qx = value(qt[ct], RT == 1 ? rt : x, r);
-          dots[x][r] = __builtin_fmaf(qx, r1[x][ct][r], dots[x][r]);
-          dots[x][r] = __builtin_fmaf(kx, r2[x][ct][r] - r3[x][ct][r], dots[x][r]);
+          dot = __builtin_fmaf(qx, r1[x][ct][r], dot);
+          dot = __builtin_fmaf(kx, r2[x][ct][r] - r3[x][ct][r], dot);
           if constexpr (SHARED) {
             dq[x][ct][r] += r1[x][ct][r];
             dk[x][ct][r] += r2[x][ct][r] + r3[x][ct][r];
@@ -623,14 +591,8 @@ __global__ void __launch_bounds__(512, 2) delta_grad_kernel(const GradArgs<TA> p
           }
         }
 #pragma unroll
-        for (int m = 1; m < 16; m <<= 1) {
-          dots[x][r] += __shfl_xor(dots[x][r], m);
-          bdot[x][r] += __shfl_xor(bdot[x][r], m);
-        }
-        if (n == 0) {
-          sdot[0][cg][16 * rt + 4 * g + r] = dots[x][r];
-          sdot[1][cg][16 * rt + 4 * g + r] = bdot[x][r];
-        }
+        for (int m = 1; m < 16; m <<= 1) dot += __shfl_xor(dot, m);
+        if (n == 0) sdot[cg][16 * rt + 4 * g + r] = dot;
       }
     }
     if (rg != 0) ss = 0.0f;  // (the row groups read the same states)
@@ -645,17 +607,14 @@ __global__ void __launch_bounds__(512, 2) delta_grad_kernel(const GradArgs<TA> p
     }
     __syncthreads();
     if (wave == 0) {
-      float last = 0.0f, top = 0.0f, d = 0.0f, e = sdb[0][lane] + sdb[1][lane];
+      float last = 0.0f, top = 0.0f, d = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         last += sone[1][i];
         top += sone[0][i];
       }
 #pragma unroll
-      for (int i = 0; i < CG; ++i) {
-        d += sdot[0][i][lane];
-        e += sdot[1][i][lane];
-      }
+      for (int i = 0; i < CG; ++i) d += sdot[i][lane];
       last = __builtin_fmaf(sga[kDeltaC - 1], top, last);
 #pragma unroll
       for (int m = 1; m < 64; m <<= 1) {  // the sum from behind
@@ -663,7 +622,7 @@ __global__ void __launch_bounds__(512, 2) delta_grad_kernel(const GradArgs<TA> p
         if (lane + m < 64) d += up;
       }
       if (lane < valid) {
-        p.dbeta[(t0 + lane) * p.hv + h] = e;
+        p.dbeta[(t0 + lane) * p.hv + h] = sdb[lane];
         if (p.dg) p.dg[(t0 + lane) * p.hv + h] = d + last;
       }
     }
@@ -725,16 +684,13 @@ void launch_bwd(const BackArgs<TA>& a, const GradArgs<TA>& e, int64_t chunks, hi
 }
 
 template <typename TA>
-int run_bwd(const char* fn, const void* q, const void* k, const void* v, const float* beta, const float* g,
-            float scale, const float* mids, const void* dout, const float* dlast, void* dq, void* dk, void* dv,
+int run_bwd(const char* fn, const float* beta, const float* g, float scale, const float* mids, const void* dout, const float* dlast, void* dq, void* dk, void* dv,
             float* dbeta, float* dg, float* dfirst, const int32_t* cu, const DeltaDims& d, const BackSpace& s,
             hipStream_t stream) {
   const BackArgs<TA> a{static_cast<const TA*>(dout), static_cast<TA*>(dv), dlast, beta, dfirst, s.dmid, s.y, cu,
                        s.back, scale, d.nseq, d.L, d.hk, d.hv, d.K, d.V, (d.V + 15) / 16};
-  const GradArgs<TA> e{static_cast<const TA*>(q), static_cast<const TA*>(k), static_cast<const TA*>(v),
-                       static_cast<const TA*>(dout), beta, g, mids, s.dmid, s.y, static_cast<TA*>(dq),
-                       static_cast<TA*>(dk), dbeta, dg, cu, s.back, scale, d.nseq, d.L, d.qs, d.ks, d.vs, d.hk, d.hv,
-                       d.K, d.V};
+  const GradArgs<TA> e{static_cast<const TA*>(dout), beta, g, mids, s.dmid, s.y, static_cast<TA*>(dq),
+                       static_cast<TA*>(dk), dbeta, dg, cu, s.back, scale, d.nseq, d.L, d.hk, d.hv, d.K, d.V};
   switch (delta_kt(d.K)) {
     case 1: launch_bwd<TA, 1>(a, e, d.chunks(), stream); break;
     case 2: launch_bwd<TA, 2>(a, e, d.chunks(), stream); break;
@@ -812,7 +768,7 @@ int delta_bwd(const char* fn, const void* q, const void* k, const void* v, const
     delta_prep(dtype, true, q, k, beta, g, cu, d, x.back, stream);
   }
   return (dtype == SSM_DTYPE_F32 ? run_bwd<float> : run_bwd<bf16_t>)(
-      fn, q, k, v, beta, g, scale, mids ? mids : x.mids, dout, dlast, dq, dk, dv, dbeta, dg, dfirst, cu, d, x, stream);
+      fn, beta, g, scale, mids ? mids : x.mids, dout, dlast, dq, dk, dv, dbeta, dg, dfirst, cu, d, x, stream);
 }
 
 size_t query(int64_t nseq, int64_t L, int64_t hk, int64_t hv, int64_t K, int64_t V, bool packed, int dtype, int have) {

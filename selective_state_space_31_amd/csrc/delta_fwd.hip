@@ -20,12 +20,12 @@ struct RecArgs {
 
 // The chunks one after another.  With S0 the state before a chunk, per column
 // block of 16 NC values:
-//   X = V - gamma (K S0);  U = T diag(beta) X;  S1 = gamma_C S0 + K^T (d U)
-//   out = scale (gamma (Q S0) + P U)
+//   X = V - gamma (K S0);  E = T X;  S1 = gamma_63 S0 + K^T (d E)
+//   out = scale (gamma (Q S0) + P E)
 // A workgroup takes one column block of a head (columns do not meet).  Its first
-// four waves carry the chain X, U, S1: wave w has the tokens 16 w .. + 15 and
+// four waves carry the chain X, E, S1: wave w has the tokens 16 w .. + 15 and
 // every fourth row block of S, in registers.  The other four form the outputs, 16
-// tokens each, in the time that the chain leaves.  S, X and d U pass through LDS
+// tokens each, in the time that the chain leaves.  S, X and d E pass through LDS
 // as right operands in bf16 parts; the left operands come from memory as
 // fragments, each needed by one wave alone, the next chunk's while this one is
 // worked on.  What bounds it is the chain through a chunk: three products, three
@@ -34,7 +34,7 @@ template <typename TA, int KT, int NC, bool MIDS>
 __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const RecArgs<TA> p) {
   constexpr int IN = ActParts<TA>::in, OUT = ActParts<TA>::out, TW = (KT + 1) / 2;
   __shared__ u32x4 sS[3][KT][NC][64], sX[3][2][NC][64], sD[3][2][NC][64];
-  __shared__ f32x4 sU[4][NC][64];
+  __shared__ f32x4 sE[4][NC][64];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave & 3;
   // The workgroups of a head read the same fragments: they go to the same XCD
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
     for (int c = 0;; ++c) {
       const int64_t slot = q.slot + c;
       const int more = c + 1 < nc ? 1 : 0;  // (the last chunk's loads ahead are its own again)
-      if (c > 0) {  // the chunk before: its u came behind the last barrier but one
+      if (c > 0) {  // the chunk before: its e came behind the last barrier but one
 #pragma unroll
         for (int nb = 0; nb < NC; ++nb) {
           y[nb] = mul_parts<OUT>(fp[0], up[nb][0], y[nb]);
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           u32x2 part[OUT];
-          split4(sU[t][nb][lane], part);
+          split4(sE[t][nb][lane], part);
 #pragma unroll
           for (int i = 0; i < OUT; ++i) {
             up[nb][t >> 1][i][2 * (t & 1)] = part[i][0];
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
     __builtin_amdgcn_sched_barrier(0);
     load_rows(slot + more);
     __syncthreads();
-    // ---- U ----
+    // ---- E ----
     u32x4 xp[2][NC][3];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
       for (int nb = 0; nb < NC; ++nb) u[nb] = mul_parts<3>(ft[1], xp[1][nb], u[nb]);
 #pragma unroll
     for (int nb = 0; nb < NC; ++nb) {
-      sU[w][nb][lane] = u[nb];
+      sE[w][nb][lane] = u[nb];
       put_tok<3, NC>(&sD[0][0][0][0], 2, w, nb, lane, u[nb] * de);
     }
     __builtin_amdgcn_sched_barrier(0);

@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
     sG[lane] = G;
     float* const vec = p.c.vec + (slot * p.hv + h) * 2 * kDeltaC;
     vec[lane] = expf(static_cast<float>(G));
-    vec[kDeltaC + lane] = expf(static_cast<float>(__shfl(G, 63) - G));
+    vec[kDeltaC + lane] = expf(static_cast<float>(__shfl(G, 63) - G)) * (BACK ? 1.0f : sbeta[lane]);
   }
 #pragma unroll
   for (int kb = 0; kb < KT; ++kb)
@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
     }
   __syncthreads();
 
-  // ---- A (into LDS) and P: D_ij k_i.k_j and D_ij q_i.k_j, lane's i = row ----
+  // ---- A (into LDS) and P: beta_j D_ij k_i.k_j and beta_j D_ij q_i.k_j, lane's
+  // i = row; for the backward A alone, with beta_i ----
   const double Gr = sG[row];
   const float br = sbeta[row];
   const int64_t at = slot * p.hv + h;
@@ -141,8 +142,9 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
         for (int e = 0; e < 4; ++e) {
           const int o = 16 * jt + 4 * g + e;
           const float D = row >= o ? expf(static_cast<float>(Gr - sG[o])) : 0.0f;
-          qk[e] *= D;
-          reinterpret_cast<float*>(&a4)[e] = row > o ? br * D * kk[e] : 0.0f;
+          const float bo = BACK ? br : sbeta[o];
+          qk[e] *= D * bo;
+          reinterpret_cast<float*>(&a4)[e] = row > o ? bo * D * kk[e] : 0.0f;
         }
         *reinterpret_cast<float4*>(&sA[row][16 * jt + 4 * g]) = a4;
       }
@@ -200,7 +202,7 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
   }
   __syncthreads();
 
-  // ---- fragments of T diag(beta), or of T^T; wave w its row block ----
+  // ---- fragments of T, or of T^T; wave w its row block ----
   for (int kb = BACK ? w >> 1 : 0; kb <= (BACK ? 1 : w >> 1); ++kb) {
     u32x4 ft[3];
 #pragma unroll
@@ -208,7 +210,7 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
       uint32_t part[3];
       const int x = 32 * kb + frag_tok(g, 2 * e);
       if constexpr (BACK) split2(sT[x][row], sT[x + 1][row], part);
-      else split2(sT[row][x] * sbeta[x], sT[row][x + 1] * sbeta[x + 1], part);
+      else split2(sT[row][x], sT[row][x + 1], part);
 #pragma unroll
       for (int i = 0; i < 3; ++i) ft[i][e] = part[i];
     }

@@ -99,13 +99,14 @@ __global__ void __launch_bounds__(256) delta_walk_kernel(const WalkArgs<TA> p) {
     }
     __syncthreads();
     kq = (redkq[0] + redkq[1]) + (redkq[2] + redkq[3]);
-    float u[VEC];
+    float u[VEC], miss[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const int c = col * VEC + e;
       const float a = (red[0][0][c] + red[0][1][c]) + (red[0][2][c] + red[0][3][c]);
       const float o = (red[1][0][c] + red[1][1][c]) + (red[1][2][c] + red[1][3][c]);
-      u[e] = beta * (vv[e] - decay * a);
+      miss[e] = vv[e] - decay * a;
+      u[e] = beta * miss[e];
       vv[e] = p.scale * __builtin_fmaf(kq, u[e], decay * o);
     }
 #pragma unroll
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(256) delta_walk_kernel(const WalkArgs<TA> p) {
       float* const m = p.mids + ((q.slot + (t - q.lo) / kDeltaC) * p.hv + h) * mv + sv + c0;
       for (int64_t i = (t - q.lo) % kDeltaC; i < (t + 1 < q.hi ? (t - q.lo) % kDeltaC + 1 : kDeltaC); ++i)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) m[i * p.V + e] = i == (t - q.lo) % kDeltaC ? u[e] : 0.0f;
+        for (int e = 0; e < VEC; ++e) m[i * p.V + e] = i == (t - q.lo) % kDeltaC ? miss[e] : 0.0f;
     }
     if (row == 0 && mine) {
       TA* const o = p.out + (static_cast<size_t>(t) * p.hv + h) * p.V + c0;

@@ -158,7 +158,7 @@ def ssm_delta_rule_fwd(q, k, v, beta, g=None, scale=None, initial_state=None, re
 
     Returns ``out`` (contiguous), followed by ``last_state`` and by
     ``chunk_states`` where they are asked for or passed (for the gradients:
-    per chunk of 64 tokens the state before it and the tokens' u, (batch,
+    per chunk of 64 tokens the state before it and the tokens' v - S^T k, (batch,
     chunks, heads_v, headdim_k + 64, headdim_v) float32).
     """
     return _delta_fwd(q, k, v, beta, None, g, scale, initial_state, return_last_state, return_chunk_states, out,

@@ -110,11 +110,11 @@ def check_forward(p, out, last, s, t0=None, t1=None, what="", mids=None):
         K = ref_last.shape[1]
         mids = np64(mids)
         check_close(mids[:, :, :K], before[::64], size + 1e-30, what + " chunk_states")
-        u = delta.updates(**h)
+        u = delta.missing(**h)
         for c in range(mids.shape[0]):
             part = u[64 * c:64 * c + 64].transpose(1, 0, 2)
             check_close(mids[c, :, K:K + part.shape[1]], part, 64 * HALF * largest(top, (0, 2, 3))[0] + 64 * HALF *
-                        largest(u, (0, 2))[0][:, :, None] + 1e-30, what + " u")
+                        largest(u, (0, 2))[0][:, :, None] + 1e-30, what + " e")
             assert (mids[c, :, K + part.shape[1]:] == 0).all(), what
 
 
