@@ -87,25 +87,6 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
         if (two) fp[1][i] = (src + (i * kTri + 1) * 64)[lane];
       }
     };
-    // The next chunks' operands into L2, two chunks before they are asked for:
-    // lines 128 bytes apart, a share for each of the head's workgroups.
-    uint32_t touched = 0;
-    const auto touch = [&](int64_t slot) {
-      const char* src;
-      int bytes;
-      if (w < 3) {
-        src = reinterpret_cast<const char*>((w == 0 ? p.c.kf : w == 1 ? p.c.qf : p.c.ktf) + (slot * p.hk + j) * (IN * 4 * KT * 64));
-        bytes = IN * 4 * KT * 1024;
-      } else {
-        src = reinterpret_cast<const char*>(p.c.tf + (slot * p.hv + h) * (3 * kTri * 64));
-        bytes = 3 * kTri * 1024;
-      }
-      const int at = (lane * p.slices + c0 / (16 * NC)) * 128;
-      if (at < bytes) touched = *reinterpret_cast<const uint32_t*>(src + at);
-      if (w == 3 && at < OUT * kTri * 1024)
-        touched ^= *reinterpret_cast<const uint32_t*>(
-            reinterpret_cast<const char*>(p.c.pf + (slot * p.hv + h) * (OUT * kTri * 64)) + at);
-    };
     if (nc > 0) {
       load_rows(q.slot);
       load_p(q.slot);
@@ -136,8 +117,6 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
         if (c == nc) break;
       }
       __syncthreads();
-      asm volatile("" ::"v"(touched));
-      touch(q.slot + (c + 3 < nc ? c + 3 : nc - 1));
 #pragma unroll
       for (int nb = 0; nb < NC; ++nb) {
         y[nb] = zero;
@@ -366,7 +345,18 @@ void run_chunks(const void* v, float scale, void* out, float* last, const float*
   }
 }
 
-size_t fwd_bytes(const DeltaDims& d, int dtype) { return chunk_space(d, dtype, false, nullptr, nullptr); }
+// Sequences of few tokens go token by token: one launch, the state read and
+// written once.  Up to 8 tokens that is quicker everywhere (16 heads of 128, bf16:
+// 1 token 4.4 against 15.5 us, 8 tokens 14.1 and 15.5, 16 tokens 25 and 14), up to
+// 16 where the heads fill the device (32 sequences: 46 against 52 us, 32 tokens 80
+// and 53).  Of packed sequences only the sum of the lengths is known here.
+bool few_tokens(const DeltaDims& d) {
+  return d.L <= 8 || (!d.packed && d.L <= 16 && d.nseq * d.hv > device_cus());
+}
+
+size_t fwd_bytes(const DeltaDims& d, int dtype) {
+  return few_tokens(d) ? 0 : chunk_space(d, dtype, false, nullptr, nullptr);
+}
 
 int delta_fwd(const char* fn, const void* q, const void* k, const void* v, const float* beta, const float* g,
               float scale, void* out, float* last, const float* first, float* mids, const int32_t* cu, bool packed,
@@ -419,6 +409,8 @@ int delta_fwd(const char* fn, const void* q, const void* k, const void* v, const
     return fail(SSM_ERR_ALIGN, "%s: workspace is not 256-byte aligned", fn);
   if (L == 0 && !last) return SSM_OK;
   if (!packed) cu = nullptr;
+  if (few_tokens(d))
+    return delta_walk(fn, dtype, q, k, v, beta, g, scale, out, last, first, mids, cu, d, stream);
   ChunkSpace c;
   chunk_space(d, dtype, false, static_cast<char*>(ws), &c);
   if (L > 0) delta_prep(dtype, false, q, k, beta, g, cu, d, c, stream);

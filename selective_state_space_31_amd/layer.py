@@ -85,15 +85,25 @@ def ssm_delta_rule_bwd_varlen_workspace_bytes(nseq, total_len, nheads_k, nheads_
                                                                  int(bool(with_chunk_states))))
 
 
+def _tokens(t, name, lead, D, like):
+    """(heads, token stride) of a lead + (heads, D) tensor like ``like``."""
+    shape = t.shape
+    if t.dtype is like.dtype and shape[:-2] == lead and shape[-1] == D and t.get_device() == like.get_device() \
+            and t.is_contiguous():
+        return shape[-2], shape[-2] * D
+    if len(lead) == 1:
+        return _heads(t[None], name, 1, lead[0], D, like)
+    return _heads(t, name, lead[0], lead[1], D, like)
+
+
 class _Delta:
     """A delta rule call's inputs, checked: sizes, addresses, shapes."""
 
     def __init__(self, q, k, v, beta, g, scale, initial_state, cu_seqlens):
         self.packed = cu_seqlens is not None
         _, self.dt = _act(q, "q")
-        for t, name in ((k, "k"), (v, "v"), (beta, "beta")):
-            if not isinstance(t, torch.Tensor):
-                raise TypeError("%s must be a torch.Tensor" % name)
+        if not (isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor) and isinstance(beta, torch.Tensor)):
+            raise TypeError("k, v and beta must be torch.Tensors")
         if self.packed:
             if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
                 raise ValueError("q, k and v must be (total_len, heads, headdim)")
@@ -101,18 +111,18 @@ class _Delta:
                 raise ValueError("cu_seqlens must be (nseq + 1,) with nseq >= 1")
             lead, self.n = q.shape[:1], cu_seqlens.numel() - 1
             self.cu = _in(cu_seqlens, "cu_seqlens", (self.n + 1,), torch.int32, q)
-            L, q4, k4, v4 = lead[0], q[None], k[None], v[None]
-            rows, chunks = 1, (L // SSM_DELTA_CHUNK + self.n,)
+            L = lead[0]
+            chunks = (L // SSM_DELTA_CHUNK + self.n,)
         else:
             if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
                 raise ValueError("q, k and v must be (batch, seqlen, heads, headdim)")
             lead, self.cu = q.shape[:2], None
-            (self.n, L), q4, k4, v4 = lead, q, k, v
-            rows, chunks = self.n, (self.n, (L + SSM_DELTA_CHUNK - 1) // SSM_DELTA_CHUNK)
+            self.n, L = lead
+            chunks = (self.n, (L + SSM_DELTA_CHUNK - 1) // SSM_DELTA_CHUNK)
         K, V = q.shape[-1], v.shape[-1]
-        Hk, qs = _heads(q4, "q", rows, L, K, q)
-        Hkk, ks = _heads(k4, "k", rows, L, K, q)
-        Hv, vs = _heads(v4, "v", rows, L, V, q)
+        Hk, qs = _tokens(q, "q", lead, K, q)
+        Hkk, ks = _tokens(k, "k", lead, K, q)
+        Hv, vs = _tokens(v, "v", lead, V, q)
         if Hkk != Hk:
             raise ValueError("q has %d heads, k %d" % (Hk, Hkk))
         self.lead, self.like, self.gate = lead, q, lead + (Hv,)
@@ -230,16 +240,15 @@ def ssm_delta_state_update(state, q, k, v, beta, g=None, scale=None, out=None, s
     returns ``out`` (batch, heads_v, headdim_v) in q's dtype."""
     lib = _load()
     _, dt = _act(q, "q")
-    for t, name in ((k, "k"), (v, "v"), (beta, "beta")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("%s must be a torch.Tensor" % name)
+    if not (isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor)):
+        raise TypeError("k and v must be torch.Tensors")
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k and v must be (batch, heads, headdim)")
-    batch, _, K = q.shape
-    V = v.shape[2]
-    Hk, qs = _heads(q[None], "q", 1, batch, K, q)
-    Hkk, ks = _heads(k[None], "k", 1, batch, K, q)
-    Hv, vs = _heads(v[None], "v", 1, batch, V, q)
+    lead, K, V = q.shape[:1], q.shape[2], v.shape[2]
+    batch = lead[0]
+    Hk, qs = _tokens(q, "q", lead, K, q)
+    Hkk, ks = _tokens(k, "k", lead, K, q)
+    Hv, vs = _tokens(v, "v", lead, V, q)
     if Hkk != Hk:
         raise ValueError("q has %d heads, k %d" % (Hk, Hkk))
     args = (_in(state, "state", (batch, Hv, K, V), _F32, q), q.data_ptr(), k.data_ptr(), v.data_ptr(),
