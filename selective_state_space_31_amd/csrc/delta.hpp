@@ -178,6 +178,31 @@ __device__ __forceinline__ void put_key(u32x4* base, int blocks, int t, int nb, 
     reinterpret_cast<u32x2*>(base + ((i * blocks + (t >> 1)) * NC + nb) * 64 + at)[q & 1] = p[i];
 }
 
+// The float32 values that put_key left in three parts (their sum is exact), rows
+// of `row` bytes, columns c0 .. of V: a wave of four stores every fourth block of
+// 32 rows.
+template <int KT, int NC>
+__device__ __forceinline__ void store_parts(float* dst, uint32_t bytes, uint32_t row, const u32x4* base, int w, int lane,
+                                            int c0, int V) {
+  const rsrc_t rs = make_rsrc(dst, bytes);
+  const int n = lane & 15, g = lane >> 4;
+  for (int kb = w; kb < KT; kb += 4)
+#pragma unroll
+    for (int nb = 0; nb < NC; ++nb) {
+      const int col = c0 + 16 * nb + n;
+      const uint32_t at = col < V ? (32u * kb + 8u * g) * row + col * 4u : 0x80000000u;
+      const u32x4 a = base[(kb * NC + nb) * 64 + lane], m = base[((KT + kb) * NC + nb) * 64 + lane],
+                  z = base[((2 * KT + kb) * NC + nb) * 64 + lane];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(bf_lo(a[e]) + (bf_lo(m[e]) + bf_lo(z[e]))), rs,
+                                              at + (2 * e) * row, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(bf_hi(a[e]) + (bf_hi(m[e]) + bf_hi(z[e]))), rs,
+                                              at + (2 * e + 1) * row, 0, 0);
+      }
+    }
+}
+
 // Triangles of 64 x 64 in 16 x 32 blocks.  Lower: row blocks 0 and 1 have one,
 // 2 and 3 have two.  Upper (a lower one transposed): 0 and 1 have two, 2 and 3
 // the second alone.
@@ -234,7 +259,7 @@ struct ChunkSpace {
   // per place and value head: fragments of T in three parts and of P (forward), of
   // T^T and P^T in three parts each (backward)
   u32x4 *tf, *pf;
-  float* vec;  // gamma (64), d (64)
+  float* vec;  // gamma (64), d (64); for the backward -beta gamma (64) too
 };
 
 template <typename TA>
@@ -268,7 +293,7 @@ inline size_t chunk_space(const DeltaDims& d, int dtype, bool back, char* base, 
   s.qtf = reinterpret_cast<u32x4*>(take(back ? rows : 0));
   s.tf = reinterpret_cast<u32x4*>(take(3 * tri));
   s.pf = reinterpret_cast<u32x4*>(take(out * tri));
-  s.vec = reinterpret_cast<float*>(take(n * d.hv * 2 * kDeltaC * 4));
+  s.vec = reinterpret_cast<float*>(take(n * d.hv * (back ? 3 : 2) * kDeltaC * 4));
   if (c) *c = s;
   return at;
 }

@@ -21,227 +21,282 @@ struct BackArgs {
   int hk, hv, K, V, slices;
 };
 
-// With dS1 the gradient of the state behind a chunk, per block of 16 NC columns:
+// With dS1 the gradient of the state behind a chunk, per block of 16 columns:
 //   dU = d (K dS1) + scale P^T dO;  Y = T^T dU;  dV = beta Y
-//   dS0 = gamma_C dS1 + scale Q^T (gamma dO) - K^T (gamma beta Y)
-// The forward's layout: wave w has the tokens 16 w .. + 15 and every fourth row
-// block of dS.
-template <typename TA, int KT, int NC>
-__global__ void __launch_bounds__(256) delta_back_kernel(const BackArgs<TA> p) {
-  constexpr int IN = ActParts<TA>::in, TW = (KT + 1) / 2;
-  __shared__ u32x4 sS[3][KT][NC][64], sU[3][2][NC][64], sZ[3][2][NC][64], sG[3][2][NC][64], sO[IN][2][NC][64];
+//   dS0 = gamma_63 dS1 + scale Q^T (gamma dO) - K^T (gamma beta Y)
+// The forward's layout: four waves carry the chain dU, Y, dS0 (wave w the tokens
+// 16 w .. + 15 and every fourth row block of dS), the other four what it does not
+// wait for: a chunk ahead dO's parts, scale P^T dO and scale Q^T (gamma dO), which
+// the chain adds, and the stores.
+//   window A (up to barrier 1)  chain: dU     others: the next dO's parts in, Q^T (gamma dO) out
+//   window B (up to barrier 2)  chain: Y      others: the next P^T dO, the states' gradients
+//   window C (up to barrier 3)  chain: dS0    others: the next Q^T (gamma dO), Y and dV
+template <typename TA, int KT>
+__global__ void __launch_bounds__(512, 2) delta_back_kernel(const BackArgs<TA> p) {
+  constexpr int IN = ActParts<TA>::in, TW = (KT + 1) / 2, NC = 1;
+  __shared__ u32x4 sS[3][KT][1][64], sU[3][2][1][64], sZ[3][2][1][64], sG[3][2][1][64], sO[IN][2][1][64];
+  __shared__ f32x4 sP[4][64], sY[4][64], sW[2 * KT][64];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave & 3;
   // (a head's workgroups on one XCD, as in the forward)
   const unsigned wide = 8u * static_cast<unsigned>(p.slices);
   const int64_t pair = int64_t{blockIdx.x / wide} * 8 + (blockIdx.x % wide & 7);
   if (pair >= p.nseq * p.hv) return;
-  const int c0 = static_cast<int>(blockIdx.x % wide >> 3) * 16 * NC;
+  const int c0 = static_cast<int>(blockIdx.x % wide >> 3) * 16;
   const int64_t b = pair / p.hv;
   const int h = static_cast<int>(pair - b * p.hv), j = h / (p.hv / p.hk);
   const DeltaSeq q = delta_seq(p.cu, b, p.L);
   const int nc = static_cast<int>((q.hi - q.lo + kDeltaC - 1) / kDeltaC);
   const size_t sv = static_cast<size_t>(p.K) * p.V;
-  const bool tiles = TW > 1 || w < 2 * KT;
-
-  const auto state_io = [&](auto&& f) {
-#pragma unroll
-    for (int i = 0; i < TW; ++i)
-#pragma unroll
-      for (int nb = 0; nb < NC; ++nb)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 16 * (w + 4 * i) + 4 * g + r, col = c0 + 16 * nb + n;
-          if (tiles && row < p.K && col < p.V) f(i, nb, r, static_cast<size_t>(row) * p.V + col);
-        }
+  constexpr uint32_t es = sizeof(TA), kNone = 0x80000000u;
+  const uint32_t sbytes = static_cast<uint32_t>(sv * 4), srow = static_cast<uint32_t>(p.V) * 4;
+  const uint32_t orow = static_cast<uint32_t>(p.hv * p.V) * es;
+  const auto rows_of = [&](int64_t t0) {
+    return static_cast<uint32_t>(q.hi - t0 < kDeltaC ? q.hi - t0 : kDeltaC);
   };
-  f32x4 S[TW][NC];
-#pragma unroll
-  for (int i = 0; i < TW; ++i)
-#pragma unroll
-    for (int nb = 0; nb < NC; ++nb) S[i][nb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  if (p.dlast) {
-    const float* const src = p.dlast + pair * sv;
-    state_io([&](int i, int nb, int r, size_t at) { S[i][nb][r] = src[at]; });
-  }
-  const auto put_state = [&]() {
-    if (tiles)
-#pragma unroll
-      for (int i = 0; i < TW; ++i)
-#pragma unroll
-        for (int nb = 0; nb < NC; ++nb) put_key<3, NC>(&sS[0][0][0][0], KT, w + 4 * i, nb, lane, S[i][nb]);
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  const bool mine = c0 + n < p.V, tiles = TW > 1 || w < 2 * KT;  // (with 32 rows two waves hold none)
+  const uint32_t sat = mine ? (16u * w + 4u * g) * srow + (c0 + n) * 4u : kNone;
+  const int kb0 = w >> 1;  // the transposed triangles' rows w have the blocks kb0 .. 1
+  const auto vec_of = [&](int64_t slot, int i) {
+    return reinterpret_cast<const f32x4*>(p.c.vec + (slot * p.hv + h) * 3 * kDeltaC + i * kDeltaC)[4 * w + g];
   };
-
-  // left operands of one chunk, and its gradients of out
-  u32x4 fk[KT][IN], ft[2][3], fp[2][3], fqt[TW][2][IN], fkt[TW][2][IN];
-  float ga[4], de[4], be[4], gC, nga[4], nde[4], nbe[4], ngC;
-  f32x4 dO[NC], ndO[NC];
-  const int kb0 = w >> 1;  // the triangles' rows w have the blocks kb0 .. 1
-  const auto load_k = [&](int64_t slot) {
-    const size_t at = static_cast<size_t>(slot * p.hk + j) * IN * 4 * KT * 64 + lane;
-#pragma unroll
-    for (int kb = 0; kb < KT; ++kb)
-#pragma unroll
-      for (int i = 0; i < IN; ++i) fk[kb][i] = p.c.kf[at + ((i * 4 + w) * KT + kb) * 64];
-  };
-  const auto load_tri = [&](int64_t slot, const u32x4* src, u32x4 (&f)[2][3]) {
-    const size_t at = static_cast<size_t>(slot * p.hv + h) * 3 * kTri * 64 + lane;
+  const auto load_tri = [&](const u32x4* base, int64_t slot, u32x4 (&f)[2][3]) {
+    const u32x4* const src = base + (slot * p.hv + h) * (3 * kTri) * 64;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
       for (int i = 0; i < 3; ++i)
-        if (kb >= kb0) f[kb][i] = src[at + (i * kTri + tri_up(w, kb)) * 64];
+        if (kb >= kb0) f[kb][i] = (src + (i * kTri + tri_up(w, kb)) * 64)[lane];
   };
-  const auto load_cols = [&](int64_t slot) {
-    const size_t at = static_cast<size_t>(slot * p.hk + j) * IN * 2 * KT * 2 * 64 + lane;
+  const auto load_cols = [&](const u32x4* base, int64_t slot, u32x4 (&f)[TW][2][IN]) {
+    const u32x4* const src = base + ((slot * p.hk + j) * (IN * 4 * KT) + 2 * w) * 64;
     if (tiles)
 #pragma unroll
       for (int x = 0; x < TW; ++x)
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-          for (int i = 0; i < IN; ++i) {
-            fqt[x][kb][i] = p.c.qtf[at + ((i * 2 * KT + w + 4 * x) * 2 + kb) * 64];
-            fkt[x][kb][i] = p.c.ktf[at + ((i * 2 * KT + w + 4 * x) * 2 + kb) * 64];
-          }
+          for (int i = 0; i < IN; ++i) f[x][kb][i] = (src + (i * 4 * KT + 8 * x + kb) * 64)[lane];
   };
-  const auto load_o = [&](int64_t slot, int64_t t0) {
-    const float* const vec = p.c.vec + (slot * p.hv + h) * 2 * kDeltaC;
+
+  if (wave >= 4) {
+    u32x4 fp[2][3], fqt[TW][2][IN];
+    uint32_t oat[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      nga[r] = vec[16 * w + 4 * g + r];
-      nde[r] = vec[kDeltaC + 16 * w + 4 * g + r];
-      const int64_t t = t0 + 16 * w + 4 * g + r;
-      nbe[r] = t < q.hi ? p.beta[t * p.hv + h] : 0.0f;
+    for (int r = 0; r < 4; ++r) oat[r] = mine ? (16u * w + 4u * g + r) * orow + n * es : kNone;
+    typename Io<TA>::raw_t ro[4];
+    f32x4 rga, W[TW];
+    float be[4];
+    const auto load_o = [&](int64_t slot, int64_t t0) {
+      const rsrc_t rs = make_rsrc(p.dout + (t0 * p.hv + h) * p.V + c0,
+                                  (rows_of(t0) - 1) * orow + static_cast<uint32_t>(p.V - c0) * es);
 #pragma unroll
-      for (int nb = 0; nb < NC; ++nb) {
-        const int col = c0 + 16 * nb + n;
-        ndO[nb][r] = t < q.hi && col < p.V ? to_f32(p.dout[(t * p.hv + h) * p.V + col]) : 0.0f;
+      for (int r = 0; r < 4; ++r) ro[r] = Io<TA>::load(rs, oat[r], 0);
+      rga = vec_of(slot, 0);
+    };
+    const auto put_o = [&]() {
+      f32x4 o, z;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        o[r] = Io<TA>::f32(ro[r]);
+        z[r] = p.scale * rga[r] * o[r];
       }
-    }
-    ngC = vec[kDeltaC - 1];
-  };
-  const auto take_o = [&]() {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      ga[r] = nga[r];
-      de[r] = nde[r];
-      be[r] = nbe[r];
-    }
-    gC = ngC;
-#pragma unroll
-    for (int nb = 0; nb < NC; ++nb) {
-      dO[nb] = ndO[nb];
-      put_tok<IN, NC>(&sO[0][0][0][0], 2, w, nb, lane, dO[nb]);
-    }
-  };
-  if (nc > 0) {
-    const int64_t slot = q.slot + nc - 1;
-    load_k(slot);
-    load_o(slot, q.lo + int64_t{nc - 1} * kDeltaC);
-    load_tri(slot, p.c.pf, fp);
-    load_tri(slot, p.c.tf, ft);
-    load_cols(slot);
-    put_state();
-    take_o();
-  }
-  __syncthreads();
-  for (int c = nc - 1; c >= 0; --c) {
-    const int64_t slot = q.slot + c, t0 = q.lo + int64_t{c} * kDeltaC;
-    const int more = c > 0 ? 1 : 0;  // (the first chunk's loads ahead are its own again)
-    {
-      float* const dst = p.dmid + (slot * p.hv + h) * sv;
-      state_io([&](int i, int nb, int r, size_t at) { dst[at] = S[i][nb][r]; });
-    }
-    load_o(slot - more, t0 - more * kDeltaC);
-    // ---- dU ----
-#pragma unroll
-    for (int nb = 0; nb < NC; ++nb) {
-      f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
-#pragma unroll
-      for (int kb = 0; kb < KT; ++kb) {
-        u32x4 s[3];
-#pragma unroll
-        for (int i = 0; i < 3; ++i) s[i] = sS[i][kb][nb][lane];
-        x = mul_parts<3>(fk[kb], s, x);
-      }
+      put_tok<IN, 1>(&sO[0][0][0][0], 2, w, 0, lane, o);
+      put_tok<3, 1>(&sG[0][0][0][0], 2, w, 0, lane, z);
+    };
+    const auto form_p = [&]() {
+      f32x4 y = zero;
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
         if (kb < kb0) continue;
         u32x4 o[IN];
 #pragma unroll
-        for (int i = 0; i < IN; ++i) o[i] = sO[i][kb][nb][lane];
+        for (int i = 0; i < IN; ++i) o[i] = sO[i][kb][0][lane];
         y = mul_parts<3>(fp[kb], o, y);
       }
-      f32x4 z;
+      sP[w][lane] = y * p.scale;
+    };
+    const auto form_w = [&]() {
+      if (!tiles) return;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        x[r] = de[r] * x[r] + p.scale * y[r];
-        z[r] = p.scale * ga[r] * dO[nb][r];
-      }
-      put_tok<3, NC>(&sU[0][0][0][0], 2, w, nb, lane, x);
-      put_tok<3, NC>(&sG[0][0][0][0], 2, w, nb, lane, z);
-    }
-    load_k(slot - more);
-    load_tri(slot - more, p.c.pf, fp);
-    __syncthreads();
-    // ---- Y, dV ----
-    const float decay = gC;
-#pragma unroll
-    for (int nb = 0; nb < NC; ++nb) {
-      f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int x = 0; x < TW; ++x) W[x] = zero;
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
-        if (kb < kb0) continue;
-        u32x4 u[3];
+        u32x4 z[3];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) u[i] = sU[i][kb][nb][lane];
-        y = mul_parts<3>(ft[kb], u, y);
+        for (int i = 0; i < 3; ++i) z[i] = sG[i][kb][0][lane];
+#pragma unroll
+        for (int x = 0; x < TW; ++x) W[x] = mul_parts<3>(fqt[x][kb], z, W[x]);
       }
-      const int col = c0 + 16 * nb + n;
-      float* const dst = p.y + ((slot * p.hv + h) * kDeltaC + 16 * w + 4 * g) * p.V + col;
+    };
+    const auto put_w = [&]() {
+      if (tiles)
+#pragma unroll
+        for (int x = 0; x < TW; ++x) sW[w + 4 * x][lane] = W[x];
+    };
+    const auto load_b = [&](int64_t t0) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int64_t t = t0 + 16 * w + 4 * g + r;
-        if (col < p.V) dst[static_cast<size_t>(r) * p.V] = y[r];
-        y[r] *= be[r];
-        if (t < q.hi && col < p.V) store_act(p.dv + (t * p.hv + h) * p.V + col, y[r]);
-        y[r] *= -ga[r];
+        be[r] = t < q.hi ? p.beta[t * p.hv + h] : 0.0f;
       }
-      put_tok<3, NC>(&sZ[0][0][0][0], 2, w, nb, lane, y);
+    };
+    if (nc > 0) {
+      const int64_t slot = q.slot + nc - 1, t0 = q.lo + int64_t{nc - 1} * kDeltaC;
+      const int less = nc > 1 ? 1 : 0;
+      load_o(slot, t0);
+      load_tri(p.c.pf, slot, fp);
+      load_cols(p.c.qtf, slot, fqt);
+      load_b(t0);
+      put_o();
+      load_o(slot - less, t0 - less * kDeltaC);
     }
-    load_tri(slot - more, p.c.tf, ft);
-    take_o();
+    __syncthreads();
+    if (nc > 0) {
+      const int64_t slot = q.slot + nc - 1 - (nc > 1 ? 1 : 0);
+      form_p();
+      form_w();
+      load_tri(p.c.pf, slot, fp);
+      load_cols(p.c.qtf, slot, fqt);
+    }
+    __syncthreads();
+    for (int c = nc - 1; c >= 0; --c) {
+      const int64_t slot = q.slot + c, t0 = q.lo + int64_t{c} * kDeltaC;
+      const int less2 = c > 1 ? 2 : c > 0 ? 1 : 0;  // (the first chunks' loads ahead are theirs again)
+      // ---- window A: what the chain adds this time is in W; the next chunk's dO ----
+      put_w();
+      put_o();
+      load_o(slot - less2, t0 - less2 * kDeltaC);
+      __syncthreads();
+      // ---- window B ----
+      form_p();
+      load_tri(p.c.pf, slot - less2, fp);
+      store_parts<KT, 1>(p.dmid + (slot * p.hv + h) * sv, sbytes, srow, &sS[0][0][0][0], w, lane, c0, p.V);
+      __syncthreads();
+      // ---- window C ----
+      {
+        const f32x4 y = sY[w][lane];
+        const rsrc_t ry = make_rsrc(p.y + (slot * p.hv + h) * kDeltaC * p.V, kDeltaC * srow);
+        const rsrc_t rv = make_rsrc(p.dv + (t0 * p.hv + h) * p.V + c0,
+                                    (rows_of(t0) - 1) * orow + static_cast<uint32_t>(p.V - c0) * es);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y[r]), ry, sat + r * srow, 0, 0);
+          buffer_store_act<TA>(be[r] * y[r], rv, oat[r]);
+        }
+      }
+      load_b(t0 - (c > 0 ? kDeltaC : 0));
+      form_w();
+      load_cols(p.c.qtf, slot - less2, fqt);
+      __syncthreads();
+    }
+    return;
+  }
+
+  // ---- chain ----
+  f32x4 S[TW];
+#pragma unroll
+  for (int i = 0; i < TW; ++i) S[i] = zero;
+  if (p.dlast && tiles) {
+    const rsrc_t rs = make_rsrc(p.dlast + pair * sv, sbytes);
+#pragma unroll
+    for (int i = 0; i < TW; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        S[i][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, sat + (64 * i + r) * srow, 0, 0));
+  }
+  const auto put_state = [&]() {
+    if (tiles)
+#pragma unroll
+      for (int i = 0; i < TW; ++i) put_key<3, NC>(&sS[0][0][0][0], KT, w + 4 * i, 0, lane, S[i]);
+  };
+  u32x4 fk[KT][IN], ft[2][3], fkt[TW][2][IN];
+  f32x4 nde, nz;
+  float ngC;
+  const auto load_k = [&](int64_t slot) {
+    const u32x4* const src = p.c.kf + ((slot * p.hk + j) * (IN * 4 * KT) + w * KT) * 64;
+#pragma unroll
+    for (int kb = 0; kb < KT; ++kb)
+#pragma unroll
+      for (int i = 0; i < IN; ++i) fk[kb][i] = (src + (i * 4 * KT + kb) * 64)[lane];
+  };
+  const auto load_vec = [&](int64_t slot) {
+    nde = vec_of(slot, 1);
+    nz = vec_of(slot, 2);
+    ngC = p.c.vec[(slot * p.hv + h) * 3 * kDeltaC + kDeltaC - 1 + (tid >> 9)];  // (a vector load)
+  };
+  if (nc > 0) {
+    const int64_t slot = q.slot + nc - 1;
+    load_k(slot);
+    load_vec(slot);
+    load_tri(p.c.tf, slot, ft);
+    load_cols(p.c.ktf, slot, fkt);
+    put_state();
+  }
+  __syncthreads();
+  __syncthreads();
+  for (int c = nc - 1; c >= 0; --c) {
+    const int64_t slot = q.slot + c;
+    const int less = c > 0 ? 1 : 0;
+    // ---- dU ----
+    f32x4 x = zero;
+#pragma unroll
+    for (int kb = 0; kb < KT; ++kb) {
+      u32x4 s[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) s[i] = sS[i][kb][0][lane];
+      x = mul_parts<3>(fk[kb], s, x);
+    }
+#pragma unroll
+    for (int i = 0; i < TW; ++i) S[i] *= ngC;
+    x = x * nde + sP[w][lane];
+    put_tok<3, 1>(&sU[0][0][0][0], 2, w, 0, lane, x);
+    const f32x4 z = nz;
+    __builtin_amdgcn_sched_barrier(0);
+    load_k(slot - less);
+    __syncthreads();
+    // ---- Y ----
+    u32x4 u[2][3];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int i = 0; i < 3; ++i) u[kb][i] = sU[i][kb][0][lane];
+    load_vec(slot - less);
+    f32x4 y = mul_parts<3>(ft[1], u[1], zero);
+    if (kb0 == 0) y = mul_parts<3>(ft[0], u[0], y);
+    sY[w][lane] = y;
+    put_tok<3, 1>(&sZ[0][0][0][0], 2, w, 0, lane, y * z);
     __syncthreads();
     // ---- dS0 ----
     if (tiles) {
+      u32x4 d[2][3];
 #pragma unroll
-      for (int nb = 0; nb < NC; ++nb) {
+      for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int i = 0; i < TW; ++i) S[i][nb] *= decay;
+        for (int i = 0; i < 3; ++i) d[kb][i] = sZ[i][kb][0][lane];
+      load_tri(p.c.tf, slot - less, ft);
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          u32x4 o[3], z[3];
+      for (int i = 0; i < TW; ++i) {
+        S[i] += sW[w + 4 * i][lane];
 #pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            o[i] = sG[i][kb][nb][lane];
-            z[i] = sZ[i][kb][nb][lane];
-          }
-#pragma unroll
-          for (int i = 0; i < TW; ++i) {
-            S[i][nb] = mul_parts<3>(fqt[i][kb], o, S[i][nb]);
-            S[i][nb] = mul_parts<3>(fkt[i][kb], z, S[i][nb]);
-          }
-        }
+        for (int kb = 0; kb < 2; ++kb) S[i] = mul_parts<3>(fkt[i][kb], d[kb], S[i]);
       }
       put_state();
+    } else {
+      load_tri(p.c.tf, slot - less, ft);
     }
-    load_cols(slot - more);
+    __builtin_amdgcn_sched_barrier(0);
+    load_cols(p.c.ktf, slot - less, fkt);
     __syncthreads();
   }
-  if (p.dfirst) {
-    float* const dst = p.dfirst + pair * sv;
-    state_io([&](int i, int nb, int r, size_t at) { dst[at] = S[i][nb][r]; });
+  if (p.dfirst && tiles) {
+    const rsrc_t rs = make_rsrc(p.dfirst + pair * sv, sbytes);
+#pragma unroll
+    for (int i = 0; i < TW; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][r]), rs, sat + (64 * i + r) * srow, 0, 0);
   }
 }
 
@@ -675,8 +730,8 @@ size_t bwd_bytes(const DeltaDims& d, int dtype, bool have) { return back_space(d
 template <typename TA, int KT>
 void launch_bwd(const BackArgs<TA>& a, const GradArgs<TA>& e, int64_t chunks, hipStream_t stream) {
   const int64_t pairs = a.nseq * a.hv;
-  hipLaunchKernelGGL((delta_back_kernel<TA, KT, 1>), dim3(static_cast<unsigned>((pairs + 7) / 8 * 8 * a.slices)),
-                     dim3(256), 0, stream, a);
+  hipLaunchKernelGGL((delta_back_kernel<TA, KT>), dim3(static_cast<unsigned>((pairs + 7) / 8 * 8 * a.slices)),
+                     dim3(512), 0, stream, a);
   if (a.L == 0) return;
   const dim3 grid(static_cast<unsigned>(chunks * a.hk)), block(512);
   if (a.hv > a.hk) hipLaunchKernelGGL((delta_grad_kernel<TA, KT, true>), grid, block, 0, stream, e);

@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
   // Buffer accesses outside the range read zeros and write nothing: rows behind
   // the sequence or the state, and by this offset columns behind the last one.
   constexpr uint32_t es = sizeof(TA), kNone = 0x80000000u;
+  const uint32_t sbytes = static_cast<uint32_t>(sv * 4), srow = static_cast<uint32_t>(p.V) * 4;
   const auto rows_of = [&](int64_t t0) {
     return static_cast<uint32_t>(q.hi - t0 < kDeltaC ? q.hi - t0 : kDeltaC);
   };
@@ -130,9 +131,10 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
         y[nb] *= nga;
       }
       load_rows(slot + more);
+      if constexpr (MIDS) store_parts<KT, NC>(p.mids + (slot * p.hv + h) * mv, sbytes, srow, &sS[0][0][0][0], w, lane, c0, p.V);
       __syncthreads();
 #pragma unroll
-      for (int nb = 0; nb < NC; ++nb)
+      for (int nb = 0; nb < NC; ++nb) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           u32x2 part[OUT];
@@ -143,6 +145,15 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
             up[nb][t >> 1][i][2 * (t & 1) + 1] = part[i][1];
           }
         }
+        if constexpr (MIDS) {
+          const rsrc_t rs = make_rsrc(p.mids + (slot * p.hv + h) * mv + sv, kDeltaC * srow);
+          const uint32_t at = c0 + 16 * nb + n < p.V ? (16u * w + 4u * g) * srow + (c0 + 16 * nb + n) * 4u : kNone;
+          const f32x4 e = sE[w][nb][lane];
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(e[r]), rs, at + r * srow, 0, 0);
+        }
+      }
       __syncthreads();
     }
     return;
@@ -150,7 +161,6 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
 
   // ---- chain ----
   const bool tiles = TW > 1 || w < 2 * KT;  // (with 32 rows two waves hold none)
-  const uint32_t sbytes = static_cast<uint32_t>(sv * 4), srow = static_cast<uint32_t>(p.V) * 4;
   const uint32_t vrow = static_cast<uint32_t>(p.vs) * es;
   uint32_t sat[NC], vat[NC][4];
 #pragma unroll
@@ -240,8 +250,6 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
     // ---- X ----
     const f32x4 de = nde;
     f32x4 x[NC];
-    if constexpr (MIDS)
-      if (tiles) state_store(p.mids + (slot * p.hv + h) * mv);
 #pragma unroll
     for (int nb = 0; nb < NC; ++nb) {
       x[nb] = zero;
@@ -287,14 +295,6 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
       put_tok<3, NC>(&sD[0][0][0][0], 2, w, nb, lane, u[nb] * de);
     }
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (MIDS) {
-      const rsrc_t rs = make_rsrc(p.mids + (slot * p.hv + h) * mv + sv, kDeltaC * srow);
-#pragma unroll
-      for (int nb = 0; nb < NC; ++nb)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(u[nb][r]), rs, sat[nb] + r * srow, 0, 0);
-    }
     __syncthreads();
     // ---- S1 ----
     if (tiles) {

@@ -96,8 +96,10 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
       if (lane >= m) G += up;
     }
     sG[lane] = G;
-    float* const vec = p.c.vec + (slot * p.hv + h) * 2 * kDeltaC;
-    vec[lane] = expf(static_cast<float>(G));
+    float* const vec = p.c.vec + (slot * p.hv + h) * (BACK ? 3 : 2) * kDeltaC;
+    const float gamma = expf(static_cast<float>(G));
+    vec[lane] = gamma;
+    if constexpr (BACK) vec[2 * kDeltaC + lane] = -gamma * sbeta[lane];
     vec[kDeltaC + lane] = expf(static_cast<float>(__shfl(G, 63) - G)) * (BACK ? 1.0f : sbeta[lane]);
   }
 #pragma unroll
