@@ -21,7 +21,7 @@ struct BackArgs {
   int hk, hv, K, V, slices;
 };
 
-// With dS1 the gradient of the state behind a chunk, per block of 16 columns:
+// With dS1 the gradient of the state behind a chunk, per block of 16 NC columns:
 //   dU = d (K dS1) + scale P^T dO;  Y = T^T dU;  dV = beta Y
 //   dS0 = gamma_63 dS1 + scale Q^T (gamma dO) - K^T (gamma beta Y)
 // The forward's layout: four waves carry the chain dU, Y, dS0 (wave w the tokens
@@ -31,18 +31,18 @@ struct BackArgs {
 //   window A (up to barrier 1)  chain: dU     others: the next dO's parts in, Q^T (gamma dO) out
 //   window B (up to barrier 2)  chain: Y      others: the next P^T dO, the states' gradients
 //   window C (up to barrier 3)  chain: dS0    others: the next Q^T (gamma dO), Y and dV
-template <typename TA, int KT>
+template <typename TA, int KT, int NC>
 __global__ void __launch_bounds__(512, 2) delta_back_kernel(const BackArgs<TA> p) {
-  constexpr int IN = ActParts<TA>::in, TW = (KT + 1) / 2, NC = 1;
-  __shared__ u32x4 sS[3][KT][1][64], sU[3][2][1][64], sZ[3][2][1][64], sG[3][2][1][64], sO[IN][2][1][64];
-  __shared__ f32x4 sP[4][64], sY[4][64], sW[2 * KT][64];
+  constexpr int IN = ActParts<TA>::in, TW = (KT + 1) / 2;
+  __shared__ u32x4 sS[3][KT][NC][64], sU[3][2][NC][64], sZ[3][2][NC][64], sG[3][2][NC][64], sO[IN][2][NC][64];
+  __shared__ f32x4 sP[4][NC][64], sY[4][NC][64], sW[2 * KT][NC][64];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave & 3;
   // (a head's workgroups on one XCD, as in the forward)
   const unsigned wide = 8u * static_cast<unsigned>(p.slices);
   const int64_t pair = int64_t{blockIdx.x / wide} * 8 + (blockIdx.x % wide & 7);
   if (pair >= p.nseq * p.hv) return;
-  const int c0 = static_cast<int>(blockIdx.x % wide >> 3) * 16;
+  const int c0 = static_cast<int>(blockIdx.x % wide >> 3) * 16 * NC;
   const int64_t b = pair / p.hv;
   const int h = static_cast<int>(pair - b * p.hv), j = h / (p.hv / p.hk);
   const DeltaSeq q = delta_seq(p.cu, b, p.L);
@@ -55,8 +55,11 @@ __global__ void __launch_bounds__(512, 2) delta_back_kernel(const BackArgs<TA> p
     return static_cast<uint32_t>(q.hi - t0 < kDeltaC ? q.hi - t0 : kDeltaC);
   };
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  const bool mine = c0 + n < p.V, tiles = TW > 1 || w < 2 * KT;  // (with 32 rows two waves hold none)
-  const uint32_t sat = mine ? (16u * w + 4u * g) * srow + (c0 + n) * 4u : kNone;
+  const bool tiles = TW > 1 || w < 2 * KT;  // (with 32 rows two waves hold none)
+  uint32_t sat[NC];
+#pragma unroll
+  for (int nb = 0; nb < NC; ++nb)
+    sat[nb] = c0 + 16 * nb + n < p.V ? (16u * w + 4u * g) * srow + (c0 + 16 * nb + n) * 4u : kNone;
   const int kb0 = w >> 1;  // the transposed triangles' rows w have the blocks kb0 .. 1
   const auto vec_of = [&](int64_t slot, int i) {
     return reinterpret_cast<const f32x4*>(p.c.vec + (slot * p.hv + h) * 3 * kDeltaC + i * kDeltaC)[4 * w + g];
@@ -82,58 +85,74 @@ __global__ void __launch_bounds__(512, 2) delta_back_kernel(const BackArgs<TA> p
 
   if (wave >= 4) {
     u32x4 fp[2][3], fqt[TW][2][IN];
-    uint32_t oat[4];
+    uint32_t oat[NC][4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) oat[r] = mine ? (16u * w + 4u * g + r) * orow + n * es : kNone;
-    typename Io<TA>::raw_t ro[4];
-    f32x4 rga, W[TW];
+    for (int nb = 0; nb < NC; ++nb)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        oat[nb][r] = c0 + 16 * nb + n < p.V ? (16u * w + 4u * g + r) * orow + (16 * nb + n) * es : kNone;
+    typename Io<TA>::raw_t ro[NC][4];
+    f32x4 rga, W[TW][NC];
     float be[4];
     const auto load_o = [&](int64_t slot, int64_t t0) {
       const rsrc_t rs = make_rsrc(p.dout + (t0 * p.hv + h) * p.V + c0,
                                   (rows_of(t0) - 1) * orow + static_cast<uint32_t>(p.V - c0) * es);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) ro[r] = Io<TA>::load(rs, oat[r], 0);
+      for (int nb = 0; nb < NC; ++nb)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) ro[nb][r] = Io<TA>::load(rs, oat[nb][r], 0);
       rga = vec_of(slot, 0);
     };
     const auto put_o = [&]() {
-      f32x4 o, z;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        o[r] = Io<TA>::f32(ro[r]);
-        z[r] = p.scale * rga[r] * o[r];
+      for (int nb = 0; nb < NC; ++nb) {
+        f32x4 o, z;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          o[r] = Io<TA>::f32(ro[nb][r]);
+          z[r] = p.scale * rga[r] * o[r];
+        }
+        put_tok<IN, NC>(&sO[0][0][0][0], 2, w, nb, lane, o);
+        put_tok<3, NC>(&sG[0][0][0][0], 2, w, nb, lane, z);
       }
-      put_tok<IN, 1>(&sO[0][0][0][0], 2, w, 0, lane, o);
-      put_tok<3, 1>(&sG[0][0][0][0], 2, w, 0, lane, z);
     };
     const auto form_p = [&]() {
-      f32x4 y = zero;
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        if (kb < kb0) continue;
-        u32x4 o[IN];
+      for (int nb = 0; nb < NC; ++nb) {
+        f32x4 y = zero;
 #pragma unroll
-        for (int i = 0; i < IN; ++i) o[i] = sO[i][kb][0][lane];
-        y = mul_parts<3>(fp[kb], o, y);
+        for (int kb = 0; kb < 2; ++kb) {
+          if (kb < kb0) continue;
+          u32x4 o[IN];
+#pragma unroll
+          for (int i = 0; i < IN; ++i) o[i] = sO[i][kb][nb][lane];
+          y = mul_parts<3>(fp[kb], o, y);
+        }
+        sP[w][nb][lane] = y * p.scale;
       }
-      sP[w][lane] = y * p.scale;
     };
     const auto form_w = [&]() {
       if (!tiles) return;
 #pragma unroll
-      for (int x = 0; x < TW; ++x) W[x] = zero;
+      for (int nb = 0; nb < NC; ++nb) {
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        u32x4 z[3];
+        for (int x = 0; x < TW; ++x) W[x][nb] = zero;
 #pragma unroll
-        for (int i = 0; i < 3; ++i) z[i] = sG[i][kb][0][lane];
+        for (int kb = 0; kb < 2; ++kb) {
+          u32x4 z[3];
 #pragma unroll
-        for (int x = 0; x < TW; ++x) W[x] = mul_parts<3>(fqt[x][kb], z, W[x]);
+          for (int i = 0; i < 3; ++i) z[i] = sG[i][kb][nb][lane];
+#pragma unroll
+          for (int x = 0; x < TW; ++x) W[x][nb] = mul_parts<3>(fqt[x][kb], z, W[x][nb]);
+        }
       }
     };
     const auto put_w = [&]() {
       if (tiles)
 #pragma unroll
-        for (int x = 0; x < TW; ++x) sW[w + 4 * x][lane] = W[x];
+        for (int x = 0; x < TW; ++x)
+#pragma unroll
+          for (int nb = 0; nb < NC; ++nb) sW[w + 4 * x][nb][lane] = W[x][nb];
     };
     const auto load_b = [&](int64_t t0) {
 #pragma unroll
@@ -172,18 +191,21 @@ __global__ void __launch_bounds__(512, 2) delta_back_kernel(const BackArgs<TA> p
       // ---- window B ----
       form_p();
       load_tri(p.c.pf, slot - less2, fp);
-      store_parts<KT, 1>(p.dmid + (slot * p.hv + h) * sv, sbytes, srow, &sS[0][0][0][0], w, lane, c0, p.V);
+      store_parts<KT, NC>(p.dmid + (slot * p.hv + h) * sv, sbytes, srow, &sS[0][0][0][0], w, lane, c0, p.V);
       __syncthreads();
       // ---- window C ----
       {
-        const f32x4 y = sY[w][lane];
         const rsrc_t ry = make_rsrc(p.y + (slot * p.hv + h) * kDeltaC * p.V, kDeltaC * srow);
         const rsrc_t rv = make_rsrc(p.dv + (t0 * p.hv + h) * p.V + c0,
                                     (rows_of(t0) - 1) * orow + static_cast<uint32_t>(p.V - c0) * es);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y[r]), ry, sat + r * srow, 0, 0);
-          buffer_store_act<TA>(be[r] * y[r], rv, oat[r]);
+        for (int nb = 0; nb < NC; ++nb) {
+          const f32x4 y = sY[w][nb][lane];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y[r]), ry, sat[nb] + r * srow, 0, 0);
+            buffer_store_act<TA>(be[r] * y[r], rv, oat[nb][r]);
+          }
         }
       }
       load_b(t0 - (c > 0 ? kDeltaC : 0));
@@ -195,21 +217,27 @@ __global__ void __launch_bounds__(512, 2) delta_back_kernel(const BackArgs<TA> p
   }
 
   // ---- chain ----
-  f32x4 S[TW];
+  f32x4 S[TW][NC];
 #pragma unroll
-  for (int i = 0; i < TW; ++i) S[i] = zero;
+  for (int i = 0; i < TW; ++i)
+#pragma unroll
+    for (int nb = 0; nb < NC; ++nb) S[i][nb] = zero;
   if (p.dlast && tiles) {
     const rsrc_t rs = make_rsrc(p.dlast + pair * sv, sbytes);
 #pragma unroll
     for (int i = 0; i < TW; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        S[i][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, sat + (64 * i + r) * srow, 0, 0));
+      for (int nb = 0; nb < NC; ++nb)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          S[i][nb][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, sat[nb] + (64 * i + r) * srow, 0, 0));
   }
   const auto put_state = [&]() {
     if (tiles)
 #pragma unroll
-      for (int i = 0; i < TW; ++i) put_key<3, NC>(&sS[0][0][0][0], KT, w + 4 * i, 0, lane, S[i]);
+      for (int i = 0; i < TW; ++i)
+#pragma unroll
+        for (int nb = 0; nb < NC; ++nb) put_key<3, NC>(&sS[0][0][0][0], KT, w + 4 * i, nb, lane, S[i][nb]);
   };
   u32x4 fk[KT][IN], ft[2][3], fkt[TW][2][IN];
   f32x4 nde, nz;
@@ -240,48 +268,68 @@ __global__ void __launch_bounds__(512, 2) delta_back_kernel(const BackArgs<TA> p
     const int64_t slot = q.slot + c;
     const int less = c > 0 ? 1 : 0;
     // ---- dU ----
-    f32x4 x = zero;
+    f32x4 x[NC];
 #pragma unroll
-    for (int kb = 0; kb < KT; ++kb) {
-      u32x4 s[3];
+    for (int nb = 0; nb < NC; ++nb) {
+      x[nb] = zero;
 #pragma unroll
-      for (int i = 0; i < 3; ++i) s[i] = sS[i][kb][0][lane];
-      x = mul_parts<3>(fk[kb], s, x);
+      for (int kb = 0; kb < KT; ++kb) {
+        u32x4 s[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) s[i] = sS[i][kb][nb][lane];
+        x[nb] = mul_parts<3>(fk[kb], s, x[nb]);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < TW; ++i) S[i] *= ngC;
-    x = x * nde + sP[w][lane];
-    put_tok<3, 1>(&sU[0][0][0][0], 2, w, 0, lane, x);
+    for (int i = 0; i < TW; ++i)
+#pragma unroll
+      for (int nb = 0; nb < NC; ++nb) S[i][nb] *= ngC;
+#pragma unroll
+    for (int nb = 0; nb < NC; ++nb)
+      put_tok<3, NC>(&sU[0][0][0][0], 2, w, nb, lane, x[nb] * nde + sP[w][nb][lane]);
     const f32x4 z = nz;
     __builtin_amdgcn_sched_barrier(0);
     load_k(slot - less);
     __syncthreads();
     // ---- Y ----
-    u32x4 u[2][3];
+    u32x4 u[2][NC][3];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-      for (int i = 0; i < 3; ++i) u[kb][i] = sU[i][kb][0][lane];
+      for (int nb = 0; nb < NC; ++nb)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) u[kb][nb][i] = sU[i][kb][nb][lane];
     load_vec(slot - less);
-    f32x4 y = mul_parts<3>(ft[1], u[1], zero);
-    if (kb0 == 0) y = mul_parts<3>(ft[0], u[0], y);
-    sY[w][lane] = y;
-    put_tok<3, 1>(&sZ[0][0][0][0], 2, w, 0, lane, y * z);
+    f32x4 y[NC];
+#pragma unroll
+    for (int nb = 0; nb < NC; ++nb) y[nb] = mul_parts<3>(ft[1], u[1][nb], zero);
+    if (kb0 == 0)
+#pragma unroll
+      for (int nb = 0; nb < NC; ++nb) y[nb] = mul_parts<3>(ft[0], u[0][nb], y[nb]);
+#pragma unroll
+    for (int nb = 0; nb < NC; ++nb) {
+      sY[w][nb][lane] = y[nb];
+      put_tok<3, NC>(&sZ[0][0][0][0], 2, w, nb, lane, y[nb] * z);
+    }
     __syncthreads();
     // ---- dS0 ----
     if (tiles) {
-      u32x4 d[2][3];
+      u32x4 d[2][NC][3];
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int i = 0; i < 3; ++i) d[kb][i] = sZ[i][kb][0][lane];
+        for (int nb = 0; nb < NC; ++nb)
+#pragma unroll
+          for (int i = 0; i < 3; ++i) d[kb][nb][i] = sZ[i][kb][nb][lane];
       load_tri(p.c.tf, slot - less, ft);
 #pragma unroll
-      for (int i = 0; i < TW; ++i) {
-        S[i] += sW[w + 4 * i][lane];
+      for (int i = 0; i < TW; ++i)
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) S[i] = mul_parts<3>(fkt[i][kb], d[kb], S[i]);
-      }
+        for (int nb = 0; nb < NC; ++nb) {
+          S[i][nb] += sW[w + 4 * i][nb][lane];
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb) S[i][nb] = mul_parts<3>(fkt[i][kb], d[kb][nb], S[i][nb]);
+        }
       put_state();
     } else {
       load_tri(p.c.tf, slot - less, ft);
@@ -295,8 +343,10 @@ __global__ void __launch_bounds__(512, 2) delta_back_kernel(const BackArgs<TA> p
 #pragma unroll
     for (int i = 0; i < TW; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][r]), rs, sat + (64 * i + r) * srow, 0, 0);
+      for (int nb = 0; nb < NC; ++nb)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[i][nb][r]), rs, sat[nb] + (64 * i + r) * srow, 0, 0);
   }
 }
 
@@ -727,13 +777,23 @@ size_t back_space(const DeltaDims& d, int dtype, bool have, char* base, BackSpac
 
 size_t bwd_bytes(const DeltaDims& d, int dtype, bool have) { return back_space(d, dtype, have, nullptr, nullptr); }
 
+template <typename TA, int KT, int NC>
+void launch_back(BackArgs<TA> a, hipStream_t stream) {
+  a.slices = (a.V + 16 * NC - 1) / (16 * NC);
+  const dim3 grid(static_cast<unsigned>((a.nseq * a.hv + 7) / 8 * 8 * a.slices)), block(512);
+  hipLaunchKernelGGL((delta_back_kernel<TA, KT, NC>), grid, block, 0, stream, a);
+}
+
 template <typename TA, int KT>
-void launch_bwd(const BackArgs<TA>& a, const GradArgs<TA>& e, int64_t chunks, hipStream_t stream) {
-  const int64_t pairs = a.nseq * a.hv;
-  hipLaunchKernelGGL((delta_back_kernel<TA, KT>), dim3(static_cast<unsigned>((pairs + 7) / 8 * 8 * a.slices)),
-                     dim3(512), 0, stream, a);
+void launch_bwd(const BackArgs<TA>& a, const GradArgs<TA>& e, const DeltaDims& d, hipStream_t stream) {
+  if constexpr (KT <= 4) {
+    if (two_blocks(d)) launch_back<TA, KT, 2>(a, stream);
+    else launch_back<TA, KT, 1>(a, stream);
+  } else {
+    launch_back<TA, KT, 1>(a, stream);
+  }
   if (a.L == 0) return;
-  const dim3 grid(static_cast<unsigned>(chunks * a.hk)), block(512);
+  const dim3 grid(static_cast<unsigned>(d.chunks() * a.hk)), block(512);
   if (a.hv > a.hk) hipLaunchKernelGGL((delta_grad_kernel<TA, KT, true>), grid, block, 0, stream, e);
   else hipLaunchKernelGGL((delta_grad_kernel<TA, KT, false>), grid, block, 0, stream, e);
 }
@@ -743,14 +803,14 @@ int run_bwd(const char* fn, const float* beta, const float* g, float scale, cons
             float* dbeta, float* dg, float* dfirst, const int32_t* cu, const DeltaDims& d, const BackSpace& s,
             hipStream_t stream) {
   const BackArgs<TA> a{static_cast<const TA*>(dout), static_cast<TA*>(dv), dlast, beta, dfirst, s.dmid, s.y, cu,
-                       s.back, scale, d.nseq, d.L, d.hk, d.hv, d.K, d.V, (d.V + 15) / 16};
+                       s.back, scale, d.nseq, d.L, d.hk, d.hv, d.K, d.V, 1};
   const GradArgs<TA> e{static_cast<const TA*>(dout), beta, g, mids, s.dmid, s.y, static_cast<TA*>(dq),
                        static_cast<TA*>(dk), dbeta, dg, cu, s.back, scale, d.nseq, d.L, d.hk, d.hv, d.K, d.V};
   switch (delta_kt(d.K)) {
-    case 1: launch_bwd<TA, 1>(a, e, d.chunks(), stream); break;
-    case 2: launch_bwd<TA, 2>(a, e, d.chunks(), stream); break;
-    case 4: launch_bwd<TA, 4>(a, e, d.chunks(), stream); break;
-    default: launch_bwd<TA, 8>(a, e, d.chunks(), stream); break;
+    case 1: launch_bwd<TA, 1>(a, e, d, stream); break;
+    case 2: launch_bwd<TA, 2>(a, e, d, stream); break;
+    case 4: launch_bwd<TA, 4>(a, e, d, stream); break;
+    default: launch_bwd<TA, 8>(a, e, d, stream); break;
   }
   return launch_status(fn);
 }

@@ -337,10 +337,11 @@ void run_chunks(const void* v, float scale, void* out, float* last, const float*
                 const int32_t* cu, const DeltaDims& d, const ChunkSpace& c, hipStream_t stream) {
   const RecArgs<TA> a{static_cast<const TA*>(v), static_cast<TA*>(out), first, last, mids, cu, c, scale, d.nseq, d.L,
                       d.vs, d.hk, d.hv, d.K, d.V, 1};
+  const bool pairs = two_blocks(d);
   switch (delta_kt(d.K)) {
-    case 1: launch_rec<TA, 1, 1>(a, stream); break;
-    case 2: launch_rec<TA, 2, 1>(a, stream); break;
-    case 4: launch_rec<TA, 4, 1>(a, stream); break;
+    case 1: pairs ? launch_rec<TA, 1, 2>(a, stream) : launch_rec<TA, 1, 1>(a, stream); break;
+    case 2: pairs ? launch_rec<TA, 2, 2>(a, stream) : launch_rec<TA, 2, 1>(a, stream); break;
+    case 4: pairs ? launch_rec<TA, 4, 2>(a, stream) : launch_rec<TA, 4, 1>(a, stream); break;
     default: launch_rec<TA, 8, 1>(a, stream); break;
   }
 }
