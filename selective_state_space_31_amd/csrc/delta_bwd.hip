@@ -368,6 +368,17 @@ struct GradArgs {
 
 constexpr int kGradRow = kDeltaC + 4;
 
+// A lane's x and that of the lane ROR places back in its row of 16
+template <int ROR>
+__device__ __forceinline__ float row_add(float x) {
+  return x + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x120 + ROR, 0xf, 0xf, false));
+}
+
+// The sum over the 16 lanes of a row, in each of them
+__device__ __forceinline__ float row_sum16(float x) {
+  return row_add<1>(row_add<2>(row_add<4>(row_add<8>(x))));
+}
+
 template <int N>
 __device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&f)[N]) {
 #pragma unroll
@@ -695,8 +706,7 @@ __global__ void __launch_bounds__(512, 2) delta_grad_kernel(const GradArgs<TA> p
             dk[x][ct][r] = r2[x][ct][r] + r3[x][ct][r];
           }
         }
-#pragma unroll
-        for (int m = 1; m < 16; m <<= 1) dot += __shfl_xor(dot, m);
+        dot = row_sum16(dot);
         if (n == 0) sdot[cg][16 * rt + 4 * g + r] = dot;
       }
     }
