@@ -70,8 +70,8 @@ extern "C" {
  *                     ssm_delta_rule_bwd
  *   1 <= headdim_k, headdim_v <= 256; nheads_v a multiple of nheads_k, at most
  *   65535; 1 <= batch <= 65535; seqlen >= 0 (0 only copies the initial state);
- *   batch * seqlen < 2^31; batch * ceil(seqlen / SSM_DELTA_CHUNK) * nheads_v <
- *   2^26 (SSM_ERR_SHAPE beyond).
+ *   batch * seqlen < 2^31; batch * ceil(seqlen / SSM_DELTA_CHUNK) * nheads_v and
+ *   batch * nheads_v * ceil(headdim_v / 16) < 2^22 (SSM_ERR_SHAPE beyond).
  *   workspace       : at least ssm_delta_rule_fwd_workspace_bytes(...) bytes
  * The recurrence is stable while 0 <= beta |k|^2 <= 2; beyond, states grow as
  * the formulas say and their rounding errors with them.
@@ -112,7 +112,7 @@ size_t ssm_delta_rule_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t
  *                      chunk c of sequence s at cu[s] / SSM_DELTA_CHUNK + s + c.
  *                      Places that no chunk has keep what they held.
  *   1 <= nseq < 2^20; 0 <= total_len < 2^31; (total_len / SSM_DELTA_CHUNK +
- *   nseq) * nheads_v < 2^26.
+ *   nseq) * nheads_v and nseq * nheads_v * ceil(headdim_v / 16) < 2^22.
  * Nothing passes from one sequence into another, a NaN or an infinity neither.
  */
 int ssm_delta_rule_fwd_varlen(const void* q, const void* k, const void* v, const float* beta,
@@ -188,7 +188,8 @@ size_t ssm_delta_rule_bwd_varlen_workspace_bytes(int64_t nseq, int64_t total_len
  *   out   : (batch, nheads_v, headdim_v) act, contiguous
  * Equivalent to ssm_delta_rule_fwd with seqlen = 1 and initial_state =
  * last_state = state, with sums in float32 in another order.  Here a value that
- * is not finite stays in its own head.  batch * nheads_v < 2^26.
+ * is not finite stays in its own head.  batch * nheads_v *
+ * ceil(headdim_v / 32) < 2^24.
  */
 int ssm_delta_state_update(float* state, const void* q, const void* k, const void* v,
                            const float* beta, const float* g, float scale, void* out,

@@ -41,7 +41,8 @@ inline bool delta_sizes_ok(int64_t nseq, int64_t L, int64_t hk, int64_t hv, int6
   if (K < 1 || K > kDeltaMaxWidth || V < 1 || V > kDeltaMaxWidth) return false;
   if (!packed && nseq * L >= (int64_t{1} << 31)) return false;
   const int64_t chunks = packed ? L / kDeltaC + nseq : nseq * ((L + kDeltaC - 1) / kDeltaC);
-  return (chunks > nseq ? chunks : nseq) * hv < (int64_t{1} << 26);
+  // (a launch has less than 2^32 threads, up to 512 of them for a chunk or a column block)
+  return chunks * hv < (int64_t{1} << 22) && nseq * hv * ((V + 15) / 16) < (int64_t{1} << 22);
 }
 
 inline bool delta_strides_ok(const DeltaDims& d) {
@@ -90,10 +91,6 @@ typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 
-template <int N>
-struct Parts {
-  static constexpr int value = N;
-};
 template <typename TA>
 struct ActParts;
 template <>

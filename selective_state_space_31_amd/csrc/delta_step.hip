@@ -185,9 +185,9 @@ extern "C" int ssm_delta_state_update(float* state, const void* q, const void* k
   const char* fn = "ssm_delta_state_update";
   if (dtype != SSM_DTYPE_F32 && dtype != SSM_DTYPE_BF16)
     return fail(SSM_ERR_UNSUPPORTED, "%s: unknown dtype %d", fn, dtype);
-  if (batch < 1 || batch >= (int64_t{1} << 26) ||
+  if (batch < 1 || batch >= (int64_t{1} << 24) ||
       !delta_sizes_ok(1, 1, nheads_k, nheads_v, headdim_k, headdim_v, false) ||
-      batch * nheads_v >= (int64_t{1} << 26))
+      batch * nheads_v * ((headdim_v + 31) / 32) >= (int64_t{1} << 24))  // (less than 2^32 threads)
     return fail(SSM_ERR_SHAPE, "%s: bad sizes batch %lld, heads %lld and %lld, widths %lld and %lld", fn,
                 (long long)batch, (long long)nheads_k, (long long)nheads_v, (long long)headdim_k,
                 (long long)headdim_v);

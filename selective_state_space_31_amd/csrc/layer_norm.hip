@@ -480,9 +480,8 @@ int ssm_layer_norm_fwd(const void* x, const void* residual, const float* weight,
   const size_t whole = strided(rows, dim, dim, es);
   const Span outs[] = {{out, whole, "out"}, {residual_out, residual_out ? whole : 0, "residual_out"}};
   for (const auto& o : outs)
-    for (const auto& n : ins)  // (in place: a row is read whole before it is written)
-      if (overlap(o, n) && !(o.p == n.p && ((n.p == x && x_row_stride == dim) ||
-                                            (n.p == residual && residual_row_stride == dim))))
+    for (const auto& n : ins)  // (in place, row on row: a row is read whole before it is written)
+      if (overlap(o, n) && !(o.p == n.p && o.bytes == n.bytes && (n.p == x || n.p == residual)))
         return fail(SSM_ERR_ALIAS, "%s: output %s overlaps input %s", fn, o.name, n.name);
   if (overlap(outs[0], outs[1])) return fail(SSM_ERR_ALIAS, "%s: out overlaps residual_out", fn);
   if (rows == 0) return SSM_OK;
@@ -525,7 +524,7 @@ int ssm_layer_norm_bwd(const void* s, const float* weight, float eps, const void
                        {workspace, workspace ? need : 0, "workspace"}};
   for (const auto& o : outs)
     for (const auto& n : ins)  // (dx in place of a gradient: a row is read whole before it is written)
-      if (overlap(o, n) && !(o.p == dx && n.p == dx && (n.p == dout || n.p == dresidual)))
+      if (overlap(o, n) && !(o.p == dx && n.p == dx && o.bytes == n.bytes && (n.p == dout || n.p == dresidual)))
         return fail(SSM_ERR_ALIAS, "%s: output %s overlaps input %s", fn, o.name, n.name);
   for (int a = 0; a < 4; ++a)
     for (int b = a + 1; b < 4; ++b)
