@@ -358,7 +358,7 @@ struct GradArgs {
   const TA* dout;
   const float *beta, *g, *mids, *dmid, *y;
   TA *dq, *dk;
-  float *dbeta, *dg;
+  float *dbeta, *dg, *dqh, *dkh;  // dqh, dkh: of every value head, or NULL
   const int32_t* cu;
   ChunkSpace c;
   float scale;
@@ -397,7 +397,9 @@ __device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&f)[N]) {
 //   dbeta_i = y_i.e_i
 //   dG_i = q_i.dq_i + k_i.(read - write)_i  (e^{G_i} goes with what reads, e^{-G_i}
 //   with what writes), and <S1, dS1> for the last one; dg is their sum from behind
-// One workgroup of eight waves a chunk and key head, over its value heads in turn.
+// One workgroup of eight waves a chunk and key head, over its value heads in turn
+// (SHARED), or a chunk and value head; where several of those share a key head
+// their dQ and dK go out in float32 and delta_join_kernel sums them.
 // dQ and dK are cut into RT row by CT column blocks a wave; waves 0-3 have G1's and
 // F's rows, waves 4-7 G2's and H's.  The row operands (dO, Y, E, then H and F) pass
 // through LDS in parts; S0 and dS1 come as rows straight from memory, where each is
@@ -418,8 +420,9 @@ __global__ void __launch_bounds__(512, 2) delta_grad_kernel(const GradArgs<TA> p
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave & 3;
   const int cg = wave % CG, rg = wave / CG;
-  const int64_t slot = blockIdx.x / static_cast<unsigned>(p.hk);
-  const int j = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.hk)), rep = p.hv / p.hk;
+  const unsigned heads = static_cast<unsigned>(SHARED ? p.hk : p.hv);
+  const int64_t slot = blockIdx.x / heads;
+  const int rep = p.hv / p.hk, of = static_cast<int>(blockIdx.x % heads), j = SHARED ? of : of / rep;
   const int64_t per = (p.L + kDeltaC - 1) / kDeltaC;
   const int64_t b = p.cu ? delta_owner(p.cu, static_cast<int>(p.nseq), slot) : slot / per;
   const DeltaSeq q = delta_seq(p.cu, b, p.L);
@@ -447,7 +450,8 @@ __global__ void __launch_bounds__(512, 2) delta_grad_kernel(const GradArgs<TA> p
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) dq[x][ct] = dk[x][ct] = zero;
 
-  for (int h = j * rep; h < (SHARED ? (j + 1) * rep : j + 1); ++h) {
+  const int h0 = SHARED ? j * rep : of;
+  for (int h = h0; h < h0 + (SHARED ? rep : 1); ++h) {
     const int64_t at = slot * p.hv + h;
     if (wave == 0) {  // as in the preparation
       const bool in = lane < valid;
@@ -752,18 +756,57 @@ __global__ void __launch_bounds__(512, 2) delta_grad_kernel(const GradArgs<TA> p
       for (int ct = 0; ct < CT; ++ct) {
         const int d = 16 * (cg + CG * ct) + n;
         if (i < valid && d < p.K) {
-          store_act(p.dq + ((t0 + i) * p.hk + j) * p.K + d, dq[x][ct][r]);
-          store_act(p.dk + ((t0 + i) * p.hk + j) * p.K + d, dk[x][ct][r]);
+          const size_t to = ((t0 + i) * heads + of) * p.K + d;
+          if (!SHARED && p.dqh) {
+            p.dqh[to] = dq[x][ct][r];
+            p.dkh[to] = dk[x][ct][r];
+          } else {
+            store_act(p.dq + to, dq[x][ct][r]);
+            store_act(p.dk + to, dk[x][ct][r]);
+          }
         }
       }
     }
+}
+
+// dq and dk of a key head from those of its `rep` value heads, in their order; a
+// wave a row (token and key head).
+template <typename TA>
+__global__ void __launch_bounds__(256) delta_join_kernel(const float* __restrict__ dqh, const float* __restrict__ dkh,
+                                                         TA* __restrict__ dq, TA* __restrict__ dk, const int32_t* cu,
+                                                         int64_t nseq, int64_t tokens, int hk, int rep, int K) {
+  int64_t end = tokens;
+  if (cu) {  // (rows behind the last sequence stay as they are)
+    const int64_t last = cu[nseq];
+    end = last < 0 ? 0 : last < tokens ? last : tokens;
+  }
+  const int64_t rows = end * hk;
+  for (int64_t i = int64_t{blockIdx.x} * 4 + (threadIdx.x >> 6); i < rows; i += int64_t{gridDim.x} * 4)
+    for (int d = static_cast<int>(threadIdx.x & 63); d < K; d += 64) {
+      const size_t from = static_cast<size_t>(i) * rep * K + d;
+      float a = dqh[from], b = dkh[from];
+      for (int r = 1; r < rep; ++r) {
+        a += dqh[from + static_cast<size_t>(r) * K];
+        b += dkh[from + static_cast<size_t>(r) * K];
+      }
+      store_act(dq + i * K + d, a);
+      store_act(dk + i * K + d, b);
+    }
+}
+
+// Value heads that share a key head: a workgroup each, or one for all of them?
+bool heads_apart(const DeltaDims& d) {
+  if (d.hv == d.hk) return false;
+  const int64_t cus = device_cus(), apart = (d.chunks() * d.hv + cus - 1) / cus;
+  const int64_t together = (d.chunks() * d.hk + cus - 1) / cus * (d.hv / d.hk);
+  return 5 * apart <= 4 * together;
 }
 
 // The gradients' own space: the backward's chunk parts, the state gradients, Y,
 // and without chunk_states those and the forward's chunk parts.
 struct BackSpace {
   ChunkSpace back, fwd;
-  float *dmid, *y, *mids;
+  float *dmid, *y, *mids, *dqh, *dkh;
 };
 
 size_t back_space(const DeltaDims& d, int dtype, bool have, char* base, BackSpace* s) {
@@ -776,7 +819,11 @@ size_t back_space(const DeltaDims& d, int dtype, bool have, char* base, BackSpac
   };
   x.dmid = take(static_cast<size_t>(d.chunks()) * d.state_values() * 4);
   x.y = take(static_cast<size_t>(d.chunks()) * d.hv * kDeltaC * d.V * 4);
-  x.mids = nullptr;
+  x.dqh = x.dkh = x.mids = nullptr;
+  if (heads_apart(d)) {
+    x.dqh = take(static_cast<size_t>(d.tokens()) * d.hv * d.K * 4);
+    x.dkh = take(static_cast<size_t>(d.tokens()) * d.hv * d.K * 4);
+  }
   if (!have) {
     x.mids = take(d.mid_values() * 4);
     at += chunk_space(d, dtype, false, base ? base + at : nullptr, &x.fwd);
@@ -803,9 +850,14 @@ void launch_bwd(const BackArgs<TA>& a, const GradArgs<TA>& e, const DeltaDims& d
     launch_back<TA, KT, 1>(a, stream);
   }
   if (a.L == 0) return;
-  const dim3 grid(static_cast<unsigned>(d.chunks() * a.hk)), block(512);
-  if (a.hv > a.hk) hipLaunchKernelGGL((delta_grad_kernel<TA, KT, true>), grid, block, 0, stream, e);
+  const bool together = a.hv > a.hk && !e.dqh;
+  const dim3 grid(static_cast<unsigned>(d.chunks() * (together ? a.hk : a.hv))), block(512);
+  if (together) hipLaunchKernelGGL((delta_grad_kernel<TA, KT, true>), grid, block, 0, stream, e);
   else hipLaunchKernelGGL((delta_grad_kernel<TA, KT, false>), grid, block, 0, stream, e);
+  if (!e.dqh) return;
+  const int64_t rows = d.tokens() * d.hk, most = int64_t{device_cus()} * 8;
+  hipLaunchKernelGGL((delta_join_kernel<TA>), dim3(static_cast<unsigned>(rows / 4 + 1 < most ? rows / 4 + 1 : most)),
+                     dim3(256), 0, stream, e.dqh, e.dkh, e.dq, e.dk, e.cu, d.nseq, d.tokens(), d.hk, d.hv / d.hk, d.K);
 }
 
 template <typename TA>
@@ -815,7 +867,7 @@ int run_bwd(const char* fn, const float* beta, const float* g, float scale, cons
   const BackArgs<TA> a{static_cast<const TA*>(dout), static_cast<TA*>(dv), dlast, beta, dfirst, s.dmid, s.y, cu,
                        s.back, scale, d.nseq, d.L, d.hk, d.hv, d.K, d.V, 1};
   const GradArgs<TA> e{static_cast<const TA*>(dout), beta, g, mids, s.dmid, s.y, static_cast<TA*>(dq),
-                       static_cast<TA*>(dk), dbeta, dg, cu, s.back, scale, d.nseq, d.L, d.hk, d.hv, d.K, d.V};
+                       static_cast<TA*>(dk), dbeta, dg, s.dqh, s.dkh, cu, s.back, scale, d.nseq, d.L, d.hk, d.hv, d.K, d.V};
   switch (delta_kt(d.K)) {
     case 1: launch_bwd<TA, 1>(a, e, d, stream); break;
     case 2: launch_bwd<TA, 2>(a, e, d, stream); break;

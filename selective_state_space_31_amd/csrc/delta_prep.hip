@@ -34,8 +34,11 @@ __device__ __forceinline__ void put16(Mat& m, int i, int j, f32x4 c, float sign)
 template <typename TA, int KT, bool BACK>
 __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
   constexpr int IN = ActParts<TA>::in, OUT = BACK ? 3 : ActParts<TA>::out;
-  __shared__ u32x4 sk[IN][4][KT][64];
-  __shared__ Mat sA, sT;
+  typedef u32x4 Frags[IN][4][KT][64];
+  __shared__ union { Frags k; Mat t; } both;  // T takes K's place (and Q, in the backward, T's)
+  __shared__ Mat sA;
+  Frags& sk = both.k;
+  Mat& sT = both.t;
   __shared__ double sG[kDeltaC];
   __shared__ float sbeta[kDeltaC];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
@@ -166,6 +169,31 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
 #pragma unroll
         for (int i = 0; i < OUT; ++i) p.c.pf[((at * OUT + i) * kTri + tri_at(w, pair)) * 64 + lane] = fp[i];
   }
+  // ---- fragments of K^T (later Q^T): products with the unit matrix's columns ----
+  u32x4 unit;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int c = 8 * g + 2 * e - 16 * (w & 1);
+    unit[e] = (c == n ? 0x3f80u : 0u) | (c + 1 == n ? 0x3f800000u : 0u);
+  }
+  const auto transposed = [&](u32x4* dst) {
+    for (int t = w; t < 2 * KT; t += 4)
+#pragma unroll
+      for (int i = 0; i < IN; ++i)
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          u32x4 v;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const f32x4 x = mfma16(sk[i][2 * kb + half][t >> 1][lane], unit, zero);
+            v[2 * half] = pack_bf16(x[0], x[1]);
+            v[2 * half + 1] = pack_bf16(x[2], x[3]);
+          }
+          dst[((((slot * p.hk + j) * IN + i) * 2 * KT + t) * 2 + kb) * 64 + lane] = v;
+        }
+  };
+  if (first) transposed(p.c.ktf);
+  __syncthreads();
   if (w % 2 == 0)  // the block right of the diagonal completes a fragment's 32 columns
     *reinterpret_cast<float4*>(&sT[row][16 * w + 16 + 4 * g]) = float4{0.0f, 0.0f, 0.0f, 0.0f};
   __syncthreads();
@@ -220,35 +248,8 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
 #pragma unroll
     for (int i = 0; i < 3; ++i) p.c.tf[((at * 3 + i) * kTri + f) * 64 + lane] = ft[i];
   }
-  // ---- fragments of K^T (and Q^T): products with the unit matrix's columns ----
-  u32x4 unit[2];
-#pragma unroll
-  for (int half = 0; half < 2; ++half)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int c = 8 * g + 2 * e - 16 * half;
-      unit[half][e] = (c == n ? 0x3f80u : 0u) | (c + 1 == n ? 0x3f800000u : 0u);
-    }
-  const auto transposed = [&](u32x4* dst) {
-    const u32x4 e = w & 1 ? unit[1] : unit[0];
-    for (int t = w; t < 2 * KT; t += 4)
-#pragma unroll
-      for (int i = 0; i < IN; ++i)
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          u32x4 v;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const f32x4 x = mfma16(sk[i][2 * kb + half][t >> 1][lane], e, zero);
-            v[2 * half] = pack_bf16(x[0], x[1]);
-            v[2 * half + 1] = pack_bf16(x[2], x[3]);
-          }
-          dst[((((slot * p.hk + j) * IN + i) * 2 * KT + t) * 2 + kb) * 64 + lane] = v;
-        }
-  };
-  if (first) transposed(p.c.ktf);
-  // ---- P^T: D_ij q_i.k_j with the lane's j = row.  Q takes K's place in LDS,
-  // whose fragments the wave still has ----
+  // ---- P^T: D_ij q_i.k_j with the lane's j = row.  Q goes where K was, whose
+  // fragments the wave still has ----
   if constexpr (BACK) {
     __syncthreads();
 #pragma unroll
