@@ -409,8 +409,12 @@ struct GradCut {
   static constexpr int RT = KT < 4 ? KT : 4, RG = 4 / RT, CG = 8 / RG, CT = 2 * KT / CG;
 };
 
+// What bounds it (4 sequences of 2048 tokens, 12 heads of 128, bf16: 180 us, 440 MB
+// at 2.4 TB/s): no unit by itself (vector ALU 32%, matrix cores 17%, LDS about 30%
+// of the time), but the phases between barriers, each on another one.  Two
+// workgroups a CU (128 registers, 58 of them spilled once) are 4% faster than one.
 template <typename TA, int KT, bool SHARED>
-__global__ void __launch_bounds__(512, 2) delta_grad_kernel(const GradArgs<TA> p) {
+__global__ void __launch_bounds__(512, SHARED || ActParts<TA>::in > 1 || KT > 4 ? 2 : 4) delta_grad_kernel(const GradArgs<TA> p) {
   constexpr int IN = ActParts<TA>::in, RT = GradCut<KT>::RT, CG = GradCut<KT>::CG, CT = GradCut<KT>::CT;
   typedef float Mat[kDeltaC][kGradRow];
   __shared__ u32x4 sF[12][3][64];  // dO, Y, E: 4 row blocks of 32 columns; then two triangles' 6 blocks
@@ -547,60 +551,62 @@ __global__ void __launch_bounds__(512, 2) delta_grad_kernel(const GradArgs<TA> p
         sF[(wave < 4 ? 8 : 4) + w][i][lane] = fa[i];
         if (i < IN && wave >= 4) sF[w][i][lane] = fo[i < IN ? i : 0];
       }
-      u32x4 fs[CT][3], fd[CT][3];
+      u32x4 fs[CT][3];
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(xs[ct][e], xd[ct][e], ss);
         split8(xs[ct], fs[ct]);
-        split8(xd[ct], fd[ct]);
       }
       __syncthreads();
 #pragma unroll
       for (int x = 0; x < RT; ++x) {
         const int rt = rg * RT + x;
-        u32x4 a[IN], y[3], u[3];
+        u32x4 a[IN], y[3];
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
           if (i < IN) a[i < IN ? i : 0] = sF[rt][i][lane];
           y[i] = sF[4 + rt][i][lane];
-          u[i] = sF[8 + rt][i][lane];
         }
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
           r1[x][ct] = mul_parts<3>(a, fs[ct], r1[x][ct]);
           r2[x][ct] = mul_parts<3>(y, fs[ct], r2[x][ct]);
-          r3[x][ct] = mul_parts<3>(u, fd[ct], r3[x][ct]);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (wave < 4)
+      u32x4 fd[CT][3];
 #pragma unroll
-        for (int i = 0; i < IN; ++i) fo[i] = sF[w][i][lane];
+      for (int ct = 0; ct < CT; ++ct) split8(xd[ct], fd[ct]);
+#pragma unroll
+      for (int x = 0; x < RT; ++x) {
+        u32x4 u[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) u[i] = sF[8 + rg * RT + x][i][lane];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) r3[x][ct] = mul_parts<3>(u, fd[ct], r3[x][ct]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      u32x4 left[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < IN || wave >= 4) left[i] = sF[(wave < 4 ? 0 : 4) + w][i][lane];
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
         if (jt > w) continue;
         u32x4 u[3];
 #pragma unroll
         for (int i = 0; i < 3; ++i) u[i] = sF[8 + jt][i][lane];
-        if (wave < 4) gg[jt] = mul_parts<3>(fo, u, gg[jt]);
-        else gg[jt] = mul_parts<3>(fa, u, gg[jt]);
+        if (wave < 4) {
+          u32x4 fo[IN];
+#pragma unroll
+          for (int i = 0; i < IN; ++i) fo[i] = left[i];
+          gg[jt] = mul_parts<3>(fo, u, gg[jt]);
+        } else {
+          gg[jt] = mul_parts<3>(left, u, gg[jt]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-    }
-    // K^T and Q^T of the wave's columns: right operands of the triangles' products,
-    // and value by value what a result's place is multiplied with in the sums
-    u32x4 kt[CT][2][IN], qt[CT][2][IN];
-    {
-      const size_t cat = static_cast<size_t>(slot * p.hk + j) * IN * 2 * KT * 2 * 64 + lane;
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-          for (int i = 0; i < IN; ++i) {
-            kt[ct][kb][i] = p.c.ktf[cat + ((i * 2 * KT + cg + CG * ct) * 2 + kb) * 64];
-            qt[ct][kb][i] = p.c.qtf[cat + ((i * 2 * KT + cg + CG * ct) * 2 + kb) * 64];
-          }
     }
     // ---- F (waves 0-3) and H (waves 4-7) ----
     Mat& mine = wave < 4 ? sP : sH;
@@ -625,6 +631,22 @@ __global__ void __launch_bounds__(512, 2) delta_grad_kernel(const GradArgs<TA> p
       ye += __shfl_xor(ye, 16);
       ye += __shfl_xor(ye, 32);
       if (g == 0) sdb[row] = ye;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    // K^T and Q^T of the wave's columns: right operands of the triangles' products,
+    // and value by value what a result's place is multiplied with in the sums
+    u32x4 kt[CT][2][IN], qt[CT][2][IN];
+    {
+      const size_t cat = static_cast<size_t>(slot * p.hk + j) * IN * 2 * KT * 2 * 64 + lane;
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int i = 0; i < IN; ++i) {
+            kt[ct][kb][i] = p.c.ktf[cat + ((i * 2 * KT + cg + CG * ct) * 2 + kb) * 64];
+            qt[ct][kb][i] = p.c.qtf[cat + ((i * 2 * KT + cg + CG * ct) * 2 + kb) * 64];
+          }
     }
     // ---- the rows' scales, and K^T d E's part of <S1, dS1> ----
     float cross = 0.0f;
