@@ -156,9 +156,11 @@ int launch_walk(const char* fn, const void* q, const void* k, const void* v, con
     else if (d.K <= 128) go(vec, tpr, Count<MOST / 2>{});
     else go(vec, tpr, Count<MOST>{});
   };
+  // Four columns a lane where alignment allows (then eight lanes, 32 columns a
+  // workgroup: 1 x 16 heads of 128 4.0 us, with 32 lanes 6.4; 256 x 12 of 128 x 64
+  // 35 and 42; 256 x 40 of 128, float32, 264 and 264, 5.1 TB/s).
   const bool quads = d.V % 4 == 0 && aligned(first, 16) && aligned(last, 16) && aligned(mids, 16);
-  if (quads && (d.V <= 64 || d.nseq * d.hv < device_cus())) deep(Count<4>{}, Count<8>{});
-  else if (quads) deep(Count<4>{}, Count<32>{});
+  if (quads) deep(Count<4>{}, Count<8>{});
   else deep(Count<1>{}, Count<32>{});
   return launch_status(fn);
 }

@@ -1,5 +1,5 @@
 """The delta rule where its calls take another way through the kernels: many
-heads (two column blocks a workgroup), few tokens (token by token), two graphs
+heads (two column blocks a workgroup; shared key heads), few tokens (token by token), two graphs
 at once, and offsets that pass 2^31 (GPU)."""
 import numpy as np
 import pytest
@@ -31,6 +31,17 @@ def test_many_heads(shape, dtype):
     out, last, mids, grads = train(p)
     for s in range(b):
         check_forward(p, out[s], last[s], s, what="sequence %d" % s, mids=mids[s])
+        check_grads(p, {k: t[s] for k, t in grads.items()}, s, what="sequence %d" % s)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("K,V", [(16, 9), (64, 20), (128, 33), (200, 9)])
+def test_shared_heads_together(K, V, dtype):
+    """Key heads enough to fill the device: a workgroup goes through all value
+    heads of one."""
+    p = Delta((4, 65), 4, 32, 64, K, V, dtype, DEV, seed=K)
+    _, _, _, grads = train(p)
+    for s in (0, 3):
         check_grads(p, {k: t[s] for k, t in grads.items()}, s, what="sequence %d" % s)
 
 
