@@ -420,7 +420,8 @@ __global__ void __launch_bounds__(512, SHARED || ActParts<TA>::in > 1 || KT > 4 
   __shared__ u32x4 sF[12][3][64];  // dO, Y, E: 4 row blocks of 32 columns; then two triangles' 6 blocks
   __shared__ Mat sH, sP;
   __shared__ double sG[kDeltaC];
-  __shared__ float sga[kDeltaC], sde[kDeltaC], sbe[kDeltaC], sdb[kDeltaC], sdot[CG][kDeltaC], sone[2][8];
+  __shared__ float sga[kDeltaC], sde[kDeltaC], sbe[kDeltaC], sdb[kDeltaC], sdot[CG][kDeltaC];
+  __shared__ double sone[2][8];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave & 3;
   const int cg = wave % CG, rg = wave / CG;
@@ -478,7 +479,8 @@ __global__ void __launch_bounds__(512, SHARED || ActParts<TA>::in > 1 || KT > 4 
     for (int x = 0; x < RT; ++x)
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) r1[x][ct] = r2[x][ct] = r3[x][ct] = zero;
-    float ye = 0.0f, ss = 0.0f;
+    float ye = 0.0f;
+    double ss = 0.0;  // (dg is what is left of larger sums: those over many terms are in float64)
     // Rows of 32 columns at a time: waves 0-3 E (and Y for y.e), waves 4-7 Y and dO.
     // Where the last block is not full, columns behind V are made zeros in the left
     // operands and in S0 (what is multiplied with them is finite: the next row's).
@@ -554,8 +556,10 @@ __global__ void __launch_bounds__(512, SHARED || ActParts<TA>::in > 1 || KT > 4 
       u32x4 fs[CT][3];
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
+        float sd = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(xs[ct][e], xd[ct][e], ss);
+        for (int e = 0; e < 8; ++e) sd = __builtin_fmaf(xs[ct][e], xd[ct][e], sd);
+        ss += sd;
         split8(xs[ct], fs[ct]);
       }
       __syncthreads();
@@ -736,19 +740,20 @@ __global__ void __launch_bounds__(512, SHARED || ActParts<TA>::in > 1 || KT > 4 
         if (n == 0) sdot[cg][16 * rt + 4 * g + r] = dot;
       }
     }
-    if (rg != 0) ss = 0.0f;  // (the row groups read the same states)
+    if (rg != 0) ss = 0.0;  // (the row groups read the same states)
+    double crosses = cross;
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) {
       ss += __shfl_xor(ss, m);
-      cross += __shfl_xor(cross, m);
+      crosses += __shfl_xor(crosses, m);
     }
     if (lane == 0) {
       sone[0][wave] = ss;
-      sone[1][wave] = cross;
+      sone[1][wave] = crosses;
     }
     __syncthreads();
     if (wave == 0) {
-      float last = 0.0f, top = 0.0f, d = 0.0f;
+      double last = 0.0, top = 0.0, d = 0.0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         last += sone[1][i];
@@ -756,15 +761,15 @@ __global__ void __launch_bounds__(512, SHARED || ActParts<TA>::in > 1 || KT > 4 
       }
 #pragma unroll
       for (int i = 0; i < CG; ++i) d += sdot[i][lane];
-      last = __builtin_fmaf(sga[kDeltaC - 1], top, last);
+      last += sga[kDeltaC - 1] * top;
 #pragma unroll
       for (int m = 1; m < 64; m <<= 1) {  // the sum from behind
-        const float up = __shfl_down(d, m);
+        const double up = __shfl_down(d, m);
         if (lane + m < 64) d += up;
       }
       if (lane < valid) {
         p.dbeta[(t0 + lane) * p.hv + h] = sdb[lane];
-        if (p.dg) p.dg[(t0 + lane) * p.hv + h] = d + last;
+        if (p.dg) p.dg[(t0 + lane) * p.hv + h] = static_cast<float>(d + last);
       }
     }
     __syncthreads();
