@@ -326,9 +326,10 @@ __global__ void __launch_bounds__(512, 2) delta_back_kernel(const BackArgs<TA> p
       for (int i = 0; i < TW; ++i)
 #pragma unroll
         for (int nb = 0; nb < NC; ++nb) {
-          S[i][nb] += sW[w + 4 * i][nb][lane];
+          f32x4 add = sW[w + 4 * i][nb][lane];  // (summed apart: the state itself is rounded once)
 #pragma unroll
-          for (int kb = 0; kb < 2; ++kb) S[i][nb] = mul_parts<3>(fkt[i][kb], d[kb][nb], S[i][nb]);
+          for (int kb = 0; kb < 2; ++kb) add = mul_parts<3>(fkt[i][kb], d[kb][nb], add);
+          S[i][nb] += add;
         }
       put_state();
     } else {

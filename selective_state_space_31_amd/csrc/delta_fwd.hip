@@ -309,9 +309,12 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
 #pragma unroll
       for (int i = 0; i < TW; ++i)
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int nb = 0; nb < NC; ++nb) {
+          f32x4 add = zero;  // (summed apart: the state itself is rounded once)
 #pragma unroll
-          for (int nb = 0; nb < NC; ++nb) S[i][nb] = mul_parts<3>(fkt[i][kb], d[kb][nb], S[i][nb]);
+          for (int kb = 0; kb < 2; ++kb) add = mul_parts<3>(fkt[i][kb], d[kb][nb], add);
+          S[i][nb] += add;
+        }
       put_state();
     } else {
       load_t(slot + more);
