@@ -136,6 +136,19 @@ __device__ __forceinline__ f32x4 mul_parts(const u32x4 (&a)[NA], const u32x4 (&b
   return c;
 }
 
+// The same with c rounded twice, whatever the number of products: what the lower
+// parts give is summed apart.
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mul_parts_apart(const u32x4 (&a)[NA], const u32x4 (&b)[NB], f32x4 c) {
+  f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int s = 2; s > 0; --s)
+#pragma unroll
+    for (int i = 0; i <= s; ++i)
+      if (i < NA && s - i < NB) t = mfma16(a[i], b[s - i], t);
+  return mfma16(a[0], b[0], c + t);
+}
+
 // Matrix fragments.  A product's left operand: lane l holds row l % 16 and eight
 // of 32 columns; the right one likewise with rows and columns exchanged; the
 // result has column l % 16, rows 4 (l / 16) + 0..3.  Which eight is free as long

@@ -575,8 +575,8 @@ __global__ void __launch_bounds__(512, SHARED || ActParts<TA>::in > 1 || KT > 4 
         }
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
-          r1[x][ct] = mul_parts<3>(a, fs[ct], r1[x][ct]);
-          r2[x][ct] = mul_parts<3>(y, fs[ct], r2[x][ct]);
+          r1[x][ct] = mul_parts_apart(a, fs[ct], r1[x][ct]);
+          r2[x][ct] = mul_parts_apart(y, fs[ct], r2[x][ct]);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(512, SHARED || ActParts<TA>::in > 1 || KT > 4 
 #pragma unroll
         for (int i = 0; i < 3; ++i) u[i] = sF[8 + rg * RT + x][i][lane];
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) r3[x][ct] = mul_parts<3>(u, fd[ct], r3[x][ct]);
+        for (int ct = 0; ct < CT; ++ct) r3[x][ct] = mul_parts_apart(u, fd[ct], r3[x][ct]);
         __builtin_amdgcn_sched_barrier(0);
       }
       u32x4 left[3];
@@ -707,11 +707,11 @@ __global__ void __launch_bounds__(512, SHARED || ActParts<TA>::in > 1 || KT > 4 
 #pragma unroll
           for (int ct = 0; ct < CT; ++ct) {
             if (turn) {
-              r3[x][ct] = mul_parts<3>(e, kt[ct][kb], r3[x][ct]);
-              r3[x][ct] = mul_parts<3>(y, qt[ct][kb], r3[x][ct]);
+              r3[x][ct] = mul_parts_apart(e, kt[ct][kb], r3[x][ct]);
+              r3[x][ct] = mul_parts_apart(y, qt[ct][kb], r3[x][ct]);
             } else {
-              r2[x][ct] = mul_parts<3>(e, kt[ct][kb], r2[x][ct]);
-              r1[x][ct] = mul_parts<3>(y, kt[ct][kb], r1[x][ct]);
+              r2[x][ct] = mul_parts_apart(e, kt[ct][kb], r2[x][ct]);
+              r1[x][ct] = mul_parts_apart(y, kt[ct][kb], r1[x][ct]);
             }
           }
         }

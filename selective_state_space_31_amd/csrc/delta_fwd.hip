@@ -307,14 +307,17 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
           for (int i = 0; i < 3; ++i) d[kb][nb][i] = sD[i][kb][nb][lane];
       load_t(slot + more);
 #pragma unroll
-      for (int i = 0; i < TW; ++i)
+      for (int i = 0; i < TW; ++i) {
+        f32x4 add[NC];  // (summed apart: the state itself is rounded once)
 #pragma unroll
-        for (int nb = 0; nb < NC; ++nb) {
-          f32x4 add = zero;  // (summed apart: the state itself is rounded once)
+        for (int nb = 0; nb < NC; ++nb) add[nb] = zero;
 #pragma unroll
-          for (int kb = 0; kb < 2; ++kb) add = mul_parts<3>(fkt[i][kb], d[kb][nb], add);
-          S[i][nb] += add;
-        }
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int nb = 0; nb < NC; ++nb) add[nb] = mul_parts<3>(fkt[i][kb], d[kb][nb], add[nb]);
+#pragma unroll
+        for (int nb = 0; nb < NC; ++nb) S[i][nb] += add[nb];
+      }
       put_state();
     } else {
       load_t(slot + more);
