@@ -312,7 +312,7 @@ inline size_t chunk_space(const DeltaDims& d, int dtype, bool back, char* base, 
 // rather than one: the same left operands then serve twice the columns, and rows of
 // the states are written in whole lines, but a chunk takes longer.  So where three
 // workgroups for four compute units are left (4 x 2048 x 12 heads of 128: forward
-// 77 against 83 us, with the states for the backward 114 and 143; 16 heads over
+// 77 against 83 us, with the states for the backward 113 and 143; 16 heads over
 // 131072 tokens, 64 workgroups, 4490 and 3270), and not for packed sequences, of
 // which a few may be all that is left to do (7 x 5 heads, 3001 tokens 90 and 61).
 inline bool two_blocks(const DeltaDims& d) {

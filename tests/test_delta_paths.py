@@ -219,3 +219,37 @@ def test_layer_norm_past_32_bits(big):
     g = pkg.ssm_layer_norm_bwd(total, dy, w)
     g2 = pkg.ssm_layer_norm_bwd(total[e], dy[e], w)
     same(g["dx"][e], g2["dx"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("K,V,hv", [(64, 77, 4), (128, 33, 2), (40, 16, 2), (200, 50, 2)])
+@pytest.mark.parametrize("packed", [False, True])
+def test_what_buffers_held_before(packed, K, V, hv, dtype):
+    """Workspaces and outputs full of NaN change nothing: nothing is read before
+    it is written, also of chunks that are not full."""
+    T, cu = 170, torch.tensor([0, 70, 70, 71, 165], dtype=torch.int32, device=DEV)
+    p = Delta((T,) if packed else (2, T), 4 if packed else 2, 2, hv, K, V, dtype, DEV, seed=K)
+    off = (cu,) if packed else ()
+    f, b = (pkg.ssm_delta_rule_fwd_varlen, pkg.ssm_delta_rule_bwd_varlen) if packed else \
+        (pkg.ssm_delta_rule_fwd, pkg.ssm_delta_rule_bwd)
+    size = (4, T, 2, hv, K, V, p.v.dtype) if packed else (2, T, 2, hv, K, V, p.v.dtype)
+    fb, bb = (pkg.ssm_delta_rule_fwd_varlen_workspace_bytes, pkg.ssm_delta_rule_bwd_varlen_workspace_bytes) if packed else \
+        (pkg.ssm_delta_rule_fwd_workspace_bytes, pkg.ssm_delta_rule_bwd_workspace_bytes)
+    res = []
+    for fill in (0, 0xFF):
+        raw = lambda n: torch.full((max(n, 256),), fill, dtype=torch.uint8, device=DEV)
+        buf = lambda t: raw(t.numel() * t.element_size())[:t.numel() * t.element_size()].view(t.dtype).view(t.shape)
+        like = f(*p.args(), *off, return_last_state=True, return_chunk_states=True, **p.kw())
+        out, last, mids = (buf(t) for t in like)
+        f(*p.args(), *off, out=out, last_state=last, chunk_states=mids, workspace=raw(fb(*size)), **p.kw())
+        got = [out, last]
+        for have in (True, False):
+            grads = {k: buf(t) for k, t in b(*p.args(), *off, p.dout, dlast_state=p.dlast, **p.kw()).items()}
+            b(*p.args(), *off, p.dout, dlast_state=p.dlast, chunk_states=mids if have else None, grads=grads,
+              workspace=raw(bb(*size, with_chunk_states=have)), **p.kw())
+            got += [grads[k] for k in sorted(grads)]
+        torch.cuda.synchronize()
+        end = 165 if packed else T
+        res.append([t[:end] if packed and t.shape[0] == T else t for t in got])
+    for a, z in zip(*res):
+        assert torch.isfinite(a.float()).all() and torch.equal(a, z)
