@@ -253,3 +253,22 @@ def test_what_buffers_held_before(packed, K, V, hv, dtype):
         res.append([t[:end] if packed and t.shape[0] == T else t for t in got])
     for a, z in zip(*res):
         assert torch.isfinite(a.float()).all() and torch.equal(a, z)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_outputs_at_any_element(off, dtype):
+    """Outputs, states and gradients in buffers that start `off` elements behind an
+    aligned address: the same values."""
+    p = Delta((2, 100), 2, 2, 4, 48, 32, dtype, DEV, seed=off)
+    out, last, mids, grads = train(p)
+
+    def buf(t):
+        return torch.empty(t.numel() + 8, dtype=t.dtype, device=DEV)[off:off + t.numel()].view(t.shape)
+    o, l, m = buf(out), buf(last), buf(mids)
+    pkg.ssm_delta_rule_fwd(*p.args(), out=o, last_state=l, chunk_states=m, **p.kw())
+    g = {k: buf(t) for k, t in grads.items()}
+    pkg.ssm_delta_rule_bwd(*p.args(), p.dout, dlast_state=p.dlast, chunk_states=m, grads=g, **p.kw())
+    torch.cuda.synchronize()
+    assert torch.equal(o, out) and torch.equal(l, last) and torch.equal(m, mids)
+    assert all(torch.equal(g[k], grads[k]) for k in grads)
