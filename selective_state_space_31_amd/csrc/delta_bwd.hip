@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(512, 2) delta_back_kernel(const BackArgs<TA> p
 #pragma unroll
         for (int nb = 0; nb < NC; ++nb) put_key<3, NC>(&sS[0][0][0][0], KT, w + 4 * i, nb, lane, S[i][nb]);
   };
+  constexpr bool kTight = KT * IN > 12;  // (K's and K^T's fragments: as in the forward)
   u32x4 fk[KT][IN], ft[2][3], fkt[TW][2][IN];
   f32x4 nde, nz;
   float ngC;
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(512, 2) delta_back_kernel(const BackArgs<TA> p
     load_k(slot);
     load_vec(slot);
     load_tri(p.c.tf, slot, ft);
-    load_cols(p.c.ktf, slot, fkt);
+    if constexpr (!kTight) load_cols(p.c.ktf, slot, fkt);
     put_state();
   }
   __syncthreads();
@@ -291,7 +292,8 @@ __global__ void __launch_bounds__(512, 2) delta_back_kernel(const BackArgs<TA> p
       put_tok<3, NC>(&sU[0][0][0][0], 2, w, nb, lane, x[nb] * nde + sP[w][nb][lane]);
     const f32x4 z = nz;
     __builtin_amdgcn_sched_barrier(0);
-    load_k(slot - less);
+    if constexpr (kTight) load_cols(p.c.ktf, slot, fkt);
+    else load_k(slot - less);
     __syncthreads();
     // ---- Y ----
     u32x4 u[2][NC][3];
@@ -338,7 +340,8 @@ __global__ void __launch_bounds__(512, 2) delta_back_kernel(const BackArgs<TA> p
       load_tri(p.c.tf, slot - less, ft);
     }
     __builtin_amdgcn_sched_barrier(0);
-    load_cols(p.c.ktf, slot - less, fkt);
+    if constexpr (kTight) load_k(slot - less);
+    else load_cols(p.c.ktf, slot - less, fkt);
     __syncthreads();
   }
   if (p.dfirst && tiles) {

@@ -205,6 +205,11 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
 #pragma unroll
         for (int nb = 0; nb < NC; ++nb) put_key<3, NC>(&sS[0][0][0][0], KT, w + 4 * i, nb, lane, S[i][nb]);
   };
+  // K's and K^T's fragments are fetched a chunk ahead, or where both do not fit
+  // the registers each behind the other's use (float32 keys beyond 128, 2 x 1024 x
+  // 4 heads of 256: 78 us, with both ahead and 100 registers spilled 127; the pass
+  // back 79 and 100).
+  constexpr bool kTight = KT * IN > 12;
   u32x4 ft[2][3], fkt[TW][2][IN];
   f32x4 nga, nde;
   float ngC;
@@ -243,7 +248,7 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
     load_rows(q.slot);
     load_v(q.slot, q.lo);
     load_t(q.slot);
-    load_kt(q.slot);
+    if constexpr (!kTight) load_kt(q.slot);
     put_state();
   }
   __syncthreads();
@@ -275,7 +280,8 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
       put_tok<3, NC>(&sX[0][0][0][0], 2, w, nb, lane, x[nb]);
     }
     __builtin_amdgcn_sched_barrier(0);
-    load_rows(slot + more);
+    if constexpr (kTight) load_kt(slot);
+    else load_rows(slot + more);
     __syncthreads();
     // ---- E ----
     u32x4 xp[2][NC][3];
@@ -326,7 +332,8 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
       load_t(slot + more);
     }
     __builtin_amdgcn_sched_barrier(0);
-    load_kt(slot + more);
+    if constexpr (kTight) load_rows(slot + more);
+    else load_kt(slot + more);
     __syncthreads();
   }
   if (p.last && tiles) state_store(p.last + pair * sv);
