@@ -83,7 +83,10 @@ inline size_t strided_bytes(int64_t rows, int64_t width, int64_t stride, size_t 
 // later parts round what the earlier ones left).  A product of two such values
 // keeps the partial products whose parts' indices add up to less than three:
 // six of nine, the dropped ones below 2^-26 of it.  A bf16 input is its own first
-// part, exactly.  (The float32 matrix instruction has the precision too, at 1/16
+// part, exactly; what is computed has three parts, also where it reaches bf16
+// outputs alone: those are often what is left of a key's much larger old value
+// (with two parts outputs of size 1 behind a state of size 1000 are off by 1.7e-2,
+// with three by 1.5e-3).  (The float32 matrix instruction has the precision too, at 1/16
 // of the bf16 rate: six products are 2.7 times as fast, three 5.3.)
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
@@ -92,15 +95,7 @@ typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 
 template <typename TA>
-struct ActParts;
-template <>
-struct ActParts<float> {
-  static constexpr int in = 3, out = 3;  // of an input; of what reaches act outputs alone
-};
-template <>
-struct ActParts<bf16_t> {
-  static constexpr int in = 1, out = 2;
-};
+constexpr int kInParts = sizeof(TA) == 4 ? 3 : 1;
 
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
@@ -125,11 +120,11 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t (&p)[N]) {
   }
 }
 
-// c += a b over the parts, up to `LIM` of their indices' sum
-template <int LIM, int NA, int NB>
+// c += a b over the parts
+template <int NA, int NB>
 __device__ __forceinline__ f32x4 mul_parts(const u32x4 (&a)[NA], const u32x4 (&b)[NB], f32x4 c) {
 #pragma unroll
-  for (int s = LIM - 1; s >= 0; --s)
+  for (int s = 2; s >= 0; --s)
 #pragma unroll
     for (int i = 0; i <= s; ++i)
       if (i < NA && s - i < NB) c = mfma16(a[i], b[s - i], c);
@@ -266,8 +261,8 @@ struct ChunkSpace {
   // per place and key head, parts in turn: fragments of K and Q (4 row blocks x
   // KT of 32 columns) and of K^T and Q^T (2 KT row blocks x 2 of 32 tokens)
   u32x4 *kf, *qf, *ktf, *qtf;
-  // per place and value head: fragments of T in three parts and of P (forward), of
-  // T^T and P^T in three parts each (backward)
+  // per place and value head, in three parts: fragments of T and P (forward), of
+  // T^T and P^T (backward)
   u32x4 *tf, *pf;
   float* vec;  // gamma (64), d (64); for the backward -beta gamma (64) too
 };
@@ -287,7 +282,7 @@ inline int delta_kt(int K) { return K <= 32 ? 1 : K <= 64 ? 2 : K <= 128 ? 4 : 8
 // Carves the forward's or the backward's space from `base` (NULL: counts only);
 // returns the bytes.
 inline size_t chunk_space(const DeltaDims& d, int dtype, bool back, char* base, ChunkSpace* c) {
-  const size_t in = dtype == SSM_DTYPE_F32 ? 3 : 1, out = dtype == SSM_DTYPE_F32 || back ? 3 : 2, kt = delta_kt(d.K);
+  const size_t in = dtype == SSM_DTYPE_F32 ? 3 : 1, kt = delta_kt(d.K);
   const size_t n = static_cast<size_t>(d.chunks()), frag = 64 * sizeof(u32x4);
   const size_t rows = n * d.hk * in * 4 * kt * frag, tri = n * d.hv * kTri * frag;
   size_t at = 0;
@@ -302,7 +297,7 @@ inline size_t chunk_space(const DeltaDims& d, int dtype, bool back, char* base, 
   s.ktf = reinterpret_cast<u32x4*>(take(rows));
   s.qtf = reinterpret_cast<u32x4*>(take(back ? rows : 0));
   s.tf = reinterpret_cast<u32x4*>(take(3 * tri));
-  s.pf = reinterpret_cast<u32x4*>(take(out * tri));
+  s.pf = reinterpret_cast<u32x4*>(take(3 * tri));
   s.vec = reinterpret_cast<float*>(take(n * d.hv * (back ? 3 : 2) * kDeltaC * 4));
   if (c) *c = s;
   return at;

@@ -35,7 +35,7 @@ struct BackArgs {
 // 340 MB at 2.7 TB/s; packed float32 3001 x 5 heads of 80 x 103 63 us).
 template <typename TA, int KT, int NC>
 __global__ void __launch_bounds__(512, 2) delta_back_kernel(const BackArgs<TA> p) {
-  constexpr int IN = ActParts<TA>::in, TW = (KT + 1) / 2;
+  constexpr int IN = kInParts<TA>, TW = (KT + 1) / 2;
   __shared__ u32x4 sS[3][KT][NC][64], sU[3][2][NC][64], sZ[3][2][NC][64], sG[3][2][NC][64], sO[IN][2][NC][64];
   __shared__ f32x4 sP[4][NC][64], sY[4][NC][64], sW[2 * KT][NC][64];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(512, 2) delta_back_kernel(const BackArgs<TA> p
           u32x4 o[IN];
 #pragma unroll
           for (int i = 0; i < IN; ++i) o[i] = sO[i][kb][nb][lane];
-          y = mul_parts<3>(fp[kb], o, y);
+          y = mul_parts(fp[kb], o, y);
         }
         sP[w][nb][lane] = y * p.scale;
       }
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(512, 2) delta_back_kernel(const BackArgs<TA> p
 #pragma unroll
           for (int i = 0; i < 3; ++i) z[i] = sG[i][kb][nb][lane];
 #pragma unroll
-          for (int x = 0; x < TW; ++x) W[x][nb] = mul_parts<3>(fqt[x][kb], z, W[x][nb]);
+          for (int x = 0; x < TW; ++x) W[x][nb] = mul_parts(fqt[x][kb], z, W[x][nb]);
         }
       }
     };
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(512, 2) delta_back_kernel(const BackArgs<TA> p
         u32x4 s[3];
 #pragma unroll
         for (int i = 0; i < 3; ++i) s[i] = sS[i][kb][nb][lane];
-        x[nb] = mul_parts<3>(fk[kb], s, x[nb]);
+        x[nb] = mul_parts(fk[kb], s, x[nb]);
       }
     }
 #pragma unroll
@@ -306,10 +306,10 @@ __global__ void __launch_bounds__(512, 2) delta_back_kernel(const BackArgs<TA> p
     load_vec(slot - less);
     f32x4 y[NC];
 #pragma unroll
-    for (int nb = 0; nb < NC; ++nb) y[nb] = mul_parts<3>(ft[1], u[1][nb], zero);
+    for (int nb = 0; nb < NC; ++nb) y[nb] = mul_parts(ft[1], u[1][nb], zero);
     if (kb0 == 0)
 #pragma unroll
-      for (int nb = 0; nb < NC; ++nb) y[nb] = mul_parts<3>(ft[0], u[0][nb], y[nb]);
+      for (int nb = 0; nb < NC; ++nb) y[nb] = mul_parts(ft[0], u[0][nb], y[nb]);
 #pragma unroll
     for (int nb = 0; nb < NC; ++nb) {
       sY[w][nb][lane] = y[nb];
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(512, 2) delta_back_kernel(const BackArgs<TA> p
         for (int nb = 0; nb < NC; ++nb) {
           f32x4 add = sW[w + 4 * i][nb][lane];  // (summed apart: the state itself is rounded once)
 #pragma unroll
-          for (int kb = 0; kb < 2; ++kb) add = mul_parts<3>(fkt[i][kb], d[kb][nb], add);
+          for (int kb = 0; kb < 2; ++kb) add = mul_parts(fkt[i][kb], d[kb][nb], add);
           S[i][nb] += add;
         }
       put_state();
@@ -421,8 +421,8 @@ struct GradCut {
 // each on another one.  Two workgroups a CU (128 registers, 59 spilled) are 4%
 // faster than one without spills; float32 has too many values for two.
 template <typename TA, int KT, bool SHARED>
-__global__ void __launch_bounds__(512, SHARED || ActParts<TA>::in > 1 || KT > 4 ? 2 : 4) delta_grad_kernel(const GradArgs<TA> p) {
-  constexpr int IN = ActParts<TA>::in, RT = GradCut<KT>::RT, CG = GradCut<KT>::CG, CT = GradCut<KT>::CT;
+__global__ void __launch_bounds__(512, SHARED || kInParts<TA> > 1 || KT > 4 ? 2 : 4) delta_grad_kernel(const GradArgs<TA> p) {
+  constexpr int IN = kInParts<TA>, RT = GradCut<KT>::RT, CG = GradCut<KT>::CG, CT = GradCut<KT>::CT;
   typedef float Mat[kDeltaC][kGradRow];
   __shared__ u32x4 sF[12][3][64];  // dO, Y, E: 4 row blocks of 32 columns; then two triangles' 6 blocks
   __shared__ Mat sH, sP;
@@ -612,9 +612,9 @@ __global__ void __launch_bounds__(512, SHARED || ActParts<TA>::in > 1 || KT > 4 
           u32x4 fo[IN];
 #pragma unroll
           for (int i = 0; i < IN; ++i) fo[i] = left[i];
-          gg[jt] = mul_parts<3>(fo, u, gg[jt]);
+          gg[jt] = mul_parts(fo, u, gg[jt]);
         } else {
-          gg[jt] = mul_parts<3>(left, u, gg[jt]);
+          gg[jt] = mul_parts(left, u, gg[jt]);
         }
         __builtin_amdgcn_sched_barrier(0);
       }

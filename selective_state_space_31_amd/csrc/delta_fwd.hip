@@ -35,7 +35,7 @@ struct RecArgs {
 // 8192 x 13 heads of 64 x 77 116 us).
 template <typename TA, int KT, int NC, bool MIDS>
 __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const RecArgs<TA> p) {
-  constexpr int IN = ActParts<TA>::in, OUT = ActParts<TA>::out, TW = (KT + 1) / 2;
+  constexpr int IN = kInParts<TA>, TW = (KT + 1) / 2;
   __shared__ u32x4 sS[3][KT][NC][64], sX[3][2][NC][64], sD[3][2][NC][64];
   __shared__ f32x4 sE[4][NC][64];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
@@ -80,13 +80,13 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         oat[nb][r] = c0 + 16 * nb + n < p.V ? (16u * w + 4u * g + r) * orow + (16 * nb + n) * es : kNone;
-    u32x4 fp[2][OUT];
+    u32x4 fp[2][3];
     f32x4 nga;
     const auto load_p = [&](int64_t slot) {
       nga = reinterpret_cast<const f32x4*>(p.c.vec + (slot * p.hv + h) * 2 * kDeltaC)[4 * w + g];
-      const u32x4* const src = p.c.pf + ((slot * p.hv + h) * (OUT * kTri) + tri_at(w, 0)) * 64;
+      const u32x4* const src = p.c.pf + ((slot * p.hv + h) * (3 * kTri) + tri_at(w, 0)) * 64;
 #pragma unroll
-      for (int i = 0; i < OUT; ++i) {
+      for (int i = 0; i < 3; ++i) {
         fp[0][i] = (src + i * kTri * 64)[lane];
         if (two) fp[1][i] = (src + (i * kTri + 1) * 64)[lane];
       }
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
       load_p(q.slot);
     }
     f32x4 y[NC];
-    u32x4 up[NC][2][OUT];
+    u32x4 up[NC][2][3];
     __syncthreads();
     if (nc == 0) return;  // (the chain waits at no further barrier either)
     for (int c = 0;; ++c) {
@@ -105,8 +105,8 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
       if (c > 0) {  // the chunk before: its e came behind the last barrier but one
 #pragma unroll
         for (int nb = 0; nb < NC; ++nb) {
-          y[nb] = mul_parts<OUT>(fp[0], up[nb][0], y[nb]);
-          if (two) y[nb] = mul_parts<OUT>(fp[1], up[nb][1], y[nb]);
+          y[nb] = mul_parts(fp[0], up[nb][0], y[nb]);
+          if (two) y[nb] = mul_parts(fp[1], up[nb][1], y[nb]);
         }
         if (c < nc) load_p(slot);
         if (p.out) {
@@ -126,10 +126,10 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
         y[nb] = zero;
 #pragma unroll
         for (int kb = 0; kb < KT; ++kb) {
-          u32x4 s[OUT];
+          u32x4 s[3];
 #pragma unroll
-          for (int i = 0; i < OUT; ++i) s[i] = sS[i][kb][nb][lane];
-          y[nb] = mul_parts<OUT>(fr[kb], s, y[nb]);
+          for (int i = 0; i < 3; ++i) s[i] = sS[i][kb][nb][lane];
+          y[nb] = mul_parts(fr[kb], s, y[nb]);
         }
         y[nb] *= nga;
       }
@@ -140,10 +140,10 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
       for (int nb = 0; nb < NC; ++nb) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          u32x2 part[OUT];
+          u32x2 part[3];
           split4(sE[t][nb][lane], part);
 #pragma unroll
-          for (int i = 0; i < OUT; ++i) {
+          for (int i = 0; i < 3; ++i) {
             up[nb][t >> 1][i][2 * (t & 1)] = part[i][0];
             up[nb][t >> 1][i][2 * (t & 1) + 1] = part[i][1];
           }
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
         u32x4 s[3];
 #pragma unroll
         for (int i = 0; i < 3; ++i) s[i] = sS[i][kb][nb][lane];
-        x[nb] = mul_parts<3>(fr[kb], s, x[nb]);
+        x[nb] = mul_parts(fr[kb], s, x[nb]);
       }
     }
 #pragma unroll
@@ -294,10 +294,10 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
     load_v(slot + more, t0 + more * kDeltaC);
     f32x4 u[NC];
 #pragma unroll
-    for (int nb = 0; nb < NC; ++nb) u[nb] = mul_parts<3>(ft[0], xp[0][nb], zero);
+    for (int nb = 0; nb < NC; ++nb) u[nb] = mul_parts(ft[0], xp[0][nb], zero);
     if (two)
 #pragma unroll
-      for (int nb = 0; nb < NC; ++nb) u[nb] = mul_parts<3>(ft[1], xp[1][nb], u[nb]);
+      for (int nb = 0; nb < NC; ++nb) u[nb] = mul_parts(ft[1], xp[1][nb], u[nb]);
 #pragma unroll
     for (int nb = 0; nb < NC; ++nb) {
       sE[w][nb][lane] = u[nb];
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-          for (int nb = 0; nb < NC; ++nb) add[nb] = mul_parts<3>(fkt[i][kb], d[kb][nb], add[nb]);
+          for (int nb = 0; nb < NC; ++nb) add[nb] = mul_parts(fkt[i][kb], d[kb][nb], add[nb]);
 #pragma unroll
         for (int nb = 0; nb < NC; ++nb) S[i][nb] += add[nb];
       }

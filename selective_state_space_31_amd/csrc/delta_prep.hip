@@ -36,7 +36,7 @@ __device__ __forceinline__ void put16(Mat& m, int i, int j, f32x4 c, float sign)
 // 2048 x 12 heads 42 us, 3.5 TB/s), the chain of the inverse's barriers.
 template <typename TA, int KT, bool BACK>
 __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
-  constexpr int IN = ActParts<TA>::in, OUT = BACK ? 3 : ActParts<TA>::out;
+  constexpr int IN = kInParts<TA>;
   typedef u32x4 Frags[IN][4][KT][64];
   __shared__ union { Frags k; Mat t; } both;  // T takes K's place (and Q, in the backward, T's)
   __shared__ Mat sA;
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
   const int64_t at = slot * p.hv + h;
 #pragma unroll
   for (int pair = 0; pair < 2; ++pair) {
-    u32x4 fp[OUT];
+    u32x4 fp[3];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int jt = 2 * pair + half;
@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
           u32x4 a[IN];
 #pragma unroll
           for (int i = 0; i < IN; ++i) a[i] = sk[i][jt][kb][lane];
-          kk = mul_parts<3>(a, fk[kb], kk);
-          if constexpr (!BACK) qk = mul_parts<3>(a, fq[kb], qk);
+          kk = mul_parts(a, fk[kb], kk);
+          if constexpr (!BACK) qk = mul_parts(a, fq[kb], qk);
         }
       }
       float4 a4 = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -157,11 +157,11 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
         *reinterpret_cast<float4*>(&sA[row][16 * jt + 4 * g]) = a4;
       }
       if constexpr (!BACK) {
-        uint32_t lo[OUT], hi[OUT];
+        uint32_t lo[3], hi[3];
         split2(qk[0], qk[1], lo);
         split2(qk[2], qk[3], hi);
 #pragma unroll
-        for (int i = 0; i < OUT; ++i) {
+        for (int i = 0; i < 3; ++i) {
           fp[i][2 * half] = lo[i];
           fp[i][2 * half + 1] = hi[i];
         }
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
     if constexpr (!BACK)
       if (pair <= w >> 1)
 #pragma unroll
-        for (int i = 0; i < OUT; ++i) p.c.pf[((at * OUT + i) * kTri + tri_at(w, pair)) * 64 + lane] = fp[i];
+        for (int i = 0; i < 3; ++i) p.c.pf[((at * 3 + i) * kTri + tri_at(w, pair)) * 64 + lane] = fp[i];
   }
   // ---- fragments of K^T (later Q^T): products with the unit matrix's columns ----
   u32x4 unit;
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
             u32x4 a[IN];
 #pragma unroll
             for (int i = 0; i < IN; ++i) a[i] = sk[i][it][kb][lane];
-            qk = mul_parts<3>(a, fk[kb], qk);
+            qk = mul_parts(a, fk[kb], qk);
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
