@@ -25,8 +25,11 @@ struct RecArgs {
 // A workgroup takes one column block of a head (columns do not meet).  Its first
 // four waves carry the chain X, E, S1: wave w has the tokens 16 w .. + 15 and
 // every fourth row block of S, in registers.  The other four form the outputs, 16
-// tokens each, in the time that the chain leaves.  S, X and d E pass through LDS
-// as right operands in bf16 parts; the left operands come from memory as
+// tokens each, in the time that the chain leaves; two waves of a SIMD have a short
+// and a long row of the triangles (waves are dealt to the four SIMDs in turn).  S,
+// X, d E and E pass through LDS as right operands in bf16 parts, each split by one
+// wave (16 heads over 131072 tokens: with the outputs' waves each splitting all of E
+// 4.20 ms, so 4.12, with short rows beside long ones 4.05); the left operands come from memory as
 // fragments, each needed by one wave alone, the next chunk's while this one is
 // worked on.  What bounds it is the chain through a chunk: three products, three
 // splits and three barriers, one after another (heads of 128, bf16: 1.6 us a chunk
@@ -36,10 +39,10 @@ struct RecArgs {
 template <typename TA, int KT, int NC, bool MIDS>
 __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const RecArgs<TA> p) {
   constexpr int IN = kInParts<TA>, TW = (KT + 1) / 2;
-  __shared__ u32x4 sS[3][KT][NC][64], sX[3][2][NC][64], sD[3][2][NC][64];
+  __shared__ u32x4 sS[3][KT][NC][64], sX[3][2][NC][64], sD[3][2][NC][64], sU[3][2][NC][64];  // (sU: the parts of E)
   __shared__ f32x4 sE[4][NC][64];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave & 3;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave < 4 ? wave : 7 - wave;
   // The workgroups of a head read the same fragments: they go to the same XCD
   // (workgroups are dealt to the eight XCDs in turn).
   const unsigned wide = 8u * static_cast<unsigned>(p.slices);
@@ -96,7 +99,6 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
       load_p(q.slot);
     }
     f32x4 y[NC];
-    u32x4 up[NC][2][3];
     __syncthreads();
     if (nc == 0) return;  // (the chain waits at no further barrier either)
     for (int c = 0;; ++c) {
@@ -105,8 +107,13 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
       if (c > 0) {  // the chunk before: its e came behind the last barrier but one
 #pragma unroll
         for (int nb = 0; nb < NC; ++nb) {
-          y[nb] = mul_parts(fp[0], up[nb][0], y[nb]);
-          if (two) y[nb] = mul_parts(fp[1], up[nb][1], y[nb]);
+          u32x4 e[2][3];
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int i = 0; i < 3; ++i) e[kb][i] = sU[i][kb][nb][lane];
+          y[nb] = mul_parts(fp[0], e[0], y[nb]);
+          if (two) y[nb] = mul_parts(fp[1], e[1], y[nb]);
         }
         if (c < nc) load_p(slot);
         if (p.out) {
@@ -138,20 +145,11 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
       __syncthreads();
 #pragma unroll
       for (int nb = 0; nb < NC; ++nb) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          u32x2 part[3];
-          split4(sE[t][nb][lane], part);
-#pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            up[nb][t >> 1][i][2 * (t & 1)] = part[i][0];
-            up[nb][t >> 1][i][2 * (t & 1) + 1] = part[i][1];
-          }
-        }
+        const f32x4 e = sE[w][nb][lane];
+        put_tok<3, NC>(&sU[0][0][0][0], 2, w, nb, lane, e);
         if constexpr (MIDS) {
           const rsrc_t rs = make_rsrc(p.mids + (slot * p.hv + h) * mv + sv, kDeltaC * srow);
           const uint32_t at = c0 + 16 * nb + n < p.V ? (16u * w + 4u * g) * srow + (c0 + 16 * nb + n) * 4u : kNone;
-          const f32x4 e = sE[w][nb][lane];
 #pragma unroll
           for (int r = 0; r < 4; ++r)
             __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(e[r]), rs, at + r * srow, 0, 0);
