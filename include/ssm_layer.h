@@ -75,9 +75,9 @@ extern "C" {
  *   workspace       : at least ssm_delta_rule_fwd_workspace_bytes(...) bytes
  * The recurrence is stable while 0 <= beta |k|^2 <= 2; beyond, states grow as
  * the formulas say and their rounding errors with them.
- * A value that is not finite leaves its own token's outputs and those behind it
- * in its sequence and head unspecified, and those of the up to 63 tokens before
- * it that share its chunk of SSM_DELTA_CHUNK tokens; nothing else is touched.
+ * A value that is not finite (or beyond the largest bf16 value, 3.38e38) leaves
+ * its own token's outputs and those behind it in its sequence and head
+ * unspecified, and the chunk_states behind its token; nothing else is touched.
  * Bitwise reproducible run to run on one device.
  */
 int ssm_delta_rule_fwd(const void* q, const void* k, const void* v, const float* beta,
@@ -143,6 +143,8 @@ size_t ssm_delta_rule_fwd_varlen_workspace_bytes(int64_t nseq, int64_t total_len
  *     dbeta        : (batch, seqlen, nheads_v) float32
  *     dg           : the same or NULL (not wanted)
  *     dinitial_state : the shape of initial_state, float32, or NULL
+ * A value that is not finite leaves all gradients of its sequence and head (of
+ * the key head: of dq and dk) unspecified, and no others.
  * Sums are formed in a fixed order: bitwise reproducible run to run on one
  * device.  A decay that rounds to 0 (g below about -104) has no slope.
  */

@@ -108,6 +108,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
+// The largest value that has parts: its first one would be infinite beyond, the
+// others NaN.
+constexpr float kPartsMost = 0x1.fep127f;
+__device__ __forceinline__ bool has_parts(float x) { return __builtin_fabsf(x) <= kPartsMost; }
+
 // Two values into N parts each, packed
 template <int N>
 __device__ __forceinline__ void split2(float a, float b, uint32_t (&p)[N]) {

@@ -25,13 +25,11 @@ struct RecArgs {
 // A workgroup takes one column block of a head (columns do not meet).  Its first
 // four waves carry the chain X, E, S1: wave w has the tokens 16 w .. + 15 and
 // every fourth row block of S, in registers.  The other four form the outputs, 16
-// tokens each, in the time that the chain leaves; two waves of a SIMD have a short
-// and a long row of the triangles (waves are dealt to the four SIMDs in turn).  S,
-// X, d E and E pass through LDS as right operands in bf16 parts, each split by one
-// wave (16 heads over 131072 tokens: with the outputs' waves each splitting all of E
-// 4.20 ms, so 4.12, with short rows beside long ones 4.05); the left operands come from memory as
-// fragments, each needed by one wave alone, the next chunk's while this one is
-// worked on.  What bounds it is the chain through a chunk: three products, three
+// tokens each, in the time that the chain leaves.  S, X, d E and E pass through LDS
+// as right operands in bf16 parts, each split by one wave (16 heads over 131072
+// tokens: 4.12 ms for the call, with the outputs' waves each splitting all of E
+// 4.20); the left operands come from memory as fragments, each needed by one wave
+// alone, the next chunk's while this one is worked on.  What bounds it is the chain through a chunk: three products, three
 // splits and three barriers, one after another (heads of 128, bf16: 1.6 us a chunk
 // with one column block, 131072 tokens of 16 heads 3.2 ms at 1.2 TB/s, matrix cores
 // busy a fifth of the time; 2.5 us with two, 4 x 2048 x 12 heads 80 us; float32
@@ -42,7 +40,7 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
   __shared__ u32x4 sS[3][KT][NC][64], sX[3][2][NC][64], sD[3][2][NC][64], sU[3][2][NC][64];  // (sU: the parts of E)
   __shared__ f32x4 sE[4][NC][64];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave < 4 ? wave : 7 - wave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave & 3;
   // The workgroups of a head read the same fragments: they go to the same XCD
   // (workgroups are dealt to the eight XCDs in turn).
   const unsigned wide = 8u * static_cast<unsigned>(p.slices);
@@ -91,42 +89,78 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
         fp[0][i] = (src + i * kTri * 64)[lane];
-        if (two) fp[1][i] = (src + (i * kTri + 1) * 64)[lane];
+        fp[1][i] = (src + (i * kTri + (two ? 1 : 0)) * 64)[lane];  // (short rows' own again: see below)
       }
     };
     if (nc > 0) {
-      load_rows(q.slot);
       load_p(q.slot);
+      load_rows(q.slot);
     }
+    // A token whose x is not finite meets the zeros of T's rows before it in its
+    // column: their e is formed again without it, and that of the rows from it on is
+    // NaN, as the column's state is by the chain.  (What finds it is e itself: it
+    // reaches every row behind it.)
+    const auto e_without = [&](int64_t slot, int nb) {
+      const u32x4* const src = p.c.tf + ((slot * p.hv + h) * (3 * kTri) + tri_at(w, 0)) * 64;
+      f32x4 e = zero;
+      int first = kDeltaC;
+      for (int kb = 0; kb <= w >> 1; ++kb) {
+        u32x4 t[3], x[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          t[i] = (src + (i * kTri + kb) * 64)[lane];
+          x[i] = sX[i][kb][nb][lane];
+        }
+#pragma unroll
+        for (int k = 7; k >= 0; --k) {
+          const uint32_t half = k & 1 ? 0xffff0000u : 0xffffu, top = half & 0x7f807f80u;
+          if ((x[0][k >> 1] & top) != top) continue;
+          first = min(first, 32 * kb + frag_tok(g, k));
+#pragma unroll
+          for (int i = 0; i < 3; ++i) x[i][k >> 1] &= ~half;
+        }
+        e = mul_parts(t, x, e);
+      }
+      first = min(first, __shfl_xor(first, 16));
+      first = min(first, __shfl_xor(first, 32));
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (16 * w + 4 * g + r >= first) e[r] = __builtin_nanf("");
+      return e;
+    };
     f32x4 y[NC];
+#pragma unroll
+    for (int nb = 0; nb < NC; ++nb) y[nb] = zero;
     __syncthreads();
     if (nc == 0) return;  // (the chain waits at no further barrier either)
+    // (The first round finishes no chunk: it stores nothing.  Loads and stores are
+    // the same in every round, so that a wait for the oldest waits for no others: the
+    // call with 131072 tokens 3.94 ms, with branches around them 4.22.)
     for (int c = 0;; ++c) {
       const int64_t slot = q.slot + c;
       const int more = c + 1 < nc ? 1 : 0;  // (the last chunk's loads ahead are its own again)
-      if (c > 0) {  // the chunk before: its e came behind the last barrier but one
+      // the chunk before: its e came behind the last barrier but one
 #pragma unroll
-        for (int nb = 0; nb < NC; ++nb) {
-          u32x4 e[2][3];
+      for (int nb = 0; nb < NC; ++nb) {
+        u32x4 e[2][3];
 #pragma unroll
-          for (int kb = 0; kb < 2; ++kb)
+        for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-            for (int i = 0; i < 3; ++i) e[kb][i] = sU[i][kb][nb][lane];
-          y[nb] = mul_parts(fp[0], e[0], y[nb]);
-          if (two) y[nb] = mul_parts(fp[1], e[1], y[nb]);
-        }
-        if (c < nc) load_p(slot);
-        if (p.out) {
-          const int64_t t0 = q.lo + int64_t{c - 1} * kDeltaC;
-          const rsrc_t rs = make_rsrc(p.out + (t0 * p.hv + h) * p.V + c0,
-                                      (rows_of(t0) - 1) * orow + static_cast<uint32_t>(p.V - c0) * es);
-#pragma unroll
-          for (int nb = 0; nb < NC; ++nb)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) buffer_store_act<TA>(p.scale * y[nb][r], rs, oat[nb][r]);
-        }
-        if (c == nc) break;
+          for (int i = 0; i < 3; ++i) e[kb][i] = sU[i][kb][nb][lane];
+        y[nb] = mul_parts(fp[0], e[0], y[nb]);
+        if (two) y[nb] = mul_parts(fp[1], e[1], y[nb]);
       }
+      if (p.out) {
+        const int64_t t0 = q.lo + int64_t{c - 1} * kDeltaC;
+        const rsrc_t rs = make_rsrc(p.out + (t0 * p.hv + h) * p.V + c0,
+                                    c > 0 ? (rows_of(t0) - 1) * orow + static_cast<uint32_t>(p.V - c0) * es : 0);
+#pragma unroll
+        for (int nb = 0; nb < NC; ++nb)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) buffer_store_act<TA>(p.scale * y[nb][r], rs, oat[nb][r]);
+      }
+      if (c == nc) break;
+      load_p(slot);
       __syncthreads();
 #pragma unroll
       for (int nb = 0; nb < NC; ++nb) {
@@ -143,16 +177,35 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
       load_rows(slot + more);
       if constexpr (MIDS) store_parts<KT, NC>(p.mids + (slot * p.hv + h) * mv, sbytes, srow, &sS[0][0][0][0], w, lane, c0, p.V);
       __syncthreads();
+      f32x4 e[NC];
+      float size = 0.0f;
 #pragma unroll
       for (int nb = 0; nb < NC; ++nb) {
-        const f32x4 e = sE[w][nb][lane];
-        put_tok<3, NC>(&sU[0][0][0][0], 2, w, nb, lane, e);
-        if constexpr (MIDS) {
-          const rsrc_t rs = make_rsrc(p.mids + (slot * p.hv + h) * mv + sv, kDeltaC * srow);
+        e[nb] = sE[w][nb][lane];
+        put_tok<3, NC>(&sU[0][0][0][0], 2, w, nb, lane, e[nb]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) size += __builtin_fabsf(e[nb][r]);
+      }
+      if (__any(!has_parts(size)))  // (or a sum of large ones: no harm)
+#pragma unroll
+        for (int nb = 0; nb < NC; ++nb) {
+          f32x4 kept = e[nb] = e_without(slot, nb);
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (!has_parts(kept[r])) {
+              kept[r] = 0.0f;
+              y[nb][r] = __builtin_nanf("");
+            }
+          put_tok<3, NC>(&sU[0][0][0][0], 2, w, nb, lane, kept);
+        }
+      if constexpr (MIDS) {
+        const rsrc_t rs = make_rsrc(p.mids + (slot * p.hv + h) * mv + sv, kDeltaC * srow);
+#pragma unroll
+        for (int nb = 0; nb < NC; ++nb) {
           const uint32_t at = c0 + 16 * nb + n < p.V ? (16u * w + 4u * g) * srow + (c0 + 16 * nb + n) * 4u : kNone;
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(e[r]), rs, at + r * srow, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(e[nb][r]), rs, at + r * srow, 0, 0);
         }
       }
       __syncthreads();

@@ -44,6 +44,7 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
   Mat& sT = both.t;
   __shared__ double sG[kDeltaC];
   __shared__ float sbeta[kDeltaC];
+  __shared__ int sbad;  // T holds a value that is not finite
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t slot = blockIdx.x / static_cast<unsigned>(p.hv);
@@ -89,6 +90,7 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
   };
   load_rows(p.k + (t0 + row) * p.ks + j * p.K, fk);
   load_rows(p.q + (t0 + row) * p.qs + j * p.K, fq);
+  if (tid == 0) sbad = 0;
   if (w == 0) {
     const bool in = lane < valid;
     sbeta[lane] = in ? p.beta[(t0 + lane) * p.hv + h] : 0.0f;
@@ -151,7 +153,7 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
           const int o = 16 * jt + 4 * g + e;
           const float D = row >= o ? expf(static_cast<float>(Gr - sG[o])) : 0.0f;
           const float bo = BACK ? br : sbeta[o];
-          qk[e] *= D * bo;
+          qk[e] = row >= o ? qk[e] * (D * bo) : 0.0f;  // (a later token that is not finite stays out)
           reinterpret_cast<float*>(&a4)[e] = row > o ? bo * D * kk[e] : 0.0f;
         }
         *reinterpret_cast<float4*>(&sA[row][16 * jt + 4 * g]) = a4;
@@ -202,7 +204,9 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
   __syncthreads();
 
   // ---- T = (I + A)^-1: the diagonal blocks of 16 by substitution, a column a
-  // lane; then [[T1, 0], [-T2 A21 T1, T2]] joins two blocks to one ----
+  // lane; then [[T1, 0], [-T2 A21 T1, T2]] joins two blocks to one.  The inner
+  // product goes through blocks above the diagonal, which nothing reads. ----
+  float size = 0.0f;
   {
     float t[16];
 #pragma unroll
@@ -211,29 +215,50 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
 #pragma unroll
       for (int c = 0; c < i; ++c) x = __builtin_fmaf(-sA[16 * w + i][16 * w + c], t[c], x);
       t[i] = x;
+      size += __builtin_fabsf(x);
     }
     if (g == 0)
 #pragma unroll
       for (int i = 0; i < 16; ++i) sT[16 * w + i][16 * w + n] = t[i];
   }
   __syncthreads();
-  // blocks (1, 0) and (3, 2); the inner product goes through A's own block
-  if (w < 2) put16(sA, 2 * w + 1, 2 * w, mul16(sA, 2 * w + 1, 2 * w, sT, 2 * w, 2 * w, zero), 1.0f);
+  // blocks (1, 0) and (3, 2)
+  if (w < 2) put16(sT, w, w + 2, mul16(sA, 2 * w + 1, 2 * w, sT, 2 * w, 2 * w, zero), 1.0f);
   __syncthreads();
-  if (w < 2) put16(sT, 2 * w + 1, 2 * w, mul16(sT, 2 * w + 1, 2 * w + 1, sA, 2 * w + 1, 2 * w, zero), -1.0f);
+  if (w < 2) {
+    const f32x4 m = mul16(sT, 2 * w + 1, 2 * w + 1, sT, w, w + 2, zero);
+    put16(sT, 2 * w + 1, 2 * w, m, -1.0f);
+    size += (__builtin_fabsf(m[0]) + __builtin_fabsf(m[1])) + (__builtin_fabsf(m[2]) + __builtin_fabsf(m[3]));
+  }
   __syncthreads();
   {  // blocks (2..3, 0..1), one a wave
     const int bi = 2 + (w >> 1), bj = w & 1;
     f32x4 m = mul16(sA, bi, 1, sT, 1, bj, zero);
     if (bj == 0) m = mul16(sA, bi, 0, sT, 0, 0, m);
+    put16(sT, bi - 2, bj + 2, m, 1.0f);
     __syncthreads();
-    put16(sA, bi, bj, m, 1.0f);
-    __syncthreads();
-    m = mul16(sT, bi, 2, sA, 2, bj, zero);
-    if (bi == 3) m = mul16(sT, 3, 3, sA, 3, bj, m);
+    m = mul16(sT, bi, 2, sT, 0, bj + 2, zero);
+    if (bi == 3) m = mul16(sT, 3, 3, sT, 1, bj + 2, m);
     put16(sT, bi, bj, m, -1.0f);
+    size += (__builtin_fabsf(m[0]) + __builtin_fabsf(m[1])) + (__builtin_fabsf(m[2]) + __builtin_fabsf(m[3]));
   }
+  if constexpr (!BACK)
+    if (!has_parts(size)) sbad = 1;
   __syncthreads();
+  // A token that is not finite, or an overflow, may not reach the rows before it by
+  // way of the products' zeros: then T by substitution, each column by itself from
+  // its diagonal on.  (The backward's tokens depend on those behind them anyway.)
+  if constexpr (!BACK)
+    if (sbad) {
+      if (w == 0)
+        for (int i = 0; i < kDeltaC; ++i) {
+          float x = i == lane ? 1.0f : 0.0f;
+          for (int c = 0; c < i; ++c)
+            if (c >= lane) x = __builtin_fmaf(-sA[i][c], sT[c][lane], x);
+          sT[i][lane] = x;
+        }
+      __syncthreads();
+    }
 
   // ---- fragments of T, or of T^T; wave w its row block ----
   for (int kb = BACK ? w >> 1 : 0; kb <= (BACK ? 1 : w >> 1); ++kb) {
