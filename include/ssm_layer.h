@@ -146,7 +146,7 @@ size_t ssm_delta_rule_fwd_varlen_workspace_bytes(int64_t nseq, int64_t total_len
  * A value that is not finite leaves all gradients of its sequence and head (of
  * the key head: of dq and dk) unspecified, and no others.
  * Sums are formed in a fixed order: bitwise reproducible run to run on one
- * device.  A decay that rounds to 0 (g below about -104) has no slope.
+ * device.  A decay that rounds to 0 (g below about -104) has no slope: dg is 0.
  */
 int ssm_delta_rule_bwd(const void* q, const void* k, const void* v, const float* beta,
                        const float* g, float scale, const float* initial_state,

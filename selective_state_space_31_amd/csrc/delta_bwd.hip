@@ -465,9 +465,11 @@ __global__ void __launch_bounds__(512, SHARED || kInParts<TA> > 1 || KT > 4 ? 2 
   const int h0 = SHARED ? j * rep : of;
   for (int h = h0; h < h0 + (SHARED ? rep : 1); ++h) {
     const int64_t at = slot * p.hv + h;
+    bool gone = false;  // (wave 0) this token's decay is 0: no slope, where dg's sums leave the rest of what cancels
     if (wave == 0) {  // as in the preparation
       const bool in = lane < valid;
       const float x = in && p.g ? p.g[(t0 + lane) * p.hv + h] : 0.0f;
+      gone = expf(x) == 0.0f;
       double G = x < -1e4f ? -1e4 : static_cast<double>(x);
 #pragma unroll
       for (int m = 1; m < 64; m <<= 1) {
@@ -776,7 +778,7 @@ __global__ void __launch_bounds__(512, SHARED || kInParts<TA> > 1 || KT > 4 ? 2 
       }
       if (lane < valid) {
         p.dbeta[(t0 + lane) * p.hv + h] = sdb[lane];
-        if (p.dg) p.dg[(t0 + lane) * p.hv + h] = static_cast<float>(d + last);
+        if (p.dg) p.dg[(t0 + lane) * p.hv + h] = gone ? 0.0f : static_cast<float>(d + last);
       }
     }
     __syncthreads();
