@@ -259,7 +259,8 @@ __global__ void __launch_bounds__(MULTI ? 1024 : 256) norm_bwd_kernel(const Norm
         s[i][j] = rs.at(i, j);
         y[i][j] = ry.at(i, j);
       }
-    const float rstd = centre<MULTI>(s, rg, first, step, dim, p.eps);
+    float rstd = centre<MULTI>(s, rg, first, step, dim, p.eps);
+    if (!there) rstd = 0.0f;  // (1 / 0 with eps = 0: its NaN would reach dw)
     float t0 = 0.0f, t1 = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)

@@ -1,4 +1,5 @@
-"""Layer norm's sums: rows far from zero and constant rows (GPU)."""
+"""Layer norm's sums: rows far from zero, constant rows, and eps other than the
+default with row counts that leave row groups empty (GPU)."""
 import numpy as np
 import pytest
 import torch
@@ -75,3 +76,10 @@ def test_constant_rows(value, dim, dtype):
     # the first mean is off by a sum's error (relative), the second by that again; divided by sqrt(eps)
     err = 3.0 * abs(value) * ops_bound(1.0, dim) ** 2 / np.sqrt(1e-5)
     within(out, np.full((3, dim), 0.25), err + 4 * HALF * 0.25 + (0.25 * 2.0 ** -8 if dtype == "bf16" else 0), "out")
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("eps", [0.0, 0.5])
+@pytest.mark.parametrize("rows,dim", [(1, 64), (3, 64), (5, 512), (2, 515), (17, 2560), (1, 2560), (1025, 1536), (1030, 1000),
+                                      (2, 8191), (1023, 300)])
+def test_eps(rows, dim, eps, dtype):
+    check(Norm(rows, dim, dtype, rows + dim), eps, dresidual=rows % 2 == 0)
