@@ -310,13 +310,25 @@ inline size_t chunk_space(const DeltaDims& d, int dtype, bool back, char* base, 
 
 // Whether a workgroup of the passes over chunks takes two column blocks of 16
 // rather than one: the same left operands then serve twice the columns, and rows of
-// the states are written in whole lines, but a chunk takes longer.  So where three
-// workgroups for four compute units are left (4 x 2048 x 12 heads of 128: forward
-// 77 against 83 us, with the states for the backward 113 and 143; 16 heads over
-// 131072 tokens, 64 workgroups, 4490 and 3270), and not for packed sequences, of
-// which a few may be all that is left to do (7 x 5 heads, 3001 tokens 90 and 61).
+// the states are written in whole lines, but a chunk takes longer.  So where one
+// block each would be more workgroups than compute units.  Calls of 1024 tokens a
+// sequence, heads of 128, one block and two (workgroups of one block; bf16 and
+// float32):
+//   96 (1 x 12 heads)   forward 45 / 57 us, 61 / 74; gradients 84 / 99, 100 / 122
+//   192                 46 / 58, 66 / 78; 100 / 113, 132 / 155
+//   256 (heads of 64)   45 / 56, 61 / 73; 98 / 110, 152 / 166
+//   288                 62 / 60, 116 / 93; with the states 77 / 64, 124 / 104
+//   480                 66 / 66, 146 / 120; states 81 / 69, 185 / 154
+//   576                 92 / 107, 227 / 196; states 141 / 134, 280 / 242
+//   768                 114 / 121, 282 / 233; states 168 / 157, 324 / 278
+//   1536                266 / 224, 533 / 395; states 388 / 293, 619 / 457
+// Of packed sequences a few long ones may be all that is left to do: only beyond
+// five times that many (11 of 0 to 3000 tokens: 715 workgroups 108 / 137 and 160 /
+// 181, 1056 139 / 155 and 345 / 301, 3520 464 / 393 and 914 / 690; 16 of 512,
+// 1536: 118 / 113 and 298 / 216).
 inline bool two_blocks(const DeltaDims& d) {
-  return !d.packed && d.K <= 128 && d.V > 16 && 4 * d.nseq * d.hv * ((d.V + 31) / 32) >= 3 * device_cus();
+  const int64_t one = d.nseq * d.hv * ((d.V + 15) / 16);
+  return d.K <= 128 && d.V > 16 && one > (d.packed ? 5 : 1) * device_cus();
 }
 
 // Launches the preparation of every chunk, the forward's or the backward's.
