@@ -13,7 +13,8 @@ LENGTHS = [70, 0, 1, 129, 64, 30, 9]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-@pytest.mark.parametrize("hk,hv,K,V", [(16, 48, 64, 77), (40, 40, 32, 60), (7, 28, 128, 80), (2, 2, 128, 96), (18, 18, 64, 129)])
+@pytest.mark.parametrize("hk,hv,K,V", [(16, 48, 64, 77), (60, 60, 32, 60), (14, 56, 128, 80), (40, 40, 32, 60), (2, 2, 128, 96),
+                                       (18, 18, 64, 129)])
 def test_packed_many_heads(hk, hv, K, V, dtype):
     """Outputs, states and gradients of every sequence."""
     cu = np.concatenate([[0], np.cumsum(LENGTHS)])
