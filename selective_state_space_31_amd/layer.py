@@ -96,6 +96,12 @@ def _tokens(t, name, lead, D, like):
     return _heads(t, name, lead[0], lead[1], D, like)
 
 
+def _scale(scale, K):
+    if K < 1:
+        raise ValueError("headdim_k must be at least 1")
+    return K ** -0.5 if scale is None else float(scale)
+
+
 class _Delta:
     """A delta rule call's inputs, checked: sizes, addresses, shapes."""
 
@@ -107,6 +113,8 @@ class _Delta:
         if self.packed:
             if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
                 raise ValueError("q, k and v must be (total_len, heads, headdim)")
+            if not isinstance(cu_seqlens, torch.Tensor):
+                raise TypeError("cu_seqlens must be a torch.Tensor")
             if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
                 raise ValueError("cu_seqlens must be (nseq + 1,) with nseq >= 1")
             lead, self.n = q.shape[:1], cu_seqlens.numel() - 1
@@ -128,7 +136,7 @@ class _Delta:
         self.lead, self.like, self.gate = lead, q, lead + (Hv,)
         self.out, self.key = lead + (Hv, V), lead + (Hk, K)
         self.state, self.mids = (self.n, Hv, K, V), chunks + (Hv, K + SSM_DELTA_CHUNK, V)
-        self.scale = K ** -0.5 if scale is None else float(scale)
+        self.scale = _scale(scale, K)
         self.head = (q.data_ptr(), k.data_ptr(), v.data_ptr(), _in(beta, "beta", self.gate, _F32, q),
                      _opt(g, "g", self.gate, _F32, q), self.scale)
         self.h0 = _opt(initial_state, "initial_state", self.state, _F32, q)
@@ -253,7 +261,7 @@ def ssm_delta_state_update(state, q, k, v, beta, g=None, scale=None, out=None, s
         raise ValueError("q has %d heads, k %d" % (Hk, Hkk))
     args = (_in(state, "state", (batch, Hv, K, V), _F32, q), q.data_ptr(), k.data_ptr(), v.data_ptr(),
             _in(beta, "beta", (batch, Hv), _F32, q), _opt(g, "g", (batch, Hv), _F32, q),
-            K ** -0.5 if scale is None else float(scale))
+            _scale(scale, K))
     stream = _other(stream, q)
     out = _out(out, "out", (batch, Hv, V), dt, q, stream)
     _call(lib.ssm_delta_state_update, q, stream, *args, out.data_ptr(), batch, Hk, Hv, K, V, qs, ks, vs, _DTYPES[dt])
