@@ -75,6 +75,8 @@ extern "C" {
  *   workspace       : at least ssm_delta_rule_fwd_workspace_bytes(...) bytes
  * The recurrence is stable while 0 <= beta |k|^2 <= 2; beyond, states grow as
  * the formulas say and their rounding errors with them.
+ * Float32's precision is that of values above 2^-108 (3e-33); of smaller ones,
+ * here and in the gradients, what lies below 2^-126 or so is lost.
  * A value that is not finite (or beyond the largest bf16 value, 3.38e38) leaves
  * its own token's outputs and those behind it in its sequence and head
  * unspecified, and the chunk_states behind its token; nothing else is touched.
@@ -214,7 +216,8 @@ int ssm_delta_state_update(float* state, const void* q, const void* k, const voi
  *                     wanted); receives s; needs residual.  May be x or residual
  *                     where that is contiguous.
  *   0 <= rows < 2^31; 1 <= dim <= 16384; eps >= 0 (rows whose var + eps is below
- *   2^-126 give unspecified values).
+ *   2^-126 give unspecified values, and rows with values 2^57 or more apart,
+ *   whose squares' sum may pass float32's range).
  * A row that holds a NaN or an infinity is NaN, and no other one.
  */
 int ssm_layer_norm_fwd(const void* x, const void* residual, const float* weight, const float* bias,
