@@ -31,8 +31,8 @@ struct BackArgs {
 //   window A (up to barrier 1)  chain: dU     others: the next dO's parts in, Q^T (gamma dO) out
 //   window B (up to barrier 2)  chain: Y      others: the next P^T dO, the states' gradients
 //   window C (up to barrier 3)  chain: dS0    others: the next Q^T (gamma dO), Y and dV
-// The chain bounds it as in the forward (4 x 2048 x 12 heads of 128, bf16: 125 us,
-// 340 MB at 2.7 TB/s; packed float32 3001 x 5 heads of 80 x 103 63 us).
+// The chain bounds it as in the forward (4 x 2048 x 12 heads of 128, bf16: 122 us,
+// 340 MB at 2.8 TB/s; packed float32 3001 x 5 heads of 80 x 103 63 us).
 template <typename TA, int KT, int NC>
 __global__ void __launch_bounds__(512, 2) delta_back_kernel(const BackArgs<TA> p) {
   constexpr int IN = kInParts<TA>, TW = (KT + 1) / 2;
@@ -415,7 +415,7 @@ struct GradCut {
   static constexpr int RT = KT < 4 ? KT : 4, RG = 4 / RT, CG = 8 / RG, CT = 2 * KT / CG;
 };
 
-// What bounds it (4 sequences of 2048 tokens, 12 heads of 128, bf16: 183 us for 440
+// What bounds it (4 sequences of 2048 tokens, 12 heads of 128, bf16: 182 us for 440
 // MB and 280 MB of spilled registers, 3.9 TB/s): no unit by itself (vector ALU 32%,
 // matrix cores 17%, LDS about 30% of the time), but the phases between barriers,
 // each on another one.  Two workgroups a CU (128 registers, 59 spilled) are 4%

@@ -9,8 +9,8 @@
 // A row stays in the registers of one wave (or, wide ones and few ones, of four
 // or sixteen waves), so the mean square is taken around the mean itself and
 // every value is read once and written once: memory bounds it (8192 x 2560 bf16 with
-// the sum 27.7 us, 6.1 TB/s; 131072 x 2048 187 us, 5.7; gradients of 8192 x 1536 26.6
-// us, 3.8, and 4.1 for the partial rows' sum).
+// the sum 28.1 us, 6.0 TB/s; 131072 x 2048 187 to 204 us, 5.7 to 5.3; gradients of 8192
+// x 1536 26.9 us, 3.7, and 4.1 for the partial rows' sum).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
