@@ -322,13 +322,13 @@ inline size_t chunk_space(const DeltaDims& d, int dtype, bool back, char* base, 
 //   576                 92 / 107, 227 / 196; states 141 / 134, 280 / 242
 //   768                 114 / 121, 282 / 233; states 168 / 157, 324 / 278
 //   1536                266 / 224, 533 / 395; states 388 / 293, 619 / 457
-// Of packed sequences a few long ones may be all that is left to do: only beyond
-// five times that many (11 of 0 to 3000 tokens: 715 workgroups 108 / 137 and 160 /
-// 181, 1056 139 / 155 and 345 / 301, 3520 464 / 393 and 914 / 690; 16 of 512,
-// 1536: 118 / 113 and 298 / 216).
+// Not for packed sequences: a few long ones may be all that is there to do, and a
+// chunk of theirs takes 2.8 us instead of 1.65 (11 of 0 to 3000 tokens: 715
+// workgroups 108 / 137 and 160 / 181, 1056 139 / 155 and 345 / 301, 3520 464 / 393
+// and 914 / 690; of equal lengths two would be better: 16 of 512, 1536: 118 / 113
+// and 298 / 216), and the lengths are not known here; nor is how many are empty.
 inline bool two_blocks(const DeltaDims& d) {
-  const int64_t one = d.nseq * d.hv * ((d.V + 15) / 16);
-  return d.K <= 128 && d.V > 16 && one > (d.packed ? 5 : 1) * device_cus();
+  return !d.packed && d.K <= 128 && d.V > 16 && d.nseq * d.hv * ((d.V + 15) / 16) > device_cus();
 }
 
 // Launches the preparation of every chunk, the forward's or the backward's.

@@ -418,15 +418,12 @@ void run_chunks(const void* v, float scale, void* out, float* last, const float*
 // 1 token 4.4 against 15.5 us, 8 tokens 14.1 and 15.5, 16 tokens 25 and 14), up to
 // 16 where the heads fill the device (32 sequences: 46 against 52 us, 32 tokens 80
 // and 53).  Of packed sequences only the sum of the lengths is known here, and one
-// may have them all: a token takes 1.9 us then, and the chunks of many sequences
-// 0.11 us for each of their heads (bf16; float32 0.16).  So where one token takes
-// the place of 16 of those or more (16 heads of 128, bf16 and float32: 256
-// sequences of 1 token 109 against 440 us and 109 against 668, 32 of 1 19 and 61,
-// 18 and 80; where the rule says chunks, 256 of 2 tokens 127 and 444, of 16 590 and
-// 441, but 255 of 1 and one of 500 1065 and 462).
+// may have them all, at 1.9 us a token: so by the same 8, although many short ones
+// would gain (16 heads of 128, bf16 and float32: 256 sequences of 1 token 109
+// against 490 us in chunks and 109 against 988, of 8 tokens 327 and 506, 289 and
+// 1009; but 255 of 1 and one of 500 1065 and 507).
 bool few_tokens(const DeltaDims& d) {
-  const int64_t heads = d.nseq * d.hv;
-  return d.L <= 8 || (d.packed ? 16 * d.L <= heads : d.L <= 16 && heads > device_cus());
+  return d.L <= 8 || (!d.packed && d.L <= 16 && d.nseq * d.hv > device_cus());
 }
 
 size_t fwd_bytes(const DeltaDims& d, int dtype) {

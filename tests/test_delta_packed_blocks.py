@@ -1,5 +1,5 @@
-"""Packed sequences of many heads, where a workgroup takes two column blocks, on
-both sides of that rule (GPU)."""
+"""Packed sequences of many heads, which as whole ones would go by two column
+blocks a workgroup, and the results of which do not depend on that (GPU)."""
 import numpy as np
 import pytest
 import torch
@@ -34,8 +34,8 @@ def test_packed_many_heads(hk, hv, K, V, dtype):
 
 
 def test_a_sequence_is_the_same_alone():
-    """The number of column blocks does not show in the results: bit for bit
-    those of a call with this sequence and two of the heads alone."""
+    """Bit for bit the results of packed and whole calls with this sequence and
+    two of the heads alone, and of a whole call with all heads."""
     cu = np.concatenate([[0], np.cumsum(LENGTHS)])
     p = Delta((int(cu[-1]),), len(LENGTHS), 40, 40, 64, 77, "bf16", DEV, seed=3)
     off = torch.tensor(cu, dtype=torch.int32, device=DEV)
@@ -45,5 +45,12 @@ def test_a_sequence_is_the_same_alone():
     one = torch.tensor([0, z - a], dtype=torch.int32, device=DEV)
     o2, l2 = pkg.ssm_delta_rule_fwd_varlen(*(cut(t) for t in p.args()), one, g=cut(p.g), initial_state=p.h0[3:4, 7:9].contiguous(),
                                            return_last_state=True)
+    o3, l3 = pkg.ssm_delta_rule_fwd(*(t[a:z][None].contiguous() for t in p.args()), g=p.g[a:z][None].contiguous(),
+                                    initial_state=p.h0[3:4], return_last_state=True)
+    o4, l4 = pkg.ssm_delta_rule_fwd(*(torch.cat([cut(t)[None]] * 40) for t in p.args()), g=torch.cat([cut(p.g)[None]] * 40),
+                                    initial_state=torch.cat([p.h0[3:4, 7:9]] * 40), return_last_state=True)
     torch.cuda.synchronize()
     assert torch.equal(out[a:z, 7:9], o2) and torch.equal(last[3, 7:9], l2[0])
+    assert torch.equal(out[a:z], o3[0]) and torch.equal(last[3], l3[0])
+    for i in (0, 39):  # (80 heads of five column blocks: two blocks a workgroup)
+        assert torch.equal(o2, o4[i]) and torch.equal(l2[0], l4[i])

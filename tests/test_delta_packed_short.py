@@ -1,5 +1,5 @@
-"""Packed batches of many short sequences, on both sides of the rule by which
-they go token by token (GPU)."""
+"""Packed batches of many short sequences, empty ones among them, in chunks and
+token by token (GPU)."""
 import numpy as np
 import pytest
 import torch
@@ -13,18 +13,18 @@ DEV = torch.device("cuda:0")
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("n,hk,hv,K,V,lengths", [
-    (40, 8, 16, 64, 24, [1]),            # one token each: 40 of 40 heads' worth
-    (40, 8, 16, 64, 24, [1, 0, 1, 1]),   # the odd one empty
-    (20, 32, 64, 40, 33, [2, 5, 1, 4]),  # a few each
+    (40, 8, 16, 64, 24, [1]),               # one token each
+    (40, 8, 16, 64, 24, [1, 0, 1, 1]),      # the odd one empty
+    (20, 32, 64, 40, 33, [2, 5, 1, 4]),     # a few each
     (20, 32, 64, 40, 33, [0] * 19 + [66]),  # all in one, beyond a chunk
-    (20, 8, 16, 64, 24, [2])], ids=str)  # chunks
+    (30, 8, 16, 64, 24, [0] * 9 + [1] + [0, 0] + [4] + [0] * 17)], ids=str)  # token by token
 def test_many_short(n, hk, hv, K, V, lengths, dtype):
     """Outputs, states, chunk states (and their unused places), the rows behind
     the last sequence, and the gradients from those states."""
     lengths = (lengths * n)[:n]
     cu = np.concatenate([[0], np.cumsum(lengths)])
     end, T = int(cu[-1]), int(cu[-1]) + 3
-    by_token = 16 * T <= n * hv
+    by_token = T <= 8
     assert by_token == (pkg.ssm_delta_rule_fwd_varlen_workspace_bytes(n, T, hk, hv, K, V) == 0)
     p = Delta((T,), n, hk, hv, K, V, dtype, DEV, seed=T, fused=True)
     off = torch.tensor(cu, dtype=torch.int32, device=DEV)
