@@ -58,7 +58,11 @@ struct Raw {
   __device__ __forceinline__ float at(int i, int j) const { return to_f32(v[i].v[j]); }
 };
 
-template <typename TA, int NV>
+// (FRESH forms the addresses of a row's last values where they are needed, rather
+// than keeping two registers for each from row to row: gradients of 8192 x 8192 bf16
+// 142 us, 152 without; the forward is better off keeping them, 65536 x 300 bf16 35
+// and 39.)
+template <typename TA, int NV, bool FRESH = false>
 __device__ __forceinline__ void store_row(const float (&x)[NV][Piece<TA>::n], TA* p, int first, int step, int dim) {
   constexpr int VEC = Piece<TA>::n;
 #pragma unroll
@@ -70,9 +74,11 @@ __device__ __forceinline__ void store_row(const float (&x)[NV][Piece<TA>::n], TA
     if (c + VEC <= dim) {
       __builtin_memcpy(p + c, &raw, sizeof(raw));
     } else {
+      int at = c;
+      if constexpr (FRESH) asm volatile("" : "+v"(at));
 #pragma unroll
       for (int j = 0; j < VEC; ++j)
-        if (c + j < dim) p[c + j] = raw.v[j];
+        if (at + j < dim) p[at + j] = raw.v[j];
     }
   }
 }
@@ -97,6 +103,21 @@ __device__ __forceinline__ void load_param(float (&w)[NV][VEC], const float* p, 
   }
 }
 
+// Sums over 16 lanes side by side, in each of them, and over a wave: without LDS,
+// whose cross-lane operations the two statistics' sums would wait for (65536 x 300
+// bf16 with the sum 35 us, by them 45; gradients of 8192 x 1536 float32 49 and 60).
+template <int ROR>
+__device__ __forceinline__ float row_add(float x) {
+  return x + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x120 + ROR, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float row_sum16(float x) { return row_add<1>(row_add<2>(row_add<4>(row_add<8>(x)))); }
+
+__device__ __forceinline__ float wave_sum(float x) {
+  x = row_sum16(x);
+  const auto row = [&](int r) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 16 * r)); };
+  return (row(0) + row(1)) + (row(2) + row(3));
+}
+
 // A workgroup works on GROUPS rows at a time, `waves` waves each.  Sums over a
 // row go through the lanes of its waves and, with MULTI, through LDS in a fixed
 // order; a slot is written again only behind the barrier of another one, so one
@@ -114,11 +135,8 @@ struct RowGroup {
     red = r;
   }
   __device__ __forceinline__ void sum2(float& a, float& b, int slot) const {
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) {
-      a += __shfl_xor(a, m);
-      b += __shfl_xor(b, m);
-    }
+    a = wave_sum(a);
+    b = wave_sum(b);
     if constexpr (MULTI) {
       float* const p = red + (slot * 16 + group * waves) * 2;
       if ((lane & 63) == 0) {
@@ -126,11 +144,11 @@ struct RowGroup {
         p[2 * w + 1] = b;
       }
       __syncthreads();
-      a = b = 0.0f;
-      for (int i = 0; i < waves; ++i) {
-        a += p[2 * i];
-        b += p[2 * i + 1];
-      }
+      const int i = lane & 15;  // (at most 16 waves)
+      a = i < waves ? p[2 * i] : 0.0f;
+      b = i < waves ? p[2 * i + 1] : 0.0f;
+      a = row_sum16(a);
+      b = row_sum16(b);
     }
   }
   __device__ __forceinline__ float sum(float a, int slot) const {
@@ -234,6 +252,9 @@ template <typename TA, int NV, bool MULTI>
 __global__ void __launch_bounds__(MULTI ? 1024 : 256) norm_bwd_kernel(const NormArgs<TA> p) {
   constexpr int VEC = Piece<TA>::n;
   __shared__ float red[MULTI ? 96 : 1];
+  // dresidual is fetched behind the sums where a row's values fill the registers
+  // (2048 x 16384 float32 141 us, before them 166)
+  constexpr bool LATE = MULTI && NV * VEC > 8;
   extern __shared__ float fold[];  // [2][64 waves VEC], with several groups
   const RowGroup<MULTI> rg(p.waves, red);
   const int first = rg.lane * VEC, dim = p.dim, step = 64 * rg.waves * VEC;
@@ -250,7 +271,7 @@ __global__ void __launch_bounds__(MULTI ? 1024 : 256) norm_bwd_kernel(const Norm
     Raw<TA, NV> rs, ry, rd;
     rs.load(p.x + row * p.xs, first, step, dim, there);
     ry.load(p.res + row * dim, first, step, dim, there);
-    if (p.dres) rd.load(p.dres + row * dim, first, step, dim, there);
+    if (!LATE && p.dres) rd.load(p.dres + row * dim, first, step, dim, there);
     float s[NV][VEC], y[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -275,6 +296,7 @@ __global__ void __launch_bounds__(MULTI ? 1024 : 256) norm_bwd_kernel(const Norm
         t1 = __builtin_fmaf(y[i][j], h, t1);
       }
     rg.sum2(t0, t1, 2);
+    if (LATE && p.dres) rd.load(p.dres + row * dim, first, step, dim, there);
     const float inv = 1.0f / static_cast<float>(dim);
     t0 *= inv;
     t1 *= inv;
@@ -283,7 +305,7 @@ __global__ void __launch_bounds__(MULTI ? 1024 : 256) norm_bwd_kernel(const Norm
 #pragma unroll
       for (int j = 0; j < VEC; ++j)
         y[i][j] = __builtin_fmaf(rstd, y[i][j] - t0 - s[i][j] * t1, p.dres ? rd.at(i, j) : 0.0f);
-    if (there) store_row<TA, NV>(y, p.out + row * dim, first, step, dim);
+    if (there) store_row<TA, NV, NV == 1>(y, p.out + row * dim, first, step, dim);
   }
   if (!p.part) return;
   const int lanes = 64 * rg.waves;
