@@ -33,7 +33,7 @@ struct RecArgs {
 // splits and three barriers, one after another (heads of 128, bf16: 1.65 us a chunk
 // with one column block, 131072 tokens of 16 heads 3.4 ms at 1.2 TB/s, matrix cores
 // busy a fifth of the time on the compute units in use; 2.8 us with two, 4 x 2048
-// x 12 heads 90 us; float32 8192 x 13 heads of 64 x 77 119 us).
+// x 12 heads 91 us; float32 8192 x 13 heads of 64 x 77 116 us).
 template <typename TA, int KT, int NC, bool MIDS>
 __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const RecArgs<TA> p) {
   constexpr int IN = kInParts<TA>, TW = (KT + 1) / 2;

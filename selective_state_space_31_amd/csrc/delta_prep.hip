@@ -32,8 +32,8 @@ __device__ __forceinline__ void put16(Mat& m, int i, int j, f32x4 c, float sign)
 // side by side are a fragment of P.  K^T comes out of products with the columns
 // of the unit matrix, which are exact.
 // Memory bounds it where chunks are many (16 heads of 128 over 131072 tokens, bf16:
-// 521 us for 3.2 GB read and written, 6.2 TB/s); a round of few takes 17 us (4 x
-// 2048 x 12 heads 44 us, 4.4 TB/s), the chain of the inverse's barriers.
+// 519 us for 3.2 GB read and written, 6.2 TB/s); a round of few takes 17 us (4 x
+// 2048 x 12 heads 43 us, 4.4 TB/s), the chain of the inverse's barriers.
 template <typename TA, int KT, bool BACK>
 __global__ void __launch_bounds__(256) delta_prep_kernel(const PrepArgs<TA> p) {
   constexpr int IN = kInParts<TA>;

@@ -9,8 +9,8 @@
 // A row stays in the registers of one wave (or, wide ones and few ones, of four
 // or sixteen waves), so the mean square is taken around the mean itself and
 // every value is read once and written once: memory bounds it (8192 x 2560 bf16 with
-// the sum 28.1 us, 6.0 TB/s; 131072 x 2048 187 to 204 us, 5.7 to 5.3; gradients of 8192
-// x 1536 26.9 us, 3.7, and 4.1 for the partial rows' sum).
+// the sum 27.3 us, 6.1 TB/s; 131072 x 2048 187 to 197 us, 5.7 to 5.5; gradients of 8192
+// x 1536 25.3 us, 4.0, and 4.1 for the partial rows' sum).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -386,12 +386,12 @@ struct NormPlan {
 
 // One wave a row while its share of a row stays within `most` pieces a lane:
 // five in the forward (8192 x 2560 bf16 with the sum 27.7 us, shared by five waves
-// 30.6; 131072 x 2048 188 and 201 us), three in the backward, which keeps three
-// times as many values (8192 x 1536 bf16 26.6 us, by three waves 32.7; 3001 x 515
-// float32 9.8 and 13.1 us).  Wider rows, and rows too few to fill the device, are
-// shared by waves (1 x 2560 bf16 with the sum 3.3 us, by one wave 4.6; 512 rows 4.5
-// and 5.4, 1000 rows 5.6 and 6.2; gradients of 1000 x 1536 11.0 and 11.7, of 512
-// rows 10.0 and 9.5).
+// 30.3; 131072 x 2048 191 and 235 us), three in the backward, which keeps three
+// times as many values (both launches, 8192 x 1536 bf16 27.6 us, by three waves
+// 34.4; 3001 x 515 float32 11.8 and 14.3 us).  Wider rows, and rows too few to fill
+// the device, are shared by waves (1 x 2560 bf16 with the sum 3.3 us, by one wave
+// 4.6; 512 rows 4.9 and 5.6, 1000 rows 6.5 and 6.3; gradients of 1000 x 1536 11.4
+// and 11.7, of 512 rows 10.4 and 9.4).
 NormPlan norm_plan(int64_t rows, int dim, int vec, int most) {
   const int pieces = (dim + vec - 1) / vec, nv = (pieces + 63) / 64;
   const bool few = rows < 4 * device_cus();
@@ -430,8 +430,8 @@ NormPlan bwd_plan(int64_t rows, int dim, int vec) {
 
 int norm_parts(const NormPlan& p, int64_t rows) {
   const int64_t n = (rows + p.groups - 1) / p.groups;
-  // (two workgroups a compute unit with one wave a row: 8192 x 1536 bf16 26.6 us,
-  // one 40.8, three 33.0)
+  // (two workgroups a compute unit with one wave a row: 8192 x 1536 bf16 27.6 us,
+  // one 36.1, three 33.8)
   const int64_t most = device_cus() * (p.multi ? 1 : 2);
   return static_cast<int>(n < 1 ? 1 : n > most ? most : n);
 }
