@@ -15,8 +15,8 @@
  * The conventions are those of ssm_scan.h: device pointers on the current HIP
  * device, row-major tensors (contiguous where no stride is given), "act"
  * tensors of the element type `dtype`, everything else float32; the state and
- * every sum that it or a gradient goes through are held to float32's precision,
- * bf16 results rounded to nearest even; the caller owns every buffer, the
+ * every sum that a state, an output or a gradient goes through are held to
+ * float32's precision, bf16 results rounded to nearest even; the caller owns every buffer, the
  * library allocates nothing and never synchronises; argument errors return a
  * negative ssm_status_t before anything is enqueued, with a message in
  * ssm_last_error().  Alignment: act tensors to their element size, float32 and

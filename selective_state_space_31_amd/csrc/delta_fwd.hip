@@ -133,8 +133,8 @@ __global__ void __launch_bounds__(512, KT <= 4 ? 2 : 1) delta_rec_kernel(const R
     for (int nb = 0; nb < NC; ++nb) y[nb] = zero;
     __syncthreads();
     if (nc == 0) return;  // (the chain waits at no further barrier either)
-    // (The first round finishes no chunk: it stores nothing.  Loads and stores are
-    // the same in every round, so that a wait for the oldest waits for no others: the
+    // (The first trip finishes no chunk: it stores nothing.  Loads and stores are the
+    // same in every trip, so that a wait for the oldest waits for no others: the
     // call with 131072 tokens 3.94 ms, with branches around them 4.22.)
     for (int c = 0;; ++c) {
       const int64_t slot = q.slot + c;
